@@ -68,11 +68,13 @@ enum wr_op {             /* operations that need workspace, for wr_workspace_byt
   WR_OP_WRING_GPTQ = 5,  /* rows, n, group, rank: wr_wring_solve with WR_RECODE_GPTQ */
   WR_OP_TRELLIS = 6,     /* rows, n, group = number of trellis states: wr_trellis_quantize */
   WR_OP_GEMV = 7,        /* rows = number of input vectors, n = n_store: wr_packed_gemv */
-  WR_OP_STATS = 8        /* rows: wr_quant_stats */
+  WR_OP_STATS = 8,       /* rows: wr_quant_stats */
+  WR_OP_NORM_BWD = 9     /* rows, n, group = gate_rows (0 when at least rows): wr_block_norm_backward */
 };
 
 enum wr_hessian_flags { WR_H_ZERO = 1 };               /* zero S before accumulating */
 enum wr_rotate_mode { WR_ROT_ROWS = 0, WR_ROT_ROWS_INVERSE = 1, WR_ROT_SYM = 2 };
+enum wr_i8_flags { WR_I8_SWIGLU = 1 };                 /* silu(first half of the rows) * second half */
 enum wr_wring_flags { WR_RECODE_NEAREST = 1, WR_RECODE_GPTQ = 2, WR_RECODE_SEARCH = 4 };
 
 typedef struct wr_ctx wr_ctx;
@@ -325,6 +327,87 @@ int wr_wring_target(wr_ctx* ctx, const void* target, int t_dtype, int64_t ldt, c
 int wr_quant_stats(wr_ctx* ctx, const float* T, int64_t ldt, const uint8_t* codes, const uint16_t* scales,
                    const uint8_t* bits, int64_t rows, int64_t n, int32_t group, const uint8_t* codes_ref,
                    const float* scales_raw, double* out);
+
+/*
+ * (g) Running a block in 8 bits.  The linear layers that are not worth 2 or 3 bits, and whole
+ * layers while a body is being quantized, run as 8-bit integer products: weights with one scale
+ * per output channel (wr_quant_rows_i8 of wr_materialize's output, or of the parent's weights),
+ * activations with one scale per token, made by wr_quant_rows_i8 or by the norm in front of the
+ * product (wr_block_norm).
+ *
+ * wr_quant_rows_i8: for each row of x (rows x n, WR_BF16 or WR_F32, ld ldx), with m = max |x|:
+ *   scales[r] = m / 127 (fp32, rounded to nearest),  q = rint(127 x / m), ties to even,
+ * decided as the correctly rounded fp32 quotient of fl(127 x) and m (exact ties for bf16 x).  A row
+ * of zeros gets scale 0 and codes 0; a row that holds an infinity or a NaN gets scale NaN and codes
+ * 0, so that everything computed from it is NaN.  q: rows x n int8, ld ldq >= n.  1 <= n; rows may
+ * be 0.  Any alignment and leading dimension; 16-byte aligned rows are read fastest.  No workspace.
+ */
+int wr_quant_rows_i8(wr_ctx* ctx, const void* x, int x_dtype, int64_t rows, int64_t n, int64_t ldx, int8_t* q,
+                     int64_t ldq, float* scales);
+
+/*
+ * wr_matmul_i8: y = tokens x weights^T in 8-bit integers.  x: batch x n int8 (ld ldx) with scales
+ * x_scales (batch fp32); w: rows x n int8 (ld ldw) with w_scales (rows fp32); bias: rows fp32 or null:
+ *   z[t][r] = x_scales[t] * w_scales[r] * sum_j x[t][j] w[r][j] + bias[r],   y = z (batch x rows),
+ * or with WR_I8_SWIGLU (rows even, h = rows / 2): y[t][r] = silu(z[t][r]) * z[t][h + r], batch x h,
+ * silu(v) = v / (1 + exp(-v)).  The sums are exact int32 (n <= 131071, WR_EUNSUPPORTED above); the
+ * scales and the bias are applied in fp32 and y (WR_BF16 or WR_F32, ld ldy) is rounded once.
+ * batch, rows and n may each be 0 (an empty sum is 0).  Any alignment and leading dimension of x
+ * and w; 16-byte aligned rows with n a multiple of 16 are fastest.  No workspace.
+ */
+int wr_matmul_i8(wr_ctx* ctx, const int8_t* x, int64_t ldx, const float* x_scales, int64_t batch, const int8_t* w,
+                 int64_t ldw, const float* w_scales, int64_t rows, int64_t n, const float* bias, int flags, void* y,
+                 int y_dtype, int64_t ldy);
+
+/*
+ * (h) The norms before and after a block, with the gate and the residual scale between them, in
+ * one pass.  For each of `rows` tokens, with the block's output b = branch and the residual stream
+ * x = resid, both of n values:
+ *   u  = w_post * b / rms(b)                       (u = b when w_post is null)
+ *   x' = resid_scale * x + branch_scale * g * u    (without x when resid is null, without the
+ *                                                   second term when branch is null, g = 1 when
+ *                                                   gate is null)
+ *   y  = w_pre * x' / rms(x'),                     rms(v) = sqrt(mean(v^2) + eps).
+ * gate has one row of n values for every gate_rows consecutive tokens (ceil(rows / gate_rows) rows,
+ * ld ldg), or one row for all of them when gate_rows is 0.  Types: branch, gate and y b_dtype;
+ * resid and resid_out r_dtype; w_post and w_pre w_dtype (n values each).
+ * Outputs, each of which may be null: resid_out = x' (ld ldo), y (ld ldy), the 8-bit form of y (q, ld
+ * ldq, with q_scales: as wr_quant_rows_i8 of the unrounded y), and stats (rows x 2 fp32: 1 / rms(b),
+ * 1 / rms(x'); 1 where that norm is absent), which wr_block_norm_backward takes.  y and q need w_pre.
+ * All sums and everything between the inputs and the outputs are fp32; y comes from the unrounded x'.
+ * A mean square beyond fp32's range makes that norm 0 * inf or 0, as the formula does in fp32.
+ * resid_out may be resid, and y may be branch, with the same type and leading dimension; other
+ * overlaps of outputs with inputs are not allowed.  1 <= n <= 16384 (WR_EUNSUPPORTED above); rows may be
+ * 0.  Any leading dimension; pointers aligned to their type.  No workspace.
+ */
+int wr_block_norm(wr_ctx* ctx, int64_t rows, int64_t n, const void* branch, int b_dtype, int64_t ldb,
+                  const void* w_post, const void* gate, int64_t ldg, int64_t gate_rows, float branch_scale,
+                  const void* resid, int r_dtype, int64_t ldr, float resid_scale, const void* w_pre, int w_dtype,
+                  float eps, void* resid_out, int64_t ldo, void* y, int64_t ldy, int8_t* q, int64_t ldq,
+                  float* q_scales, float* stats);
+
+/*
+ * Gradient of wr_block_norm: the same inputs and its stats, the gradients dy (b_dtype) of y and
+ * dresid_out (r_dtype) of x' (either may be null: zero; dy needs w_pre).  With xn = x' / rms(x'),
+ * bn = b / rms(b), d = dy * w_pre and e = branch_scale * g * w_post * dx':
+ *   dx'     = dresid_out + (d - xn mean(d xn)) / rms(x')
+ *   dresid  = resid_scale dx'                                  dw_pre  = sum over tokens of dy xn
+ *   dbranch = (e - bn mean(e bn)) / rms(b)   (e, without post norm)
+ *   dw_post = sum over tokens of branch_scale g dx' bn         dgate   = sum over the tokens of a
+ *                                                                        gate row of branch_scale dx' u.
+ * dbranch (b_dtype, ld lddb), dresid (r_dtype, ld lddr) and the fp32 dw_post (n), dw_pre (n) and dgate
+ * (gate rows x n, contiguous) may each be null; each needs its input.  With rows 0 the sums
+ * are written as 0 (dgate if gate_rows is 0).  The sums over tokens are fp32 in a
+ * fixed order (deterministic, no atomics).  x' is formed again from branch and resid.  dbranch may be
+ * dy or branch, and dresid may be dresid_out or resid, with the same type and leading dimension.
+ * Workspace: WR_OP_NORM_BWD (rows, n, gate_rows).
+ */
+int wr_block_norm_backward(wr_ctx* ctx, int64_t rows, int64_t n, const void* branch, int b_dtype, int64_t ldb,
+                           const void* w_post, const void* gate, int64_t ldg, int64_t gate_rows, float branch_scale,
+                           const void* resid, int r_dtype, int64_t ldr, float resid_scale, const void* w_pre,
+                           int w_dtype, const float* stats, const void* dy, int64_t lddy, const void* dresid_out,
+                           int64_t lddo, void* dbranch, int64_t lddb, void* dresid, int64_t lddr, float* dw_post,
+                           float* dgate, float* dw_pre);
 
 /* Static description of a status code. */
 const char* wr_strerror(int status);

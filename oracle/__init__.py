@@ -42,6 +42,7 @@ from .solve import solve_module, solve_rows
 from .materialize import bf16_rne_bits, bf16_bits_to_f64, materialize, materialize_exact
 from .trellis import viterbi as trellis_viterbi, greedy as trellis_greedy, decode as trellis_decode
 from .gemv import packed_gemv
+from .block import block_norm, block_norm_backward, gate_per_token, quant_rows_i8, matmul_i8
 
 __all__ = [
     "second_moment", "second_moment_chunks", "sum_of_products", "pad_square", "damp",
@@ -57,4 +58,5 @@ __all__ = [
     "bf16_rne_bits", "bf16_bits_to_f64", "materialize", "materialize_exact",
     "trellis_viterbi", "trellis_greedy", "trellis_decode",
     "packed_gemv",
+    "block_norm", "block_norm_backward", "gate_per_token", "quant_rows_i8", "matmul_i8",
 ]

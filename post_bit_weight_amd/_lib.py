@@ -18,9 +18,10 @@ WR_OK, WR_EINVAL, WR_EWORKSPACE, WR_EHIP, WR_EUNSUPPORTED, WR_ESCRATCH = 0, 1, 2
 WR_STATIC_SCRATCH_BYTES = 64 << 20
 WR_F32, WR_BF16 = 0, 1
 (WR_OP_HESSIAN, WR_OP_GPTQ, WR_OP_WRING, WR_OP_ROTATE, WR_OP_FINALIZE, WR_OP_WRING_GPTQ, WR_OP_TRELLIS,
- WR_OP_GEMV, WR_OP_STATS) = range(9)
+ WR_OP_GEMV, WR_OP_STATS, WR_OP_NORM_BWD) = range(10)
 WR_H_ZERO = 1
 WR_ROT_ROWS, WR_ROT_ROWS_INVERSE, WR_ROT_SYM = 0, 1, 2
+WR_I8_SWIGLU = 1
 WR_RECODE_NEAREST = 1
 WR_RECODE_GPTQ = 2
 WR_RECODE_SEARCH = 4
@@ -29,7 +30,8 @@ EXPORTED = (
     "wr_create", "wr_destroy", "wr_workspace_bytes", "wr_set_workspace",
     "wr_hessian_accumulate", "wr_hessian_accumulate_noalloc", "wr_hessian_finalize", "wr_hadamard_rotate",
     "wr_gptq_sweep", "wr_wring_solve", "wr_pack", "wr_unpack", "wr_materialize", "wr_trellis_quantize",
-    "wr_packed_gemv", "wr_set_scale_trace", "wr_wring_target", "wr_quant_stats", "wr_strerror",
+    "wr_packed_gemv", "wr_set_scale_trace", "wr_wring_target", "wr_quant_stats",
+    "wr_quant_rows_i8", "wr_matmul_i8", "wr_block_norm", "wr_block_norm_backward", "wr_strerror",
 )
 
 
@@ -76,6 +78,12 @@ def load():
         "wr_set_scale_trace": (I, [P, P, I64]),
         "wr_wring_target": (I, [P, P, I, I64, P, P, c.c_int32, F, I, I64, I64, P, c.c_int32, P, P, P, P]),
         "wr_quant_stats": (I, [P, P, I64, P, P, P, I64, I64, c.c_int32, P, P, P]),
+        "wr_quant_rows_i8": (I, [P, P, I, I64, I64, I64, P, I64, P]),
+        "wr_matmul_i8": (I, [P, P, I64, P, I64, P, I64, P, I64, I64, P, I, P, I, I64]),
+        "wr_block_norm": (I, [P, I64, I64, P, I, I64, P, P, I64, I64, F, P, I, I64, F, P, I, F, P, I64, P, I64, P, I64,
+                              P, P]),
+        "wr_block_norm_backward": (I, [P, I64, I64, P, I, I64, P, P, I64, I64, F, P, I, I64, F, P, I, P, P, I64, P, I64,
+                                       P, I64, P, I64, P, P, P]),
         "wr_strerror": (c.c_char_p, [I]),
     }
     for name, (res, args) in sig.items():
@@ -405,3 +413,128 @@ def wr_quant_stats(ctx, codes, scales, bits, group, out, T=None, codes_ref=None,
     _check("wr_quant_stats", load().wr_quant_stats(
         ctx.handle, _ptr(T), _rowmajor(T, "T") if T is not None else 0, _ptr(codes), _ptr(scales), _ptr(bits), rows, n,
         int(group), _ptr(codes_ref), _ptr(scales_raw), _ptr(out)))
+
+
+def _matrix(t, name, dtypes, shape):
+    """Row stride of a row-major GPU matrix of the given type and shape."""
+    _dev(t, name, dtypes)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must be row-major")
+    return t.stride(0)
+
+
+def _vector(t, name, dtypes, count):
+    _dev(t, name, dtypes)
+    if t is not None and (t.numel() != count or not t.is_contiguous()):
+        raise ValueError(f"{name} must hold {count} contiguous values")
+
+
+_F32 = (torch.float32,)
+_I8 = (torch.int8,)
+
+
+def wr_quant_rows_i8(ctx, x, q, scales):
+    """8-bit codes q (rows x n int8) and scales (rows fp32) of each row of x (bf16 or fp32)."""
+    if x.dim() != 2:
+        raise ValueError("x must be rows x n")
+    rows, n = x.shape
+    ldx = _matrix(x, "x", FLOATS, (rows, n))
+    ldq = _matrix(q, "q", _I8, (rows, n))
+    _vector(scales, "scales", _F32, rows)
+    _check("wr_quant_rows_i8", load().wr_quant_rows_i8(ctx.handle, x.data_ptr(), _wdtype(x), rows, n, ldx,
+                                                       q.data_ptr(), ldq, scales.data_ptr()))
+
+
+def wr_matmul_i8(ctx, x, x_scales, w, w_scales, y, bias=None, swiglu=False):
+    """y (batch x rows, bf16 or fp32) = x (batch x n int8) times w (rows x n int8) transposed, scaled per token
+    and per row, plus bias; with swiglu y is batch x rows / 2: silu(first half of the rows) * second half."""
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x must be batch x n and w rows x n")
+    batch, n = x.shape
+    rows = w.shape[0]
+    ldx = _matrix(x, "x", _I8, (batch, n))
+    ldw = _matrix(w, "w", _I8, (rows, n))
+    if swiglu and rows % 2:
+        raise ValueError("swiglu needs an even number of rows")
+    ldy = _matrix(y, "y", FLOATS, (batch, rows // 2 if swiglu else rows))
+    _vector(x_scales, "x_scales", _F32, batch)
+    _vector(w_scales, "w_scales", _F32, rows)
+    _vector(bias, "bias", _F32, rows)
+    _check("wr_matmul_i8", load().wr_matmul_i8(
+        ctx.handle, x.data_ptr(), ldx, x_scales.data_ptr(), batch, w.data_ptr(), ldw, w_scales.data_ptr(), rows, n,
+        _ptr(bias), WR_I8_SWIGLU if swiglu else 0, y.data_ptr(), _wdtype(y), ldy))
+
+
+def _norm_inputs(branch, resid, w_post, gate, gate_rows, w_pre, b_type, r_type):
+    """(rows, n, the C call's leading arguments up to w_dtype without the scales) of a block norm's inputs."""
+    like = branch if branch is not None else resid
+    if like is None or like.dim() != 2:
+        raise ValueError("branch or resid must be given, as rows x n")
+    rows, n = shape = tuple(like.shape)
+    bt = (b_type,)
+    ldb = _matrix(branch, "branch", bt, shape) if branch is not None else n
+    ldr = _matrix(resid, "resid", (r_type,), shape) if resid is not None else n
+    ldg = n
+    if gate is not None:
+        gates = -(-rows // gate_rows) if gate_rows else 1
+        ldg = _matrix(gate, "gate", bt, (gates, n))
+    weights = [w for w in (w_post, w_pre) if w is not None]
+    if len(weights) == 2 and w_post.dtype != w_pre.dtype:
+        raise ValueError("w_post and w_pre must have one dtype")
+    _vector(w_post, "w_post", FLOATS, n)
+    _vector(w_pre, "w_pre", FLOATS, n)
+    return rows, n, ldb, ldg, ldr, _wdtype(weights[0]) if weights else WR_F32
+
+
+def wr_block_norm(ctx, eps, branch=None, resid=None, w_post=None, gate=None, gate_rows=0, branch_scale=1.0,
+                  resid_scale=1.0, w_pre=None, resid_out=None, y=None, q=None, q_scales=None, stats=None):
+    """resid_out = x' = resid_scale resid + branch_scale gate w_post branch / rms(branch); y = w_pre x' / rms(x'),
+    and / or its 8-bit form (q, q_scales); stats (rows x 2 fp32) for wr_block_norm_backward.  Outputs left out are
+    not written.  gate: one row for every gate_rows consecutive rows (0: one row for all)."""
+    acts = [t for t in (branch, y, gate) if t is not None]
+    b_type = acts[0].dtype if acts else (resid.dtype if resid is not None else torch.float32)
+    res = [t for t in (resid, resid_out) if t is not None]
+    r_type = res[0].dtype if res else b_type
+    rows, n, ldb, ldg, ldr, wt = _norm_inputs(branch, resid, w_post, gate, gate_rows, w_pre, b_type, r_type)
+    shape = (rows, n)
+    ldo = _matrix(resid_out, "resid_out", (r_type,), shape) if resid_out is not None else n
+    ldy = _matrix(y, "y", (b_type,), shape) if y is not None else n
+    ldq = _matrix(q, "q", _I8, shape) if q is not None else n
+    _vector(q_scales, "q_scales", _F32, rows)
+    _vector(stats, "stats", _F32, 2 * rows)
+    _check("wr_block_norm", load().wr_block_norm(
+        ctx.handle, rows, n, _ptr(branch), WR_BF16 if b_type == torch.bfloat16 else WR_F32, ldb, _ptr(w_post),
+        _ptr(gate), ldg, int(gate_rows), float(branch_scale), _ptr(resid),
+        WR_BF16 if r_type == torch.bfloat16 else WR_F32, ldr, float(resid_scale), _ptr(w_pre), wt, float(eps),
+        _ptr(resid_out), ldo, _ptr(y), ldy, _ptr(q), ldq, _ptr(q_scales), _ptr(stats)))
+
+
+def wr_block_norm_backward(ctx, stats, branch=None, resid=None, w_post=None, gate=None, gate_rows=0, branch_scale=1.0,
+                           resid_scale=1.0, w_pre=None, dy=None, dresid_out=None, dbranch=None, dresid=None,
+                           dw_post=None, dgate=None, dw_pre=None):
+    """Gradients of wr_block_norm's inputs from dy (of y) and dresid_out (of x'), either of which may be None.
+    Outputs left out are not formed; dw_post, dgate (as gate's shape) and dw_pre are fp32."""
+    acts = [t for t in (branch, dy, gate) if t is not None]
+    b_type = acts[0].dtype if acts else (resid.dtype if resid is not None else torch.float32)
+    res = [t for t in (resid, dresid_out) if t is not None]
+    r_type = res[0].dtype if res else b_type
+    rows, n, ldb, ldg, ldr, wt = _norm_inputs(branch, resid, w_post, gate, gate_rows, w_pre, b_type, r_type)
+    shape = (rows, n)
+    lddy = _matrix(dy, "dy", (b_type,), shape) if dy is not None else n
+    lddo = _matrix(dresid_out, "dresid_out", (r_type,), shape) if dresid_out is not None else n
+    lddb = _matrix(dbranch, "dbranch", (b_type,), shape) if dbranch is not None else n
+    lddr = _matrix(dresid, "dresid", (r_type,), shape) if dresid is not None else n
+    _vector(stats, "stats", _F32, 2 * rows)
+    _vector(dw_post, "dw_post", _F32, n)
+    _vector(dw_pre, "dw_pre", _F32, n)
+    if dgate is not None:
+        _vector(dgate, "dgate", _F32, gate.numel() if gate is not None else 0)
+    ctx.ensure_workspace(wr_workspace_bytes(WR_OP_NORM_BWD, rows, n, min(int(gate_rows), rows)))
+    _check("wr_block_norm_backward", load().wr_block_norm_backward(
+        ctx.handle, rows, n, _ptr(branch), WR_BF16 if b_type == torch.bfloat16 else WR_F32, ldb, _ptr(w_post),
+        _ptr(gate), ldg, int(gate_rows), float(branch_scale), _ptr(resid),
+        WR_BF16 if r_type == torch.bfloat16 else WR_F32, ldr, float(resid_scale), _ptr(w_pre), wt, _ptr(stats),
+        _ptr(dy), lddy, _ptr(dresid_out), lddo, _ptr(dbranch), lddb, _ptr(dresid), lddr, _ptr(dw_post), _ptr(dgate),
+        _ptr(dw_pre)))

@@ -33,13 +33,34 @@ int wr_trellis_quantize_impl(wr_ctx*, const float*, int64_t, int64_t, int64_t, i
                              uint8_t*, int64_t, float*, int64_t, double*);
 int wr_materialize_impl(wr_ctx*, const uint8_t*, int64_t, int64_t, int32_t, int32_t, int32_t, const int8_t*, int64_t,
                         uint16_t*, int64_t);
+int wr_quant_rows_i8_impl(wr_ctx*, const void*, int, int64_t, int64_t, int64_t, int8_t*, int64_t, float*);
+int wr_matmul_i8_impl(wr_ctx*, const int8_t*, int64_t, const float*, int64_t, const int8_t*, int64_t, const float*,
+                      int64_t, int64_t, const float*, bool, void*, int, int64_t);
+int wr_block_norm_impl(wr_ctx*, int64_t, int64_t, const void*, int, int64_t, const void*, const void*, int64_t, int64_t,
+                       float, const void*, int, int64_t, float, const void*, int, float, void*, int64_t, void*, int64_t,
+                       int8_t*, int64_t, float*, float*);
+size_t wr_norm_bwd_ws_bytes(int64_t rows, int64_t n, int64_t gate_rows);
+int wr_block_norm_backward_impl(wr_ctx*, int64_t, int64_t, const void*, int, int64_t, const void*, const void*, int64_t,
+                                int64_t, float, const void*, int, int64_t, float, const void*, int, const float*,
+                                const void*, int64_t, const void*, int64_t, void*, int64_t, void*, int64_t, float*,
+                                float*, float*);
 
 namespace {
 
 constexpr int kDefaultCUs = 256;
 
+constexpr int64_t kNormMax = 16384;   // widest row of the block norm (a workgroup's registers)
+constexpr int64_t kI8Max = 131071;    // longest exact int32 sum of 8-bit products: 131071 * 2^14 < 2^31
+constexpr int64_t kRowsMax = 2147483647;
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 bool valid_dtype(int d) { return d == WR_F32 || d == WR_BF16; }
+size_t dtype_bytes(int d) { return d == WR_BF16 ? 2 : 4; }
+// A matrix of `rows` rows of n values: absent, or aligned to its type with ld >= n (a single row's ld is
+// not used).
+bool rows_ok(const void* p, int dtype, int64_t rows, int64_t n, int64_t ld) {
+  return !p || (aligned(p, dtype_bytes(dtype)) && (ld >= n || rows <= 1));
+}
 bool pow2(int64_t v) { return v > 0 && (v & (v - 1)) == 0; }
 size_t dsize(int d) { return d == WR_F32 ? 4 : 2; }
 
@@ -106,6 +127,7 @@ size_t wr_workspace_bytes(int op, int64_t rows, int64_t n, int32_t group, int32_
     case WR_OP_WRING_GPTQ: return group > 0 ? wr_wring_gptq_ws_bytes(rows, n, group, rank > 0 ? rank : 0) : 0;
     case WR_OP_TRELLIS: return group >= 2 && group <= 16 ? wr_trellis_ws_bytes(rows, n, group) : 0;
     case WR_OP_GEMV: return rows >= 1 && rows <= 8 ? wr_gemv_ws_bytes(n, (int32_t)rows) : 0;
+    case WR_OP_NORM_BWD: return n <= kNormMax && group >= 0 ? wr_norm_bwd_ws_bytes(rows, n, group) : 0;
     case WR_OP_STATS: return wr_stats_ws_bytes(rows > 0 ? rows : 1);
     default: return 0;
   }
@@ -317,6 +339,99 @@ int wr_quant_stats(wr_ctx* ctx, const float* T, int64_t ldt, const uint8_t* code
   DeviceScope ds(ctx->device);
   if (!ds.ok) return WR_EHIP;
   return wr_quant_stats_impl(ctx, T, ldt, codes, scales, bits, rows, n, group, codes_ref, scales_raw, out);
+}
+
+int wr_quant_rows_i8(wr_ctx* ctx, const void* x, int x_dtype, int64_t rows, int64_t n, int64_t ldx, int8_t* q,
+                     int64_t ldq, float* scales) {
+  if (!ctx || !valid_dtype(x_dtype) || rows < 0 || rows > kRowsMax || n <= 0) return WR_EINVAL;
+  if (rows == 0) return WR_OK;
+  if (!x || !q || !scales || !rows_ok(x, x_dtype, rows, n, ldx) || (ldq < n && rows > 1) || !aligned(scales, 4))
+    return WR_EINVAL;
+  DeviceScope ds(ctx->device);
+  if (!ds.ok) return WR_EHIP;
+  return wr_quant_rows_i8_impl(ctx, x, x_dtype, rows, n, ldx, q, ldq, scales);
+}
+
+int wr_matmul_i8(wr_ctx* ctx, const int8_t* x, int64_t ldx, const float* x_scales, int64_t batch, const int8_t* w,
+                 int64_t ldw, const float* w_scales, int64_t rows, int64_t n, const float* bias, int flags, void* y,
+                 int y_dtype, int64_t ldy) {
+  const bool glu = flags & WR_I8_SWIGLU;
+  if (!ctx || !valid_dtype(y_dtype) || batch < 0 || batch > kRowsMax || rows < 0 || rows > kRowsMax / 2 || n < 0 ||
+      (flags & ~WR_I8_SWIGLU) || (glu && rows % 2 != 0))
+    return WR_EINVAL;
+  if (batch == 0 || rows == 0) return WR_OK;
+  const int64_t outs = glu ? rows / 2 : rows;
+  if (!x_scales || !w_scales || !y || (n > 0 && (!x || !w)) || (ldx < n && batch > 1) || (ldw < n && rows > 1) ||
+      !rows_ok(y, y_dtype, batch, outs, ldy) || !aligned(x_scales, 4) || !aligned(w_scales, 4) || !aligned(bias, 4))
+    return WR_EINVAL;
+  if (n > kI8Max) return WR_EUNSUPPORTED;
+  DeviceScope ds(ctx->device);
+  if (!ds.ok) return WR_EHIP;
+  return wr_matmul_i8_impl(ctx, x, ldx, x_scales, batch, w, ldw, w_scales, rows, n, bias, glu, y, y_dtype, ldy);
+}
+
+// What the norm and its gradient check alike.
+static int norm_args(wr_ctx* ctx, int64_t rows, int64_t n, const void* branch, int b_dtype, int64_t ldb,
+                     const void* w_post, const void* gate, int64_t ldg, int64_t gate_rows, float branch_scale,
+                     const void* resid, int r_dtype, int64_t ldr, float resid_scale, const void* w_pre, int w_dtype) {
+  if (!ctx || rows < 0 || rows > kRowsMax || n <= 0 || gate_rows < 0 || !valid_dtype(b_dtype) ||
+      !valid_dtype(r_dtype) || !valid_dtype(w_dtype) || !std::isfinite(branch_scale) || !std::isfinite(resid_scale))
+    return WR_EINVAL;
+  if (rows == 0) return WR_OK;
+  if ((!branch && !resid) || (!branch && (w_post || gate))) return WR_EINVAL;
+  const int64_t gates = gate_rows == 0 || gate_rows >= rows ? 1 : (rows + gate_rows - 1) / gate_rows;
+  if (!rows_ok(branch, b_dtype, rows, n, ldb) || !rows_ok(resid, r_dtype, rows, n, ldr) ||
+      !rows_ok(gate, b_dtype, gates, n, ldg) || !rows_ok(w_post, w_dtype, 1, n, n) ||
+      !rows_ok(w_pre, w_dtype, 1, n, n))
+    return WR_EINVAL;
+  return n > kNormMax ? WR_EUNSUPPORTED : WR_OK;
+}
+
+int wr_block_norm(wr_ctx* ctx, int64_t rows, int64_t n, const void* branch, int b_dtype, int64_t ldb,
+                  const void* w_post, const void* gate, int64_t ldg, int64_t gate_rows, float branch_scale,
+                  const void* resid, int r_dtype, int64_t ldr, float resid_scale, const void* w_pre, int w_dtype,
+                  float eps, void* resid_out, int64_t ldo, void* y, int64_t ldy, int8_t* q, int64_t ldq,
+                  float* q_scales, float* stats) {
+  const int rc = norm_args(ctx, rows, n, branch, b_dtype, ldb, w_post, gate, ldg, gate_rows, branch_scale, resid,
+                           r_dtype, ldr, resid_scale, w_pre, w_dtype);
+  if (rc != WR_OK) return rc;
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return WR_EINVAL;
+  if (rows == 0) return WR_OK;
+  if (((y || q) && !w_pre) || (!resid_out && !y && !q && !stats) || (q == nullptr) != (q_scales == nullptr))
+    return WR_EINVAL;
+  if (!rows_ok(resid_out, r_dtype, rows, n, ldo) || !rows_ok(y, b_dtype, rows, n, ldy) ||
+      (q && ldq < n && rows > 1) || !aligned(q_scales, 4) || !aligned(stats, 4))
+    return WR_EINVAL;
+  DeviceScope ds(ctx->device);
+  if (!ds.ok) return WR_EHIP;
+  return wr_block_norm_impl(ctx, rows, n, branch, b_dtype, ldb, w_post, gate, ldg, gate_rows, branch_scale, resid,
+                            r_dtype, ldr, resid_scale, w_pre, w_dtype, eps, resid_out, ldo, y, ldy, q, ldq, q_scales,
+                            stats);
+}
+
+int wr_block_norm_backward(wr_ctx* ctx, int64_t rows, int64_t n, const void* branch, int b_dtype, int64_t ldb,
+                           const void* w_post, const void* gate, int64_t ldg, int64_t gate_rows, float branch_scale,
+                           const void* resid, int r_dtype, int64_t ldr, float resid_scale, const void* w_pre,
+                           int w_dtype, const float* stats, const void* dy, int64_t lddy, const void* dresid_out,
+                           int64_t lddo, void* dbranch, int64_t lddb, void* dresid, int64_t lddr, float* dw_post,
+                           float* dgate, float* dw_pre) {
+  const int rc = norm_args(ctx, rows, n, branch, b_dtype, ldb, w_post, gate, ldg, gate_rows, branch_scale, resid,
+                           r_dtype, ldr, resid_scale, w_pre, w_dtype);
+  if (rc != WR_OK) return rc;
+  if (rows > 0 && ((!dy && !dresid_out) || (dy && !w_pre) || ((w_post || dy) && !stats) || (dbranch && !branch) ||
+                   (dresid && !resid)))
+    return WR_EINVAL;
+  if ((dw_post && rows > 0 && !w_post) || (dgate && rows > 0 && !gate) || (dw_pre && rows > 0 && !dy)) return WR_EINVAL;
+  if (!rows_ok(dy, b_dtype, rows, n, lddy) || !rows_ok(dresid_out, r_dtype, rows, n, lddo) ||
+      !rows_ok(dbranch, b_dtype, rows, n, lddb) || !rows_ok(dresid, r_dtype, rows, n, lddr) || !aligned(stats, 4) ||
+      !aligned(dw_post, 4) || !aligned(dgate, 4) || !aligned(dw_pre, 4))
+    return WR_EINVAL;
+  if (n > kNormMax) return WR_EUNSUPPORTED;
+  DeviceScope ds(ctx->device);
+  if (!ds.ok) return WR_EHIP;
+  return wr_block_norm_backward_impl(ctx, rows, n, branch, b_dtype, ldb, w_post, gate, ldg, gate_rows, branch_scale,
+                                     resid, r_dtype, ldr, resid_scale, w_pre, w_dtype, stats, dy, lddy, dresid_out,
+                                     lddo, dbranch, lddb, dresid, lddr, dw_post, dgate, dw_pre);
 }
 
 const char* wr_strerror(int status) {
