@@ -125,9 +125,112 @@ __global__ __launch_bounds__(256) void matmul_i8_tile_kernel(const I8Args a) {
     }
 }
 
+// Few tokens (up to 64): the weights are read once, straight from memory into matrix-core operands, and
+// everything else is hidden behind that.  A workgroup owns 16 outputs (with GLU or RF = 2, 32 weight rows) for
+// all tokens; its NW waves cut the sum into contiguous ranges of 64-byte steps, so that a wave has
+// many rows' loads in flight at once, and add their int32 sums in LDS.  A 16x16x64 MFMA takes 64
+// bytes of 16 weight rows (lane l: row l % 16, bytes 16 (l / 16) .. + 15) against 16 tokens; tokens
+// past the batch repeat its last one and are not stored.
+template <typename TY, bool GLU, int RF, int NT, int NW, int U>
+__global__ __launch_bounds__(64 * NW) void matmul_i8_few_kernel(const I8Args a) {
+  __shared__ int32_t red[NW][RF * NT][256];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int outs = GLU ? a.rows / 2 : a.rows;
+  const int o0 = blockIdx.x * (GLU ? 16 : 16 * RF), t0 = blockIdx.y * 16 * NT;
+  const int r = lane & 15, kb = 16 * (lane >> 4);
+  const int8_t* wrow[RF];
+  const int8_t* xrow[NT];
+#pragma unroll
+  for (int f = 0; f < RF; ++f) {
+    const int o = GLU ? std::min(o0 + r, outs - 1) + f * outs : std::min(o0 + 16 * f + r, outs - 1);
+    wrow[f] = a.w + o * a.ldw;
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) xrow[t] = a.x + std::min(t0 + 16 * t + r, a.batch - 1) * a.ldx;
+
+  i32x4 acc[RF][NT] = {};
+  const int steps = a.n / 64, s0 = steps * wave / NW, s1 = steps * (wave + 1) / NW;
+  for (int s = s0; s < s1; s += U) {
+    i32x4 fw[U][RF], fx[U][NT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = 64 * std::min(s + u, s1 - 1) + kb;
+#pragma unroll
+      for (int f = 0; f < RF; ++f) fw[u][f] = __builtin_bit_cast(i32x4, (u32x4)*reinterpret_cast<const u32x4_any*>(wrow[f] + c));
+#pragma unroll
+      for (int t = 0; t < NT; ++t) fx[u][t] = __builtin_bit_cast(i32x4, (u32x4)*reinterpret_cast<const u32x4_any*>(xrow[t] + c));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool past = s + u >= s1;  // a step past the range was read again and counts nothing
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const i32x4 x = past ? i32x4{0, 0, 0, 0} : fx[u][t];
+#pragma unroll
+        for (int f = 0; f < RF; ++f) acc[f][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u][f], x, acc[f][t], 0, 0, 0);
+      }
+    }
+  }
+  if (a.n % 64 != 0 && wave == NW - 1) {
+    const int c = 64 * steps + kb;
+    i32x4 fw[RF];
+#pragma unroll
+    for (int f = 0; f < RF; ++f) fw[f] = __builtin_bit_cast(i32x4, load16(wrow[f], c, a.n));
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const i32x4 x = __builtin_bit_cast(i32x4, load16(xrow[t], c, a.n));
+#pragma unroll
+      for (int f = 0; f < RF; ++f) acc[f][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[f], x, acc[f][t], 0, 0, 0);
+    }
+  }
+  // Register v of lane l holds weight row 4 (l / 16) + v and token l % 16 of a 16 x 16 block.
+#pragma unroll
+  for (int f = 0; f < RF; ++f)
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) red[wave][f * NT + t][16 * (lane & 15) + 4 * (lane >> 4) + v] = acc[f][t][v];
+  __syncthreads();
+  TY* y = (TY*)a.y;
+  constexpr int kBlocks = GLU ? NT : RF * NT;  // blocks of 16 outputs x 16 tokens to store
+  for (int i = threadIdx.x; i < kBlocks * 256; i += 64 * NW) {
+    const int blk = i >> 8, e = i & 255, f = blk / NT, t = t0 + 16 * (blk % NT) + (e >> 4), o = o0 + 16 * f + (e & 15);
+    if (t >= a.batch || o >= outs) continue;
+    int32_t sum = 0, up = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      sum += red[w][blk][e];
+      if constexpr (GLU) up += red[w][NT + blk][e];
+    }
+    const float xs = a.xs[t];
+    float z = (float)sum * xs * a.ws[o];
+    if (a.bias) z += a.bias[o];
+    if constexpr (GLU) {
+      float u = (float)up * xs * a.ws[outs + o];
+      if (a.bias) u += a.bias[outs + o];
+      z = silu(z) * u;
+    }
+    put(y + t * a.ldy + o, z);
+  }
+}
+
 }  // namespace wr
 
 using namespace wr;
+
+template <typename TY, bool GLU, int NT>
+static void few_launch(wr_ctx* ctx, const I8Args& a) {
+  const int outs = GLU ? a.rows / 2 : a.rows;
+  constexpr int RF = GLU ? 2 : 1;
+  const dim3 grid((outs + 15) / 16, (a.batch + 16 * NT - 1) / (16 * NT));
+  constexpr int U = NT == 1 ? 8 : 4;
+  if (a.n >= 4096) {
+    constexpr int NW = NT <= 2 ? 16 : 8;
+    hipLaunchKernelGGL((matmul_i8_few_kernel<TY, GLU, RF, NT, NW, U>), grid, dim3(64 * NW), 0, ctx->stream, a);
+  } else {
+    hipLaunchKernelGGL((matmul_i8_few_kernel<TY, GLU, RF, NT, 8, U>), grid, dim3(512), 0, ctx->stream, a);
+  }
+}
 
 int wr_matmul_i8_impl(wr_ctx* ctx, const int8_t* x, int64_t ldx, const float* x_scales, int64_t batch, const int8_t* w,
                       int64_t ldw, const float* w_scales, int64_t rows, int64_t n, const float* bias, bool glu, void* y,
@@ -137,6 +240,21 @@ int wr_matmul_i8_impl(wr_ctx* ctx, const int8_t* x, int64_t ldx, const float* x_
   for (int64_t t0 = 0; t0 < batch; t0 += slice) {
     const I8Args a{x + t0 * ldx, ldx, x_scales + t0, (int)std::min(slice, batch - t0), w, ldw, w_scales, (int)rows,
                    (int)n, bias, (char*)y + t0 * ldy * (y_dtype == WR_BF16 ? 2 : 4), ldy};
+    if (a.batch <= 64) {
+      auto few = [&](auto ty, auto g) {
+        using TY = decltype(ty);
+        constexpr bool kGlu = decltype(g)::value;
+        if (a.batch <= 16) few_launch<TY, kGlu, 1>(ctx, a);
+        else if (a.batch <= 32) few_launch<TY, kGlu, 2>(ctx, a);
+        else few_launch<TY, kGlu, 4>(ctx, a);
+      };
+      if (y_dtype == WR_BF16 && glu) few(uint16_t{}, std::true_type{});
+      else if (y_dtype == WR_BF16) few(uint16_t{}, std::false_type{});
+      else if (glu) few(float{}, std::true_type{});
+      else few(float{}, std::false_type{});
+      WR_CHECK_LAUNCH();
+      continue;
+    }
     const dim3 grid((unsigned)((outs + per - 1) / per), (unsigned)((a.batch + T8 - 1) / T8));
     if (y_dtype == WR_BF16 && glu) hipLaunchKernelGGL((matmul_i8_tile_kernel<uint16_t, true>), grid, dim3(256), 0, ctx->stream, a);
     else if (y_dtype == WR_BF16) hipLaunchKernelGGL((matmul_i8_tile_kernel<uint16_t, false>), grid, dim3(256), 0, ctx->stream, a);
