@@ -416,35 +416,43 @@ def wr_quant_stats(ctx, codes, scales, bits, group, out, T=None, codes_ref=None,
 
 
 def _matrix(t, name, dtypes, shape):
-    """Row stride of a row-major GPU matrix of the given type and shape."""
-    _dev(t, name, dtypes)
-    if tuple(t.shape) != shape:
+    """Row stride of a row-major GPU matrix of one of the types and the shape; one test for the usual case, since
+    for a single token these checks are a good part of a call."""
+    if t.dtype not in dtypes or t.shape != shape or not t.is_cuda:
+        _dev(t, name, dtypes)
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    if shape[1] > 1 and t.stride(1) != 1:
+    strides = t.stride()
+    if strides[1] != 1 and shape[1] > 1:
         raise ValueError(f"{name} must be row-major")
-    return t.stride(0)
+    return strides[0]
 
 
 def _vector(t, name, dtypes, count):
-    _dev(t, name, dtypes)
-    if t is not None and (t.numel() != count or not t.is_contiguous()):
+    """Address of a contiguous GPU vector of `count` values, None for none."""
+    if t is None:
+        return None
+    if t.dtype not in dtypes or t.numel() != count or not t.is_cuda or not t.is_contiguous():
+        _dev(t, name, dtypes)
         raise ValueError(f"{name} must hold {count} contiguous values")
+    return t.data_ptr()
 
 
 _F32 = (torch.float32,)
 _I8 = (torch.int8,)
+_WR_DTYPE = {torch.float32: WR_F32, torch.bfloat16: WR_BF16}
 
 
 def wr_quant_rows_i8(ctx, x, q, scales):
     """8-bit codes q (rows x n int8) and scales (rows fp32) of each row of x (bf16 or fp32)."""
     if x.dim() != 2:
         raise ValueError("x must be rows x n")
-    rows, n = x.shape
-    ldx = _matrix(x, "x", FLOATS, (rows, n))
-    ldq = _matrix(q, "q", _I8, (rows, n))
-    _vector(scales, "scales", _F32, rows)
-    _check("wr_quant_rows_i8", load().wr_quant_rows_i8(ctx.handle, x.data_ptr(), _wdtype(x), rows, n, ldx,
-                                                       q.data_ptr(), ldq, scales.data_ptr()))
+    shape = x.shape
+    rows, n = shape
+    ldx = _matrix(x, "x", FLOATS, shape)
+    ldq = _matrix(q, "q", _I8, shape)
+    s = _vector(scales, "scales", _F32, rows)
+    _check("wr_quant_rows_i8", load().wr_quant_rows_i8(ctx.handle, x.data_ptr(), _WR_DTYPE[x.dtype], rows, n, ldx,
+                                                       q.data_ptr(), ldq, s))
 
 
 def wr_matmul_i8(ctx, x, x_scales, w, w_scales, y, bias=None, swiglu=False):
@@ -454,38 +462,62 @@ def wr_matmul_i8(ctx, x, x_scales, w, w_scales, y, bias=None, swiglu=False):
         raise ValueError("x must be batch x n and w rows x n")
     batch, n = x.shape
     rows = w.shape[0]
-    ldx = _matrix(x, "x", _I8, (batch, n))
-    ldw = _matrix(w, "w", _I8, (rows, n))
     if swiglu and rows % 2:
         raise ValueError("swiglu needs an even number of rows")
+    ldx = _matrix(x, "x", _I8, (batch, n))
+    ldw = _matrix(w, "w", _I8, (rows, n))
     ldy = _matrix(y, "y", FLOATS, (batch, rows // 2 if swiglu else rows))
-    _vector(x_scales, "x_scales", _F32, batch)
-    _vector(w_scales, "w_scales", _F32, rows)
-    _vector(bias, "bias", _F32, rows)
+    xs = _vector(x_scales, "x_scales", _F32, batch)
+    ws = _vector(w_scales, "w_scales", _F32, rows)
+    b = _vector(bias, "bias", _F32, rows)
     _check("wr_matmul_i8", load().wr_matmul_i8(
-        ctx.handle, x.data_ptr(), ldx, x_scales.data_ptr(), batch, w.data_ptr(), ldw, w_scales.data_ptr(), rows, n,
-        _ptr(bias), WR_I8_SWIGLU if swiglu else 0, y.data_ptr(), _wdtype(y), ldy))
+        ctx.handle, x.data_ptr(), ldx, xs, batch, w.data_ptr(), ldw, ws, rows, n, b, WR_I8_SWIGLU if swiglu else 0,
+        y.data_ptr(), _WR_DTYPE[y.dtype], ldy))
 
 
-def _norm_inputs(branch, resid, w_post, gate, gate_rows, w_pre, b_type, r_type):
-    """(rows, n, the C call's leading arguments up to w_dtype without the scales) of a block norm's inputs."""
+def _norm_inputs(branch, resid, w_post, gate, gate_rows, branch_scale, resid_scale, w_pre, acts, res):
+    """The leading arguments of a block norm's C calls, rows to w_dtype, checked; the first of `acts` and of `res`
+    that is given has the type of the activations and of the residual stream."""
     like = branch if branch is not None else resid
     if like is None or like.dim() != 2:
         raise ValueError("branch or resid must be given, as rows x n")
-    rows, n = shape = tuple(like.shape)
-    bt = (b_type,)
-    ldb = _matrix(branch, "branch", bt, shape) if branch is not None else n
-    ldr = _matrix(resid, "resid", (r_type,), shape) if resid is not None else n
-    ldg = n
+    bt = rt = None
+    for t in acts:
+        if t is not None:
+            bt = t.dtype
+            break
+    for t in res:
+        if t is not None:
+            rt = t.dtype
+            break
+    bt, rt = bt or rt, rt or bt
+    if bt not in _WR_DTYPE or rt not in _WR_DTYPE:
+        raise ValueError(f"activations of {bt} and a residual stream of {rt}: expected types among {FLOATS}")
+    shape = like.shape
+    rows, n = shape
+    pb = pr = pg = None
+    ldb = ldr = ldg = n
+    if branch is not None:
+        ldb, pb = _matrix(branch, "branch", (bt,), shape), branch.data_ptr()
+    if resid is not None:
+        ldr, pr = _matrix(resid, "resid", (rt,), shape), resid.data_ptr()
     if gate is not None:
-        gates = -(-rows // gate_rows) if gate_rows else 1
-        ldg = _matrix(gate, "gate", bt, (gates, n))
-    weights = [w for w in (w_post, w_pre) if w is not None]
-    if len(weights) == 2 and w_post.dtype != w_pre.dtype:
-        raise ValueError("w_post and w_pre must have one dtype")
-    _vector(w_post, "w_post", FLOATS, n)
-    _vector(w_pre, "w_pre", FLOATS, n)
-    return rows, n, ldb, ldg, ldr, _wdtype(weights[0]) if weights else WR_F32
+        ldg, pg = _matrix(gate, "gate", (bt,), (-(-rows // gate_rows) if gate_rows else 1, n)), gate.data_ptr()
+    weight = w_pre if w_pre is not None else w_post
+    wt = FLOATS if weight is None else (weight.dtype,)
+    if weight is not None and weight.dtype not in _WR_DTYPE:
+        raise ValueError(f"weights of {weight.dtype}: expected one of {FLOATS}")
+    post, pre = _vector(w_post, "w_post", wt, n), _vector(w_pre, "w_pre", wt, n)
+    return bt, rt, shape, (rows, n, pb, _WR_DTYPE[bt], ldb, post, pg, ldg, gate_rows, branch_scale, pr, _WR_DTYPE[rt],
+                           ldr, resid_scale, pre, _WR_DTYPE[wt[0]])
+
+
+def _rows_of(t, name, dtype, shape):
+    """(address, row stride) of an optional matrix."""
+    if t is None:
+        return None, shape[1]
+    ld = _matrix(t, name, (dtype,), shape)
+    return t.data_ptr(), ld
 
 
 def wr_block_norm(ctx, eps, branch=None, resid=None, w_post=None, gate=None, gate_rows=0, branch_scale=1.0,
@@ -493,22 +525,15 @@ def wr_block_norm(ctx, eps, branch=None, resid=None, w_post=None, gate=None, gat
     """resid_out = x' = resid_scale resid + branch_scale gate w_post branch / rms(branch); y = w_pre x' / rms(x'),
     and / or its 8-bit form (q, q_scales); stats (rows x 2 fp32) for wr_block_norm_backward.  Outputs left out are
     not written.  gate: one row for every gate_rows consecutive rows (0: one row for all)."""
-    acts = [t for t in (branch, y, gate) if t is not None]
-    b_type = acts[0].dtype if acts else (resid.dtype if resid is not None else torch.float32)
-    res = [t for t in (resid, resid_out) if t is not None]
-    r_type = res[0].dtype if res else b_type
-    rows, n, ldb, ldg, ldr, wt = _norm_inputs(branch, resid, w_post, gate, gate_rows, w_pre, b_type, r_type)
-    shape = (rows, n)
-    ldo = _matrix(resid_out, "resid_out", (r_type,), shape) if resid_out is not None else n
-    ldy = _matrix(y, "y", (b_type,), shape) if y is not None else n
-    ldq = _matrix(q, "q", _I8, shape) if q is not None else n
-    _vector(q_scales, "q_scales", _F32, rows)
-    _vector(stats, "stats", _F32, 2 * rows)
-    _check("wr_block_norm", load().wr_block_norm(
-        ctx.handle, rows, n, _ptr(branch), WR_BF16 if b_type == torch.bfloat16 else WR_F32, ldb, _ptr(w_post),
-        _ptr(gate), ldg, int(gate_rows), float(branch_scale), _ptr(resid),
-        WR_BF16 if r_type == torch.bfloat16 else WR_F32, ldr, float(resid_scale), _ptr(w_pre), wt, float(eps),
-        _ptr(resid_out), ldo, _ptr(y), ldy, _ptr(q), ldq, _ptr(q_scales), _ptr(stats)))
+    bt, rt, shape, lead = _norm_inputs(branch, resid, w_post, gate, gate_rows, branch_scale, resid_scale, w_pre,
+                                       (branch, y, gate), (resid, resid_out))
+    rows = shape[0]
+    po, ldo = _rows_of(resid_out, "resid_out", rt, shape)
+    py, ldy = _rows_of(y, "y", bt, shape)
+    pq, ldq = _rows_of(q, "q", torch.int8, shape)
+    ps = _vector(q_scales, "q_scales", _F32, rows)
+    pt = _vector(stats, "stats", _F32, 2 * rows)
+    _check("wr_block_norm", load().wr_block_norm(ctx.handle, *lead, eps, po, ldo, py, ldy, pq, ldq, ps, pt))
 
 
 def wr_block_norm_backward(ctx, stats, branch=None, resid=None, w_post=None, gate=None, gate_rows=0, branch_scale=1.0,
@@ -516,25 +541,17 @@ def wr_block_norm_backward(ctx, stats, branch=None, resid=None, w_post=None, gat
                            dw_post=None, dgate=None, dw_pre=None):
     """Gradients of wr_block_norm's inputs from dy (of y) and dresid_out (of x'), either of which may be None.
     Outputs left out are not formed; dw_post, dgate (as gate's shape) and dw_pre are fp32."""
-    acts = [t for t in (branch, dy, gate) if t is not None]
-    b_type = acts[0].dtype if acts else (resid.dtype if resid is not None else torch.float32)
-    res = [t for t in (resid, dresid_out) if t is not None]
-    r_type = res[0].dtype if res else b_type
-    rows, n, ldb, ldg, ldr, wt = _norm_inputs(branch, resid, w_post, gate, gate_rows, w_pre, b_type, r_type)
-    shape = (rows, n)
-    lddy = _matrix(dy, "dy", (b_type,), shape) if dy is not None else n
-    lddo = _matrix(dresid_out, "dresid_out", (r_type,), shape) if dresid_out is not None else n
-    lddb = _matrix(dbranch, "dbranch", (b_type,), shape) if dbranch is not None else n
-    lddr = _matrix(dresid, "dresid", (r_type,), shape) if dresid is not None else n
-    _vector(stats, "stats", _F32, 2 * rows)
-    _vector(dw_post, "dw_post", _F32, n)
-    _vector(dw_pre, "dw_pre", _F32, n)
-    if dgate is not None:
-        _vector(dgate, "dgate", _F32, gate.numel() if gate is not None else 0)
-    ctx.ensure_workspace(wr_workspace_bytes(WR_OP_NORM_BWD, rows, n, min(int(gate_rows), rows)))
+    bt, rt, shape, lead = _norm_inputs(branch, resid, w_post, gate, gate_rows, branch_scale, resid_scale, w_pre,
+                                       (branch, dy, gate), (resid, dresid_out))
+    rows, n = shape
+    py, lddy = _rows_of(dy, "dy", bt, shape)
+    po, lddo = _rows_of(dresid_out, "dresid_out", rt, shape)
+    pb, lddb = _rows_of(dbranch, "dbranch", bt, shape)
+    px, lddr = _rows_of(dresid, "dresid", rt, shape)
+    pt = _vector(stats, "stats", _F32, 2 * rows)
+    pp = _vector(dw_post, "dw_post", _F32, n)
+    pg = _vector(dgate, "dgate", _F32, gate.numel() if gate is not None else 0)
+    pw = _vector(dw_pre, "dw_pre", _F32, n)
+    ctx.ensure_workspace(wr_workspace_bytes(WR_OP_NORM_BWD, rows, n, min(gate_rows, rows)))
     _check("wr_block_norm_backward", load().wr_block_norm_backward(
-        ctx.handle, rows, n, _ptr(branch), WR_BF16 if b_type == torch.bfloat16 else WR_F32, ldb, _ptr(w_post),
-        _ptr(gate), ldg, int(gate_rows), float(branch_scale), _ptr(resid),
-        WR_BF16 if r_type == torch.bfloat16 else WR_F32, ldr, float(resid_scale), _ptr(w_pre), wt, _ptr(stats),
-        _ptr(dy), lddy, _ptr(dresid_out), lddo, _ptr(dbranch), lddb, _ptr(dresid), lddr, _ptr(dw_post), _ptr(dgate),
-        _ptr(dw_pre)))
+        ctx.handle, *lead, pt, py, lddy, po, lddo, pb, lddb, px, lddr, pp, pg, pw))

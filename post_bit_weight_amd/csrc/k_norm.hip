@@ -5,7 +5,7 @@
 //
 // Every value of a row stays in registers from its one load to its stores: the two sums of squares and
 // the maximum are reductions over the lanes that share the row.  Rows of up to 512 values take 16, 32 or
-// 64 lanes of a wave (no barrier); wider rows take a workgroup of up to 512 threads with one, two or four
+// 64 lanes of a wave (no barrier); wider rows take a workgroup of up to 1024 threads with one or two
 // chunks of eight values per thread.
 #include "rowops.hpp"
 
@@ -35,145 +35,147 @@ struct NormArgs {
   float* stats;
 };
 
+// This thread's place in its row, first row, row step and column step.
 template <int LANES>
-__device__ __forceinline__ int row_lane() {
-  return LANES > 0 ? threadIdx.x % (LANES > 0 ? LANES : 1) : threadIdx.x;
-}
-// First row, step and column step of this thread's row group.
-template <int LANES>
-__device__ __forceinline__ void row_walk(int& first, int& step, int& cstep) {
-  if constexpr (LANES > 0) {
-    const int per = blockDim.x / LANES;
-    first = blockIdx.x * per + threadIdx.x / LANES;
-    step = gridDim.x * per;
-    cstep = 8 * LANES;
-  } else {
-    first = blockIdx.x;
-    step = gridDim.x;
-    cstep = 8 * blockDim.x;
+struct RowWalk {
+  int lane, first, step, cstep;
+  __device__ __forceinline__ RowWalk() {
+    if constexpr (LANES > 0) {
+      const int per = blockDim.x / LANES;
+      lane = threadIdx.x % LANES;
+      first = blockIdx.x * per + threadIdx.x / LANES;
+      step = gridDim.x * per;
+      cstep = 8 * LANES;
+    } else {
+      lane = threadIdx.x;
+      first = blockIdx.x;
+      step = gridDim.x;
+      cstep = 8 * blockDim.x;
+    }
   }
-}
+};
 
-template <typename TB, typename TR, typename TW, int CH, int LANES>
-__global__ __launch_bounds__(LANES > 0 ? 256 : 512) void block_norm_kernel(const NormArgs a) {
+// Inputs that are absent take a value that leaves the formula as it is (weights and gate 1, branch and
+// residual 0), so that the row's arithmetic has no branches.
+template <typename TB, typename TR, typename TW, int CH, int LANES, int MAXT>
+__global__ __launch_bounds__(MAXT) void block_norm_kernel(const NormArgs a) {
   __shared__ uint32_t red[2][3][RowGroup<LANES>::kMaxWaves];
   RowGroup<LANES> grp{red};
-  int first, step, cstep;
-  row_walk<LANES>(first, step, cstep);
-  const int lane = row_lane<LANES>(), n = a.n;
+  const RowWalk<LANES> walk;
+  const int n = a.n;
+  const RowMap<CH, LANES> map(walk.lane, walk.cstep, n);
   const float inv_n = 1.0f / (float)n;
-  for (int64_t row = first; row < a.rows; row += step) {
-    Raw8<TB> b[CH], g[CH];
-    Raw8<TR> x[CH];
-    Raw8<TW> wp[CH], wq[CH];
-    const TB* brow = (const TB*)a.branch + row * a.ldb;
-    const TR* xrow = (const TR*)a.resid + row * a.ldr;
-    const TB* grow = (const TB*)a.gate + (a.gate_rows ? (uint32_t)row / (uint32_t)a.gate_rows : 0u) * a.ldg;
+
+  Raw8<TW> wp[CH], wq[CH];
+  Raw8<TB> b[CH], g[CH];
+  Raw8<TR> x[CH];
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    wp[k].fill(1.0f);
+    wq[k].fill(1.0f);
+    b[k].fill(0.0f);
+    g[k].fill(1.0f);
+    x[k].fill(0.0f);
+    if (a.w_post) map.load(wp[k], (const TW*)a.w_post, k, n);
+    if (a.w_pre) map.load(wq[k], (const TW*)a.w_pre, k, n);
+  }
+  auto load_row = [&](int64_t row) {
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int c = 8 * lane + k * cstep;
-      if (c < n) {
-        if (a.branch) load8(b[k], brow, c, n);
-        if (a.resid) load8(x[k], xrow, c, n);
-        if (a.w_post) load8(wp[k], (const TW*)a.w_post, c, n);
-        if (a.gate) load8(g[k], grow, c, n);
-        if (a.w_pre) load8(wq[k], (const TW*)a.w_pre, c, n);
-      }
+      if (a.branch) map.load(b[k], (const TB*)a.branch + row * a.ldb, k, n);
+      if (a.resid) map.load(x[k], (const TR*)a.resid + row * a.ldr, k, n);
+      if (a.gate) map.load(g[k], (const TB*)a.gate + (a.gate_rows ? (uint32_t)row / (uint32_t)a.gate_rows : 0u) * a.ldg, k, n);
     }
+  };
+  if (walk.first < a.rows) load_row(walk.first);
+  for (int64_t row = walk.first; row < a.rows; row += walk.step) {
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      map.own(b[k], k);
+      map.own(x[k], k);
+    }
+    float v[CH][8];
     float r1 = 1.0f, r2 = 1.0f;
     if (a.w_post) {
       float ss = 0.0f;
 #pragma unroll
       for (int k = 0; k < CH; ++k)
-        if (8 * lane + k * cstep < n)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) ss = fmaf(b[k].get(e), b[k].get(e), ss);
+        for (int e = 0; e < 8; ++e) ss = fmaf(b[k].get(e), b[k].get(e), ss);
       r1 = 1.0f / sqrtf(grp.sum(ss) * inv_n + a.eps);
     }
-    float v[CH][8];
     float ss = 0.0f;
 #pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      const int c = 8 * lane + k * cstep;
-      if (c >= n) continue;
+    for (int k = 0; k < CH; ++k)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        float u = 0.0f;
-        if (a.branch) {
-          u = b[k].get(e);
-          if (a.w_post) u = u * r1 * wp[k].get(e);
-          if (a.gate) u *= g[k].get(e);
-          u *= a.bscale;
-        }
-        v[k][e] = a.resid ? fmaf(a.rscale, x[k].get(e), u) : u;
+        const float u = b[k].get(e) * r1 * wp[k].get(e) * g[k].get(e) * a.bscale;
+        v[k][e] = fmaf(a.rscale, x[k].get(e), u);
         ss = fmaf(v[k][e], v[k][e], ss);
       }
-      if (a.resid_out) store8((TR*)a.resid_out + row * a.ldo, c, n, v[k]);
-    }
+    // the next row's loads are in flight during the rest of this one
+    if (row + walk.step < a.rows) load_row(row + walk.step);
+    if (a.resid_out)
+#pragma unroll
+      for (int k = 0; k < CH; ++k) map.store((TR*)a.resid_out + row * a.ldo, k, v[k]);
     if (a.w_pre) {
       r2 = 1.0f / sqrtf(grp.sum(ss) * inv_n + a.eps);
-      uint32_t top = 0u;
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
-        const int c = 8 * lane + k * cstep;
-        if (c >= n) continue;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          v[k][e] = v[k][e] * r2 * wq[k].get(e);
-          if (c + e < n) top = MaxU32::op(top, __float_as_uint(v[k][e]) & 0x7fffffffu);
-        }
-        if (a.y) store8((TB*)a.y + row * a.ldy, c, n, v[k]);
+        for (int e = 0; e < 8; ++e) v[k][e] = v[k][e] * r2 * wq[k].get(e);
+        if (a.y) map.store((TB*)a.y + row * a.ldy, k, v[k]);
       }
       if (a.q) {
+        uint32_t top = 0u;
+#pragma unroll
+        for (int k = 0; k < CH; ++k)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) top = MaxU32::op(top, __float_as_uint(v[k][e]) & 0x7fffffffu);
         const RowCoder code(grp.max(top));
 #pragma unroll
-        for (int k = 0; k < CH; ++k) {
-          const int c = 8 * lane + k * cstep;
-          if (c < n) store_codes(a.q + row * a.ldq, c, n, code.codes(v[k]));
-        }
-        if (lane == 0) a.q_scales[row] = code.scale;
+        for (int k = 0; k < CH; ++k) map.store(a.q + row * a.ldq, k, code.codes(v[k]));
+        if (walk.lane == 0) a.q_scales[row] = code.scale;
       }
     }
-    if (a.stats && lane == 0) {
+    if (a.stats && walk.lane == 0) {
       a.stats[2 * row] = r1;
       a.stats[2 * row + 1] = r2;
     }
   }
 }
 
-template <typename T, int CH, int LANES>
-__global__ __launch_bounds__(LANES > 0 ? 256 : 512) void quant_rows_kernel(const T* __restrict__ x, int64_t ldx,
-                                                                           int rows, int n, int8_t* __restrict__ q,
-                                                                           int64_t ldq, float* __restrict__ scales) {
+template <typename T, int CH, int LANES, int MAXT>
+__global__ __launch_bounds__(MAXT) void quant_rows_kernel(const T* __restrict__ x, int64_t ldx, int rows, int n,
+                                                          int8_t* __restrict__ q, int64_t ldq,
+                                                          float* __restrict__ scales) {
   __shared__ uint32_t red[2][3][RowGroup<LANES>::kMaxWaves];
   RowGroup<LANES> grp{red};
-  int first, step, cstep;
-  row_walk<LANES>(first, step, cstep);
-  const int lane = row_lane<LANES>();
-  for (int64_t row = first; row < rows; row += step) {
-    Raw8<T> r[CH];
+  const RowWalk<LANES> walk;
+  const RowMap<CH, LANES> map(walk.lane, walk.cstep, n);
+  Raw8<T> r[CH];
+  auto load_row = [&](int64_t row) {
+#pragma unroll
+    for (int k = 0; k < CH; ++k) map.load(r[k], x + row * ldx, k, n);
+  };
+  if (walk.first < rows) load_row(walk.first);
+  for (int64_t row = walk.first; row < rows; row += walk.step) {
+    float v[CH][8];
     uint32_t top = 0u;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int c = 8 * lane + k * cstep;
-      if (c < n) {
-        load8(r[k], x + row * ldx, c, n);
+      map.own(r[k], k);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = MaxU32::op(top, __float_as_uint(r[k].get(e)) & 0x7fffffffu);
+      for (int e = 0; e < 8; ++e) {
+        v[k][e] = r[k].get(e);
+        top = MaxU32::op(top, __float_as_uint(v[k][e]) & 0x7fffffffu);
       }
     }
+    if (row + walk.step < rows) load_row(row + walk.step);
     const RowCoder code(grp.max(top));
 #pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      const int c = 8 * lane + k * cstep;
-      if (c < n) {
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = r[k].get(e);
-        store_codes(q + row * ldq, c, n, code.codes(v));
-      }
-    }
-    if (lane == 0) scales[row] = code.scale;
+    for (int k = 0; k < CH; ++k) map.store(q + row * ldq, k, code.codes(v[k]));
+    if (walk.lane == 0) scales[row] = code.scale;
   }
 }
 
@@ -185,22 +187,23 @@ __global__ __launch_bounds__(512) void quant_rows_wide_kernel(const T* __restric
   __shared__ uint32_t red[2][3][RowGroup<0>::kMaxWaves];
   RowGroup<0> grp{red};
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    const T* from = x + row * ldx;
     uint32_t top = 0u;
     for (int64_t c = 8 * threadIdx.x; c < n; c += 8 * 512) {
       Raw8<T> r;
-      load8(r, x + row * ldx + c, 0, (int)std::min<int64_t>(n - c, 8));
+      r.load(from + std::min(c, n - 8));  // a value read twice does not change the maximum
 #pragma unroll
       for (int e = 0; e < 8; ++e) top = MaxU32::op(top, __float_as_uint(r.get(e)) & 0x7fffffffu);
     }
     const RowCoder code(grp.max(top));
     for (int64_t c = 8 * threadIdx.x; c < n; c += 8 * 512) {
+      const int64_t at = std::min(c, n - 8);  // nor does a code written twice
       Raw8<T> r;
-      const int cnt = (int)std::min<int64_t>(n - c, 8);
-      load8(r, x + row * ldx + c, 0, cnt);
+      r.load(from + at);
       float v[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = r.get(e);
-      store_codes(q + row * ldq + c, 0, cnt, code.codes(v));
+      *reinterpret_cast<u32x2_any*>(q + row * ldq + at) = code.codes(v);
     }
     if (threadIdx.x == 0) scales[row] = code.scale;
   }
@@ -210,33 +213,56 @@ __global__ __launch_bounds__(512) void quant_rows_wide_kernel(const T* __restric
 
 using namespace wr;
 
-// Lanes per row, chunks per thread and threads for rows of n values (n <= 16384): `launch` gets them as
-// integral constants (chunks, lanes) and the number of threads and workgroups.
+template <int N>
+using Int = std::integral_constant<int, N>;
+
+// Calls launch(chunks, lanes, most threads, threads, workgroups) -- the first three integral constants -- for rows
+// of n values.  Workgroups walk the rows with the next row's loads in flight, so there are only as many as
+// `per_cu` threads a CU make.
+template <int LANES, int CH, typename F>
+static void wave_rows(int num_cu, int per_cu, int64_t rows, F&& launch) {
+  const int64_t per = 256 / LANES;
+  launch(Int<CH>{}, Int<LANES>{}, Int<256>{}, 256, (int)std::min<int64_t>((int64_t)num_cu * (per_cu / 256), (rows + per - 1) / per));
+}
+template <int CH, int MAXT, typename F>
+static void group_rows(int num_cu, int per_cu, int64_t rows, int64_t n, F&& launch) {
+  const int threads = ((int)((n + 7) / 8 + CH - 1) / CH + 63) / 64 * 64;
+  launch(Int<CH>{}, Int<0>{}, Int<MAXT>{}, threads, (int)std::min<int64_t>((int64_t)num_cu * std::max(1, per_cu / threads), rows));
+}
+// Norm: 16384 x 2560 bf16 with 1280 threads a CU takes 64 us, with 768, 1600 and 2048 it takes 75, 70 and 70 (at
+// 5.2 TB/s a copy of as many bytes takes 65).
 template <typename F>
-static void row_shape(int64_t rows, int64_t n, F&& launch) {
-  const int64_t most = (int64_t)1 << 20;  // workgroups; each walks further rows beyond that
-  const int chunks = (int)((n + 7) / 8);
-  auto lanes = [&](auto l) {
-    const int64_t per = 256 / decltype(l)::value;
-    launch(std::integral_constant<int, 1>{}, l, 256, (int)std::min(most, (rows + per - 1) / per));
-  };
-  auto wide = [&](auto ch) {
-    const int threads = ((chunks + decltype(ch)::value - 1) / decltype(ch)::value + 63) / 64 * 64;
-    launch(ch, std::integral_constant<int, 0>{}, threads, (int)std::min(most, rows));
-  };
-  if (n <= 128) lanes(std::integral_constant<int, 16>{});
-  else if (n <= 256) lanes(std::integral_constant<int, 32>{});
-  else if (n <= 512) lanes(std::integral_constant<int, 64>{});
-  else if (n <= 4096) wide(std::integral_constant<int, 1>{});
-  else if (n <= 8192) wide(std::integral_constant<int, 2>{});
-  else wide(std::integral_constant<int, 4>{});
+static void norm_shape(int num_cu, int64_t rows, int64_t n, F&& launch) {
+  if (n < 8) wave_rows<8, 1>(num_cu, 1024, rows, launch);
+  else if (n <= 128) wave_rows<16, 1>(num_cu, 1024, rows, launch);
+  else if (n <= 256) wave_rows<32, 1>(num_cu, 1024, rows, launch);
+  else if (n <= 512) wave_rows<64, 1>(num_cu, 1024, rows, launch);
+  else if (n <= 4096) group_rows<1, 512>(num_cu, 1280, rows, n, launch);
+  else if (n <= 8192) group_rows<1, 1024>(num_cu, 1280, rows, n, launch);
+  else if (n <= 12288) group_rows<2, 768>(num_cu, 1280, rows, n, launch);
+  else group_rows<2, 1024>(num_cu, 1280, rows, n, launch);
+}
+// Quantizer: with one input and one byte out per value, a thread needs more chunks in flight: 16384 x 4096 bf16
+// takes 40 us with four chunks and 1024 threads a CU, 72 with one chunk and 2048 (a copy of as many bytes: 39).
+// A few rows are a matter of latency, and take the most threads.
+template <typename F>
+static void quant_shape(int num_cu, int64_t rows, int64_t n, F&& launch) {
+  if (n < 8) wave_rows<8, 1>(num_cu, 2048, rows, launch);
+  else if (n <= 128) wave_rows<16, 1>(num_cu, 2048, rows, launch);
+  else if (n <= 256) wave_rows<32, 1>(num_cu, 2048, rows, launch);
+  else if (n <= 512) wave_rows<64, 1>(num_cu, 2048, rows, launch);
+  else if (n <= 8192 && rows <= num_cu) group_rows<1, 1024>(num_cu, 1024, rows, n, launch);
+  else if (rows <= num_cu) group_rows<2, 1024>(num_cu, 1024, rows, n, launch);
+  else if (n <= 1024) wave_rows<64, 2>(num_cu, 1024, rows, launch);
+  else if (n <= 2048) wave_rows<64, 4>(num_cu, 1024, rows, launch);
+  else group_rows<4, 512>(num_cu, 1024, rows, n, launch);
 }
 
 template <typename TB, typename TR, typename TW>
 static int norm_launch(wr_ctx* ctx, const NormArgs& a) {
-  row_shape(a.rows, a.n, [&](auto ch, auto lanes, int threads, int grid) {
-    hipLaunchKernelGGL((block_norm_kernel<TB, TR, TW, decltype(ch)::value, decltype(lanes)::value>), dim3(grid),
-                       dim3(threads), 0, ctx->stream, a);
+  norm_shape(ctx->num_cu, a.rows, a.n, [&](auto ch, auto lanes, auto most, int threads, int grid) {
+    hipLaunchKernelGGL((block_norm_kernel<TB, TR, TW, decltype(ch)::value, decltype(lanes)::value, decltype(most)::value>),
+                       dim3(grid), dim3(threads), 0, ctx->stream, a);
   });
   WR_CHECK_LAUNCH();
   return WR_OK;
@@ -270,9 +296,9 @@ static int quant_launch(wr_ctx* ctx, const T* x, int64_t rows, int64_t n, int64_
     hipLaunchKernelGGL(quant_rows_wide_kernel<T>, dim3((int)std::min<int64_t>(rows, 1 << 20)), dim3(512), 0,
                        ctx->stream, x, ldx, (int)rows, n, q, ldq, scales);
   } else {
-    row_shape(rows, n, [&](auto ch, auto lanes, int threads, int grid) {
-      hipLaunchKernelGGL((quant_rows_kernel<T, decltype(ch)::value, decltype(lanes)::value>), dim3(grid),
-                         dim3(threads), 0, ctx->stream, x, ldx, (int)rows, (int)n, q, ldq, scales);
+    quant_shape(ctx->num_cu, rows, n, [&](auto ch, auto lanes, auto most, int threads, int grid) {
+      hipLaunchKernelGGL((quant_rows_kernel<T, decltype(ch)::value, decltype(lanes)::value, decltype(most)::value>),
+                         dim3(grid), dim3(threads), 0, ctx->stream, x, ldx, (int)rows, (int)n, q, ldq, scales);
     });
   }
   WR_CHECK_LAUNCH();

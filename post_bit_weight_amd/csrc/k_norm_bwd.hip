@@ -19,18 +19,23 @@ namespace wr {
 struct BwdPlan {
   int64_t units, span, gate_rows, gates, segs, blocks;
   int lanes, threads, chunks;
+  bool wide;
 };
 
-constexpr int64_t kBwdBlocks = 1024;  // four workgroups for each of 256 CUs
-
-static BwdPlan bwd_plan(int64_t rows, int64_t n, int64_t gate_rows) {
+static BwdPlan bwd_plan(int64_t rows, int64_t n, int64_t gate_rows, bool fp32) {
   BwdPlan p;
   const int64_t per8 = (n + 7) / 8;
-  p.lanes = n <= 128 ? 16 : n <= 256 ? 32 : n <= 512 ? 64 : 0;
-  p.chunks = n <= 4096 ? 1 : n <= 8192 ? 2 : 4;
+  p.lanes = n < 8 ? 8 : n <= 128 ? 16 : n <= 256 ? 32 : n <= 512 ? 64 : 0;
+  // A workgroup's 512 threads hold rows of up to 4096 values with one chunk each, and of up to 8192 with two if
+  // nothing is fp32; other rows are walked (`wide`) by up to 1024 threads.
+  p.wide = n > 8192 || (n > 4096 && fp32);
+  p.chunks = p.wide ? (int)((n + 8191) / 8192) : n <= 4096 ? 1 : 2;
   p.threads = p.lanes ? 256 : (int)(((per8 + p.chunks - 1) / p.chunks + 63) / 64 * 64);
+  // Two workgroups for each of 256 CUs, one where a workgroup fills the registers: more of them write more
+  // partial sums and hide nothing that the next row's loads do not.
+  const int64_t most = p.wide || p.chunks > 1 ? 256 : 512;
   const int64_t per = p.lanes ? 256 / p.lanes : 1;  // units per workgroup
-  p.span = std::max<int64_t>(1, (rows + kBwdBlocks * per - 1) / (kBwdBlocks * per));
+  p.span = std::max<int64_t>(1, (rows + most * per - 1) / (most * per));
   p.gate_rows = gate_rows == 0 || gate_rows >= rows ? rows : gate_rows;
   p.gates = (rows + p.gate_rows - 1) / p.gate_rows;
   if (p.gate_rows <= p.span) {
@@ -48,6 +53,7 @@ static BwdPlan bwd_plan(int64_t rows, int64_t n, int64_t gate_rows) {
 
 struct BwdArgs {
   int rows, n, span, segs, gate_rows;
+  bool one_gate;
   int64_t units;
   const void* branch;
   int64_t ldb;
@@ -70,23 +76,36 @@ struct BwdArgs {
   int64_t lddr;
   float* part_post;  // blocks x n, or null
   float* part_pre;   // blocks x n, or null
-  float* part_gate;  // units x n (segs > 0), or null
+  float* part_gate;  // units x n (segs > 0), blocks x n for a single gate row, or null
   float* dgate;      // gates x n (segs == 0), or null
 };
 
-template <typename TB, typename TR, typename TW, int CH, int LANES>
-__global__ __launch_bounds__(LANES > 0 ? 256 : 512) void block_norm_bwd_kernel(const BwdArgs a) {
-  __shared__ uint32_t red[2][3][RowGroup<LANES>::kMaxWaves];
-  __shared__ float comb[LANES > 0 ? 8 * 256 : 1];
-  RowGroup<LANES> grp{red};
-  const int lane = LANES > 0 ? threadIdx.x % (LANES > 0 ? LANES : 1) : threadIdx.x;
-  const int cstep = LANES > 0 ? 8 * LANES : 8 * blockDim.x;
-  const int64_t unit = LANES > 0 ? (int64_t)blockIdx.x * (256 / (LANES > 0 ? LANES : 1)) + threadIdx.x / (LANES > 0 ? LANES : 1)
-                                 : (int64_t)blockIdx.x;
-  const int n = a.n;
-  const float inv_n = 1.0f / (float)n;
-  int64_t r0, r1;
-  int64_t gidx;
+// One value's share of a row: bn, x' without the residual (along), xn, dres + r2 d (t) and bscale g (cg).
+struct NormTerms {
+  float bn, along, xn, t, cg;
+  NormTerms() = default;
+  __device__ __forceinline__ NormTerms(const BwdArgs& a, float ib, float ix, float b, float g, float x, float dy,
+                                       float dr, float wp, float wq) {
+    bn = b * ib;
+    cg = a.bscale * g;
+    along = cg * wp * bn;
+    xn = fmaf(a.rscale, x, along) * ix;
+    t = fmaf(ix, dy * wq, dr);
+  }
+  // Adds the value's terms to the row's three sums.
+  __device__ __forceinline__ void add(float (&sums)[3], float dy, float wq) const {
+    sums[0] = fmaf(dy * wq, xn, sums[0]);
+    sums[1] = fmaf(along, t, sums[1]);
+    sums[2] = fmaf(along, xn, sums[2]);
+  }
+};
+// r2 mean(d xn) and mean(c dx') of a row from its sums.
+__device__ __forceinline__ void row_means(const float (&sums)[3], float inv_n, float ix, float& m1, float& m2) {
+  m1 = sums[0] * inv_n * ix;
+  m2 = (sums[1] - m1 * sums[2]) * inv_n;
+}
+// The tokens of a unit and its first gate row.
+__device__ __forceinline__ void unit_range(const BwdArgs& a, int64_t unit, int64_t& r0, int64_t& r1, int64_t& gidx) {
   if (a.segs) {
     gidx = unit / a.segs;
     r0 = gidx * a.gate_rows + unit % a.segs * a.span;
@@ -96,154 +115,296 @@ __global__ __launch_bounds__(LANES > 0 ? 256 : 512) void block_norm_bwd_kernel(c
     r1 = std::min<int64_t>(r0 + a.span, a.rows);
     gidx = r0 / a.gate_rows;
   }
+}
+
+// Absent inputs take a value that leaves the formula as it is, so that the row's arithmetic has no branches.
+template <typename TB, typename TR, typename TW, int CH, int LANES>
+__global__ __launch_bounds__(LANES > 0 ? 256 : 512) void block_norm_bwd_kernel(const BwdArgs a) {
+  __shared__ uint32_t red[2][3][RowGroup<LANES>::kMaxWaves];
+  constexpr int kPer = LANES > 0 ? 256 / (LANES > 0 ? LANES : 1) : 1;  // units per workgroup
+  constexpr int kWidth = 8 * LANES;
+  __shared__ float comb[LANES > 0 ? 8 * 256 : 1];
+  RowGroup<LANES> grp{red};
+  const int lane = LANES > 0 ? threadIdx.x % (LANES > 0 ? LANES : 1) : threadIdx.x;
+  const int64_t unit = (int64_t)blockIdx.x * kPer + (LANES > 0 ? threadIdx.x / (LANES > 0 ? LANES : 1) : 0);
+  const int n = a.n;
+  const RowMap<CH, LANES> map(lane, LANES > 0 ? kWidth : 8 * blockDim.x, n);
+  const float inv_n = 1.0f / (float)n;
+  int64_t r0, r1, gidx;
+  unit_range(a, unit, r0, r1, gidx);
   int64_t gend = (gidx + 1) * a.gate_rows;
 
+  Raw8<TW> wp[CH], wq[CH];
+  Raw8<TB> b[CH], g[CH], dy[CH];
+  Raw8<TR> x[CH], dr[CH];
+  Raw8<TR> odx[CH];  // the previous row's results, not yet stored
+  Raw8<TB> odb[CH];
   float s_pre[CH][8], s_post[CH][8], s_gate[CH][8];
 #pragma unroll
-  for (int k = 0; k < CH; ++k)
+  for (int k = 0; k < CH; ++k) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) s_pre[k][e] = s_post[k][e] = s_gate[k][e] = 0.0f;
-
-  for (int64_t row = r0; row < r1; ++row) {
-    Raw8<TB> b[CH], g[CH], dy[CH];
-    Raw8<TR> x[CH], dr[CH];
-    Raw8<TW> wp[CH], wq[CH];
+    wp[k].fill(1.0f);
+    wq[k].fill(1.0f);
+    b[k].fill(0.0f);
+    g[k].fill(1.0f);
+    dy[k].fill(0.0f);
+    x[k].fill(0.0f);
+    dr[k].fill(0.0f);
+    if (a.w_post) map.load(wp[k], (const TW*)a.w_post, k, n);
+    if (a.dy) map.load(wq[k], (const TW*)a.w_pre, k, n);
+  }
+  float ib = 1.0f, ix = 0.0f;
+  auto load_row = [&](int64_t row, int64_t gate_row) {
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int c = 8 * lane + k * cstep;
-      if (c < n) {
-        if (a.branch) load8(b[k], (const TB*)a.branch + row * a.ldb, c, n);
-        if (a.resid) load8(x[k], (const TR*)a.resid + row * a.ldr, c, n);
-        if (a.dy) load8(dy[k], (const TB*)a.dy + row * a.lddy, c, n);
-        if (a.dres) load8(dr[k], (const TR*)a.dres + row * a.lddo, c, n);
-        if (a.gate) load8(g[k], (const TB*)a.gate + gidx * a.ldg, c, n);
-        if (a.w_post) load8(wp[k], (const TW*)a.w_post, c, n);
-        if (a.dy) load8(wq[k], (const TW*)a.w_pre, c, n);
-      }
+      if (a.branch) map.load(b[k], (const TB*)a.branch + row * a.ldb, k, n);
+      if (a.resid) map.load(x[k], (const TR*)a.resid + row * a.ldr, k, n);
+      if (a.dy) map.load(dy[k], (const TB*)a.dy + row * a.lddy, k, n);
+      if (a.dres) map.load(dr[k], (const TR*)a.dres + row * a.lddo, k, n);
+      if (a.gate) map.load(g[k], (const TB*)a.gate + gate_row * a.ldg, k, n);
     }
-    const float ib = a.w_post ? a.stats[2 * row] : 1.0f, ix = a.dy ? a.stats[2 * row + 1] : 0.0f;
-    float bn[CH][8], xn[CH][8], t[CH][8], cg[CH][8];  // t: dres + r2 d;  cg: bscale g
+    if (a.w_post) ib = a.stats[2 * row];
+    if (a.dy) ix = a.stats[2 * row + 1];
+  };
+  // A row's results are stored during the next row, before the loads of the one after it: the wait for
+  // those loads, which cannot pass older accesses, then waits for no store made late in the same row.
+  auto store_row = [&](int64_t row) {
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      if (a.dx) map.store((TR*)a.dx + row * a.lddr, k, odx[k]);
+      if (a.db) map.store((TB*)a.db + row * a.lddb, k, odb[k]);
+    }
+  };
+  if (r0 < r1) load_row(r0, gidx);
+  for (int64_t row = r0; row < r1; ++row) {
+    const float jb = ib, jx = ix;
+    NormTerms kept[CH][8];
     float sums[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int c = 8 * lane + k * cstep;
-      if (c >= n) continue;
+      map.own(b[k], k);
+      map.own(x[k], k);
+      map.own(dy[k], k);
+      map.own(dr[k], k);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        bn[k][e] = a.branch ? b[k].get(e) * ib : 0.0f;
-        cg[k][e] = a.gate ? a.bscale * g[k].get(e) : a.bscale;
-        const float cw = a.w_post ? cg[k][e] * wp[k].get(e) : cg[k][e];  // derivative of x' by bn
-        const float xo = a.resid ? fmaf(a.rscale, x[k].get(e), cw * bn[k][e]) : cw * bn[k][e];
-        xn[k][e] = xo * ix;
-        const float d = a.dy ? dy[k].get(e) : 0.0f;
-        s_pre[k][e] = fmaf(d, xn[k][e], s_pre[k][e]);
-        const float dw = a.dy ? d * wq[k].get(e) : 0.0f;
-        t[k][e] = fmaf(ix, dw, a.dres ? dr[k].get(e) : 0.0f);
-        sums[0] = fmaf(dw, xn[k][e], sums[0]);
-        sums[1] = fmaf(cw * bn[k][e], t[k][e], sums[1]);
-        sums[2] = fmaf(cw * bn[k][e], xn[k][e], sums[2]);
+        const float d = dy[k].get(e), w = wq[k].get(e);
+        const NormTerms m(a, jb, jx, b[k].get(e), g[k].get(e), x[k].get(e), d, dr[k].get(e), wp[k].get(e), w);
+        s_pre[k][e] = fmaf(d, m.xn, s_pre[k][e]);
+        m.add(sums, d, w);
+        kept[k][e] = m;
       }
     }
-    grp.template reduce<AddF32>(sums);
-    const float m1 = sums[0] * inv_n * ix;           // r2 mean(d xn)
-    const float m2 = (sums[1] - m1 * sums[2]) * inv_n;  // mean(c dx')
-#pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      const int c = 8 * lane + k * cstep;
-      if (c >= n) continue;
-      float dxo[8], out[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        dxo[e] = fmaf(-m1, xn[k][e], t[k][e]);
-        out[e] = a.rscale * dxo[e];
-      }
-      if (a.dx) store8((TR*)a.dx + row * a.lddr, c, n, out);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float w = a.w_post ? wp[k].get(e) : 1.0f;
-        const float du = cg[k][e] * dxo[e];
-        s_post[k][e] = fmaf(du, bn[k][e], s_post[k][e]);
-        s_gate[k][e] = fmaf(a.bscale * dxo[e], w * bn[k][e], s_gate[k][e]);
-        out[e] = a.w_post ? ib * fmaf(-m2, bn[k][e], du * w) : du;
-      }
-      if (a.db) store8((TB*)a.db + row * a.lddb, c, n, out);
-    }
-    if (a.segs == 0 && (row + 1 == gend || row + 1 == r1)) {
-#pragma unroll
-      for (int k = 0; k < CH; ++k) {
-        const int c = 8 * lane + k * cstep;
-        if (a.dgate && c < n) store8(a.dgate + gidx * n, c, n, s_gate[k]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s_gate[k][e] = 0.0f;
-      }
+    const int64_t here = gidx;
+    if (a.segs == 0 && row + 1 == gend) {
       ++gidx;
       gend += a.gate_rows;
     }
-  }
-
-  if (a.part_gate && unit < a.units) {
+    const bool last = row + 1 == r1;
+    if (row > r0) store_row(row - 1);
+    if (!last) load_row(row + 1, gidx);  // in flight during the rest of this row
+    grp.template reduce<AddF32>(sums);
+    float m1, m2;
+    row_means(sums, inv_n, jx, m1, m2);
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int c = 8 * lane + k * cstep;
-      if (c < n) store8(a.part_gate + unit * n, c, n, s_gate[k]);
+      float dx_f[8], db_f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const NormTerms m = kept[k][e];
+        const float w = wp[k].get(e), dxo = fmaf(-m1, m.xn, m.t), du = m.cg * dxo;
+        dx_f[e] = a.rscale * dxo;
+        s_post[k][e] = fmaf(du, m.bn, s_post[k][e]);
+        s_gate[k][e] = fmaf(a.bscale * dxo, w * m.bn, s_gate[k][e]);
+        db_f[e] = a.w_post ? jb * fmaf(-m2, m.bn, du * w) : du;
+      }
+      odx[k].round(dx_f);
+      odb[k].round(db_f);
+    }
+    if (a.dgate && (last || gidx != here)) {  // a gate row's last token
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        map.store(a.dgate + here * n, k, s_gate[k]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s_gate[k][e] = 0.0f;
+      }
     }
   }
+  if (r0 < r1) store_row(r1 - 1);
+  if (a.part_gate && !(LANES > 0 && a.one_gate) && unit < a.units)
+#pragma unroll
+    for (int k = 0; k < CH; ++k) map.store(a.part_gate + unit * n, k, s_gate[k]);
   if constexpr (LANES > 0) {
     // the workgroup's units, added in order; a unit past the last one holds zeros
-    constexpr int per = 256 / (LANES > 0 ? LANES : 1), width = 8 * LANES;
     auto combine = [&](const float (&s)[8], float* part) {
       __syncthreads();
 #pragma unroll
-      for (int e = 0; e < 8; ++e) comb[threadIdx.x * 8 + e] = s[e];
+      for (int e = 0; e < 8; ++e)
+        if (map.keep[0] >> e & 1) comb[threadIdx.x / LANES * kWidth + map.col[0] + e] = s[e];
       __syncthreads();
       for (int c = threadIdx.x; c < n; c += 256) {
         float sum = 0.0f;
-        for (int u = 0; u < per; ++u) sum += comb[u * width + c];
+        for (int u = 0; u < kPer; ++u) sum += comb[u * kWidth + c];
         part[(int64_t)blockIdx.x * n + c] = sum;
       }
     };
     if (a.part_pre) combine(s_pre[0], a.part_pre);
     if (a.part_post) combine(s_post[0], a.part_post);
+    if (a.part_gate && a.one_gate) combine(s_gate[0], a.part_gate);
   } else {
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int c = 8 * lane + k * cstep;
-      if (c >= n) continue;
-      if (a.part_pre) store8(a.part_pre + (int64_t)blockIdx.x * n, c, n, s_pre[k]);
-      if (a.part_post) store8(a.part_post + (int64_t)blockIdx.x * n, c, n, s_post[k]);
+      if (a.part_pre) map.store(a.part_pre + (int64_t)blockIdx.x * n, k, s_pre[k]);
+      if (a.part_post) map.store(a.part_post + (int64_t)blockIdx.x * n, k, s_post[k]);
     }
   }
 }
 
-// out[g][c] = sum over p < count of part[g * count + p][c], p in order within 32 strided shares, the shares
-// in order.  blockIdx.x: 32 columns; blockIdx.y: output row.
-constexpr int CS_COLS = 32, CS_SHARES = 32;
-__global__ __launch_bounds__(CS_COLS* CS_SHARES) void column_sum_kernel(const float* __restrict__ part, int64_t count,
-                                                                        int n, float* __restrict__ out) {
-  __shared__ float red[CS_SHARES][CS_COLS + 1];
-  const int cx = threadIdx.x % CS_COLS, sh = threadIdx.x / CS_COLS, c = blockIdx.x * CS_COLS + cx;
-  const int64_t first = blockIdx.y * count;
-  float s = 0.0f;
-  if (c < n) {
-    const float* p = part + first * n + c;
-    int64_t i = sh;
-    for (; i + 3 * CS_SHARES < count; i += 4 * CS_SHARES) {
-      const float v0 = p[i * n], v1 = p[(i + CS_SHARES) * n], v2 = p[(i + 2 * CS_SHARES) * n],
-                  v3 = p[(i + 3 * CS_SHARES) * n];
-      s += v0;
-      s += v1;
-      s += v2;
-      s += v3;
-    }
-    for (; i < count; i += CS_SHARES) s += p[i * n];
-  }
-  red[sh][cx] = s;
-  __syncthreads();
-  if (sh == 0 && c < n) {
-    float total = 0.0f;
+// Rows too wide for a workgroup's registers: the row is walked in chunks of eight columns per thread twice, once for
+// its three sums and once, read again from the caches, for the results; the parameters' sums stay in the
+// unit's own partials (read and written by the thread that owns the columns), which the caches hold too.
+template <typename TB, typename TR, typename TW>
+__global__ __launch_bounds__(1024) void block_norm_bwd_wide_kernel(const BwdArgs a) {
+  __shared__ uint32_t red[2][3][RowGroup<0>::kMaxWaves];
+  RowGroup<0> grp{red};
+  const int n = a.n;
+  const float inv_n = 1.0f / (float)n;
+  const int64_t unit = blockIdx.x;
+  int64_t r0, r1, gidx;
+  unit_range(a, unit, r0, r1, gidx);
+  int64_t gend = (gidx + 1) * a.gate_rows;
+  float* const post = a.part_post ? a.part_post + unit * n : nullptr;
+  float* const pre = a.part_pre ? a.part_pre + unit * n : nullptr;
+  const float zeros[8] = {};
+
+  Raw8<TW> wp, wq;
+  Raw8<TB> b, g, dy;
+  Raw8<TR> x, dr;
+  wp.fill(1.0f);
+  wq.fill(1.0f);
+  b.fill(0.0f);
+  g.fill(1.0f);
+  dy.fill(0.0f);
+  x.fill(0.0f);
+  dr.fill(0.0f);
+  // adds v to the columns' running sums, which start at the first token
+  auto accumulate = [&](const RowMap<1, 0>& map, float* sum, bool first, const float (&v)[8]) {
+    float out[8];
+    Raw8<float> old;
+    if (!first) map.load(old, sum, 0, n);
 #pragma unroll
-    for (int k = 0; k < CS_SHARES; ++k) total += red[k][cx];
-    out[blockIdx.y * (int64_t)n + c] = total;
+    for (int e = 0; e < 8; ++e) out[e] = first ? v[e] : old.get(e) + v[e];
+    map.store(sum, 0, out);
+  };
+  for (int64_t row = r0; row < r1; ++row) {
+    const float ib = a.w_post ? a.stats[2 * row] : 1.0f, ix = a.dy ? a.stats[2 * row + 1] : 0.0f;
+    auto load_chunk = [&](const RowMap<1, 0>& map) {
+      if (a.w_post) map.load(wp, (const TW*)a.w_post, 0, n);
+      if (a.dy) map.load(wq, (const TW*)a.w_pre, 0, n);
+      if (a.branch) map.load(b, (const TB*)a.branch + row * a.ldb, 0, n);
+      if (a.resid) map.load(x, (const TR*)a.resid + row * a.ldr, 0, n);
+      if (a.dy) map.load(dy, (const TB*)a.dy + row * a.lddy, 0, n);
+      if (a.dres) map.load(dr, (const TR*)a.dres + row * a.lddo, 0, n);
+      if (a.gate) map.load(g, (const TB*)a.gate + gidx * a.ldg, 0, n);
+      map.own(b, 0);
+      map.own(x, 0);
+      map.own(dy, 0);
+      map.own(dr, 0);
+    };
+    float sums[3] = {0.0f, 0.0f, 0.0f};
+    for (int c = 0; c < n; c += 8 * blockDim.x) {
+      const RowMap<1, 0> map(threadIdx.x + c / 8, 0, n);
+      load_chunk(map);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float d = dy.get(e), w = wq.get(e);
+        NormTerms(a, ib, ix, b.get(e), g.get(e), x.get(e), d, dr.get(e), wp.get(e), w).add(sums, d, w);
+      }
+    }
+    grp.template reduce<AddF32>(sums);
+    float m1, m2;
+    row_means(sums, inv_n, ix, m1, m2);
+    const bool gate_first = row == r0 || row + a.gate_rows == gend;
+    for (int c = 0; c < n; c += 8 * blockDim.x) {
+      const RowMap<1, 0> map(threadIdx.x + c / 8, 0, n);
+      load_chunk(map);
+      float dx_f[8], db_f[8], v_pre[8], v_post[8], v_gate[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float d = dy.get(e), w = wp.get(e);
+        const NormTerms m(a, ib, ix, b.get(e), g.get(e), x.get(e), d, dr.get(e), w, wq.get(e));
+        const float dxo = fmaf(-m1, m.xn, m.t), du = m.cg * dxo;
+        dx_f[e] = a.rscale * dxo;
+        v_pre[e] = d * m.xn;
+        v_post[e] = du * m.bn;
+        v_gate[e] = a.bscale * dxo * (w * m.bn);
+        db_f[e] = a.w_post ? ib * fmaf(-m2, m.bn, du * w) : du;
+      }
+      if (a.dx) map.store((TR*)a.dx + row * a.lddr, 0, dx_f);
+      if (a.db) map.store((TB*)a.db + row * a.lddb, 0, db_f);
+      if (pre) accumulate(map, pre, row == r0, v_pre);
+      if (post) accumulate(map, post, row == r0, v_post);
+      if (a.dgate) accumulate(map, a.dgate + gidx * n, gate_first, v_gate);
+      if (a.part_gate) accumulate(map, a.part_gate + unit * n, row == r0, v_gate);
+    }
+    if (a.segs == 0 && row + 1 == gend) {
+      ++gidx;
+      gend += a.gate_rows;
+    }
+  }
+  if (r0 >= r1)  // no tokens: its partials are zero
+    for (int c = 0; c < n; c += 8 * blockDim.x) {
+      const RowMap<1, 0> map(threadIdx.x + c / 8, 0, n);
+      if (pre) map.store(pre, 0, zeros);
+      if (post) map.store(post, 0, zeros);
+      if (a.part_gate) map.store(a.part_gate + unit * n, 0, zeros);
+    }
+}
+
+// Up to three sums over partials in one launch: out[g][c] = sum over p < count of part[g * count + p][c], p in
+// order within SHARES strided shares, the shares in order.  blockIdx.x: COLS columns; blockIdx.y: output row, the
+// sums' rows one after the other.
+struct ColumnSums {
+  struct One {
+    const float* part;
+    float* out;
+    int64_t count, groups;
+  } s[3];
+  int n;
+};
+template <int COLS, int SHARES>
+__global__ __launch_bounds__(COLS* SHARES) void column_sum_kernel(const ColumnSums a) {
+  __shared__ float red[SHARES][COLS + 1];
+  const int cx = threadIdx.x % COLS, sh = threadIdx.x / COLS, c = blockIdx.x * COLS + cx, n = a.n;
+  for (int64_t row = blockIdx.y;; row += gridDim.y) {
+    int64_t g = row;
+    int k = 0;
+    while (k < 3 && g >= a.s[k].groups) g -= a.s[k++].groups;
+    if (k == 3) return;
+    const int64_t count = a.s[k].count;
+    float s = 0.0f;
+    if (c < n) {
+      const float* p = a.s[k].part + g * count * n + c;
+      for (int64_t i = sh; i < count; i += 8 * SHARES) {
+        float v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = i + u * SHARES < count ? p[(i + u * SHARES) * n] : 0.0f;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) s += v[u];
+      }
+    }
+    if constexpr (SHARES > 1) {
+      red[sh][cx] = s;
+      __syncthreads();
+      for (int half = SHARES / 2; half > 0; half >>= 1) {
+        if (sh < half) red[sh][cx] += red[sh + half][cx];
+        __syncthreads();
+      }
+      s = red[0][cx];
+      __syncthreads();
+    }
+    if (sh == 0 && c < n) a.s[k].out[g * n + c] = s;
   }
 }
 
@@ -251,12 +412,19 @@ __global__ __launch_bounds__(CS_COLS* CS_SHARES) void column_sum_kernel(const fl
 
 using namespace wr;
 
+template <int N>
+using Int = std::integral_constant<int, N>;
+
 static size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 size_t wr_norm_bwd_ws_bytes(int64_t rows, int64_t n, int64_t gate_rows) {
   if (rows <= 0) return 256;
-  const BwdPlan p = bwd_plan(rows, n, gate_rows);
-  return 2 * round256((size_t)p.blocks * n * 4) + (p.segs ? round256((size_t)p.units * n * 4) : 0);
+  size_t most = 0;  // the larger of what the types need
+  for (const bool fp32 : {false, true}) {
+    const BwdPlan p = bwd_plan(rows, n, gate_rows, fp32);
+    most = std::max(most, 2 * round256((size_t)p.blocks * n * 4) + (p.segs ? round256((size_t)p.units * n * 4) : 0));
+  }
+  return most;
 }
 
 template <typename TB, typename TR, typename TW>
@@ -265,14 +433,14 @@ static void bwd_launch(wr_ctx* ctx, const BwdPlan& p, const BwdArgs& a) {
     hipLaunchKernelGGL((block_norm_bwd_kernel<TB, TR, TW, decltype(ch)::value, decltype(lanes)::value>),
                        dim3((unsigned)p.blocks), dim3(p.threads), 0, ctx->stream, a);
   };
-  const std::integral_constant<int, 1> one;
-  const std::integral_constant<int, 0> group;
-  if (p.lanes == 16) go(one, std::integral_constant<int, 16>{});
-  else if (p.lanes == 32) go(one, std::integral_constant<int, 32>{});
-  else if (p.lanes == 64) go(one, std::integral_constant<int, 64>{});
-  else if (p.chunks == 1) go(one, group);
-  else if (p.chunks == 2) go(std::integral_constant<int, 2>{}, group);
-  else go(std::integral_constant<int, 4>{}, group);
+  if (p.lanes == 8) go(Int<1>{}, Int<8>{});
+  else if (p.lanes == 16) go(Int<1>{}, Int<16>{});
+  else if (p.lanes == 32) go(Int<1>{}, Int<32>{});
+  else if (p.lanes == 64) go(Int<1>{}, Int<64>{});
+  else if (p.wide)
+    hipLaunchKernelGGL((block_norm_bwd_wide_kernel<TB, TR, TW>), dim3((unsigned)p.blocks), dim3(p.threads), 0, ctx->stream, a);
+  else if (p.chunks == 1) go(Int<1>{}, Int<0>{});
+  else if constexpr (sizeof(TB) + sizeof(TR) == 4) go(Int<2>{}, Int<0>{});
 }
 
 int wr_block_norm_backward_impl(wr_ctx* ctx, int64_t rows, int64_t n, const void* branch, int b_dtype, int64_t ldb,
@@ -281,23 +449,21 @@ int wr_block_norm_backward_impl(wr_ctx* ctx, int64_t rows, int64_t n, const void
                                 const void* w_pre, int w_dtype, const float* stats, const void* dy, int64_t lddy,
                                 const void* dresid_out, int64_t lddo, void* dbranch, int64_t lddb, void* dresid,
                                 int64_t lddr, float* dw_post, float* dgate, float* dw_pre) {
-  const unsigned cols = (unsigned)((n + CS_COLS - 1) / CS_COLS);
-  auto sum = [&](const float* from, int64_t count, int64_t groups, float* to) {
-    for (int64_t g0 = 0; g0 < groups; g0 += 65535) {
-      const unsigned gs = (unsigned)std::min<int64_t>(65535, groups - g0);
-      hipLaunchKernelGGL(column_sum_kernel, dim3(cols, gs), dim3(CS_COLS * CS_SHARES), 0, ctx->stream,
-                         from + g0 * count * n, count, (int)n, to + g0 * n);
-    }
+  auto add_up = [&](const ColumnSums& c, auto cols, auto shares) {
+    const int64_t outs = c.s[0].groups + c.s[1].groups + c.s[2].groups;
+    if (outs == 0) return;
+    constexpr int kCols = decltype(cols)::value, kShares = decltype(shares)::value;
+    const dim3 grid((unsigned)((n + kCols - 1) / kCols), (unsigned)std::min<int64_t>(outs, 65535));
+    hipLaunchKernelGGL((column_sum_kernel<kCols, kShares>), grid, dim3(kCols * kShares), 0, ctx->stream, c);
   };
   if (rows == 0) {  // sums over no tokens
-    if (dw_post) sum(nullptr, 0, 1, dw_post);
-    if (dw_pre) sum(nullptr, 0, 1, dw_pre);
-    if (dgate && gate_rows == 0) sum(nullptr, 0, 1, dgate);
+    add_up({{{nullptr, dw_post, 0, dw_post ? 1 : 0}, {nullptr, dw_pre, 0, dw_pre ? 1 : 0},
+             {nullptr, dgate, 0, dgate && gate_rows == 0 ? 1 : 0}}, (int)n}, Int<256>{}, Int<1>{});
     WR_CHECK_LAUNCH();
     return WR_OK;
   }
   if (ctx->ws_bytes < wr_norm_bwd_ws_bytes(rows, n, gate_rows) || !ctx->ws) return WR_EWORKSPACE;
-  const BwdPlan p = bwd_plan(rows, n, gate_rows);
+  const BwdPlan p = bwd_plan(rows, n, gate_rows, b_dtype == WR_F32 || r_dtype == WR_F32);
   char* ws = (char*)ctx->ws;
   const size_t part = round256((size_t)p.blocks * n * 4);
   BwdArgs a{};
@@ -306,6 +472,7 @@ int wr_block_norm_backward_impl(wr_ctx* ctx, int64_t rows, int64_t n, const void
   a.span = (int)p.span;
   a.segs = (int)p.segs;
   a.gate_rows = (int)p.gate_rows;
+  a.one_gate = p.gates == 1;
   a.units = p.units;
   a.branch = branch;
   a.ldb = ldb;
@@ -342,9 +509,17 @@ int wr_block_norm_backward_impl(wr_ctx* ctx, int64_t rows, int64_t n, const void
     default: bwd_launch<uint16_t, uint16_t, uint16_t>(ctx, p, a); break;
   }
   WR_CHECK_LAUNCH();
-  if (dw_post) sum(a.part_post, p.blocks, 1, dw_post);
-  if (dw_pre) sum(a.part_pre, p.blocks, 1, dw_pre);
-  if (a.part_gate) sum(a.part_gate, p.segs, p.gates, dgate);
+  // Many short sums (gate rows of a few units) take a thread for each column; the others share a column's
+  // partials among threads, with narrower workgroups where there are few columns.
+  const ColumnSums::One none{nullptr, nullptr, 0, 0};
+  const int64_t shares = p.gates == 1 ? p.blocks : p.segs;
+  const ColumnSums::One gates{a.part_gate, dgate, shares, a.part_gate ? p.gates : 0};
+  const bool apart = shares <= 32;
+  if (apart) add_up({{gates, none, none}, (int)n}, Int<256>{}, Int<1>{});
+  const ColumnSums sums{{{a.part_post, dw_post, p.blocks, dw_post ? 1 : 0}, {a.part_pre, dw_pre, p.blocks, dw_pre ? 1 : 0},
+                         apart ? none : gates}, (int)n};
+  if (n >= 1024) add_up(sums, Int<32>{}, Int<32>{});
+  else add_up(sums, Int<8>{}, Int<128>{});
   WR_CHECK_LAUNCH();
   return WR_OK;
 }

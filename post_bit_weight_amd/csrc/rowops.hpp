@@ -12,76 +12,150 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
 typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
 
-// Eight consecutive values of a row as they are stored.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {  // round to nearest even
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+}
+
+// Eight values of a row as they are stored.
 template <typename T>
 struct Raw8;
 template <>
 struct Raw8<uint16_t> {  // bf16 bit patterns
   u32x4 v;
   __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const u32x4_any*>(p); }
-  __device__ __forceinline__ void load_part(const uint16_t* p, int cnt) {
-    v = u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < cnt) v[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+  __device__ __forceinline__ void fill(float f) {
+    const uint32_t h = f32_to_bf16_bits(f) * 0x10001u;
+    v = u32x4{h, h, h, h};
   }
+  __device__ __forceinline__ void set(int e, uint16_t h) {
+    v[e >> 1] = e & 1 ? (v[e >> 1] & 0xffffu) | (uint32_t)h << 16 : (v[e >> 1] & 0xffff0000u) | h;
+  }
+  __device__ __forceinline__ void mask(int keep) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+      v[d] &= (uint32_t)(__builtin_amdgcn_sbfe(keep, 2 * d, 1) & 0xffff) | (uint32_t)__builtin_amdgcn_sbfe(keep, 2 * d + 1, 1) << 16;
+  }
+  __device__ __forceinline__ void round(const float (&f)[8]) {  // to nearest even
+#pragma unroll
+    for (int d = 0; d < 4; ++d) v[d] = pack_bf16(f[2 * d], f[2 * d + 1]);
+  }
+  __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<u32x4_any*>(p) = v; }
+  __device__ __forceinline__ uint16_t at(int e) const { return (uint16_t)(v[e >> 1] >> (16 * (e & 1))); }
   __device__ __forceinline__ float get(int e) const {
     return __uint_as_float(e & 1 ? v[e >> 1] & 0xffff0000u : v[e >> 1] << 16);
   }
 };
 template <>
 struct Raw8<float> {
-  u32x4 lo, hi;
+  u32x4 v[2];
   __device__ __forceinline__ void load(const float* p) {
-    lo = *reinterpret_cast<const u32x4_any*>(p);
-    hi = *reinterpret_cast<const u32x4_any*>(p + 4);
+    v[0] = *reinterpret_cast<const u32x4_any*>(p);
+    v[1] = *reinterpret_cast<const u32x4_any*>(p + 4);
   }
-  __device__ __forceinline__ void load_part(const float* p, int cnt) {
+  __device__ __forceinline__ void fill(float f) {
+    const uint32_t h = __float_as_uint(f);
+    v[0] = v[1] = u32x4{h, h, h, h};
+  }
+  __device__ __forceinline__ void set(int e, float f) { v[e >> 2][e & 3] = __float_as_uint(f); }
+  __device__ __forceinline__ void mask(int keep) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      lo[e] = e < cnt ? __float_as_uint(p[e]) : 0u;
-      hi[e] = e + 4 < cnt ? __float_as_uint(p[e + 4]) : 0u;
-    }
+    for (int e = 0; e < 8; ++e) v[e >> 2][e & 3] &= (uint32_t)__builtin_amdgcn_sbfe(keep, e, 1);
   }
-  __device__ __forceinline__ float get(int e) const { return __uint_as_float(e < 4 ? lo[e & 3] : hi[e & 3]); }
+  __device__ __forceinline__ void round(const float (&f)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) set(e, f[e]);
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    *reinterpret_cast<u32x4_any*>(p) = v[0];
+    *reinterpret_cast<u32x4_any*>(p + 4) = v[1];
+  }
+  __device__ __forceinline__ float at(int e) const { return get(e); }
+  __device__ __forceinline__ float get(int e) const { return __uint_as_float(v[e >> 2][e & 3]); }
 };
 
-// The eight values at column c of a row of n (zeros past its end).
-template <typename T>
-__device__ __forceinline__ void load8(Raw8<T>& r, const T* row, int c, int n) {
-  if (c + 8 <= n) {
-    r.load(row + c);
-  } else {
-    r.load_part(row + c, n - c);
-  }
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {  // round to nearest even
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
-}
-
-__device__ __forceinline__ void store8(uint16_t* row, int c, int n, const float (&f)[8]) {
-  const u32x4 v = {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
-  if (c + 8 <= n) {
-    *reinterpret_cast<u32x4_any*>(row + c) = v;
-  } else {
+// ---------------------------------------------------------------- which values a thread owns
+// A row of n values lies on LANES lanes of a wave, or (LANES == 0) on a whole workgroup; a thread owns CH
+// chunks of eight columns.  So that every load is one full vector load inside the row, the chunk that
+// would pass the row's end starts at n - 8 instead, and so do those of lanes that have none; `keep`
+// says which of its eight values are the thread's own.  LANES == 8 is for rows of fewer than eight
+// values: the first lane of eight holds them all, loaded one by one.
+template <int CH, int LANES>
+struct RowMap {
+  uint32_t col[CH];
+  int keep[CH];
+  bool ragged;  // some lane of this wave does not own all it loads (uniform)
+  __device__ __forceinline__ RowMap(int lane, int cstep, int n) {
+    bool part = false;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (c + e < n) row[c + e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+    for (int k = 0; k < CH; ++k) {
+      const int c = 8 * lane + k * cstep;
+      if constexpr (LANES == 8) {
+        col[k] = 0;
+        keep[k] = lane == 0 ? (1 << n) - 1 : 0;
+      } else {
+        col[k] = c < n - 8 ? c : n - 8;
+        keep[k] = c < n ? (0xff << (c - (int)col[k])) & 0xff : 0;
+      }
+      part |= keep[k] != 0xff;
+    }
+    ragged = __builtin_amdgcn_ballot_w64(part) != 0;
   }
-}
-__device__ __forceinline__ void store8(float* row, int c, int n, const float (&f)[8]) {
-  if (c + 8 <= n) {
-    const u32x4 lo = {__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
-    const u32x4 hi = {__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])};
-    *reinterpret_cast<u32x4_any*>(row + c) = lo;
-    *reinterpret_cast<u32x4_any*>(row + c + 4) = hi;
-  } else {
+  // keep[k] for the rare paths, unknown to the compiler before them: it would else form every mask and
+  // condition ahead of the row loop and hold them in registers.
+  __device__ __forceinline__ int bits(int k) const {
+    int b = keep[k];
+    asm volatile("" : "+v"(b));
+    return b;
+  }
+  // Where chunk k of a row starts: a uniform pointer plus a 32-bit offset of the lane, which needs no 64-bit
+  // address registers.
+  template <typename T>
+  __device__ __forceinline__ T* at(T* row, int k) const {
+    using C = typename std::conditional<std::is_const<T>::value, const char, char>::type;
+    return reinterpret_cast<T*>(reinterpret_cast<C*>(row) + (uint32_t)(col[k] * sizeof(T)));
+  }
+  // The chunk's values; those that are not the thread's own are zero after own().
+  template <typename T>
+  __device__ __forceinline__ void load(Raw8<T>& r, const T* row, int k, int n) const {
+    if constexpr (LANES == 8) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (c + e < n) row[c + e] = f[e];
+      for (int e = 0; e < 8; ++e) r.set(e, row[e < n ? e : n - 1]);
+    } else {
+      r.load(at(row, k));
+    }
   }
-}
+  template <typename T>
+  __device__ __forceinline__ void own(Raw8<T>& r, int k) const {
+    if (ragged) r.mask(bits(k));
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(T* row, int k, const Raw8<T>& r) const {
+    if (keep[k] == 0xff) {
+      r.store(at(row, k));
+    } else if (keep[k]) {
+      const int own_bits = bits(k);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (own_bits >> e & 1) at(row, k)[e] = r.at(e);
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(T* row, int k, const float (&f)[8]) const {
+    Raw8<T> r;
+    r.round(f);
+    store(row, k, r);
+  }
+  __device__ __forceinline__ void store(int8_t* row, int k, const u32x2_any& v) const {
+    if (keep[k] == 0xff) {
+      *reinterpret_cast<u32x2_any*>(at(row, k)) = v;
+    } else if (keep[k]) {
+      const int own_bits = bits(k);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (own_bits >> e & 1) at(row, k)[e] = (int8_t)(v[e >> 2] >> (8 * (e & 3)));
+    }
+  }
+};
 
 // ---------------------------------------------------------------- reductions over the lanes of a row
 struct AddF32 {
@@ -97,15 +171,24 @@ __device__ __forceinline__ T dpp(T v) {
 }
 
 // Over aligned groups of LANES (a power of two, 8..64) lanes; every lane gets the result, formed in
-// the same order on each.  Up to 16 lanes the partners come by DPP inside a row of 16, then by shuffles.
+// the same order on each.  The partners come by DPP inside a row of 16 lanes, then by swapping rows
+// and halves of the wave (a swap of a register with itself leaves one half in each result).
 template <typename OP, int LANES, typename T>
 __device__ __forceinline__ T lanes_reduce(T v) {
   v = OP::op(v, dpp<0xB1>(v));   // lane ^ 1
   v = OP::op(v, dpp<0x4E>(v));   // lane ^ 2
   v = OP::op(v, dpp<0x141>(v));  // the other four of eight
   if constexpr (LANES >= 16) v = OP::op(v, dpp<0x140>(v));  // the other eight of sixteen
-  if constexpr (LANES >= 32) v = OP::op(v, __shfl_xor(v, 16));
-  if constexpr (LANES >= 64) v = OP::op(v, __shfl_xor(v, 32));
+  if constexpr (LANES >= 32) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    v = OP::op(__builtin_bit_cast(T, (uint32_t)r[0]), __builtin_bit_cast(T, (uint32_t)r[1]));
+  }
+  if constexpr (LANES >= 64) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    v = OP::op(__builtin_bit_cast(T, (uint32_t)r[0]), __builtin_bit_cast(T, (uint32_t)r[1]));
+  }
   return v;
 }
 
@@ -124,18 +207,20 @@ struct RowGroup {
 #pragma unroll
       for (int k = 0; k < K; ++k) v[k] = lanes_reduce<OP, LANES>(v[k]);
     } else {
+      const int waves = blockDim.x >> 6, lane = threadIdx.x & 63;
 #pragma unroll
       for (int k = 0; k < K; ++k) v[k] = lanes_reduce<OP, 64>(v[k]);
-      const int waves = blockDim.x >> 6;
       if (waves > 1) {
-        if ((threadIdx.x & 63) == 0)
+        if (lane == 0)
 #pragma unroll
           for (int k = 0; k < K; ++k) lds[side][k][threadIdx.x >> 6] = __builtin_bit_cast(uint32_t, v[k]);
-        __syncthreads();
+        // LDS only: loads of a later row may stay in flight across the barrier
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        // every 16 lanes add the waves' values in the same order (0 is neutral for both operations)
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          v[k] = __builtin_bit_cast(T, lds[side][k][0]);
-          for (int w = 1; w < waves; ++w) v[k] = OP::op(v[k], __builtin_bit_cast(T, lds[side][k][w]));
+          const uint32_t u = lds[side][k][lane & 15];
+          v[k] = lanes_reduce<OP, 16>(__builtin_bit_cast(T, (lane & 15) < waves ? u : 0u));
         }
         side ^= 1;
       }
@@ -193,15 +278,5 @@ struct RowCoder {
     return u32x2_any{w[0], w[1]};
   }
 };
-
-__device__ __forceinline__ void store_codes(int8_t* row, int c, int n, const u32x2_any& v) {
-  if (c + 8 <= n) {
-    *reinterpret_cast<u32x2_any*>(row + c) = v;
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (c + e < n) row[c + e] = (int8_t)(v[e >> 2] >> (8 * (e & 3)));
-  }
-}
 
 }  // namespace wr
