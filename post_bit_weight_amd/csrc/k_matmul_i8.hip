@@ -1,14 +1,17 @@
 // Tokens times weights in 8-bit integers: y[t][r] = xs[t] ws[r] sum_j x[t][j] w[r][j] + bias[r], and
 // silu(gate) * up of two halves of the weights' rows.
 //
-// Both operands have the summed index contiguous, which is what a matrix-core operand wants: lane l of
-// a 32x32x32 int8 MFMA holds 16 consecutive bytes of row l % 32.  The sums are exact in int32, so their
-// order and any split of them change nothing.
+// Both operands have the summed index contiguous, which is what a matrix-core operand wants: lane l of a 16x16x64
+// int8 MFMA holds 16 consecutive bytes of row l % 16, of a 32x32x32 one of row l % 32.  The sums are exact in
+// int32, so neither their order nor any split of them changes the result.  Two kernels: small products cut the
+// sum over a workgroup's waves (matmul_i8_stream_kernel), large ones share operand tiles among them
+// (matmul_i8_big_kernel).
 #include "rowops.hpp"
 
 namespace wr {
 
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
 
 struct I8Args {
@@ -25,192 +28,424 @@ struct I8Args {
   int64_t ldy;
 };
 
-// Sixteen bytes at column c of a row of n bytes, zeros past its end.
+// Sixteen bytes at column c of a row of n >= 16 bytes, zeros past its end: one load inside the row, shifted down.
 __device__ __forceinline__ u32x4 load16(const int8_t* row, int c, int n) {
-  if (c + 16 <= n) return *reinterpret_cast<const u32x4_any*>(row + c);
-  u32x4 v = {0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int e = 0; e < 16; ++e)
-    if (c + e < n) v[e >> 2] |= (uint32_t)(uint8_t)row[c + e] << (8 * (e & 3));
-  return v;
+  const int at = std::min(c, n - 16), d = c - at;
+  const u32x4 v = *reinterpret_cast<const u32x4_any*>(row + at);
+  const uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
+  const int sh = 8 * (d & 7);
+  const uint64_t low = sh ? lo >> sh | hi << (64 - sh) : lo, high = hi >> sh;
+  const uint64_t a = d < 8 ? low : d < 16 ? high : 0, b = d < 8 ? high : 0;
+  return u32x4{(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)};
 }
 
 __device__ __forceinline__ void put(uint16_t* p, float v) { *p = (uint16_t)pack_bf16(v, v); }
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 
-__device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
-
-// 128 tokens x 128 weight rows per workgroup, four waves of 64 x 64, 64 bytes of the sum per step.  With
-// GLU the tile's weight rows are 64 gate rows and the 64 up rows of the same outputs, alternating by 32,
-// so that a lane holds both sums of an output.
-constexpr int T8 = 128, T8_K = 64, T8_LD = T8_K + 16;
-
-template <typename TY, bool GLU>
-__global__ __launch_bounds__(256) void matmul_i8_tile_kernel(const I8Args a) {
-  __shared__ __attribute__((aligned(16))) int8_t lx[T8 * T8_LD], lw[T8 * T8_LD];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wi = wave >> 1, wj = wave & 1;
-  const int outs = GLU ? a.rows / 2 : a.rows;
-  constexpr int kOuts = GLU ? T8 / 2 : T8;
-  const int t0 = blockIdx.y * T8, o0 = blockIdx.x * kOuts;
-  // the weight row of tile row i, or -1
-  auto weight_row = [&](int i) {
-    if constexpr (GLU) {
-      const int o = o0 + (i >> 6) * 32 + (i & 31);
-      return o < outs ? o + ((i >> 5) & 1) * outs : -1;
-    } else {
-      return o0 + i < outs ? o0 + i : -1;
-    }
-  };
-  i32x16 acc[2][2] = {};
-  for (int k0 = 0; k0 < a.n; k0 += T8_K) {
-    u32x4 vx[2], vw[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int i = (tid >> 2) + 64 * u, c = k0 + 16 * (tid & 3), wr_ = weight_row(i);
-      vx[u] = t0 + i < a.batch ? load16(a.x + (t0 + i) * a.ldx, c, a.n) : u32x4{0u, 0u, 0u, 0u};
-      vw[u] = wr_ >= 0 ? load16(a.w + wr_ * a.ldw, c, a.n) : u32x4{0u, 0u, 0u, 0u};
-    }
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int at = ((tid >> 2) + 64 * u) * T8_LD + 16 * (tid & 3);
-      *reinterpret_cast<u32x4*>(lx + at) = vx[u];
-      *reinterpret_cast<u32x4*>(lw + at) = vw[u];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < T8_K; k += 32) {
-      i32x4 fx[2], fw[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int at = (32 * u + (lane & 31)) * T8_LD + k + 16 * (lane >> 5);
-        fx[u] = *reinterpret_cast<const i32x4*>(lx + 64 * wi * T8_LD + at);
-        fw[u] = *reinterpret_cast<const i32x4*>(lw + 64 * wj * T8_LD + at);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fx[i], fw[j], acc[i][j], 0, 0, 0);
-    }
-  }
-  TY* y = (TY*)a.y;
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      const int t = t0 + 64 * wi + 32 * i + acc_row(v, lane);
-      if (t >= a.batch) continue;
-      const float xs = a.xs[t];
-      if constexpr (GLU) {
-        const int o = o0 + 32 * wj + (lane & 31);
-        if (o < outs) {
-          float g = (float)acc[i][0][v] * xs * a.ws[o], u = (float)acc[i][1][v] * xs * a.ws[outs + o];
-          if (a.bias) {
-            g += a.bias[o];
-            u += a.bias[outs + o];
-          }
-          put(y + t * a.ldy + o, silu(g) * u);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int o = o0 + 64 * wj + 32 * j + (lane & 31);
-          if (o < outs) {
-            const float z = (float)acc[i][j][v] * xs * a.ws[o];
-            put(y + t * a.ldy + o, a.bias ? z + a.bias[o] : z);
-          }
-        }
-      }
-    }
+__device__ __forceinline__ void put4(uint16_t* p, const float (&v)[4]) {
+  *reinterpret_cast<u32x2_any*>(p) = u32x2_any{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+}
+__device__ __forceinline__ void put4(float* p, const float (&v)[4]) {
+  *reinterpret_cast<u32x4_any*>(p) = u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
 }
 
-// Few tokens (up to 64): the weights are read once, straight from memory into matrix-core operands, and
-// everything else is hidden behind that.  A workgroup owns 16 outputs (with GLU or RF = 2, 32 weight rows) for
-// all tokens; its NW waves cut the sum into contiguous ranges of 64-byte steps, so that a wave has
-// many rows' loads in flight at once, and add their int32 sums in LDS.  A 16x16x64 MFMA takes 64
-// bytes of 16 weight rows (lane l: row l % 16, bytes 16 (l / 16) .. + 15) against 16 tokens; tokens
-// past the batch repeat its last one and are not stored.
-template <typename TY, bool GLU, int RF, int NT, int NW, int U>
-__global__ __launch_bounds__(64 * NW) void matmul_i8_few_kernel(const I8Args a) {
-  __shared__ int32_t red[NW][RF * NT][256];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int outs = GLU ? a.rows / 2 : a.rows;
-  const int o0 = blockIdx.x * (GLU ? 16 : 16 * RF), t0 = blockIdx.y * 16 * NT;
-  const int r = lane & 15, kb = 16 * (lane >> 4);
-  const int8_t* wrow[RF];
-  const int8_t* xrow[NT];
-#pragma unroll
-  for (int f = 0; f < RF; ++f) {
-    const int o = GLU ? std::min(o0 + r, outs - 1) + f * outs : std::min(o0 + 16 * f + r, outs - 1);
-    wrow[f] = a.w + o * a.ldw;
-  }
-#pragma unroll
-  for (int t = 0; t < NT; ++t) xrow[t] = a.x + std::min(t0 + 16 * t + r, a.batch - 1) * a.ldx;
+// v / (1 + exp(-v)) by the hardware's base-2 exponential and reciprocal (one unit in the last place each); rounding -v
+// log2(e) is worth |v| 2^-24 in exp(-v), which changes the result by less than a rounding of v itself does.
+__device__ __forceinline__ float silu(float v) {
+  return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504f));
+}
 
-  i32x4 acc[RF][NT] = {};
-  const int steps = a.n / 64, s0 = steps * wave / NW, s1 = steps * (wave + 1) / NW;
-  for (int s = s0; s < s1; s += U) {
-    i32x4 fw[U][RF], fx[U][NT];
+// Scales and stores four consecutive outputs o .. o + 3 of token t from their sums (with GLU also the up rows').
+template <typename TY, bool GLU>
+__device__ __forceinline__ void store_outputs(const I8Args& a, int outs, int t, int o, const i32x4& sum, const i32x4& up,
+                                              float xs, const f32x4& ws, const f32x4& wu, const f32x4& bs, const f32x4& bu) {
+  float z[4];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int c = 64 * std::min(s + u, s1 - 1) + kb;
-#pragma unroll
-      for (int f = 0; f < RF; ++f) fw[u][f] = __builtin_bit_cast(i32x4, (u32x4)*reinterpret_cast<const u32x4_any*>(wrow[f] + c));
-#pragma unroll
-      for (int t = 0; t < NT; ++t) fx[u][t] = __builtin_bit_cast(i32x4, (u32x4)*reinterpret_cast<const u32x4_any*>(xrow[t] + c));
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool past = s + u >= s1;  // a step past the range was read again and counts nothing
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const i32x4 x = past ? i32x4{0, 0, 0, 0} : fx[u][t];
-#pragma unroll
-        for (int f = 0; f < RF; ++f) acc[f][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u][f], x, acc[f][t], 0, 0, 0);
-      }
-    }
+  for (int e = 0; e < 4; ++e) {
+    z[e] = fmaf((float)sum[e] * xs, ws[e], bs[e]);
+    if constexpr (GLU) z[e] = silu(z[e]) * fmaf((float)up[e] * xs, wu[e], bu[e]);
   }
-  if (a.n % 64 != 0 && wave == NW - 1) {
-    const int c = 64 * steps + kb;
-    i32x4 fw[RF];
-#pragma unroll
-    for (int f = 0; f < RF; ++f) fw[f] = __builtin_bit_cast(i32x4, load16(wrow[f], c, a.n));
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const i32x4 x = __builtin_bit_cast(i32x4, load16(xrow[t], c, a.n));
-#pragma unroll
-      for (int f = 0; f < RF; ++f) acc[f][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[f], x, acc[f][t], 0, 0, 0);
-    }
+  if (t >= a.batch || o >= outs) return;
+  TY* p = (TY*)a.y + t * a.ldy + o;
+  if (o + 4 <= outs) {
+    put4(p, z);
+  } else {
+    for (int e = 0; e < outs - o; ++e) put(p + e, z[e]);
   }
-  // Register v of lane l holds weight row 4 (l / 16) + v and token l % 16 of a 16 x 16 block.
+}
+// Four values at o .. o + 3 of a vector of `outs` (the last one again past its end; zeros without a vector).
+__device__ __forceinline__ f32x4 load_outputs(const float* v, int outs, int o) {
+  if (!v) return f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  if (o + 4 <= outs) return __builtin_bit_cast(f32x4, (u32x4)*reinterpret_cast<const u32x4_any*>(v + o));
+  f32x4 r;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) r[e] = v[std::min(o + e, outs - 1)];
+  return r;
+}
+
+// The end of a workgroup whose NW waves hold int32 sums over shares of the summed index: adds them in LDS, scales and
+// stores.  Register v of lane l holds weight row 4 (l / 16) + v and token l % 16 of a 16 x 16 block; a token's
+// four quads of outputs lie in an order that spreads the tokens over the banks.
+template <typename TY, bool GLU, int RF, int NT, int NW>
+__device__ __forceinline__ void add_and_store(const I8Args& a, const i32x4 (&acc)[RF][NT], int32_t (*red)[RF * NT][256],
+                                              int o0, int t0) {
+  constexpr int OF = GLU ? RF / 2 : RF, OQ = 4 * OF, T = 64 * NW, kIter = (OF * NT * 64 + T - 1) / T;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, outs = GLU ? a.rows / 2 : a.rows;
+  // a thread's outputs are the same for all its tokens
+  const int oq = threadIdx.x % OQ, o = o0 + 4 * oq;
+  const f32x4 ws = load_outputs(a.ws, outs, o), bs = load_outputs(a.bias, outs, o);
+  f32x4 wu = {}, bu = {};
+  if constexpr (GLU) {
+    wu = load_outputs(a.ws + outs, outs, o);
+    bu = load_outputs(a.bias ? a.bias + outs : nullptr, outs, o);
+  }
+  float xs[kIter];
+#pragma unroll
+  for (int k = 0; k < kIter; ++k) xs[k] = a.xs[std::min(t0 + (int)(threadIdx.x + k * T) / OQ, a.batch - 1)];
 #pragma unroll
   for (int f = 0; f < RF; ++f)
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) red[wave][f * NT + t][16 * (lane & 15) + 4 * (lane >> 4) + v] = acc[f][t][v];
+    for (int t = 0; t < NT; ++t) {
+      const int tok = lane & 15, quad = (lane >> 4) ^ (tok >> 1 & 3);
+      *reinterpret_cast<i32x4*>(&red[wave][f * NT + t][16 * tok + 4 * quad]) = acc[f][t];
+    }
   __syncthreads();
-  TY* y = (TY*)a.y;
-  constexpr int kBlocks = GLU ? NT : RF * NT;  // blocks of 16 outputs x 16 tokens to store
-  for (int i = threadIdx.x; i < kBlocks * 256; i += 64 * NW) {
-    const int blk = i >> 8, e = i & 255, f = blk / NT, t = t0 + 16 * (blk % NT) + (e >> 4), o = o0 + 16 * f + (e & 15);
-    if (t >= a.batch || o >= outs) continue;
-    int32_t sum = 0, up = 0;
+#pragma unroll
+  for (int k = 0; k < kIter; ++k) {
+    const int i = threadIdx.x + k * T, ti = i / OQ;
+    if (OF * NT * 64 % T != 0 && i >= OF * NT * 64) break;
+    const int blk = (oq >> 2) * NT + (ti >> 4), tok = ti & 15, e = 16 * tok + 4 * ((oq & 3) ^ (tok >> 1 & 3));
+    i32x4 sum = {}, up = {};
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      sum += red[w][blk][e];
-      if constexpr (GLU) up += red[w][NT + blk][e];
+      sum += *reinterpret_cast<const i32x4*>(&red[w][blk][e]);
+      if constexpr (GLU) up += *reinterpret_cast<const i32x4*>(&red[w][OF * NT + blk][e]);
     }
-    const float xs = a.xs[t];
-    float z = (float)sum * xs * a.ws[o];
-    if (a.bias) z += a.bias[o];
-    if constexpr (GLU) {
-      float u = (float)up * xs * a.ws[outs + o];
-      if (a.bias) u += a.bias[outs + o];
-      z = silu(z) * u;
+    store_outputs<TY, GLU>(a, outs, t0 + ti, o, sum, up, xs[k], ws, wu, bs, bu);
+  }
+}
+
+// Rows of fewer than 16 bytes: a thread for each output.
+template <typename TY, bool GLU>
+__global__ __launch_bounds__(256) void matmul_i8_short_kernel(const I8Args a) {
+  const int outs = GLU ? a.rows / 2 : a.rows;
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < (int64_t)a.batch * outs; i += gridDim.x * (int64_t)256) {
+    const int t = (int)(i / outs), o = (int)(i % outs);
+    auto z = [&](int r) {
+      int sum = 0;
+      for (int j = 0; j < a.n; ++j) sum += (int)a.x[t * a.ldx + j] * (int)a.w[r * a.ldw + j];
+      return fmaf((float)sum * a.xs[t], a.ws[r], a.bias ? a.bias[r] : 0.0f);
+    };
+    put((TY*)a.y + t * a.ldy + o, GLU ? silu(z(o)) * z(outs + o) : z(o));
+  }
+}
+
+// ---- LDS DMA.  Sixteen-byte chunk c of row r of a slice lies at chunk c ^ swizzle(r), so that the sixteen rows an
+// operand read touches at once lie on different banks (rows of 128 bytes: two, of 64 bytes: four fill the banks).
+typedef __attribute__((address_space(3))) char lds_char;
+template <int ROW>
+__device__ __forceinline__ int swizzle(int row) {
+  return ROW == 128 ? row >> 1 & 7 : row >> 2 & 3;
+}
+// Wave-wide LDS DMA: lane l copies the 16 bytes at base + off to LDS byte m0 + 16 l.  In assembly so that the compiler
+// does not wait for it before every LDS read; vm_wait awaits it.  The M0 write needs one wait state before the DMA.
+__device__ __forceinline__ void lds_dma16(const void* base, uint32_t off, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %2" ::"v"(off), "s"(m0), "s"(base) : "memory", "m0");
+}
+template <int N>
+__device__ __forceinline__ void vm_wait() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// Small products.  A workgroup owns RF x 16 weight rows (with GLU half of them gate rows and half the same outputs' up
+// rows) by NT x 16 tokens, and its NW waves cut the sum into contiguous ranges of 128-byte slices: few tokens or
+// few outputs still occupy the chip, and a byte is read from LDS once.  Each wave streams its range through a ring
+// of NS slots of its own, eight rows of 128 bytes (whole cache lines) per copy instruction; the waves share nothing
+// before their sums are added at the end, so the loop has no barrier.  With DMA the copies go to LDS directly, NS
+// slices ahead and without registers; rows that are not 16-byte aligned come through registers, one slice
+// ahead.  Rows and tokens past the end repeat the last one and are not stored.
+template <typename TY, bool GLU, int RF, int NT, int NW, int NS, bool DMA>
+__global__ __launch_bounds__(64 * NW) void matmul_i8_stream_kernel(const I8Args a) {
+  constexpr int F = RF + NT, OF = GLU ? RF / 2 : RF;  // blocks of 16 rows; of 16 outputs
+  constexpr int kSlot = F * 16 * 128;
+  static_assert(DMA || NS == 2, "the copies through registers alternate between two slots");
+  extern __shared__ __attribute__((aligned(1024))) char i8_lds[];
+  lds_char* const lds = (lds_char*)i8_lds;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int outs = GLU ? a.rows / 2 : a.rows;
+  const int o0 = blockIdx.x * 16 * OF, t0 = blockIdx.y * 16 * NT;
+  lds_char* const ring = lds + wave * NS * kSlot;
+  const uint32_t ring_at = (uint32_t)(uintptr_t)ring;
+
+  // Copies: instruction i (of 2 F) fills rows 8 i .. + 7 of a slot, lane l the place l % 8 of its row l / 8: the chunk at
+  // column `col` of a slice.  The row starts `off` bytes after `base`, which is the same for all lanes.
+  using Off = typename std::conditional<DMA, uint32_t, uint64_t>::type;
+  const int8_t* base[2 * F];
+  Off off[2 * F];
+  int col[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) col[h] = 16 * ((lane & 7) ^ swizzle<128>(8 * h + (lane >> 3)));
+#pragma unroll
+  for (int i = 0; i < 2 * F; ++i) {
+    const int f = i >> 1, r = 8 * (i & 1) + (lane >> 3);
+    base[i] = f < RF ? a.w + o0 * a.ldw + (int64_t)(f / OF * outs) * a.ldw : a.x + t0 * a.ldx;
+    off[i] = f < RF ? (Off)std::min(16 * (f % OF) + r, outs - 1 - o0) * (Off)a.ldw
+                    : (Off)std::min(16 * (f - RF) + r, a.batch - 1 - t0) * (Off)a.ldx;
+  }
+  const int slices = (a.n + 127) / 128, s0 = slices * wave / NW, s1 = slices * (wave + 1) / NW;
+  const int whole = std::min(s1, a.n / 128);  // slices from here on pass n
+  auto fetch = [&](int s, int i) {
+    if (s < whole) return (u32x4)*reinterpret_cast<const u32x4_any*>(base[i] + off[i] + (128 * s + col[i & 1]));
+    return load16(base[i] + off[i], 128 * s + col[i & 1], a.n);
+  };
+  auto put_lds = [&](int slot, int i, const u32x4& v) {
+    *(__attribute__((address_space(3))) u32x4*)(ring + slot * kSlot + 1024 * i + 16 * lane) = v;
+  };
+  auto issue = [&](int s, int slot) {
+    if (s < whole) {
+      const uint32_t at = __builtin_amdgcn_readfirstlane(ring_at + slot * kSlot);
+      if constexpr (DMA)
+#pragma unroll
+        for (int i = 0; i < 2 * F; ++i) lds_dma16(base[i] + 128 * s, off[i] + col[i & 1], at + 1024 * i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2 * F; ++i) put_lds(slot, i, fetch(s, i));
     }
-    put(y + t * a.ldy + o, z);
+  };
+  const int r = lane & 15;
+  uint32_t rd[2];  // where this lane reads in a block, for either half of a slice
+#pragma unroll
+  for (int u = 0; u < 2; ++u) rd[u] = r * 128 + (((4 * u + (lane >> 4)) ^ swizzle<128>(r)) << 4);
+
+  i32x4 acc[RF][NT] = {};
+  u32x4 held[DMA ? 1 : 2 * F];  // the next slice on its way through registers
+  if constexpr (DMA) {
+#pragma unroll
+    for (int p = 0; p < NS; ++p)
+      if (s0 + p < s1) issue(s0 + p, p);
+  } else if (s0 < s1) {
+#pragma unroll
+    for (int i = 0; i < 2 * F; ++i) held[i] = fetch(s0, i);
+#pragma unroll
+    for (int i = 0; i < 2 * F; ++i) put_lds(0, i, held[i]);
+    if (s0 + 1 < s1)
+#pragma unroll
+      for (int i = 0; i < 2 * F; ++i) held[i] = fetch(s0 + 1, i);
+  }
+  int slot = 0;
+  for (int s = s0; s < s1; ++s) {
+    if constexpr (DMA) {
+      // slice s has landed once only the copies of later slices are outstanding
+      if (s + NS <= whole) vm_wait<(NS - 1) * 2 * F>();
+      else vm_wait<0>();
+    }
+    const lds_char* st = ring + slot * kSlot;
+    i32x4 fr[2][F];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int f = 0; f < F; ++f) fr[u][f] = *(const __attribute__((address_space(3))) i32x4*)(st + f * 2048 + rd[u]);
+    const int next = slot == NS - 1 ? 0 : slot + 1;
+    if constexpr (DMA) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read: the slot may be filled again
+      __builtin_amdgcn_sched_barrier(0);
+      if (s + NS < s1) issue(s + NS, slot);
+    } else if (s + 1 < s1) {
+#pragma unroll
+      for (int i = 0; i < 2 * F; ++i) put_lds(next, i, held[i]);
+      if (s + 2 < s1)
+#pragma unroll
+        for (int i = 0; i < 2 * F; ++i) held[i] = fetch(s + 2, i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int f = 0; f < RF; ++f) acc[f][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fr[u][f], fr[u][RF + t], acc[f][t], 0, 0, 0);
+    slot = next;
+  }
+  __syncthreads();  // the sums go where the rings were
+  add_and_store<TY, GLU, RF, NT, NW>(a, acc, reinterpret_cast<int32_t(*)[RF * NT][256]>(i8_lds), o0, t0);
+}
+
+// Large products: WI x WJ waves share a tile of 32 FI WI tokens x 32 FJ WJ weight rows, each with 32 FI x 32 FJ of it
+// in registers (32x32x32 MFMAs).  Slices of BK bytes of the tile's rows are copied into a ring of NS slots by LDS
+// DMA, NS slices ahead; the operands of the next 32 bytes are read while the present ones are multiplied.  Chunk c
+// of row r lies at chunk c ^ f(r) (see the stream kernel; with 64-byte rows f(r) = r / 2 % 4).
+template <typename TY, bool GLU, int FI, int FJ, int WI, int WJ, int BK, int NS, bool LATE>
+__global__ __launch_bounds__(64 * WI * WJ, 1) void matmul_i8_big_kernel(const I8Args a, int tiles_t, int tiles_o) {
+  constexpr int NW = WI * WJ, TM = 32 * FI * WI, TN = 32 * FJ * WJ;
+  constexpr int CPR = BK / 16, RPI = 64 / CPR;       // chunks per row, rows per copy instruction
+  constexpr int kSlot = (TM + TN) * BK;
+  constexpr int kCopies = (TM + TN) / RPI / NW;      // copy instructions per wave and slice
+  constexpr int KS = BK / 32;                        // MFMA steps per slice
+  constexpr int kOuts = GLU ? TN / 2 : TN;
+  static_assert((TM + TN) % (RPI * NW) == 0 && KS % 2 == 0 && (!GLU || FJ % 2 == 0), "tile shape");
+  extern __shared__ __attribute__((aligned(1024))) char i8_lds[];
+  lds_char* const lds = (lds_char*)i8_lds;
+  const uint32_t lds_at = (uint32_t)(uintptr_t)lds;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wi = wave / WJ, wj = wave % WJ;
+  const int outs = GLU ? a.rows / 2 : a.rows;
+
+  // Workgroup b runs on XCD b % 8: each XCD takes a contiguous range of the tiles, in bands of eight token tiles
+  // by all output tiles, so that the workgroups it runs at once share operand rows in its L2.
+  int ti, oi;
+  {
+    const int tiles = tiles_t * tiles_o, q = tiles / 8, rem = tiles % 8, x = blockIdx.x % 8, at = blockIdx.x / 8;
+    if (at >= q + (x < rem ? 1 : 0)) return;  // the grid is rounded up to a multiple of 8
+    const int t = x * q + std::min(x, rem) + at, band = t / (8 * tiles_o), r = t - band * 8 * tiles_o;
+    const int height = std::min(8, tiles_t - 8 * band);
+    ti = 8 * band + r % height;
+    oi = r / height;
+  }
+  const int t0 = ti * TM, o0 = oi * kOuts;
+
+  // Copies: instruction k = i NW + wave of a slice fills rows k RPI .. of the slot (TN weight rows, then TM tokens),
+  // lane l the place l % CPR of its row l / CPR.  With GLU the weight rows are 32 gate rows, the same outputs' 32 up
+  // rows, and so on.
+  const int crow = lane / CPR;
+  const int8_t* base[kCopies];  // the same for all lanes
+  uint32_t off[kCopies], col[kCopies];
+#pragma unroll
+  for (int i = 0; i < kCopies; ++i) {
+    const int r = (i * NW + wave) * RPI + crow;
+    col[i] = 16 * ((lane % CPR) ^ swizzle<BK>(r));
+    off[i] = r >= TN ? (uint32_t)std::min(r - TN, a.batch - 1 - t0) * (uint32_t)a.ldx
+                     : (uint32_t)std::min(GLU ? (r >> 6) * 32 + (r & 31) : r, outs - 1 - o0) * (uint32_t)a.ldw;
+  }
+#pragma unroll
+  for (int i = 0; i < kCopies; ++i) {
+    const int r = (i * NW + wave) * RPI;
+    const int64_t up = GLU ? (int64_t)((r >> 5 & 1) * outs) * a.ldw : 0;
+    base[i] = r >= TN ? a.x + t0 * a.ldx : a.w + o0 * a.ldw + up;
+  }
+  auto issue = [&](int s, int slot) {
+    if (BK * (s + 1) <= a.n) {
+      const uint32_t at = __builtin_amdgcn_readfirstlane(lds_at + slot * kSlot + wave * 1024);
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) lds_dma16(base[i] + BK * s, off[i] + col[i], at + i * NW * 1024);
+    } else {  // past n: through registers, with zeros
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i)
+        *(__attribute__((address_space(3))) u32x4*)(lds + slot * kSlot + (i * NW + wave) * 1024 + 16 * lane) = load16(base[i] + off[i], BK * s + col[i], a.n);
+    }
+  };
+
+  uint32_t rd[KS];  // this lane's place in a block of 32 rows for each MFMA step of a slice
+#pragma unroll
+  for (int u = 0; u < KS; ++u) rd[u] = (lane & 31) * BK + (((2 * u + (lane >> 5)) ^ swizzle<BK>(lane & 31)) << 4);
+  i32x4 fw[2][FJ], fx[2][FI];
+  auto read = [&](int slot, int u, int set) {
+    const lds_char* st = lds + slot * kSlot + rd[u];
+#pragma unroll
+    for (int j = 0; j < FJ; ++j) fw[set][j] = *(const __attribute__((address_space(3))) i32x4*)(st + (wj * FJ + j) * 32 * BK);
+#pragma unroll
+    for (int i = 0; i < FI; ++i) fx[set][i] = *(const __attribute__((address_space(3))) i32x4*)(st + (TN + (wi * FI + i) * 32) * BK);
+  };
+  i32x16 acc[FI][FJ];
+#pragma unroll
+  for (int i = 0; i < FI; ++i)
+#pragma unroll
+    for (int j = 0; j < FJ; ++j) acc[i][j] = i32x16{};
+  auto multiply = [&](int set) {
+#pragma unroll
+    for (int i = 0; i < FI; ++i)
+#pragma unroll
+      for (int j = 0; j < FJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[set][j], fx[set][i], acc[i][j], 0, 0, 0);
+  };
+
+  const int slices = (a.n + BK - 1) / BK, dma = a.n / BK;  // the last slice is not copied by DMA if it passes n
+#pragma unroll
+  for (int p = 0; p < NS; ++p)
+    if (p < slices) issue(p, p);
+  if (dma >= NS) vm_wait<kCopies*(NS - 1)>();
+  else vm_wait<0>();
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  if (slices > 0) read(0, 0, 0);
+  int slot = 0;
+  for (int s = 0; s < slices; ++s) {
+    const int next = slot == NS - 1 ? 0 : slot + 1;
+#pragma unroll
+    for (int u = 0; u < KS; ++u) {
+      if (u + 1 < KS) {
+        read(slot, u + 1, (u + 1) & 1);
+        multiply(u & 1);
+      } else {
+        if (s + 1 < slices) {
+          // slice s + 1 has landed once only the copies of slices s + 2 .. s + NS - 1 are outstanding
+          if (s + NS <= dma) vm_wait<kCopies*(NS - 2)>();
+          else vm_wait<0>();
+          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+          // every wave has read all of slice s: its slot is free.  With one workgroup on a CU the copies wait
+          // until the matrix cores have work; with two, the other one's products cover them.
+          if (!LATE && s + NS < slices) issue(s + NS, slot);
+          read(next, 0, 0);
+        }
+        multiply(u & 1);
+        if (LATE && s + NS < slices) issue(s + NS, slot);
+      }
+    }
+    slot = next;
+  }
+
+  // Register v of lane l holds weight row acc_row(v, l) and token l % 32 of a 32 x 32 block: four consecutive outputs of 32
+  // tokens at a time.  Stored like that a wave would write pieces of 16 bytes; each wave instead turns 32 tokens'
+  // outputs in LDS (rows padded by 16 bytes, which spreads them over the banks) and stores whole rows.
+  constexpr int WO = GLU ? 16 * FJ : 32 * FJ;               // outputs of a wave
+  constexpr int RB = WO * (int)sizeof(TY), LS = RB + 16;    // bytes of a token's outputs, and in LDS
+  constexpr int LPR = RB / 16, kPer = 16 / (int)sizeof(TY);  // lanes that store a row, outputs of one of them
+  static_assert(NW * 32 * LS <= NS * kSlot, "the turned outputs take the ring's place");
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // no wave reads the ring any more
+  lds_char* const turn = lds + wave * 32 * LS;
+  const int ow = o0 + wj * WO;
+  f32x4 ws[FJ][4], bs[FJ][4];
+#pragma unroll
+  for (int j = 0; j < FJ; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int o = ow + (GLU ? j / 2 : j) * 32 + 8 * q + 4 * (lane >> 5), up = GLU && j % 2 ? outs : 0;
+      ws[j][q] = load_outputs(a.ws + up, outs, o);
+      bs[j][q] = load_outputs(a.bias ? a.bias + up : nullptr, outs, o);
+    }
+#pragma unroll
+  for (int i = 0; i < FI; ++i) {
+    const int tw = t0 + (wi * FI + i) * 32;
+    const float xs = a.xs[std::min(tw + (lane & 31), a.batch - 1)];
+#pragma unroll
+    for (int j = 0; j < FJ; j += GLU ? 2 : 1)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float z[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          z[e] = fmaf((float)acc[i][j][4 * q + e] * xs, ws[j][q][e], bs[j][q][e]);
+          if constexpr (GLU) z[e] = silu(z[e]) * fmaf((float)acc[i][j + 1][4 * q + e] * xs, ws[j + 1][q][e], bs[j + 1][q][e]);
+        }
+        lds_char* const to = turn + (lane & 31) * LS + ((GLU ? j / 2 : j) * 32 + 8 * q + 4 * (lane >> 5)) * (int)sizeof(TY);
+        if constexpr (sizeof(TY) == 2)
+          *(__attribute__((address_space(3))) u32x2*)to = u32x2{pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3])};
+        else
+          *(__attribute__((address_space(3))) f32x4*)to = f32x4{z[0], z[1], z[2], z[3]};
+      }
+#pragma unroll
+    for (int k = 0; k < LPR / 2; ++k) {
+      const int row = k * (64 / LPR) + lane / LPR, at = lane % LPR, t = tw + row, o = ow + at * kPer;
+      const u32x4 v = *(const __attribute__((address_space(3))) u32x4*)(turn + row * LS + 16 * at);
+      if (t >= a.batch || o >= outs) continue;
+      TY* p = (TY*)a.y + t * a.ldy + o;
+      if (o + kPer <= outs) {
+        *reinterpret_cast<u32x4_any*>(p) = v;
+      } else {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e)
+          if (o + e < outs) {
+            if constexpr (sizeof(TY) == 2) p[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+            else p[e] = __uint_as_float(v[e]);
+          }
+      }
+    }
   }
 }
 
@@ -218,48 +453,86 @@ __global__ __launch_bounds__(64 * NW) void matmul_i8_few_kernel(const I8Args a) 
 
 using namespace wr;
 
-template <typename TY, bool GLU, int NT>
-static void few_launch(wr_ctx* ctx, const I8Args& a) {
+template <typename TY, bool GLU, int RF, int NT, int NW, int NS>
+static int stream_launch(wr_ctx* ctx, const I8Args& a, bool dma) {
+  constexpr int OF = GLU ? RF / 2 : RF;
   const int outs = GLU ? a.rows / 2 : a.rows;
-  constexpr int RF = GLU ? 2 : 1;
-  const dim3 grid((outs + 15) / 16, (a.batch + 16 * NT - 1) / (16 * NT));
-  constexpr int U = NT == 1 ? 8 : 4;
-  if (a.n >= 4096) {
-    constexpr int NW = NT <= 2 ? 16 : 8;
-    hipLaunchKernelGGL((matmul_i8_few_kernel<TY, GLU, RF, NT, NW, U>), grid, dim3(64 * NW), 0, ctx->stream, a);
-  } else {
-    hipLaunchKernelGGL((matmul_i8_few_kernel<TY, GLU, RF, NT, 8, U>), grid, dim3(512), 0, ctx->stream, a);
+  const dim3 grid((outs + 16 * OF - 1) / (16 * OF), (a.batch + 16 * NT - 1) / (16 * NT));
+  auto go = [&](auto slots, auto direct) {
+    constexpr int kSlots = decltype(slots)::value;
+    constexpr int lds = NW * std::max(kSlots * (RF + NT) * 2048, RF * NT * 1024);
+    static_assert(lds <= 160 * 1024, "LDS");
+    auto* kernel = matmul_i8_stream_kernel<TY, GLU, RF, NT, NW, kSlots, decltype(direct)::value>;
+    if (!lds_limit((const void*)kernel, lds)) return WR_EHIP;
+    hipLaunchKernelGGL(kernel, grid, dim3(64 * NW), lds, ctx->stream, a);
+    return WR_OK;
+  };
+  return dma ? go(std::integral_constant<int, NS>{}, std::true_type{}) : go(std::integral_constant<int, 2>{}, std::false_type{});
+}
+
+template <typename TY, bool GLU, int FI, int FJ, int WI, int WJ, int BK, int NS, bool LATE>
+static int big_launch(wr_ctx* ctx, const I8Args& a) {
+  constexpr int TM = 32 * FI * WI, TN = 32 * FJ * WJ, kOuts = GLU ? TN / 2 : TN;
+  constexpr int lds = NS * (TM + TN) * BK;
+  static_assert(lds <= 160 * 1024, "LDS");
+  const int outs = GLU ? a.rows / 2 : a.rows;
+  const int tt = (a.batch + TM - 1) / TM, to = (outs + kOuts - 1) / kOuts;
+  auto* kernel = matmul_i8_big_kernel<TY, GLU, FI, FJ, WI, WJ, BK, NS, LATE>;
+  if (!lds_limit((const void*)kernel, lds)) return WR_EHIP;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)((tt * to + 7) / 8 * 8)), dim3(64 * WI * WJ), lds, ctx->stream, a, tt, to);
+  return WR_OK;
+}
+
+template <typename TY, bool GLU>
+static int matmul_launch(wr_ctx* ctx, const I8Args& a, bool dma) {
+  if (a.n < 16) {
+    const int64_t all = (int64_t)a.batch * (GLU ? a.rows / 2 : a.rows);
+    hipLaunchKernelGGL((matmul_i8_short_kernel<TY, GLU>), dim3((unsigned)std::min<int64_t>((all + 255) / 256, 1 << 20)),
+                       dim3(256), 0, ctx->stream, a);
+    return WR_OK;
   }
+  constexpr int R = GLU ? 2 : 1;
+  const int64_t cu = ctx->num_cu;
+  auto tiles = [&](int64_t rows, int64_t tokens) { return ((a.rows + rows - 1) / rows) * ((a.batch + tokens - 1) / tokens); };
+  // The smallest tile whose workgroups run all at once (the time of a small product is its latency), measured at
+  // n = 2560 and 9728, 4096 and 2560 outputs: 1 token 3.8 and 6.2 us on 16 x 16 (a floor of 2.0 and 4.8 at a copy's
+  // rate; 7.0 and 13.7 on 64 x 64), 64 tokens 5.2 and 9.7 on 32 x 32 (7.3 and 12.4 on 16 x 16, 8.2 and 16.5 on
+  // 64 x 64), 256 tokens 8.8 and 16.8 on 64 x 64 (15.0 and 24.9 on 32 x 32).
+  if (a.batch <= 16 && tiles(16 * R, 16) <= 2 * cu) return stream_launch<TY, GLU, R, 1, 8, 2>(ctx, a, dma);
+  if (tiles(16 * R, 32) <= cu) return stream_launch<TY, GLU, R, 2, 8, 2>(ctx, a, dma);
+  if (tiles(32, 32) <= cu) return stream_launch<TY, GLU, 2, 2, 8, 2>(ctx, a, dma);
+  if (tiles(64, 32) <= cu) return stream_launch<TY, GLU, 4, 2, 4, 3>(ctx, a, dma);
+  if (a.batch <= 16) return stream_launch<TY, GLU, R, 1, 8, 2>(ctx, a, dma);
+  if (tiles(32, 64) <= cu) return stream_launch<TY, GLU, 2, 4, 4, 2>(ctx, a, dma);
+  // Two rounds of 64 x 64 beat shared tiles where the sum is long (512 tokens, 9728 -> 2560: 32.5 us against 38.5).
+  if (!dma || tiles(64, 64) <= (!GLU && a.n >= 4096 ? 2 : 1) * cu) return stream_launch<TY, GLU, 4, 4, 4, 2>(ctx, a, dma);
+  if (tiles(128, 64) <= 2 * cu) return big_launch<TY, GLU, 1, 2, 2, 2, 128, 3, false>(ctx, a);
+  // A round of 256 x 256 tiles takes 1.6 times one of 128 x 128, of which a CU holds two, for twice the work: 8192
+  // tokens 2560 -> 2 x 9728: 437 us against 483; 1024 tokens: 74 against 61.
+  const int64_t g = (tiles(128, 128) + 2 * cu - 1) / (2 * cu), h = (tiles(256, 256) + cu - 1) / cu;
+  if (8 * h <= 5 * g) return big_launch<TY, GLU, 4, 2, 2, 4, 128, 2, true>(ctx, a);
+  return big_launch<TY, GLU, 2, 2, 2, 2, 128, 2, false>(ctx, a);
 }
 
 int wr_matmul_i8_impl(wr_ctx* ctx, const int8_t* x, int64_t ldx, const float* x_scales, int64_t batch, const int8_t* w,
                       int64_t ldw, const float* w_scales, int64_t rows, int64_t n, const float* bias, bool glu, void* y,
                       int y_dtype, int64_t ldy) {
-  const int64_t outs = glu ? rows / 2 : rows, per = glu ? T8 / 2 : T8;
-  const int64_t slice = (int64_t)T8 * 32768;  // tokens per launch (grid.y)
+  if (batch == 1) ldx = 0;  // a single row's stride is not used
+  if (rows == 1) ldw = 0;
+  if (n == 0) {  // nothing is read
+    x = w = nullptr;
+    ldx = ldw = 0;
+  }
+  // LDS DMA takes 16-byte aligned rows and, from a tile's first row, 32-bit offsets
+  const bool dma = ((uintptr_t)x | (uintptr_t)w | (uint64_t)ldx | (uint64_t)ldw) % 16 == 0 && ldx < (1 << 24) && ldw < (1 << 24);
+  const int64_t slice = (int64_t)1 << 20;  // tokens per launch (grid.y of 16 tokens each)
   for (int64_t t0 = 0; t0 < batch; t0 += slice) {
     const I8Args a{x + t0 * ldx, ldx, x_scales + t0, (int)std::min(slice, batch - t0), w, ldw, w_scales, (int)rows,
                    (int)n, bias, (char*)y + t0 * ldy * (y_dtype == WR_BF16 ? 2 : 4), ldy};
-    if (a.batch <= 64) {
-      auto few = [&](auto ty, auto g) {
-        using TY = decltype(ty);
-        constexpr bool kGlu = decltype(g)::value;
-        if (a.batch <= 16) few_launch<TY, kGlu, 1>(ctx, a);
-        else if (a.batch <= 32) few_launch<TY, kGlu, 2>(ctx, a);
-        else few_launch<TY, kGlu, 4>(ctx, a);
-      };
-      if (y_dtype == WR_BF16 && glu) few(uint16_t{}, std::true_type{});
-      else if (y_dtype == WR_BF16) few(uint16_t{}, std::false_type{});
-      else if (glu) few(float{}, std::true_type{});
-      else few(float{}, std::false_type{});
-      WR_CHECK_LAUNCH();
-      continue;
-    }
-    const dim3 grid((unsigned)((outs + per - 1) / per), (unsigned)((a.batch + T8 - 1) / T8));
-    if (y_dtype == WR_BF16 && glu) hipLaunchKernelGGL((matmul_i8_tile_kernel<uint16_t, true>), grid, dim3(256), 0, ctx->stream, a);
-    else if (y_dtype == WR_BF16) hipLaunchKernelGGL((matmul_i8_tile_kernel<uint16_t, false>), grid, dim3(256), 0, ctx->stream, a);
-    else if (glu) hipLaunchKernelGGL((matmul_i8_tile_kernel<float, true>), grid, dim3(256), 0, ctx->stream, a);
-    else hipLaunchKernelGGL((matmul_i8_tile_kernel<float, false>), grid, dim3(256), 0, ctx->stream, a);
+    int rc;
+    if (y_dtype == WR_BF16) rc = glu ? matmul_launch<uint16_t, true>(ctx, a, dma) : matmul_launch<uint16_t, false>(ctx, a, dma);
+    else rc = glu ? matmul_launch<float, true>(ctx, a, dma) : matmul_launch<float, false>(ctx, a, dma);
+    if (rc != WR_OK) return rc;
     WR_CHECK_LAUNCH();
   }
   return WR_OK;
