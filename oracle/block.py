@@ -98,8 +98,8 @@ def quant_rows_i8(v):
 
 def matmul_i8(x, x_scales, w, w_scales, bias=None, swiglu=False):
     """z = x_scales w_scales (x w^T) + bias; with swiglu silu(first half of z) * second half."""
-    sums = np.asarray(x, dtype=np.int64) @ np.asarray(w, dtype=np.int64).T
-    z = sums.astype(np.float64) * _f64(x_scales)[:, None] * _f64(w_scales)[None]
+    sums = _f64(x) @ _f64(w).T  # whole numbers far below 2^53: exact
+    z = sums * _f64(x_scales)[:, None] * _f64(w_scales)[None]
     if bias is not None:
         z = z + _f64(bias)[None]
     if not swiglu:

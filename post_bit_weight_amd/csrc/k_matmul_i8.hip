@@ -273,7 +273,7 @@ __global__ __launch_bounds__(64 * NW) void matmul_i8_stream_kernel(const I8Args 
 // in registers (32x32x32 MFMAs).  Slices of BK bytes of the tile's rows are copied into a ring of NS slots by LDS
 // DMA, NS slices ahead; the operands of the next 32 bytes are read while the present ones are multiplied.  Chunk c
 // of row r lies at chunk c ^ f(r) (see the stream kernel; with 64-byte rows f(r) = r / 2 % 4).
-template <typename TY, bool GLU, int FI, int FJ, int WI, int WJ, int BK, int NS, bool LATE>
+template <typename TY, bool GLU, int FI, int FJ, int WI, int WJ, int BK, int NS, bool LATE, bool DMA>
 __global__ __launch_bounds__(64 * WI * WJ, 1) void matmul_i8_big_kernel(const I8Args a, int tiles_t, int tiles_o) {
   constexpr int NW = WI * WJ, TM = 32 * FI * WI, TN = 32 * FJ * WJ;
   constexpr int CPR = BK / 16, RPI = 64 / CPR;       // chunks per row, rows per copy instruction
@@ -282,6 +282,7 @@ __global__ __launch_bounds__(64 * WI * WJ, 1) void matmul_i8_big_kernel(const I8
   constexpr int KS = BK / 32;                        // MFMA steps per slice
   constexpr int kOuts = GLU ? TN / 2 : TN;
   static_assert((TM + TN) % (RPI * NW) == 0 && KS % 2 == 0 && (!GLU || FJ % 2 == 0), "tile shape");
+  static_assert(DMA || NS == 2, "the copies through registers alternate between two slots");
   extern __shared__ __attribute__((aligned(1024))) char i8_lds[];
   lds_char* const lds = (lds_char*)i8_lds;
   const uint32_t lds_at = (uint32_t)(uintptr_t)lds;
@@ -306,32 +307,39 @@ __global__ __launch_bounds__(64 * WI * WJ, 1) void matmul_i8_big_kernel(const I8
   // lane l the place l % CPR of its row l / CPR.  With GLU the weight rows are 32 gate rows, the same outputs' 32 up
   // rows, and so on.
   const int crow = lane / CPR;
+  using Off = typename std::conditional<DMA, uint32_t, uint64_t>::type;
   const int8_t* base[kCopies];  // the same for all lanes
-  uint32_t off[kCopies], col[kCopies];
+  Off off[kCopies];
+  int col[kCopies];
 #pragma unroll
   for (int i = 0; i < kCopies; ++i) {
-    const int r = (i * NW + wave) * RPI + crow;
+    const int r0 = (i * NW + wave) * RPI, r = r0 + crow;
+    const int64_t up = GLU ? (int64_t)((r0 >> 5 & 1) * outs) * a.ldw : 0;
+    base[i] = r0 >= TN ? a.x + t0 * a.ldx : a.w + o0 * a.ldw + up;
     col[i] = 16 * ((lane % CPR) ^ swizzle<BK>(r));
-    off[i] = r >= TN ? (uint32_t)std::min(r - TN, a.batch - 1 - t0) * (uint32_t)a.ldx
-                     : (uint32_t)std::min(GLU ? (r >> 6) * 32 + (r & 31) : r, outs - 1 - o0) * (uint32_t)a.ldw;
+    off[i] = r >= TN ? (Off)std::min(r - TN, a.batch - 1 - t0) * (Off)a.ldx
+                     : (Off)std::min(GLU ? (r >> 6) * 32 + (r & 31) : r, outs - 1 - o0) * (Off)a.ldw;
   }
-#pragma unroll
-  for (int i = 0; i < kCopies; ++i) {
-    const int r = (i * NW + wave) * RPI;
-    const int64_t up = GLU ? (int64_t)((r >> 5 & 1) * outs) * a.ldw : 0;
-    base[i] = r >= TN ? a.x + t0 * a.ldx : a.w + o0 * a.ldw + up;
-  }
+  const int slices = (a.n + BK - 1) / BK, whole = a.n / BK;  // a last slice beyond the whole ones passes n
+  auto fetch = [&](int s, int i) {
+    if (s < whole) return (u32x4)*reinterpret_cast<const u32x4_any*>(base[i] + off[i] + (BK * s + col[i]));
+    return load16(base[i] + off[i], BK * s + col[i], a.n);
+  };
+  auto put_lds = [&](int slot, int i, const u32x4& v) {
+    *(__attribute__((address_space(3))) u32x4*)(lds + slot * kSlot + (i * NW + wave) * 1024 + 16 * lane) = v;
+  };
   auto issue = [&](int s, int slot) {
-    if (BK * (s + 1) <= a.n) {
+    if (s < whole) {
       const uint32_t at = __builtin_amdgcn_readfirstlane(lds_at + slot * kSlot + wave * 1024);
+      if constexpr (DMA)
 #pragma unroll
-      for (int i = 0; i < kCopies; ++i) lds_dma16(base[i] + BK * s, off[i] + col[i], at + i * NW * 1024);
-    } else {  // past n: through registers, with zeros
+        for (int i = 0; i < kCopies; ++i) lds_dma16(base[i] + BK * s, off[i] + col[i], at + i * NW * 1024);
+    } else {  // through registers, with zeros past n
 #pragma unroll
-      for (int i = 0; i < kCopies; ++i)
-        *(__attribute__((address_space(3))) u32x4*)(lds + slot * kSlot + (i * NW + wave) * 1024 + 16 * lane) = load16(base[i] + off[i], BK * s + col[i], a.n);
+      for (int i = 0; i < kCopies; ++i) put_lds(slot, i, fetch(s, i));
     }
   };
+  u32x4 held[DMA ? 1 : kCopies];  // without DMA: the next slice on its way through registers
 
   uint32_t rd[KS];  // this lane's place in a block of 32 rows for each MFMA step of a slice
 #pragma unroll
@@ -356,14 +364,23 @@ __global__ __launch_bounds__(64 * WI * WJ, 1) void matmul_i8_big_kernel(const I8
       for (int j = 0; j < FJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[set][j], fx[set][i], acc[i][j], 0, 0, 0);
   };
 
-  const int slices = (a.n + BK - 1) / BK, dma = a.n / BK;  // the last slice is not copied by DMA if it passes n
+  if constexpr (DMA) {
 #pragma unroll
-  for (int p = 0; p < NS; ++p)
-    if (p < slices) issue(p, p);
-  if (dma >= NS) vm_wait<kCopies*(NS - 1)>();
-  else vm_wait<0>();
+    for (int p = 0; p < NS; ++p)
+      if (p < slices) issue(p, p);
+    if (whole >= NS) vm_wait<kCopies*(NS - 1)>();
+    else vm_wait<0>();
+  } else {
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) held[i] = fetch(0, i);
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) put_lds(0, i, held[i]);
+    if (slices > 1)
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) held[i] = fetch(1, i);
+  }
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  if (slices > 0) read(0, 0, 0);
+  read(0, 0, 0);
   int slot = 0;
   for (int s = 0; s < slices; ++s) {
     const int next = slot == NS - 1 ? 0 : slot + 1;
@@ -374,17 +391,25 @@ __global__ __launch_bounds__(64 * WI * WJ, 1) void matmul_i8_big_kernel(const I8
         multiply(u & 1);
       } else {
         if (s + 1 < slices) {
-          // slice s + 1 has landed once only the copies of slices s + 2 .. s + NS - 1 are outstanding
-          if (s + NS <= dma) vm_wait<kCopies*(NS - 2)>();
-          else vm_wait<0>();
+          if constexpr (DMA) {
+            // slice s + 1 has landed once only the copies of slices s + 2 .. s + NS - 1 are outstanding
+            if (s + NS <= whole) vm_wait<kCopies*(NS - 2)>();
+            else vm_wait<0>();
+          } else {  // the other slot was last read before the previous barrier
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) put_lds(next, i, held[i]);
+          }
           asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
           // every wave has read all of slice s: its slot is free.  With one workgroup on a CU the copies wait
           // until the matrix cores have work; with two, the other one's products cover them.
-          if (!LATE && s + NS < slices) issue(s + NS, slot);
+          if (DMA && !LATE && s + NS < slices) issue(s + NS, slot);
           read(next, 0, 0);
         }
         multiply(u & 1);
-        if (LATE && s + NS < slices) issue(s + NS, slot);
+        if (DMA && LATE && s + NS < slices) issue(s + NS, slot);
+        if (!DMA && s + 2 < slices)
+#pragma unroll
+          for (int i = 0; i < kCopies; ++i) held[i] = fetch(s + 2, i);
       }
     }
     slot = next;
@@ -470,14 +495,14 @@ static int stream_launch(wr_ctx* ctx, const I8Args& a, bool dma) {
   return dma ? go(std::integral_constant<int, NS>{}, std::true_type{}) : go(std::integral_constant<int, 2>{}, std::false_type{});
 }
 
-template <typename TY, bool GLU, int FI, int FJ, int WI, int WJ, int BK, int NS, bool LATE>
+template <typename TY, bool GLU, int FI, int FJ, int WI, int WJ, int BK, int NS, bool LATE, bool DMA>
 static int big_launch(wr_ctx* ctx, const I8Args& a) {
   constexpr int TM = 32 * FI * WI, TN = 32 * FJ * WJ, kOuts = GLU ? TN / 2 : TN;
   constexpr int lds = NS * (TM + TN) * BK;
   static_assert(lds <= 160 * 1024, "LDS");
   const int outs = GLU ? a.rows / 2 : a.rows;
   const int tt = (a.batch + TM - 1) / TM, to = (outs + kOuts - 1) / kOuts;
-  auto* kernel = matmul_i8_big_kernel<TY, GLU, FI, FJ, WI, WJ, BK, NS, LATE>;
+  auto* kernel = matmul_i8_big_kernel<TY, GLU, FI, FJ, WI, WJ, BK, NS, LATE, DMA>;
   if (!lds_limit((const void*)kernel, lds)) return WR_EHIP;
   hipLaunchKernelGGL(kernel, dim3((unsigned)((tt * to + 7) / 8 * 8)), dim3(64 * WI * WJ), lds, ctx->stream, a, tt, to);
   return WR_OK;
@@ -505,13 +530,17 @@ static int matmul_launch(wr_ctx* ctx, const I8Args& a, bool dma) {
   if (a.batch <= 16) return stream_launch<TY, GLU, R, 1, 8, 2>(ctx, a, dma);
   if (tiles(32, 64) <= cu) return stream_launch<TY, GLU, 2, 4, 4, 2>(ctx, a, dma);
   // Two rounds of 64 x 64 beat shared tiles where the sum is long (512 tokens, 9728 -> 2560: 32.5 us against 38.5).
-  if (!dma || tiles(64, 64) <= (!GLU && a.n >= 4096 ? 2 : 1) * cu) return stream_launch<TY, GLU, 4, 4, 4, 2>(ctx, a, dma);
-  if (tiles(128, 64) <= 2 * cu) return big_launch<TY, GLU, 1, 2, 2, 2, 128, 3, false>(ctx, a);
+  if (tiles(64, 64) <= (!GLU && a.n >= 4096 ? 2 : 1) * cu) return stream_launch<TY, GLU, 4, 4, 4, 2>(ctx, a, dma);
+  if (tiles(128, 64) <= 2 * cu)
+    return dma ? big_launch<TY, GLU, 1, 2, 2, 2, 128, 3, false, true>(ctx, a)
+               : big_launch<TY, GLU, 1, 2, 2, 2, 128, 2, false, false>(ctx, a);
   // A round of 256 x 256 tiles takes 1.6 times one of 128 x 128, of which a CU holds two, for twice the work: 8192
-  // tokens 2560 -> 2 x 9728: 437 us against 483; 1024 tokens: 74 against 61.
+  // tokens 2560 -> 2 x 9728: 437 us against 483; 1024 tokens: 74 against 61.  (Without DMA its operands do not fit the
+  // registers.)
   const int64_t g = (tiles(128, 128) + 2 * cu - 1) / (2 * cu), h = (tiles(256, 256) + cu - 1) / cu;
-  if (8 * h <= 5 * g) return big_launch<TY, GLU, 4, 2, 2, 4, 128, 2, true>(ctx, a);
-  return big_launch<TY, GLU, 2, 2, 2, 2, 128, 2, false>(ctx, a);
+  if (!dma) return big_launch<TY, GLU, 2, 2, 2, 2, 128, 2, false, false>(ctx, a);
+  if (8 * h <= 5 * g) return big_launch<TY, GLU, 4, 2, 2, 4, 128, 2, true, true>(ctx, a);
+  return big_launch<TY, GLU, 2, 2, 2, 2, 128, 2, false, true>(ctx, a);
 }
 
 int wr_matmul_i8_impl(wr_ctx* ctx, const int8_t* x, int64_t ldx, const float* x_scales, int64_t batch, const int8_t* w,

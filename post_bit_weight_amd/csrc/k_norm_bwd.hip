@@ -36,6 +36,7 @@ static BwdPlan bwd_plan(int64_t rows, int64_t n, int64_t gate_rows, bool fp32) {
   const int64_t most = p.wide || p.chunks > 1 ? 256 : 512;
   const int64_t per = p.lanes ? 256 / p.lanes : 1;  // units per workgroup
   p.span = std::max<int64_t>(1, (rows + most * per - 1) / (most * per));
+  if (rows <= 4) p.span = rows;  // one workgroup, whose sums are the result: no second launch
   p.gate_rows = gate_rows == 0 || gate_rows >= rows ? rows : gate_rows;
   p.gates = (rows + p.gate_rows - 1) / p.gate_rows;
   if (p.gate_rows <= p.span) {
@@ -495,8 +496,13 @@ int wr_block_norm_backward_impl(wr_ctx* ctx, int64_t rows, int64_t n, const void
   a.lddr = lddr;
   a.part_post = dw_post ? (float*)ws : nullptr;
   a.part_pre = dw_pre ? (float*)(ws + part) : nullptr;
+  if (p.blocks == 1) {
+    a.part_post = dw_post;
+    a.part_pre = dw_pre;
+  }
   a.part_gate = dgate && p.segs ? (float*)(ws + 2 * part) : nullptr;
   a.dgate = p.segs ? nullptr : dgate;
+  if (p.blocks == 1 && a.one_gate && a.part_gate) a.part_gate = dgate;
   const int key = (b_dtype == WR_BF16 ? 4 : 0) + (r_dtype == WR_BF16 ? 2 : 0) + (w_dtype == WR_BF16 ? 1 : 0);
   switch (key) {
     case 0: bwd_launch<float, float, float>(ctx, p, a); break;
@@ -513,10 +519,11 @@ int wr_block_norm_backward_impl(wr_ctx* ctx, int64_t rows, int64_t n, const void
   // partials among threads, with narrower workgroups where there are few columns.
   const ColumnSums::One none{nullptr, nullptr, 0, 0};
   const int64_t shares = p.gates == 1 ? p.blocks : p.segs;
-  const ColumnSums::One gates{a.part_gate, dgate, shares, a.part_gate ? p.gates : 0};
+  const ColumnSums::One gates{a.part_gate, dgate, shares, a.part_gate && a.part_gate != dgate ? p.gates : 0};
+  const bool sum = p.blocks > 1;
   const bool apart = shares <= 32;
   if (apart) add_up({{gates, none, none}, (int)n}, Int<256>{}, Int<1>{});
-  const ColumnSums sums{{{a.part_post, dw_post, p.blocks, dw_post ? 1 : 0}, {a.part_pre, dw_pre, p.blocks, dw_pre ? 1 : 0},
+  const ColumnSums sums{{{a.part_post, dw_post, p.blocks, sum && dw_post ? 1 : 0}, {a.part_pre, dw_pre, p.blocks, sum && dw_pre ? 1 : 0},
                          apart ? none : gates}, (int)n};
   if (n >= 1024) add_up(sums, Int<32>{}, Int<32>{});
   else add_up(sums, Int<8>{}, Int<128>{});

@@ -430,6 +430,10 @@ MM_CASES = [  # batch, rows, n, pad x, pad w, shift
     (127, 126, 255, 1, 1, 1), (128, 256, 256, 0, 0, 0), (129, 1026, 1040, 0, 0, 0), (257, 514, 96, 0, 0, 0),
     (300, 2562, 2560, 0, 16, 0), (513, 1024, 512, 0, 0, 0), (777, 1022, 2531, 7, 7, 0), (1000, 600, 1600, 0, 0, 0),
     (4, 6, 131071, 1, 0, 0),
+    # each tile and way of copying of the larger products, with a last slice that passes n
+    (1100, 1100, 300, 4, 4, 0), (1100, 1100, 300, 3, 0, 1), (2100, 2200, 144, 0, 0, 0), (2100, 2200, 200, 0, 1, 0),
+    (3000, 3000, 400, 0, 0, 16), (3001, 3002, 130, 14, 14, 0), (5000, 70, 260, 0, 12, 0), (40, 9000, 140, 4, 4, 0),
+    (70, 5000, 520, 8, 8, 0), (200, 2100, 4200, 8, 8, 0),
 ]
 
 
