@@ -415,109 +415,112 @@ def wr_quant_stats(ctx, codes, scales, bits, group, out, T=None, codes_ref=None,
         int(group), _ptr(codes_ref), _ptr(scales_raw), _ptr(out)))
 
 
-def _matrix(t, name, dtypes, shape):
-    """Row stride of a row-major GPU matrix of one of the types and the shape; one test for the usual case, since
-    for a single token these checks are a good part of a call."""
-    if t.dtype not in dtypes or t.shape != shape or not t.is_cuda:
-        _dev(t, name, dtypes)
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    strides = t.stride()
-    if strides[1] != 1 and shape[1] > 1:
-        raise ValueError(f"{name} must be row-major")
-    return strides[0]
+# The calls below serve single tokens as well, where the checks of their arguments are a good part of a call: each
+# tensor is asked for each property once, and the errors are worded only when there is one.
+
+def _refuse(t, name, dtypes, shape):
+    _dev(t, name, dtypes)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} must be row-major")
 
 
-def _vector(t, name, dtypes, count):
-    """Address of a contiguous GPU vector of `count` values, None for none."""
-    if t is None:
-        return None
-    if t.dtype not in dtypes or t.numel() != count or not t.is_cuda or not t.is_contiguous():
-        _dev(t, name, dtypes)
-        raise ValueError(f"{name} must hold {count} contiguous values")
-    return t.data_ptr()
+def _matrix(t, name, dtype, shape):
+    """(address, row stride) of a row-major GPU matrix of the type and shape."""
+    if t.dtype is dtype and t.is_cuda and t.shape == shape:
+        ld, one = t.stride()
+        if one == 1 or shape[1] <= 1:
+            return t.data_ptr(), ld
+    _refuse(t, name, (dtype,), shape)
 
 
-_F32 = (torch.float32,)
-_I8 = (torch.int8,)
+def _vector(t, name, dtype, count):
+    """Address of a contiguous GPU vector of `count` values."""
+    if t.dtype is dtype and t.is_cuda and t.numel() == count and t.is_contiguous():
+        return t.data_ptr()
+    _dev(t, name, (dtype,))
+    raise ValueError(f"{name} must hold {count} contiguous values")
+
+
 _WR_DTYPE = {torch.float32: WR_F32, torch.bfloat16: WR_BF16}
+
+
+def _type_code(t, name):
+    code = _WR_DTYPE.get(t.dtype)
+    if code is None:
+        _dev(t, name, FLOATS)
+    return code
 
 
 def wr_quant_rows_i8(ctx, x, q, scales):
     """8-bit codes q (rows x n int8) and scales (rows fp32) of each row of x (bf16 or fp32)."""
-    if x.dim() != 2:
-        raise ValueError("x must be rows x n")
     shape = x.shape
+    if len(shape) != 2:
+        raise ValueError("x must be rows x n")
     rows, n = shape
-    ldx = _matrix(x, "x", FLOATS, shape)
-    ldq = _matrix(q, "q", _I8, shape)
-    s = _vector(scales, "scales", _F32, rows)
-    _check("wr_quant_rows_i8", load().wr_quant_rows_i8(ctx.handle, x.data_ptr(), _WR_DTYPE[x.dtype], rows, n, ldx,
-                                                       q.data_ptr(), ldq, s))
+    code = _type_code(x, "x")
+    px, ldx = _matrix(x, "x", x.dtype, shape)
+    pq, ldq = _matrix(q, "q", torch.int8, shape)
+    status = load().wr_quant_rows_i8(ctx.handle, px, code, rows, n, ldx, pq, ldq,
+                                     _vector(scales, "scales", torch.float32, rows))
+    if status:
+        _check("wr_quant_rows_i8", status)
 
 
 def wr_matmul_i8(ctx, x, x_scales, w, w_scales, y, bias=None, swiglu=False):
     """y (batch x rows, bf16 or fp32) = x (batch x n int8) times w (rows x n int8) transposed, scaled per token
     and per row, plus bias; with swiglu y is batch x rows / 2: silu(first half of the rows) * second half."""
-    if x.dim() != 2 or w.dim() != 2:
+    xshape, wshape = x.shape, w.shape
+    if len(xshape) != 2 or len(wshape) != 2 or xshape[1] != wshape[1]:
         raise ValueError("x must be batch x n and w rows x n")
-    batch, n = x.shape
-    rows = w.shape[0]
+    batch, n = xshape
+    rows = wshape[0]
     if swiglu and rows % 2:
         raise ValueError("swiglu needs an even number of rows")
-    ldx = _matrix(x, "x", _I8, (batch, n))
-    ldw = _matrix(w, "w", _I8, (rows, n))
-    ldy = _matrix(y, "y", FLOATS, (batch, rows // 2 if swiglu else rows))
-    xs = _vector(x_scales, "x_scales", _F32, batch)
-    ws = _vector(w_scales, "w_scales", _F32, rows)
-    b = _vector(bias, "bias", _F32, rows)
-    _check("wr_matmul_i8", load().wr_matmul_i8(
-        ctx.handle, x.data_ptr(), ldx, xs, batch, w.data_ptr(), ldw, ws, rows, n, b, WR_I8_SWIGLU if swiglu else 0,
-        y.data_ptr(), _WR_DTYPE[y.dtype], ldy))
+    px, ldx = _matrix(x, "x", torch.int8, xshape)
+    pw, ldw = _matrix(w, "w", torch.int8, wshape)
+    code = _type_code(y, "y")
+    py, ldy = _matrix(y, "y", y.dtype, (batch, rows // 2 if swiglu else rows))
+    status = load().wr_matmul_i8(
+        ctx.handle, px, ldx, _vector(x_scales, "x_scales", torch.float32, batch), batch, pw, ldw,
+        _vector(w_scales, "w_scales", torch.float32, rows), rows, n,
+        None if bias is None else _vector(bias, "bias", torch.float32, rows), WR_I8_SWIGLU if swiglu else 0, py, code, ldy)
+    if status:
+        _check("wr_matmul_i8", status)
 
 
-def _norm_inputs(branch, resid, w_post, gate, gate_rows, branch_scale, resid_scale, w_pre, acts, res):
-    """The leading arguments of a block norm's C calls, rows to w_dtype, checked; the first of `acts` and of `res`
-    that is given has the type of the activations and of the residual stream."""
-    like = branch if branch is not None else resid
-    if like is None or like.dim() != 2:
-        raise ValueError("branch or resid must be given, as rows x n")
-    bt = rt = None
-    for t in acts:
-        if t is not None:
-            bt = t.dtype
-            break
-    for t in res:
-        if t is not None:
-            rt = t.dtype
-            break
-    bt, rt = bt or rt, rt or bt
-    if bt not in _WR_DTYPE or rt not in _WR_DTYPE:
-        raise ValueError(f"activations of {bt} and a residual stream of {rt}: expected types among {FLOATS}")
-    shape = like.shape
-    rows, n = shape
-    pb = pr = pg = None
-    ldb = ldr = ldg = n
+def _norm_inputs(branch, resid, w_post, gate, gate_rows, branch_scale, resid_scale, w_pre, act, res):
+    """(type of the activations, of the residual stream, shape, leading arguments of a block norm's C calls), checked.
+    act and res: the outputs or gradients that give the types where branch or resid does not."""
     if branch is not None:
-        ldb, pb = _matrix(branch, "branch", (bt,), shape), branch.data_ptr()
+        shape, bt = branch.shape, branch.dtype
+    elif resid is not None:
+        shape, bt = resid.shape, (act if act is not None else gate if gate is not None else resid).dtype
+    else:
+        raise ValueError("branch or resid must be given, as rows x n")
+    if len(shape) != 2:
+        raise ValueError("branch and resid must be rows x n")
+    rt = resid.dtype if resid is not None else res.dtype if res is not None else bt
+    bc, rc = _WR_DTYPE.get(bt), _WR_DTYPE.get(rt)
+    if bc is None or rc is None:
+        raise ValueError(f"activations of {bt} and a residual stream of {rt}: expected types among {FLOATS}")
+    rows, n = shape
+    pb = pr = pg = post = pre = None
+    ldb = ldr = ldg = n
+    wc = WR_F32
+    if branch is not None:
+        pb, ldb = _matrix(branch, "branch", bt, shape)
     if resid is not None:
-        ldr, pr = _matrix(resid, "resid", (rt,), shape), resid.data_ptr()
+        pr, ldr = _matrix(resid, "resid", rt, shape)
     if gate is not None:
-        ldg, pg = _matrix(gate, "gate", (bt,), (-(-rows // gate_rows) if gate_rows else 1, n)), gate.data_ptr()
-    weight = w_pre if w_pre is not None else w_post
-    wt = FLOATS if weight is None else (weight.dtype,)
-    if weight is not None and weight.dtype not in _WR_DTYPE:
-        raise ValueError(f"weights of {weight.dtype}: expected one of {FLOATS}")
-    post, pre = _vector(w_post, "w_post", wt, n), _vector(w_pre, "w_pre", wt, n)
-    return bt, rt, shape, (rows, n, pb, _WR_DTYPE[bt], ldb, post, pg, ldg, gate_rows, branch_scale, pr, _WR_DTYPE[rt],
-                           ldr, resid_scale, pre, _WR_DTYPE[wt[0]])
-
-
-def _rows_of(t, name, dtype, shape):
-    """(address, row stride) of an optional matrix."""
-    if t is None:
-        return None, shape[1]
-    ld = _matrix(t, name, (dtype,), shape)
-    return t.data_ptr(), ld
+        pg, ldg = _matrix(gate, "gate", bt, (-(-rows // gate_rows) if gate_rows else 1, n))
+    if w_pre is not None:
+        wc = _type_code(w_pre, "w_pre")
+        pre = _vector(w_pre, "w_pre", w_pre.dtype, n)
+    if w_post is not None:
+        wc = _type_code(w_post, "w_post")
+        post = _vector(w_post, "w_post", w_post.dtype if w_pre is None else w_pre.dtype, n)
+    return bt, rt, shape, (rows, n, pb, bc, ldb, post, pg, ldg, gate_rows, branch_scale, pr, rc, ldr, resid_scale, pre, wc)
 
 
 def wr_block_norm(ctx, eps, branch=None, resid=None, w_post=None, gate=None, gate_rows=0, branch_scale=1.0,
@@ -525,15 +528,23 @@ def wr_block_norm(ctx, eps, branch=None, resid=None, w_post=None, gate=None, gat
     """resid_out = x' = resid_scale resid + branch_scale gate w_post branch / rms(branch); y = w_pre x' / rms(x'),
     and / or its 8-bit form (q, q_scales); stats (rows x 2 fp32) for wr_block_norm_backward.  Outputs left out are
     not written.  gate: one row for every gate_rows consecutive rows (0: one row for all)."""
-    bt, rt, shape, lead = _norm_inputs(branch, resid, w_post, gate, gate_rows, branch_scale, resid_scale, w_pre,
-                                       (branch, y, gate), (resid, resid_out))
-    rows = shape[0]
-    po, ldo = _rows_of(resid_out, "resid_out", rt, shape)
-    py, ldy = _rows_of(y, "y", bt, shape)
-    pq, ldq = _rows_of(q, "q", torch.int8, shape)
-    ps = _vector(q_scales, "q_scales", _F32, rows)
-    pt = _vector(stats, "stats", _F32, 2 * rows)
-    _check("wr_block_norm", load().wr_block_norm(ctx.handle, *lead, eps, po, ldo, py, ldy, pq, ldq, ps, pt))
+    bt, rt, shape, lead = _norm_inputs(branch, resid, w_post, gate, gate_rows, branch_scale, resid_scale, w_pre, y, resid_out)
+    rows, n = shape
+    po = py = pq = ps = pt = None
+    ldo = ldy = ldq = n
+    if resid_out is not None:
+        po, ldo = _matrix(resid_out, "resid_out", rt, shape)
+    if y is not None:
+        py, ldy = _matrix(y, "y", bt, shape)
+    if q is not None:
+        pq, ldq = _matrix(q, "q", torch.int8, shape)
+    if q_scales is not None:
+        ps = _vector(q_scales, "q_scales", torch.float32, rows)
+    if stats is not None:
+        pt = _vector(stats, "stats", torch.float32, 2 * rows)
+    status = load().wr_block_norm(ctx.handle, *lead, eps, po, ldo, py, ldy, pq, ldq, ps, pt)
+    if status:
+        _check("wr_block_norm", status)
 
 
 def wr_block_norm_backward(ctx, stats, branch=None, resid=None, w_post=None, gate=None, gate_rows=0, branch_scale=1.0,
@@ -541,17 +552,31 @@ def wr_block_norm_backward(ctx, stats, branch=None, resid=None, w_post=None, gat
                            dw_post=None, dgate=None, dw_pre=None):
     """Gradients of wr_block_norm's inputs from dy (of y) and dresid_out (of x'), either of which may be None.
     Outputs left out are not formed; dw_post, dgate (as gate's shape) and dw_pre are fp32."""
-    bt, rt, shape, lead = _norm_inputs(branch, resid, w_post, gate, gate_rows, branch_scale, resid_scale, w_pre,
-                                       (branch, dy, gate), (resid, dresid_out))
+    bt, rt, shape, lead = _norm_inputs(branch, resid, w_post, gate, gate_rows, branch_scale, resid_scale, w_pre, dy,
+                                       dresid_out)
     rows, n = shape
-    py, lddy = _rows_of(dy, "dy", bt, shape)
-    po, lddo = _rows_of(dresid_out, "dresid_out", rt, shape)
-    pb, lddb = _rows_of(dbranch, "dbranch", bt, shape)
-    px, lddr = _rows_of(dresid, "dresid", rt, shape)
-    pt = _vector(stats, "stats", _F32, 2 * rows)
-    pp = _vector(dw_post, "dw_post", _F32, n)
-    pg = _vector(dgate, "dgate", _F32, gate.numel() if gate is not None else 0)
-    pw = _vector(dw_pre, "dw_pre", _F32, n)
-    ctx.ensure_workspace(wr_workspace_bytes(WR_OP_NORM_BWD, rows, n, min(gate_rows, rows)))
-    _check("wr_block_norm_backward", load().wr_block_norm_backward(
-        ctx.handle, *lead, pt, py, lddy, po, lddo, pb, lddb, px, lddr, pp, pg, pw))
+    py = po = pb = px = pt = pp = pg = pw = None
+    lddy = lddo = lddb = lddr = n
+    if dy is not None:
+        py, lddy = _matrix(dy, "dy", bt, shape)
+    if dresid_out is not None:
+        po, lddo = _matrix(dresid_out, "dresid_out", rt, shape)
+    if dbranch is not None:
+        pb, lddb = _matrix(dbranch, "dbranch", bt, shape)
+    if dresid is not None:
+        px, lddr = _matrix(dresid, "dresid", rt, shape)
+    if stats is not None:
+        pt = _vector(stats, "stats", torch.float32, 2 * rows)
+    if dw_post is not None:
+        pp = _vector(dw_post, "dw_post", torch.float32, n)
+    if dgate is not None:
+        pg = _vector(dgate, "dgate", torch.float32, gate.numel() if gate is not None else 0)
+    if dw_pre is not None:
+        pw = _vector(dw_pre, "dw_pre", torch.float32, n)
+    args = (ctx.handle, *lead, pt, py, lddy, po, lddo, pb, lddb, px, lddr, pp, pg, pw)
+    status = load().wr_block_norm_backward(*args)
+    if status == WR_EWORKSPACE:  # refused before any launch: register what it needs and call again
+        ctx.ensure_workspace(wr_workspace_bytes(WR_OP_NORM_BWD, rows, n, min(gate_rows, rows)))
+        status = load().wr_block_norm_backward(*args)
+    if status:
+        _check("wr_block_norm_backward", status)

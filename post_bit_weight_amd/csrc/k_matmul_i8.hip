@@ -167,7 +167,7 @@ template <typename TY, bool GLU, int RF, int NT, int NW, int NS, bool DMA>
 __global__ __launch_bounds__(64 * NW) void matmul_i8_stream_kernel(const I8Args a) {
   constexpr int F = RF + NT, OF = GLU ? RF / 2 : RF;  // blocks of 16 rows; of 16 outputs
   constexpr int kSlot = F * 16 * 128;
-  static_assert(DMA || NS == 2, "the copies through registers alternate between two slots");
+  static_assert(DMA || NS == 1, "copies through registers need one slot: LDS takes a wave's accesses in order");
   extern __shared__ __attribute__((aligned(1024))) char i8_lds[];
   lds_char* const lds = (lds_char*)i8_lds;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -478,21 +478,26 @@ __global__ __launch_bounds__(64 * WI * WJ, 1) void matmul_i8_big_kernel(const I8
 
 using namespace wr;
 
+template <int N>
+using Int = std::integral_constant<int, N>;
+
+// NW waves with rings of NS slots by DMA; through registers always eight with a slot each, since a wave has less in
+// flight there (777 tokens, 2531 -> 1023 on 64 x 64 tiles: 15.6 us; 15.9 with four waves and two slots; 11.4 by DMA).
 template <typename TY, bool GLU, int RF, int NT, int NW, int NS>
 static int stream_launch(wr_ctx* ctx, const I8Args& a, bool dma) {
   constexpr int OF = GLU ? RF / 2 : RF;
   const int outs = GLU ? a.rows / 2 : a.rows;
   const dim3 grid((outs + 16 * OF - 1) / (16 * OF), (a.batch + 16 * NT - 1) / (16 * NT));
-  auto go = [&](auto slots, auto direct) {
-    constexpr int kSlots = decltype(slots)::value;
-    constexpr int lds = NW * std::max(kSlots * (RF + NT) * 2048, RF * NT * 1024);
+  auto go = [&](auto waves, auto slots, auto direct) {
+    constexpr int kWaves = decltype(waves)::value, kSlots = decltype(slots)::value;
+    constexpr int lds = kWaves * std::max(kSlots * (RF + NT) * 2048, RF * NT * 1024);
     static_assert(lds <= 160 * 1024, "LDS");
-    auto* kernel = matmul_i8_stream_kernel<TY, GLU, RF, NT, NW, kSlots, decltype(direct)::value>;
+    auto* kernel = matmul_i8_stream_kernel<TY, GLU, RF, NT, kWaves, kSlots, decltype(direct)::value>;
     if (!lds_limit((const void*)kernel, lds)) return WR_EHIP;
-    hipLaunchKernelGGL(kernel, grid, dim3(64 * NW), lds, ctx->stream, a);
+    hipLaunchKernelGGL(kernel, grid, dim3(64 * kWaves), lds, ctx->stream, a);
     return WR_OK;
   };
-  return dma ? go(std::integral_constant<int, NS>{}, std::true_type{}) : go(std::integral_constant<int, 2>{}, std::false_type{});
+  return dma ? go(Int<NW>{}, Int<NS>{}, std::true_type{}) : go(Int<8>{}, Int<1>{}, std::false_type{});
 }
 
 template <typename TY, bool GLU, int FI, int FJ, int WI, int WJ, int BK, int NS, bool LATE, bool DMA>

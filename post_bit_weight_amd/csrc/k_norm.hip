@@ -76,50 +76,56 @@ __global__ __launch_bounds__(MAXT) void block_norm_kernel(const NormArgs a) {
     b[k].fill(0.0f);
     g[k].fill(1.0f);
     x[k].fill(0.0f);
-    if (a.w_post) map.load(wp[k], (const TW*)a.w_post, k, n);
-    if (a.w_pre) map.load(wq[k], (const TW*)a.w_pre, k, n);
+    if (a.w_post) map.load(wp[k], (const TW*)a.w_post, k);
+    if (a.w_pre) map.load(wq[k], (const TW*)a.w_pre, k);
   }
   auto load_row = [&](int64_t row) {
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      if (a.branch) map.load(b[k], (const TB*)a.branch + row * a.ldb, k, n);
-      if (a.resid) map.load(x[k], (const TR*)a.resid + row * a.ldr, k, n);
-      if (a.gate) map.load(g[k], (const TB*)a.gate + (a.gate_rows ? (uint32_t)row / (uint32_t)a.gate_rows : 0u) * a.ldg, k, n);
+      if (a.branch) map.load(b[k], (const TB*)a.branch + row * a.ldb, k);
+      if (a.resid) map.load(x[k], (const TR*)a.resid + row * a.ldr, k);
+      if (a.gate) map.load(g[k], (const TB*)a.gate + (a.gate_rows ? (uint32_t)row / (uint32_t)a.gate_rows : 0u) * a.ldg, k);
     }
   };
   if (walk.first < a.rows) load_row(walk.first);
   for (int64_t row = walk.first; row < a.rows; row += walk.step) {
-#pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      map.own(b[k], k);
-      map.own(x[k], k);
-    }
     float v[CH][8];
     float r1 = 1.0f, r2 = 1.0f;
     if (a.w_post) {
       float ss = 0.0f;
 #pragma unroll
-      for (int k = 0; k < CH; ++k)
+      for (int k = 0; k < CH; ++k) {
+        float t[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(b[k].get(e), b[k].get(e), ss);
+        for (int e = 0; e < 8; ++e) t[e] = b[k].get(e);
+        map.own(t, k);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(t[e], t[e], ss);
+      }
       r1 = 1.0f / sqrtf(grp.sum(ss) * inv_n + a.eps);
     }
     float ss = 0.0f;
 #pragma unroll
-    for (int k = 0; k < CH; ++k)
+    for (int k = 0; k < CH; ++k) {
+      float t[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float u = b[k].get(e) * r1 * wp[k].get(e) * g[k].get(e) * a.bscale;
-        v[k][e] = fmaf(a.rscale, x[k].get(e), u);
-        ss = fmaf(v[k][e], v[k][e], ss);
+        v[k][e] = t[e] = fmaf(a.rscale, x[k].get(e), u);
       }
+      map.own(t, k);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(t[e], t[e], ss);
+    }
     // the next row's loads are in flight during the rest of this one
     if (row + walk.step < a.rows) load_row(row + walk.step);
+    // Stored after a reduction, by which the whole row has been read: resid_out may be resid.
+    if (a.w_pre) r2 = 1.0f / sqrtf(grp.sum(ss) * inv_n + a.eps);
+    else if (LANES == 0 && !a.w_post) __syncthreads();
     if (a.resid_out)
 #pragma unroll
       for (int k = 0; k < CH; ++k) map.store((TR*)a.resid_out + row * a.ldo, k, v[k]);
     if (a.w_pre) {
-      r2 = 1.0f / sqrtf(grp.sum(ss) * inv_n + a.eps);
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
 #pragma unroll
@@ -156,7 +162,7 @@ __global__ __launch_bounds__(MAXT) void quant_rows_kernel(const T* __restrict__ 
   Raw8<T> r[CH];
   auto load_row = [&](int64_t row) {
 #pragma unroll
-    for (int k = 0; k < CH; ++k) map.load(r[k], x + row * ldx, k, n);
+    for (int k = 0; k < CH; ++k) map.load(r[k], x + row * ldx, k);
   };
   if (walk.first < rows) load_row(walk.first);
   for (int64_t row = walk.first; row < rows; row += walk.step) {
@@ -164,7 +170,6 @@ __global__ __launch_bounds__(MAXT) void quant_rows_kernel(const T* __restrict__ 
     uint32_t top = 0u;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      map.own(r[k], k);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         v[k][e] = r[k].get(e);

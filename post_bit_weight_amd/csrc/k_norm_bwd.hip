@@ -107,14 +107,15 @@ __device__ __forceinline__ void row_means(const float (&sums)[3], float inv_n, f
 }
 // The tokens of a unit and its first gate row.
 __device__ __forceinline__ void unit_range(const BwdArgs& a, int64_t unit, int64_t& r0, int64_t& r1, int64_t& gidx) {
+  const uint32_t u = (uint32_t)unit;  // units fit 32 bits, and 64-bit divisions take long
   if (a.segs) {
-    gidx = unit / a.segs;
-    r0 = gidx * a.gate_rows + unit % a.segs * a.span;
+    gidx = u / (uint32_t)a.segs;
+    r0 = gidx * a.gate_rows + (int64_t)(u % (uint32_t)a.segs) * a.span;
     r1 = std::min<int64_t>(std::min<int64_t>(r0 + a.span, (gidx + 1) * a.gate_rows), a.rows);
   } else {
     r0 = unit * a.span;
     r1 = std::min<int64_t>(r0 + a.span, a.rows);
-    gidx = r0 / a.gate_rows;
+    gidx = (uint32_t)r0 / (uint32_t)a.gate_rows;  // a unit past the last one walks no rows
   }
 }
 
@@ -152,18 +153,18 @@ __global__ __launch_bounds__(LANES > 0 ? 256 : 512) void block_norm_bwd_kernel(c
     dy[k].fill(0.0f);
     x[k].fill(0.0f);
     dr[k].fill(0.0f);
-    if (a.w_post) map.load(wp[k], (const TW*)a.w_post, k, n);
-    if (a.dy) map.load(wq[k], (const TW*)a.w_pre, k, n);
+    if (a.w_post) map.load(wp[k], (const TW*)a.w_post, k);
+    if (a.dy) map.load(wq[k], (const TW*)a.w_pre, k);
   }
   float ib = 1.0f, ix = 0.0f;
   auto load_row = [&](int64_t row, int64_t gate_row) {
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      if (a.branch) map.load(b[k], (const TB*)a.branch + row * a.ldb, k, n);
-      if (a.resid) map.load(x[k], (const TR*)a.resid + row * a.ldr, k, n);
-      if (a.dy) map.load(dy[k], (const TB*)a.dy + row * a.lddy, k, n);
-      if (a.dres) map.load(dr[k], (const TR*)a.dres + row * a.lddo, k, n);
-      if (a.gate) map.load(g[k], (const TB*)a.gate + gate_row * a.ldg, k, n);
+      if (a.branch) map.load(b[k], (const TB*)a.branch + row * a.ldb, k);
+      if (a.resid) map.load(x[k], (const TR*)a.resid + row * a.ldr, k);
+      if (a.dy) map.load(dy[k], (const TB*)a.dy + row * a.lddy, k);
+      if (a.dres) map.load(dr[k], (const TR*)a.dres + row * a.lddo, k);
+      if (a.gate) map.load(g[k], (const TB*)a.gate + gate_row * a.ldg, k);
     }
     if (a.w_post) ib = a.stats[2 * row];
     if (a.dy) ix = a.stats[2 * row + 1];
@@ -173,8 +174,8 @@ __global__ __launch_bounds__(LANES > 0 ? 256 : 512) void block_norm_bwd_kernel(c
   auto store_row = [&](int64_t row) {
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      if (a.dx) map.store((TR*)a.dx + row * a.lddr, k, odx[k]);
-      if (a.db) map.store((TB*)a.db + row * a.lddb, k, odb[k]);
+      if (a.dx) map.store_own((TR*)a.dx + row * a.lddr, k, odx[k]);
+      if (a.db) map.store_own((TB*)a.db + row * a.lddb, k, odb[k]);
     }
   };
   if (r0 < r1) load_row(r0, gidx);
@@ -226,7 +227,7 @@ __global__ __launch_bounds__(LANES > 0 ? 256 : 512) void block_norm_bwd_kernel(c
     if (a.dgate && (last || gidx != here)) {  // a gate row's last token
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
-        map.store(a.dgate + here * n, k, s_gate[k]);
+        map.store_own(a.dgate + here * n, k, s_gate[k]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) s_gate[k][e] = 0.0f;
       }
@@ -235,7 +236,7 @@ __global__ __launch_bounds__(LANES > 0 ? 256 : 512) void block_norm_bwd_kernel(c
   if (r0 < r1) store_row(r1 - 1);
   if (a.part_gate && !(LANES > 0 && a.one_gate) && unit < a.units)
 #pragma unroll
-    for (int k = 0; k < CH; ++k) map.store(a.part_gate + unit * n, k, s_gate[k]);
+    for (int k = 0; k < CH; ++k) map.store_own(a.part_gate + unit * n, k, s_gate[k]);
   if constexpr (LANES > 0) {
     // the workgroup's units, added in order; a unit past the last one holds zeros
     auto combine = [&](const float (&s)[8], float* part) {
@@ -256,8 +257,8 @@ __global__ __launch_bounds__(LANES > 0 ? 256 : 512) void block_norm_bwd_kernel(c
   } else {
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      if (a.part_pre) map.store(a.part_pre + (int64_t)blockIdx.x * n, k, s_pre[k]);
-      if (a.part_post) map.store(a.part_post + (int64_t)blockIdx.x * n, k, s_post[k]);
+      if (a.part_pre) map.store_own(a.part_pre + (int64_t)blockIdx.x * n, k, s_pre[k]);
+      if (a.part_post) map.store_own(a.part_post + (int64_t)blockIdx.x * n, k, s_post[k]);
     }
   }
 }
@@ -293,21 +294,21 @@ __global__ __launch_bounds__(1024) void block_norm_bwd_wide_kernel(const BwdArgs
   auto accumulate = [&](const RowMap<1, 0>& map, float* sum, bool first, const float (&v)[8]) {
     float out[8];
     Raw8<float> old;
-    if (!first) map.load(old, sum, 0, n);
+    if (!first) map.load(old, sum, 0);
 #pragma unroll
     for (int e = 0; e < 8; ++e) out[e] = first ? v[e] : old.get(e) + v[e];
-    map.store(sum, 0, out);
+    map.store_own(sum, 0, out);
   };
   for (int64_t row = r0; row < r1; ++row) {
     const float ib = a.w_post ? a.stats[2 * row] : 1.0f, ix = a.dy ? a.stats[2 * row + 1] : 0.0f;
     auto load_chunk = [&](const RowMap<1, 0>& map) {
-      if (a.w_post) map.load(wp, (const TW*)a.w_post, 0, n);
-      if (a.dy) map.load(wq, (const TW*)a.w_pre, 0, n);
-      if (a.branch) map.load(b, (const TB*)a.branch + row * a.ldb, 0, n);
-      if (a.resid) map.load(x, (const TR*)a.resid + row * a.ldr, 0, n);
-      if (a.dy) map.load(dy, (const TB*)a.dy + row * a.lddy, 0, n);
-      if (a.dres) map.load(dr, (const TR*)a.dres + row * a.lddo, 0, n);
-      if (a.gate) map.load(g, (const TB*)a.gate + gidx * a.ldg, 0, n);
+      if (a.w_post) map.load(wp, (const TW*)a.w_post, 0);
+      if (a.dy) map.load(wq, (const TW*)a.w_pre, 0);
+      if (a.branch) map.load(b, (const TB*)a.branch + row * a.ldb, 0);
+      if (a.resid) map.load(x, (const TR*)a.resid + row * a.ldr, 0);
+      if (a.dy) map.load(dy, (const TB*)a.dy + row * a.lddy, 0);
+      if (a.dres) map.load(dr, (const TR*)a.dres + row * a.lddo, 0);
+      if (a.gate) map.load(g, (const TB*)a.gate + gidx * a.ldg, 0);
       map.own(b, 0);
       map.own(x, 0);
       map.own(dy, 0);
@@ -342,8 +343,8 @@ __global__ __launch_bounds__(1024) void block_norm_bwd_wide_kernel(const BwdArgs
         v_gate[e] = a.bscale * dxo * (w * m.bn);
         db_f[e] = a.w_post ? ib * fmaf(-m2, m.bn, du * w) : du;
       }
-      if (a.dx) map.store((TR*)a.dx + row * a.lddr, 0, dx_f);
-      if (a.db) map.store((TB*)a.db + row * a.lddb, 0, db_f);
+      if (a.dx) map.store_own((TR*)a.dx + row * a.lddr, 0, dx_f);
+      if (a.db) map.store_own((TB*)a.db + row * a.lddb, 0, db_f);
       if (pre) accumulate(map, pre, row == r0, v_pre);
       if (post) accumulate(map, post, row == r0, v_post);
       if (a.dgate) accumulate(map, a.dgate + gidx * n, gate_first, v_gate);
@@ -357,9 +358,9 @@ __global__ __launch_bounds__(1024) void block_norm_bwd_wide_kernel(const BwdArgs
   if (r0 >= r1)  // no tokens: its partials are zero
     for (int c = 0; c < n; c += 8 * blockDim.x) {
       const RowMap<1, 0> map(threadIdx.x + c / 8, 0, n);
-      if (pre) map.store(pre, 0, zeros);
-      if (post) map.store(post, 0, zeros);
-      if (a.part_gate) map.store(a.part_gate + unit * n, 0, zeros);
+      if (pre) map.store_own(pre, 0, zeros);
+      if (post) map.store_own(post, 0, zeros);
+      if (a.part_gate) map.store_own(a.part_gate + unit * n, 0, zeros);
     }
 }
 

@@ -30,17 +30,17 @@ struct Raw8<uint16_t> {  // bf16 bit patterns
   __device__ __forceinline__ void set(int e, uint16_t h) {
     v[e >> 1] = e & 1 ? (v[e >> 1] & 0xffffu) | (uint32_t)h << 16 : (v[e >> 1] & 0xffff0000u) | h;
   }
-  __device__ __forceinline__ void mask(int keep) {
-#pragma unroll
-    for (int d = 0; d < 4; ++d)
-      v[d] &= (uint32_t)(__builtin_amdgcn_sbfe(keep, 2 * d, 1) & 0xffff) | (uint32_t)__builtin_amdgcn_sbfe(keep, 2 * d + 1, 1) << 16;
-  }
   __device__ __forceinline__ void round(const float (&f)[8]) {  // to nearest even
 #pragma unroll
     for (int d = 0; d < 4; ++d) v[d] = pack_bf16(f[2 * d], f[2 * d + 1]);
   }
   __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<u32x4_any*>(p) = v; }
   __device__ __forceinline__ uint16_t at(int e) const { return (uint16_t)(v[e >> 1] >> (16 * (e & 1))); }
+  __device__ __forceinline__ void mask(int keep) {  // zeros where bit e of keep is clear
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+      v[d] &= (uint32_t)(__builtin_amdgcn_sbfe(keep, 2 * d, 1) & 0xffff) | (uint32_t)__builtin_amdgcn_sbfe(keep, 2 * d + 1, 1) << 16;
+  }
   __device__ __forceinline__ float get(int e) const {
     return __uint_as_float(e & 1 ? v[e >> 1] & 0xffff0000u : v[e >> 1] << 16);
   }
@@ -57,10 +57,6 @@ struct Raw8<float> {
     v[0] = v[1] = u32x4{h, h, h, h};
   }
   __device__ __forceinline__ void set(int e, float f) { v[e >> 2][e & 3] = __float_as_uint(f); }
-  __device__ __forceinline__ void mask(int keep) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e >> 2][e & 3] &= (uint32_t)__builtin_amdgcn_sbfe(keep, e, 1);
-  }
   __device__ __forceinline__ void round(const float (&f)[8]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) set(e, f[e]);
@@ -69,22 +65,28 @@ struct Raw8<float> {
     *reinterpret_cast<u32x4_any*>(p) = v[0];
     *reinterpret_cast<u32x4_any*>(p + 4) = v[1];
   }
+  __device__ __forceinline__ void mask(int keep) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e >> 2][e & 3] &= (uint32_t)__builtin_amdgcn_sbfe(keep, e, 1);
+  }
   __device__ __forceinline__ float at(int e) const { return get(e); }
   __device__ __forceinline__ float get(int e) const { return __uint_as_float(v[e >> 2][e & 3]); }
 };
 
 // ---------------------------------------------------------------- which values a thread owns
 // A row of n values lies on LANES lanes of a wave, or (LANES == 0) on a whole workgroup; a thread owns CH
-// chunks of eight columns.  So that every load is one full vector load inside the row, the chunk that
-// would pass the row's end starts at n - 8 instead, and so do those of lanes that have none; `keep`
-// says which of its eight values are the thread's own.  LANES == 8 is for rows of fewer than eight
-// values: the first lane of eight holds them all, loaded one by one.
+// chunks of eight columns.  So that every access is one full vector inside the row, the chunk that would
+// pass the row's end starts at n - 8 instead: it holds up to seven values of its neighbour as well, which
+// count in sums only where they are owned (`keep`) and are otherwise treated like the thread's own, so that both
+// store the same results there.  Lanes beyond the row load the last chunk, own nothing and store nothing.
+// LANES == 8 is for rows of fewer than eight values: the first lane of eight holds them all, one by one.
 template <int CH, int LANES>
 struct RowMap {
   uint32_t col[CH];
   int keep[CH];
-  bool ragged;  // some lane of this wave does not own all it loads (uniform)
-  __device__ __forceinline__ RowMap(int lane, int cstep, int n) {
+  int n;
+  bool ragged;  // some lane of this wave does not own all it holds (uniform)
+  __device__ __forceinline__ RowMap(int lane, int cstep, int n_) : n(n_) {
     bool part = false;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
@@ -100,13 +102,6 @@ struct RowMap {
     }
     ragged = __builtin_amdgcn_ballot_w64(part) != 0;
   }
-  // keep[k] for the rare paths, unknown to the compiler before them: it would else form every mask and
-  // condition ahead of the row loop and hold them in registers.
-  __device__ __forceinline__ int bits(int k) const {
-    int b = keep[k];
-    asm volatile("" : "+v"(b));
-    return b;
-  }
   // Where chunk k of a row starts: a uniform pointer plus a 32-bit offset of the lane, which needs no 64-bit
   // address registers.
   template <typename T>
@@ -114,14 +109,28 @@ struct RowMap {
     using C = typename std::conditional<std::is_const<T>::value, const char, char>::type;
     return reinterpret_cast<T*>(reinterpret_cast<C*>(row) + (uint32_t)(col[k] * sizeof(T)));
   }
-  // The chunk's values; those that are not the thread's own are zero after own().
   template <typename T>
-  __device__ __forceinline__ void load(Raw8<T>& r, const T* row, int k, int n) const {
+  __device__ __forceinline__ void load(Raw8<T>& r, const T* row, int k) const {
     if constexpr (LANES == 8) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) r.set(e, row[e < n ? e : n - 1]);
     } else {
       r.load(at(row, k));
+    }
+  }
+  // keep[k] for the rare paths, unknown to the compiler before them: it would else form every mask and
+  // condition ahead of the row loop and hold them in registers.
+  __device__ __forceinline__ int bits(int k) const {
+    int b = keep[k];
+    asm volatile("" : "+v"(b));
+    return b;
+  }
+  // Zeros in the place of what chunk k holds but does not own.
+  __device__ __forceinline__ void own(float (&v)[8], int k) const {
+    if (ragged) {
+      const int b = bits(k);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(__float_as_uint(v[e]) & (uint32_t)__builtin_amdgcn_sbfe(b, e, 1));
     }
   }
   template <typename T>
@@ -130,13 +139,13 @@ struct RowMap {
   }
   template <typename T>
   __device__ __forceinline__ void store(T* row, int k, const Raw8<T>& r) const {
-    if (keep[k] == 0xff) {
-      r.store(at(row, k));
-    } else if (keep[k]) {
-      const int own_bits = bits(k);
+    if (keep[k] == 0) return;
+    if constexpr (LANES == 8) {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (own_bits >> e & 1) at(row, k)[e] = r.at(e);
+        if (e < n) row[e] = r.at(e);
+    } else {
+      r.store(at(row, k));
     }
   }
   template <typename T>
@@ -146,14 +155,33 @@ struct RowMap {
     store(row, k, r);
   }
   __device__ __forceinline__ void store(int8_t* row, int k, const u32x2_any& v) const {
-    if (keep[k] == 0xff) {
-      *reinterpret_cast<u32x2_any*>(at(row, k)) = v;
-    } else if (keep[k]) {
-      const int own_bits = bits(k);
+    if (keep[k] == 0) return;
+    if constexpr (LANES == 8) {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (own_bits >> e & 1) at(row, k)[e] = (int8_t)(v[e >> 2] >> (8 * (e & 3)));
+        if (e < n) row[e] = (int8_t)(v[e >> 2] >> (8 * (e & 3)));
+    } else {
+      *reinterpret_cast<u32x2_any*>(at(row, k)) = v;
     }
+  }
+  // Only what the chunk owns: for rows of which each thread has zeros in its neighbours' places (the gradient, whose
+  // registers hold no more), and for values that are read, changed and stored.
+  template <typename T>
+  __device__ __forceinline__ void store_own(T* row, int k, const Raw8<T>& r) const {
+    if (keep[k] == 0xff) {
+      r.store(at(row, k));
+    } else if (keep[k]) {
+      const int b = bits(k);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (b >> e & 1) at(row, k)[e] = r.at(e);
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void store_own(T* row, int k, const float (&f)[8]) const {
+    Raw8<T> r;
+    r.round(f);
+    store_own(row, k, r);
   }
 };
 
