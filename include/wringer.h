@@ -351,9 +351,9 @@ int wr_quant_rows_i8(wr_ctx* ctx, const void* x, int x_dtype, int64_t rows, int6
  *   z[t][r] = x_scales[t] * w_scales[r] * sum_j x[t][j] w[r][j] + bias[r],   y = z (batch x rows),
  * or with WR_I8_SWIGLU (rows even, h = rows / 2): y[t][r] = silu(z[t][r]) * z[t][h + r], batch x h,
  * silu(v) = v / (1 + exp(-v)).  The sums are exact int32 (n <= 131071, WR_EUNSUPPORTED above); the
- * scales and the bias are applied in fp32 and y (WR_BF16 or WR_F32, ld ldy) is rounded once.
- * batch, rows and n may each be 0 (an empty sum is 0).  Any alignment and leading dimension of x
- * and w; 16-byte aligned rows with n a multiple of 16 are fastest.  No workspace.
+ * scales and the bias are applied in fp32 and y (WR_BF16 or WR_F32, ld ldy) is rounded once; y overlaps no input.
+ * batch, rows and n may each be 0 (an empty sum is 0); rows <= 2^26.  Any alignment and leading dimension of x
+ * and w; rows on 16-byte boundaries (x, w, ldx and ldw multiples of 16) are fastest.  No workspace.
  */
 int wr_matmul_i8(wr_ctx* ctx, const int8_t* x, int64_t ldx, const float* x_scales, int64_t batch, const int8_t* w,
                  int64_t ldw, const float* w_scales, int64_t rows, int64_t n, const float* bias, int flags, void* y,

@@ -51,6 +51,7 @@ constexpr int kDefaultCUs = 256;
 
 constexpr int64_t kNormMax = 16384;   // widest row of the block norm (a workgroup's registers)
 constexpr int64_t kI8Max = 131071;    // longest exact int32 sum of 8-bit products: 131071 * 2^14 < 2^31
+constexpr int64_t kI8Rows = 1 << 26;   // weight rows of an 8-bit product (its grid)
 constexpr int64_t kRowsMax = 2147483647;
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -356,7 +357,7 @@ int wr_matmul_i8(wr_ctx* ctx, const int8_t* x, int64_t ldx, const float* x_scale
                  int64_t ldw, const float* w_scales, int64_t rows, int64_t n, const float* bias, int flags, void* y,
                  int y_dtype, int64_t ldy) {
   const bool glu = flags & WR_I8_SWIGLU;
-  if (!ctx || !valid_dtype(y_dtype) || batch < 0 || batch > kRowsMax || rows < 0 || rows > kRowsMax / 2 || n < 0 ||
+  if (!ctx || !valid_dtype(y_dtype) || batch < 0 || batch > kRowsMax || rows < 0 || rows > kI8Rows || n < 0 ||
       (flags & ~WR_I8_SWIGLU) || (glu && rows % 2 != 0))
     return WR_EINVAL;
   if (batch == 0 || rows == 0) return WR_OK;

@@ -559,7 +559,8 @@ int wr_matmul_i8_impl(wr_ctx* ctx, const int8_t* x, int64_t ldx, const float* x_
   }
   // LDS DMA takes 16-byte aligned rows and, from a tile's first row, 32-bit offsets
   const bool dma = ((uintptr_t)x | (uintptr_t)w | (uint64_t)ldx | (uint64_t)ldw) % 16 == 0 && ldx < (1 << 24) && ldw < (1 << 24);
-  const int64_t slice = (int64_t)1 << 20;  // tokens per launch (grid.y of 16 tokens each)
+  // tokens per launch: at most 32768 rows of the grid (of 16 tokens or more each), and tiles within 32 bits
+  const int64_t slice = std::min<int64_t>((int64_t)1 << 19, std::max<int64_t>(256, ((int64_t)1 << 36) / rows));
   for (int64_t t0 = 0; t0 < batch; t0 += slice) {
     const I8Args a{x + t0 * ldx, ldx, x_scales + t0, (int)std::min(slice, batch - t0), w, ldw, w_scales, (int)rows,
                    (int)n, bias, (char*)y + t0 * ldy * (y_dtype == WR_BF16 ? 2 : 4), ldy};

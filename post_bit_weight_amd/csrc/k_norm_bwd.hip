@@ -26,14 +26,15 @@ static BwdPlan bwd_plan(int64_t rows, int64_t n, int64_t gate_rows, bool fp32) {
   BwdPlan p;
   const int64_t per8 = (n + 7) / 8;
   p.lanes = n < 8 ? 8 : n <= 128 ? 16 : n <= 256 ? 32 : n <= 512 ? 64 : 0;
-  // A workgroup's 512 threads hold rows of up to 4096 values with one chunk each, and of up to 8192 with two if
-  // nothing is fp32; other rows are walked (`wide`) by up to 1024 threads.
-  p.wide = n > 8192 || (n > 4096 && fp32);
-  p.chunks = p.wide ? (int)((n + 8191) / 8192) : n <= 4096 ? 1 : 2;
+  // A workgroup of up to 512 threads holds rows of up to 4096 values with one chunk each, and of up to 8192 with two if
+  // nothing is fp32.  With the parameters' sums in LDS 1024 threads hold 8192 values in any type and 768 hold 12288
+  // in bf16.  Wider rows are walked (`wide`).
+  p.wide = n > (fp32 ? 8192 : 12288);
+  p.chunks = p.wide ? 2 : n <= 4096 || (fp32 && n <= 8192) ? 1 : 2;
   p.threads = p.lanes ? 256 : (int)(((per8 + p.chunks - 1) / p.chunks + 63) / 64 * 64);
   // Two workgroups for each of 256 CUs, one where a workgroup fills the registers: more of them write more
   // partial sums and hide nothing that the next row's loads do not.
-  const int64_t most = p.wide || p.chunks > 1 ? 256 : 512;
+  const int64_t most = n > 4096 ? 256 : 512;
   const int64_t per = p.lanes ? 256 / p.lanes : 1;  // units per workgroup
   p.span = std::max<int64_t>(1, (rows + most * per - 1) / (most * per));
   if (rows <= 4) p.span = rows;  // one workgroup, whose sums are the result: no second launch
@@ -120,8 +121,10 @@ __device__ __forceinline__ void unit_range(const BwdArgs& a, int64_t unit, int64
 }
 
 // Absent inputs take a value that leaves the formula as it is, so that the row's arithmetic has no branches.
-template <typename TB, typename TR, typename TW, int CH, int LANES>
-__global__ __launch_bounds__(LANES > 0 ? 256 : 512) void block_norm_bwd_kernel(const BwdArgs a) {
+// MAXT: most threads.  SUMS_LDS: the parameters' sums are in LDS (each thread's own, two float4 per chunk and sum), for
+// rows whose workgroup leaves too few registers to each thread.
+template <typename TB, typename TR, typename TW, int CH, int LANES, int MAXT, bool SUMS_LDS>
+__global__ __launch_bounds__(MAXT) void block_norm_bwd_kernel(const BwdArgs a) {
   __shared__ uint32_t red[2][3][RowGroup<LANES>::kMaxWaves];
   constexpr int kPer = LANES > 0 ? 256 / (LANES > 0 ? LANES : 1) : 1;  // units per workgroup
   constexpr int kWidth = 8 * LANES;
@@ -132,6 +135,8 @@ __global__ __launch_bounds__(LANES > 0 ? 256 : 512) void block_norm_bwd_kernel(c
   const int n = a.n;
   const RowMap<CH, LANES> map(lane, LANES > 0 ? kWidth : 8 * blockDim.x, n);
   const float inv_n = 1.0f / (float)n;
+  // The next row's loads are in flight during a row, where the registers hold both.
+  constexpr bool kAhead = !SUMS_LDS || (CH == 1 && MAXT <= 768);
   int64_t r0, r1, gidx;
   unit_range(a, unit, r0, r1, gidx);
   int64_t gend = (gidx + 1) * a.gate_rows;
@@ -141,11 +146,29 @@ __global__ __launch_bounds__(LANES > 0 ? 256 : 512) void block_norm_bwd_kernel(c
   Raw8<TR> x[CH], dr[CH];
   Raw8<TR> odx[CH];  // the previous row's results, not yet stored
   Raw8<TB> odb[CH];
-  float s_pre[CH][8], s_post[CH][8], s_gate[CH][8];
+  enum { PRE, POST, GATE };
+  constexpr int RC = SUMS_LDS ? 1 : CH;
+  float held[3][RC][8];
+  extern __shared__ __attribute__((aligned(16))) f32x4 sums_lds[];
+  auto sum_at = [&](int which, int k, int h) -> f32x4& { return sums_lds[((which * CH + k) * 2 + h) * blockDim.x + threadIdx.x]; };
+  auto get_sum = [&](int which, int k, float (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = SUMS_LDS ? sum_at(which, k, e >> 2)[e & 3] : held[which][SUMS_LDS ? 0 : k][e];
+  };
+  auto set_sum = [&](int which, int k, const float (&v)[8]) {
+    if constexpr (SUMS_LDS) {
+      sum_at(which, k, 0) = f32x4{v[0], v[1], v[2], v[3]};
+      sum_at(which, k, 1) = f32x4{v[4], v[5], v[6], v[7]};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) held[which][k][e] = v[e];
+    }
+  };
+  const float zeros[8] = {};
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s_pre[k][e] = s_post[k][e] = s_gate[k][e] = 0.0f;
+    for (int w = 0; w < 3; ++w) set_sum(w, k, zeros);
     wp[k].fill(1.0f);
     wq[k].fill(1.0f);
     b[k].fill(0.0f);
@@ -178,8 +201,9 @@ __global__ __launch_bounds__(LANES > 0 ? 256 : 512) void block_norm_bwd_kernel(c
       if (a.db) map.store_own((TB*)a.db + row * a.lddb, k, odb[k]);
     }
   };
-  if (r0 < r1) load_row(r0, gidx);
+  if (kAhead && r0 < r1) load_row(r0, gidx);
   for (int64_t row = r0; row < r1; ++row) {
+    if (!kAhead) load_row(row, gidx);
     const float jb = ib, jx = ix;
     NormTerms kept[CH][8];
     float sums[3] = {0.0f, 0.0f, 0.0f};
@@ -189,14 +213,17 @@ __global__ __launch_bounds__(LANES > 0 ? 256 : 512) void block_norm_bwd_kernel(c
       map.own(x[k], k);
       map.own(dy[k], k);
       map.own(dr[k], k);
+      float pre[8];
+      get_sum(PRE, k, pre);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float d = dy[k].get(e), w = wq[k].get(e);
         const NormTerms m(a, jb, jx, b[k].get(e), g[k].get(e), x[k].get(e), d, dr[k].get(e), wp[k].get(e), w);
-        s_pre[k][e] = fmaf(d, m.xn, s_pre[k][e]);
+        pre[e] = fmaf(d, m.xn, pre[e]);
         m.add(sums, d, w);
         kept[k][e] = m;
       }
+      set_sum(PRE, k, pre);
     }
     const int64_t here = gidx;
     if (a.segs == 0 && row + 1 == gend) {
@@ -204,46 +231,58 @@ __global__ __launch_bounds__(LANES > 0 ? 256 : 512) void block_norm_bwd_kernel(c
       gend += a.gate_rows;
     }
     const bool last = row + 1 == r1;
-    if (row > r0) store_row(row - 1);
-    if (!last) load_row(row + 1, gidx);  // in flight during the rest of this row
+    if (kAhead && row > r0) store_row(row - 1);
+    if (kAhead && !last) load_row(row + 1, gidx);  // in flight during the rest of this row
     grp.template reduce<AddF32>(sums);
     float m1, m2;
     row_means(sums, inv_n, jx, m1, m2);
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      float dx_f[8], db_f[8];
+      float dx_f[8], db_f[8], post[8], gate[8];
+      get_sum(POST, k, post);
+      get_sum(GATE, k, gate);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const NormTerms m = kept[k][e];
         const float w = wp[k].get(e), dxo = fmaf(-m1, m.xn, m.t), du = m.cg * dxo;
         dx_f[e] = a.rscale * dxo;
-        s_post[k][e] = fmaf(du, m.bn, s_post[k][e]);
-        s_gate[k][e] = fmaf(a.bscale * dxo, w * m.bn, s_gate[k][e]);
+        post[e] = fmaf(du, m.bn, post[e]);
+        gate[e] = fmaf(a.bscale * dxo, w * m.bn, gate[e]);
         db_f[e] = a.w_post ? jb * fmaf(-m2, m.bn, du * w) : du;
       }
+      set_sum(POST, k, post);
+      set_sum(GATE, k, gate);
       odx[k].round(dx_f);
       odb[k].round(db_f);
     }
+    if (!kAhead) store_row(row);
     if (a.dgate && (last || gidx != here)) {  // a gate row's last token
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
-        map.store_own(a.dgate + here * n, k, s_gate[k]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s_gate[k][e] = 0.0f;
+        float gate[8];
+        get_sum(GATE, k, gate);
+        map.store_own(a.dgate + here * n, k, gate);
+        set_sum(GATE, k, zeros);
       }
     }
   }
-  if (r0 < r1) store_row(r1 - 1);
-  if (a.part_gate && !(LANES > 0 && a.one_gate) && unit < a.units)
+  if (kAhead && r0 < r1) store_row(r1 - 1);
+  auto write_sum = [&](int which, float* part) {
 #pragma unroll
-    for (int k = 0; k < CH; ++k) map.store_own(a.part_gate + unit * n, k, s_gate[k]);
+    for (int k = 0; k < CH; ++k) {
+      float v[8];
+      get_sum(which, k, v);
+      map.store_own(part, k, v);
+    }
+  };
+  if (a.part_gate && !(LANES > 0 && a.one_gate) && unit < a.units) write_sum(GATE, a.part_gate + unit * n);
   if constexpr (LANES > 0) {
     // the workgroup's units, added in order; a unit past the last one holds zeros
-    auto combine = [&](const float (&s)[8], float* part) {
+    auto combine = [&](int which, float* part) {
       __syncthreads();
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (map.keep[0] >> e & 1) comb[threadIdx.x / LANES * kWidth + map.col[0] + e] = s[e];
+        if (map.keep[0] >> e & 1) comb[threadIdx.x / LANES * kWidth + map.col[0] + e] = held[which][0][e];
       __syncthreads();
       for (int c = threadIdx.x; c < n; c += 256) {
         float sum = 0.0f;
@@ -251,15 +290,12 @@ __global__ __launch_bounds__(LANES > 0 ? 256 : 512) void block_norm_bwd_kernel(c
         part[(int64_t)blockIdx.x * n + c] = sum;
       }
     };
-    if (a.part_pre) combine(s_pre[0], a.part_pre);
-    if (a.part_post) combine(s_post[0], a.part_post);
-    if (a.part_gate && a.one_gate) combine(s_gate[0], a.part_gate);
+    if (a.part_pre) combine(PRE, a.part_pre);
+    if (a.part_post) combine(POST, a.part_post);
+    if (a.part_gate && a.one_gate) combine(GATE, a.part_gate);
   } else {
-#pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      if (a.part_pre) map.store_own(a.part_pre + (int64_t)blockIdx.x * n, k, s_pre[k]);
-      if (a.part_post) map.store_own(a.part_post + (int64_t)blockIdx.x * n, k, s_post[k]);
-    }
+    if (a.part_pre) write_sum(PRE, a.part_pre + (int64_t)blockIdx.x * n);
+    if (a.part_post) write_sum(POST, a.part_post + (int64_t)blockIdx.x * n);
   }
 }
 
@@ -430,19 +466,35 @@ size_t wr_norm_bwd_ws_bytes(int64_t rows, int64_t n, int64_t gate_rows) {
 }
 
 template <typename TB, typename TR, typename TW>
-static void bwd_launch(wr_ctx* ctx, const BwdPlan& p, const BwdArgs& a) {
-  auto go = [&](auto ch, auto lanes) {
-    hipLaunchKernelGGL((block_norm_bwd_kernel<TB, TR, TW, decltype(ch)::value, decltype(lanes)::value>),
-                       dim3((unsigned)p.blocks), dim3(p.threads), 0, ctx->stream, a);
+static int bwd_launch(wr_ctx* ctx, const BwdPlan& p, const BwdArgs& a) {
+  auto go = [&](auto ch, auto lanes, auto most, auto in_lds) {
+    constexpr int kCh = decltype(ch)::value;
+    constexpr bool kLds = decltype(in_lds)::value;
+    auto* kernel = block_norm_bwd_kernel<TB, TR, TW, kCh, decltype(lanes)::value, decltype(most)::value, kLds>;
+    const int lds = kLds ? 3 * kCh * 32 * p.threads : 0;
+    if (kLds && !lds_limit((const void*)kernel, 3 * kCh * 32 * decltype(most)::value)) return WR_EHIP;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)p.blocks), dim3(p.threads), lds, ctx->stream, a);
+    return WR_OK;
   };
-  if (p.lanes == 8) go(Int<1>{}, Int<8>{});
-  else if (p.lanes == 16) go(Int<1>{}, Int<16>{});
-  else if (p.lanes == 32) go(Int<1>{}, Int<32>{});
-  else if (p.lanes == 64) go(Int<1>{}, Int<64>{});
-  else if (p.wide)
+  const std::false_type regs;
+  const std::true_type in_lds;
+  constexpr bool kHalf = sizeof(TB) + sizeof(TR) == 4;
+  if (p.lanes == 8) return go(Int<1>{}, Int<8>{}, Int<256>{}, regs);
+  if (p.lanes == 16) return go(Int<1>{}, Int<16>{}, Int<256>{}, regs);
+  if (p.lanes == 32) return go(Int<1>{}, Int<32>{}, Int<256>{}, regs);
+  if (p.lanes == 64) return go(Int<1>{}, Int<64>{}, Int<256>{}, regs);
+  if (p.wide) {
     hipLaunchKernelGGL((block_norm_bwd_wide_kernel<TB, TR, TW>), dim3((unsigned)p.blocks), dim3(p.threads), 0, ctx->stream, a);
-  else if (p.chunks == 1) go(Int<1>{}, Int<0>{});
-  else if constexpr (sizeof(TB) + sizeof(TR) == 4) go(Int<2>{}, Int<0>{});
+    return WR_OK;
+  }
+  if (a.n <= 4096) return go(Int<1>{}, Int<0>{}, Int<512>{}, regs);
+  if constexpr (kHalf) {
+    if (a.n <= 8192) return go(Int<2>{}, Int<0>{}, Int<512>{}, regs);
+    return go(Int<2>{}, Int<0>{}, Int<768>{}, in_lds);
+  } else {
+    if (a.n <= 6144) return go(Int<1>{}, Int<0>{}, Int<768>{}, in_lds);
+    return go(Int<1>{}, Int<0>{}, Int<1024>{}, in_lds);
+  }
 }
 
 int wr_block_norm_backward_impl(wr_ctx* ctx, int64_t rows, int64_t n, const void* branch, int b_dtype, int64_t ldb,
@@ -505,16 +557,18 @@ int wr_block_norm_backward_impl(wr_ctx* ctx, int64_t rows, int64_t n, const void
   a.dgate = p.segs ? nullptr : dgate;
   if (p.blocks == 1 && a.one_gate && a.part_gate) a.part_gate = dgate;
   const int key = (b_dtype == WR_BF16 ? 4 : 0) + (r_dtype == WR_BF16 ? 2 : 0) + (w_dtype == WR_BF16 ? 1 : 0);
+  int rc;
   switch (key) {
-    case 0: bwd_launch<float, float, float>(ctx, p, a); break;
-    case 1: bwd_launch<float, float, uint16_t>(ctx, p, a); break;
-    case 2: bwd_launch<float, uint16_t, float>(ctx, p, a); break;
-    case 3: bwd_launch<float, uint16_t, uint16_t>(ctx, p, a); break;
-    case 4: bwd_launch<uint16_t, float, float>(ctx, p, a); break;
-    case 5: bwd_launch<uint16_t, float, uint16_t>(ctx, p, a); break;
-    case 6: bwd_launch<uint16_t, uint16_t, float>(ctx, p, a); break;
-    default: bwd_launch<uint16_t, uint16_t, uint16_t>(ctx, p, a); break;
+    case 0: rc = bwd_launch<float, float, float>(ctx, p, a); break;
+    case 1: rc = bwd_launch<float, float, uint16_t>(ctx, p, a); break;
+    case 2: rc = bwd_launch<float, uint16_t, float>(ctx, p, a); break;
+    case 3: rc = bwd_launch<float, uint16_t, uint16_t>(ctx, p, a); break;
+    case 4: rc = bwd_launch<uint16_t, float, float>(ctx, p, a); break;
+    case 5: rc = bwd_launch<uint16_t, float, uint16_t>(ctx, p, a); break;
+    case 6: rc = bwd_launch<uint16_t, uint16_t, float>(ctx, p, a); break;
+    default: rc = bwd_launch<uint16_t, uint16_t, uint16_t>(ctx, p, a); break;
   }
+  if (rc != WR_OK) return rc;
   WR_CHECK_LAUNCH();
   // Many short sums (gate rows of a few units) take a thread for each column; the others share a column's
   // partials among threads, with narrower workgroups where there are few columns.
