@@ -125,7 +125,7 @@ __device__ __forceinline__ void add_and_store(const I8Args& a, const i32x4 (&acc
   }
 }
 
-// Rows of fewer than 16 bytes: a thread for each output.
+// Rows of fewer than 16 bytes, or 8 MiB apart or more: a thread for each output.
 template <typename TY, bool GLU>
 __global__ __launch_bounds__(256) void matmul_i8_short_kernel(const I8Args a) {
   const int outs = GLU ? a.rows / 2 : a.rows;
@@ -149,6 +149,7 @@ __device__ __forceinline__ int swizzle(int row) {
 }
 // Wave-wide LDS DMA: lane l copies the 16 bytes at base + off to LDS byte m0 + 16 l.  In assembly so that the compiler
 // does not wait for it before every LDS read; vm_wait awaits it.  The M0 write needs one wait state before the DMA.
+// Global addresses may have any alignment, as for every other load (rows of odd strides come this way too).
 __device__ __forceinline__ void lds_dma16(const void* base, uint32_t off, uint32_t m0) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %2" ::"v"(off), "s"(m0), "s"(base) : "memory", "m0");
 }
@@ -160,14 +161,12 @@ __device__ __forceinline__ void vm_wait() {
 // rows) by NT x 16 tokens, and its NW waves cut the sum into contiguous ranges of 128-byte slices: few tokens or
 // few outputs still occupy the chip, and a byte is read from LDS once.  Each wave streams its range through a ring
 // of NS slots of its own, eight rows of 128 bytes (whole cache lines) per copy instruction; the waves share nothing
-// before their sums are added at the end, so the loop has no barrier.  With DMA the copies go to LDS directly, NS
-// slices ahead and without registers; rows that are not 16-byte aligned come through registers, one slice
-// ahead.  Rows and tokens past the end repeat the last one and are not stored.
-template <typename TY, bool GLU, int RF, int NT, int NW, int NS, bool DMA>
+// before their sums are added at the end, so the loop has no barrier.  The copies go to LDS directly, NS slices ahead
+// and without registers.  Rows and tokens past the end repeat the last one and are not stored.
+template <typename TY, bool GLU, int RF, int NT, int NW, int NS>
 __global__ __launch_bounds__(64 * NW) void matmul_i8_stream_kernel(const I8Args a) {
   constexpr int F = RF + NT, OF = GLU ? RF / 2 : RF;  // blocks of 16 rows; of 16 outputs
   constexpr int kSlot = F * 16 * 128;
-  static_assert(DMA || NS == 1, "copies through registers need one slot: LDS takes a wave's accesses in order");
   extern __shared__ __attribute__((aligned(1024))) char i8_lds[];
   lds_char* const lds = (lds_char*)i8_lds;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -178,9 +177,8 @@ __global__ __launch_bounds__(64 * NW) void matmul_i8_stream_kernel(const I8Args 
 
   // Copies: instruction i (of 2 F) fills rows 8 i .. + 7 of a slot, lane l the place l % 8 of its row l / 8: the chunk at
   // column `col` of a slice.  The row starts `off` bytes after `base`, which is the same for all lanes.
-  using Off = typename std::conditional<DMA, uint32_t, uint64_t>::type;
   const int8_t* base[2 * F];
-  Off off[2 * F];
+  uint32_t off[2 * F];
   int col[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) col[h] = 16 * ((lane & 7) ^ swizzle<128>(8 * h + (lane >> 3)));
@@ -188,27 +186,20 @@ __global__ __launch_bounds__(64 * NW) void matmul_i8_stream_kernel(const I8Args 
   for (int i = 0; i < 2 * F; ++i) {
     const int f = i >> 1, r = 8 * (i & 1) + (lane >> 3);
     base[i] = f < RF ? a.w + o0 * a.ldw + (int64_t)(f / OF * outs) * a.ldw : a.x + t0 * a.ldx;
-    off[i] = f < RF ? (Off)std::min(16 * (f % OF) + r, outs - 1 - o0) * (Off)a.ldw
-                    : (Off)std::min(16 * (f - RF) + r, a.batch - 1 - t0) * (Off)a.ldx;
+    off[i] = f < RF ? (uint32_t)std::min(16 * (f % OF) + r, outs - 1 - o0) * (uint32_t)a.ldw
+                    : (uint32_t)std::min(16 * (f - RF) + r, a.batch - 1 - t0) * (uint32_t)a.ldx;
   }
   const int slices = (a.n + 127) / 128, s0 = slices * wave / NW, s1 = slices * (wave + 1) / NW;
   const int whole = std::min(s1, a.n / 128);  // slices from here on pass n
-  auto fetch = [&](int s, int i) {
-    if (s < whole) return (u32x4)*reinterpret_cast<const u32x4_any*>(base[i] + off[i] + (128 * s + col[i & 1]));
-    return load16(base[i] + off[i], 128 * s + col[i & 1], a.n);
-  };
-  auto put_lds = [&](int slot, int i, const u32x4& v) {
-    *(__attribute__((address_space(3))) u32x4*)(ring + slot * kSlot + 1024 * i + 16 * lane) = v;
-  };
   auto issue = [&](int s, int slot) {
     if (s < whole) {
       const uint32_t at = __builtin_amdgcn_readfirstlane(ring_at + slot * kSlot);
-      if constexpr (DMA)
 #pragma unroll
-        for (int i = 0; i < 2 * F; ++i) lds_dma16(base[i] + 128 * s, off[i] + col[i & 1], at + 1024 * i);
-    } else {
+      for (int i = 0; i < 2 * F; ++i) lds_dma16(base[i] + 128 * s, off[i] + col[i & 1], at + 1024 * i);
+    } else {  // through registers, with zeros past n
 #pragma unroll
-      for (int i = 0; i < 2 * F; ++i) put_lds(slot, i, fetch(s, i));
+      for (int i = 0; i < 2 * F; ++i)
+        *(__attribute__((address_space(3))) u32x4*)(ring + slot * kSlot + 1024 * i + 16 * lane) = load16(base[i] + off[i], 128 * s + col[i & 1], a.n);
     }
   };
   const int r = lane & 15;
@@ -217,53 +208,30 @@ __global__ __launch_bounds__(64 * NW) void matmul_i8_stream_kernel(const I8Args 
   for (int u = 0; u < 2; ++u) rd[u] = r * 128 + (((4 * u + (lane >> 4)) ^ swizzle<128>(r)) << 4);
 
   i32x4 acc[RF][NT] = {};
-  u32x4 held[DMA ? 1 : 2 * F];  // the next slice on its way through registers
-  if constexpr (DMA) {
 #pragma unroll
-    for (int p = 0; p < NS; ++p)
-      if (s0 + p < s1) issue(s0 + p, p);
-  } else if (s0 < s1) {
-#pragma unroll
-    for (int i = 0; i < 2 * F; ++i) held[i] = fetch(s0, i);
-#pragma unroll
-    for (int i = 0; i < 2 * F; ++i) put_lds(0, i, held[i]);
-    if (s0 + 1 < s1)
-#pragma unroll
-      for (int i = 0; i < 2 * F; ++i) held[i] = fetch(s0 + 1, i);
-  }
+  for (int p = 0; p < NS; ++p)
+    if (s0 + p < s1) issue(s0 + p, p);
   int slot = 0;
   for (int s = s0; s < s1; ++s) {
-    if constexpr (DMA) {
-      // slice s has landed once only the copies of later slices are outstanding
-      if (s + NS <= whole) vm_wait<(NS - 1) * 2 * F>();
-      else vm_wait<0>();
-    }
+    // slice s has landed once only the copies of later slices are outstanding
+    if (s + NS <= whole) vm_wait<(NS - 1) * 2 * F>();
+    else vm_wait<0>();
     const lds_char* st = ring + slot * kSlot;
     i32x4 fr[2][F];
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int f = 0; f < F; ++f) fr[u][f] = *(const __attribute__((address_space(3))) i32x4*)(st + f * 2048 + rd[u]);
-    const int next = slot == NS - 1 ? 0 : slot + 1;
-    if constexpr (DMA) {
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read: the slot may be filled again
-      __builtin_amdgcn_sched_barrier(0);
-      if (s + NS < s1) issue(s + NS, slot);
-    } else if (s + 1 < s1) {
-#pragma unroll
-      for (int i = 0; i < 2 * F; ++i) put_lds(next, i, held[i]);
-      if (s + 2 < s1)
-#pragma unroll
-        for (int i = 0; i < 2 * F; ++i) held[i] = fetch(s + 2, i);
-      __builtin_amdgcn_sched_barrier(0);
-    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read: the slot may be filled again
+    __builtin_amdgcn_sched_barrier(0);
+    if (s + NS < s1) issue(s + NS, slot);
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int f = 0; f < RF; ++f) acc[f][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fr[u][f], fr[u][RF + t], acc[f][t], 0, 0, 0);
-    slot = next;
+    slot = slot == NS - 1 ? 0 : slot + 1;
   }
   __syncthreads();  // the sums go where the rings were
   add_and_store<TY, GLU, RF, NT, NW>(a, acc, reinterpret_cast<int32_t(*)[RF * NT][256]>(i8_lds), o0, t0);
@@ -273,7 +241,7 @@ __global__ __launch_bounds__(64 * NW) void matmul_i8_stream_kernel(const I8Args 
 // in registers (32x32x32 MFMAs).  Slices of BK bytes of the tile's rows are copied into a ring of NS slots by LDS
 // DMA, NS slices ahead; the operands of the next 32 bytes are read while the present ones are multiplied.  Chunk c
 // of row r lies at chunk c ^ f(r) (see the stream kernel; with 64-byte rows f(r) = r / 2 % 4).
-template <typename TY, bool GLU, int FI, int FJ, int WI, int WJ, int BK, int NS, bool LATE, bool DMA>
+template <typename TY, bool GLU, int FI, int FJ, int WI, int WJ, int BK, int NS, bool LATE>
 __global__ __launch_bounds__(64 * WI * WJ, 1) void matmul_i8_big_kernel(const I8Args a, int tiles_t, int tiles_o) {
   constexpr int NW = WI * WJ, TM = 32 * FI * WI, TN = 32 * FJ * WJ;
   constexpr int CPR = BK / 16, RPI = 64 / CPR;       // chunks per row, rows per copy instruction
@@ -281,8 +249,7 @@ __global__ __launch_bounds__(64 * WI * WJ, 1) void matmul_i8_big_kernel(const I8
   constexpr int kCopies = (TM + TN) / RPI / NW;      // copy instructions per wave and slice
   constexpr int KS = BK / 32;                        // MFMA steps per slice
   constexpr int kOuts = GLU ? TN / 2 : TN;
-  static_assert((TM + TN) % (RPI * NW) == 0 && KS % 2 == 0 && (!GLU || FJ % 2 == 0), "tile shape");
-  static_assert(DMA || NS == 2, "the copies through registers alternate between two slots");
+  static_assert((TM + TN) % (RPI * NW) == 0 && KS % 2 == 0 && NW * RPI % 16 == 0 && (!GLU || FJ % 2 == 0), "tile shape");
   extern __shared__ __attribute__((aligned(1024))) char i8_lds[];
   lds_char* const lds = (lds_char*)i8_lds;
   const uint32_t lds_at = (uint32_t)(uintptr_t)lds;
@@ -307,39 +274,35 @@ __global__ __launch_bounds__(64 * WI * WJ, 1) void matmul_i8_big_kernel(const I8
   // lane l the place l % CPR of its row l / CPR.  With GLU the weight rows are 32 gate rows, the same outputs' 32 up
   // rows, and so on.
   const int crow = lane / CPR;
-  using Off = typename std::conditional<DMA, uint32_t, uint64_t>::type;
   const int8_t* base[kCopies];  // the same for all lanes
-  Off off[kCopies];
-  int col[kCopies];
+  uint32_t off[kCopies];
+  // the same for every i: NW RPI rows are a multiple of the rows after which the swizzle repeats
+  const int col = 16 * ((lane % CPR) ^ swizzle<BK>(wave * RPI + crow));
 #pragma unroll
   for (int i = 0; i < kCopies; ++i) {
     const int r0 = (i * NW + wave) * RPI, r = r0 + crow;
     const int64_t up = GLU ? (int64_t)((r0 >> 5 & 1) * outs) * a.ldw : 0;
     base[i] = r0 >= TN ? a.x + t0 * a.ldx : a.w + o0 * a.ldw + up;
-    col[i] = 16 * ((lane % CPR) ^ swizzle<BK>(r));
-    off[i] = r >= TN ? (Off)std::min(r - TN, a.batch - 1 - t0) * (Off)a.ldx
-                     : (Off)std::min(GLU ? (r >> 6) * 32 + (r & 31) : r, outs - 1 - o0) * (Off)a.ldw;
+    off[i] = r >= TN ? (uint32_t)std::min(r - TN, a.batch - 1 - t0) * (uint32_t)a.ldx
+                     : (uint32_t)std::min(GLU ? (r >> 6) * 32 + (r & 31) : r, outs - 1 - o0) * (uint32_t)a.ldw;
   }
   const int slices = (a.n + BK - 1) / BK, whole = a.n / BK;  // a last slice beyond the whole ones passes n
-  auto fetch = [&](int s, int i) {
-    if (s < whole) return (u32x4)*reinterpret_cast<const u32x4_any*>(base[i] + off[i] + (BK * s + col[i]));
-    return load16(base[i] + off[i], BK * s + col[i], a.n);
-  };
-  auto put_lds = [&](int slot, int i, const u32x4& v) {
-    *(__attribute__((address_space(3))) u32x4*)(lds + slot * kSlot + (i * NW + wave) * 1024 + 16 * lane) = v;
-  };
   auto issue = [&](int s, int slot) {
     if (s < whole) {
       const uint32_t at = __builtin_amdgcn_readfirstlane(lds_at + slot * kSlot + wave * 1024);
-      if constexpr (DMA)
 #pragma unroll
-        for (int i = 0; i < kCopies; ++i) lds_dma16(base[i] + BK * s, off[i] + col[i], at + i * NW * 1024);
+      for (int i = 0; i < kCopies; ++i) lds_dma16(base[i] + BK * s, off[i] + col, at + i * NW * 1024);
     } else {  // through registers, with zeros past n
 #pragma unroll
-      for (int i = 0; i < kCopies; ++i) put_lds(slot, i, fetch(s, i));
+      for (int i = 0; i < kCopies; ++i) {
+        // The accumulators leave few registers: no full addresses kept for this one slice, three loads in flight.
+        uint32_t from = off[i];
+        asm volatile("" : "+v"(from));
+        *(__attribute__((address_space(3))) u32x4*)(lds + slot * kSlot + (i * NW + wave) * 1024 + 16 * lane) = load16(base[i] + from, BK * s + col, a.n);
+        if (i % 3 == 2) asm volatile("" ::: "memory");
+      }
     }
   };
-  u32x4 held[DMA ? 1 : kCopies];  // without DMA: the next slice on its way through registers
 
   uint32_t rd[KS];  // this lane's place in a block of 32 rows for each MFMA step of a slice
 #pragma unroll
@@ -364,21 +327,11 @@ __global__ __launch_bounds__(64 * WI * WJ, 1) void matmul_i8_big_kernel(const I8
       for (int j = 0; j < FJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[set][j], fx[set][i], acc[i][j], 0, 0, 0);
   };
 
-  if constexpr (DMA) {
 #pragma unroll
-    for (int p = 0; p < NS; ++p)
-      if (p < slices) issue(p, p);
-    if (whole >= NS) vm_wait<kCopies*(NS - 1)>();
-    else vm_wait<0>();
-  } else {
-#pragma unroll
-    for (int i = 0; i < kCopies; ++i) held[i] = fetch(0, i);
-#pragma unroll
-    for (int i = 0; i < kCopies; ++i) put_lds(0, i, held[i]);
-    if (slices > 1)
-#pragma unroll
-      for (int i = 0; i < kCopies; ++i) held[i] = fetch(1, i);
-  }
+  for (int p = 0; p < NS; ++p)
+    if (p < slices) issue(p, p);
+  if (whole >= NS) vm_wait<kCopies*(NS - 1)>();
+  else vm_wait<0>();
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   read(0, 0, 0);
   int slot = 0;
@@ -391,25 +344,17 @@ __global__ __launch_bounds__(64 * WI * WJ, 1) void matmul_i8_big_kernel(const I8
         multiply(u & 1);
       } else {
         if (s + 1 < slices) {
-          if constexpr (DMA) {
-            // slice s + 1 has landed once only the copies of slices s + 2 .. s + NS - 1 are outstanding
-            if (s + NS <= whole) vm_wait<kCopies*(NS - 2)>();
-            else vm_wait<0>();
-          } else {  // the other slot was last read before the previous barrier
-#pragma unroll
-            for (int i = 0; i < kCopies; ++i) put_lds(next, i, held[i]);
-          }
+          // slice s + 1 has landed once only the copies of slices s + 2 .. s + NS - 1 are outstanding
+          if (s + NS <= whole) vm_wait<kCopies*(NS - 2)>();
+          else vm_wait<0>();
           asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
           // every wave has read all of slice s: its slot is free.  With one workgroup on a CU the copies wait
           // until the matrix cores have work; with two, the other one's products cover them.
-          if (DMA && !LATE && s + NS < slices) issue(s + NS, slot);
+          if (!LATE && s + NS < slices) issue(s + NS, slot);
           read(next, 0, 0);
         }
         multiply(u & 1);
-        if (DMA && LATE && s + NS < slices) issue(s + NS, slot);
-        if (!DMA && s + 2 < slices)
-#pragma unroll
-          for (int i = 0; i < kCopies; ++i) held[i] = fetch(s + 2, i);
+        if (LATE && s + NS < slices) issue(s + NS, slot);
       }
     }
     slot = next;
@@ -425,15 +370,6 @@ __global__ __launch_bounds__(64 * WI * WJ, 1) void matmul_i8_big_kernel(const I8
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // no wave reads the ring any more
   lds_char* const turn = lds + wave * 32 * LS;
   const int ow = o0 + wj * WO;
-  f32x4 ws[FJ][4], bs[FJ][4];
-#pragma unroll
-  for (int j = 0; j < FJ; ++j)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int o = ow + (GLU ? j / 2 : j) * 32 + 8 * q + 4 * (lane >> 5), up = GLU && j % 2 ? outs : 0;
-      ws[j][q] = load_outputs(a.ws + up, outs, o);
-      bs[j][q] = load_outputs(a.bias ? a.bias + up : nullptr, outs, o);
-    }
 #pragma unroll
   for (int i = 0; i < FI; ++i) {
     const int tw = t0 + (wi * FI + i) * 32;
@@ -442,11 +378,18 @@ __global__ __launch_bounds__(64 * WI * WJ, 1) void matmul_i8_big_kernel(const I8
     for (int j = 0; j < FJ; j += GLU ? 2 : 1)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
+        const int o = ow + (GLU ? j / 2 : j) * 32 + 8 * q + 4 * (lane >> 5);
+        const f32x4 ws = load_outputs(a.ws, outs, o), bs = load_outputs(a.bias, outs, o);
+        f32x4 wu = {}, bu = {};
+        if constexpr (GLU) {
+          wu = load_outputs(a.ws + outs, outs, o);
+          bu = load_outputs(a.bias ? a.bias + outs : nullptr, outs, o);
+        }
         float z[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          z[e] = fmaf((float)acc[i][j][4 * q + e] * xs, ws[j][q][e], bs[j][q][e]);
-          if constexpr (GLU) z[e] = silu(z[e]) * fmaf((float)acc[i][j + 1][4 * q + e] * xs, ws[j + 1][q][e], bs[j + 1][q][e]);
+          z[e] = fmaf((float)acc[i][j][4 * q + e] * xs, ws[e], bs[e]);
+          if constexpr (GLU) z[e] = silu(z[e]) * fmaf((float)acc[i][j + 1][4 * q + e] * xs, wu[e], bu[e]);
         }
         lds_char* const to = turn + (lane & 31) * LS + ((GLU ? j / 2 : j) * 32 + 8 * q + 4 * (lane >> 5)) * (int)sizeof(TY);
         if constexpr (sizeof(TY) == 2)
@@ -456,7 +399,7 @@ __global__ __launch_bounds__(64 * WI * WJ, 1) void matmul_i8_big_kernel(const I8
       }
 #pragma unroll
     for (int k = 0; k < LPR / 2; ++k) {
-      const int row = k * (64 / LPR) + lane / LPR, at = lane % LPR, t = tw + row, o = ow + at * kPer;
+      const int row = (k * 64 + lane) / LPR, at = (k * 64 + lane) % LPR, t = tw + row, o = ow + at * kPer;
       const u32x4 v = *(const __attribute__((address_space(3))) u32x4*)(turn + row * LS + 16 * at);
       if (t >= a.batch || o >= outs) continue;
       TY* p = (TY*)a.y + t * a.ldy + o;
@@ -481,41 +424,35 @@ using namespace wr;
 template <int N>
 using Int = std::integral_constant<int, N>;
 
-// NW waves with rings of NS slots by DMA; through registers always eight with a slot each, since a wave has less in
-// flight there (777 tokens, 2531 -> 1023 on 64 x 64 tiles: 15.6 us; 15.9 with four waves and two slots; 11.4 by DMA).
 template <typename TY, bool GLU, int RF, int NT, int NW, int NS>
-static int stream_launch(wr_ctx* ctx, const I8Args& a, bool dma) {
+static int stream_launch(wr_ctx* ctx, const I8Args& a) {
   constexpr int OF = GLU ? RF / 2 : RF;
+  constexpr int lds = NW * std::max(NS * (RF + NT) * 2048, RF * NT * 1024);
+  static_assert(lds <= 160 * 1024, "LDS");
   const int outs = GLU ? a.rows / 2 : a.rows;
   const dim3 grid((outs + 16 * OF - 1) / (16 * OF), (a.batch + 16 * NT - 1) / (16 * NT));
-  auto go = [&](auto waves, auto slots, auto direct) {
-    constexpr int kWaves = decltype(waves)::value, kSlots = decltype(slots)::value;
-    constexpr int lds = kWaves * std::max(kSlots * (RF + NT) * 2048, RF * NT * 1024);
-    static_assert(lds <= 160 * 1024, "LDS");
-    auto* kernel = matmul_i8_stream_kernel<TY, GLU, RF, NT, kWaves, kSlots, decltype(direct)::value>;
-    if (!lds_limit((const void*)kernel, lds)) return WR_EHIP;
-    hipLaunchKernelGGL(kernel, grid, dim3(64 * kWaves), lds, ctx->stream, a);
-    return WR_OK;
-  };
-  return dma ? go(Int<NW>{}, Int<NS>{}, std::true_type{}) : go(Int<8>{}, Int<1>{}, std::false_type{});
+  auto* kernel = matmul_i8_stream_kernel<TY, GLU, RF, NT, NW, NS>;
+  if (!lds_limit((const void*)kernel, lds)) return WR_EHIP;
+  hipLaunchKernelGGL(kernel, grid, dim3(64 * NW), lds, ctx->stream, a);
+  return WR_OK;
 }
 
-template <typename TY, bool GLU, int FI, int FJ, int WI, int WJ, int BK, int NS, bool LATE, bool DMA>
+template <typename TY, bool GLU, int FI, int FJ, int WI, int WJ, int BK, int NS, bool LATE>
 static int big_launch(wr_ctx* ctx, const I8Args& a) {
   constexpr int TM = 32 * FI * WI, TN = 32 * FJ * WJ, kOuts = GLU ? TN / 2 : TN;
   constexpr int lds = NS * (TM + TN) * BK;
   static_assert(lds <= 160 * 1024, "LDS");
   const int outs = GLU ? a.rows / 2 : a.rows;
   const int tt = (a.batch + TM - 1) / TM, to = (outs + kOuts - 1) / kOuts;
-  auto* kernel = matmul_i8_big_kernel<TY, GLU, FI, FJ, WI, WJ, BK, NS, LATE, DMA>;
+  auto* kernel = matmul_i8_big_kernel<TY, GLU, FI, FJ, WI, WJ, BK, NS, LATE>;
   if (!lds_limit((const void*)kernel, lds)) return WR_EHIP;
   hipLaunchKernelGGL(kernel, dim3((unsigned)((tt * to + 7) / 8 * 8)), dim3(64 * WI * WJ), lds, ctx->stream, a, tt, to);
   return WR_OK;
 }
 
 template <typename TY, bool GLU>
-static int matmul_launch(wr_ctx* ctx, const I8Args& a, bool dma) {
-  if (a.n < 16) {
+static int matmul_launch(wr_ctx* ctx, const I8Args& a) {
+  if (a.n < 16 || std::max(a.ldx, a.ldw) >= 1 << 23) {  // a tile's rows, up to 320, are at 32-bit offsets from its first
     const int64_t all = (int64_t)a.batch * (GLU ? a.rows / 2 : a.rows);
     hipLaunchKernelGGL((matmul_i8_short_kernel<TY, GLU>), dim3((unsigned)std::min<int64_t>((all + 255) / 256, 1 << 20)),
                        dim3(256), 0, ctx->stream, a);
@@ -528,24 +465,39 @@ static int matmul_launch(wr_ctx* ctx, const I8Args& a, bool dma) {
   // n = 2560 and 9728, 4096 and 2560 outputs: 1 token 3.8 and 6.2 us on 16 x 16 (a floor of 2.0 and 4.8 at a copy's
   // rate; 7.0 and 13.7 on 64 x 64), 64 tokens 5.2 and 9.7 on 32 x 32 (7.3 and 12.4 on 16 x 16, 8.2 and 16.5 on
   // 64 x 64), 256 tokens 8.8 and 16.8 on 64 x 64 (15.0 and 24.9 on 32 x 32).
-  if (a.batch <= 16 && tiles(16 * R, 16) <= 2 * cu) return stream_launch<TY, GLU, R, 1, 8, 2>(ctx, a, dma);
-  if (tiles(16 * R, 32) <= cu) return stream_launch<TY, GLU, R, 2, 8, 2>(ctx, a, dma);
-  if (tiles(32, 32) <= cu) return stream_launch<TY, GLU, 2, 2, 8, 2>(ctx, a, dma);
-  if (tiles(64, 32) <= cu) return stream_launch<TY, GLU, 4, 2, 4, 3>(ctx, a, dma);
-  if (a.batch <= 16) return stream_launch<TY, GLU, R, 1, 8, 2>(ctx, a, dma);
-  if (tiles(32, 64) <= cu) return stream_launch<TY, GLU, 2, 4, 4, 2>(ctx, a, dma);
+  if (a.batch <= 16 && tiles(16 * R, 16) <= 2 * cu) return stream_launch<TY, GLU, R, 1, 8, 2>(ctx, a);
+  if (tiles(16 * R, 32) <= cu) return stream_launch<TY, GLU, R, 2, 8, 2>(ctx, a);
+  if (tiles(32, 32) <= cu) return stream_launch<TY, GLU, 2, 2, 8, 2>(ctx, a);
+  if (tiles(64, 32) <= cu) return stream_launch<TY, GLU, 4, 2, 4, 3>(ctx, a);
+  if (a.batch <= 16) return stream_launch<TY, GLU, R, 1, 8, 2>(ctx, a);
+  if (tiles(32, 64) <= cu) return stream_launch<TY, GLU, 2, 4, 4, 2>(ctx, a);
   // Two rounds of 64 x 64 beat shared tiles where the sum is long (512 tokens, 9728 -> 2560: 32.5 us against 38.5).
-  if (tiles(64, 64) <= (!GLU && a.n >= 4096 ? 2 : 1) * cu) return stream_launch<TY, GLU, 4, 4, 4, 2>(ctx, a, dma);
+  if (tiles(64, 64) <= (!GLU && a.n >= 4096 ? 2 : 1) * cu) return stream_launch<TY, GLU, 4, 4, 4, 2>(ctx, a);
   if (tiles(128, 64) <= 2 * cu)
-    return dma ? big_launch<TY, GLU, 1, 2, 2, 2, 128, 3, false, true>(ctx, a)
-               : big_launch<TY, GLU, 1, 2, 2, 2, 128, 2, false, false>(ctx, a);
-  // A round of 256 x 256 tiles takes 1.6 times one of 128 x 128, of which a CU holds two, for twice the work: 8192
-  // tokens 2560 -> 2 x 9728: 437 us against 483; 1024 tokens: 74 against 61.  (Without DMA its operands do not fit the
-  // registers.)
-  const int64_t g = (tiles(128, 128) + 2 * cu - 1) / (2 * cu), h = (tiles(256, 256) + cu - 1) / cu;
-  if (!dma) return big_launch<TY, GLU, 2, 2, 2, 2, 128, 2, false, false>(ctx, a);
-  if (8 * h <= 5 * g) return big_launch<TY, GLU, 4, 2, 2, 4, 128, 2, true, true>(ctx, a);
-  return big_launch<TY, GLU, 2, 2, 2, 2, 128, 2, false, true>(ctx, a);
+    return big_launch<TY, GLU, 1, 2, 2, 2, 128, 3, false>(ctx, a);
+  // Shared tiles: the least number of rounds over the CUs times the time of one round, measured in hundredths of that of
+  // 256 x 256 (n = 2560: 45 us, 4096: 68): the larger tile wins by the bytes it reads from LDS, the other by
+  // a last round that is nearly empty.  8192 tokens 2560 -> 2 x 9728: 527, 455, 451 and 420 us in this order; 16384
+  // tokens 4096 -> 2560: 210, 208, 203, 234 and 166; 4096 tokens 9728 -> 2560: 130, 101, 109, 128 and 121.
+  struct Tile {
+    int64_t tokens, rows, per_cu, time;
+  };
+  constexpr Tile kTiles[5] = {{128, 128, 2, 62}, {192, 256, 1, 77}, {256, 256, 1, 100}, {320, 256, 1, 116}, {256, 320, 1, 123}};
+  constexpr int kWide = !GLU && sizeof(TY) == 2 ? 5 : 4;  // the last one's gate and up blocks would not pair, nor its fp32 outputs fit LDS
+  int best = 0;
+  int64_t least = INT64_MAX;
+  for (int i = 0; i < kWide; ++i) {
+    const int64_t at_once = kTiles[i].per_cu * cu, t = (tiles(kTiles[i].rows, kTiles[i].tokens) + at_once - 1) / at_once * kTiles[i].time;
+    if (t < least) best = i, least = t;
+  }
+  switch (best) {
+    case 0: return big_launch<TY, GLU, 2, 2, 2, 2, 128, 2, false>(ctx, a);
+    case 1: return big_launch<TY, GLU, 3, 2, 2, 4, 128, 2, true>(ctx, a);
+    case 2: return big_launch<TY, GLU, 4, 2, 2, 4, 128, 2, true>(ctx, a);
+    case 3: return big_launch<TY, GLU, 5, 2, 2, 4, 128, 2, true>(ctx, a);
+  }
+  if constexpr (kWide == 5) return big_launch<TY, GLU, 2, 5, 4, 2, 128, 2, true>(ctx, a);
+  return WR_EINVAL;
 }
 
 int wr_matmul_i8_impl(wr_ctx* ctx, const int8_t* x, int64_t ldx, const float* x_scales, int64_t batch, const int8_t* w,
@@ -557,16 +509,14 @@ int wr_matmul_i8_impl(wr_ctx* ctx, const int8_t* x, int64_t ldx, const float* x_
     x = w = nullptr;
     ldx = ldw = 0;
   }
-  // LDS DMA takes 16-byte aligned rows and, from a tile's first row, 32-bit offsets
-  const bool dma = ((uintptr_t)x | (uintptr_t)w | (uint64_t)ldx | (uint64_t)ldw) % 16 == 0 && ldx < (1 << 24) && ldw < (1 << 24);
   // tokens per launch: at most 32768 rows of the grid (of 16 tokens or more each), and tiles within 32 bits
   const int64_t slice = std::min<int64_t>((int64_t)1 << 19, std::max<int64_t>(256, ((int64_t)1 << 36) / rows));
   for (int64_t t0 = 0; t0 < batch; t0 += slice) {
     const I8Args a{x + t0 * ldx, ldx, x_scales + t0, (int)std::min(slice, batch - t0), w, ldw, w_scales, (int)rows,
                    (int)n, bias, (char*)y + t0 * ldy * (y_dtype == WR_BF16 ? 2 : 4), ldy};
     int rc;
-    if (y_dtype == WR_BF16) rc = glu ? matmul_launch<uint16_t, true>(ctx, a, dma) : matmul_launch<uint16_t, false>(ctx, a, dma);
-    else rc = glu ? matmul_launch<float, true>(ctx, a, dma) : matmul_launch<float, false>(ctx, a, dma);
+    if (y_dtype == WR_BF16) rc = glu ? matmul_launch<uint16_t, true>(ctx, a) : matmul_launch<uint16_t, false>(ctx, a);
+    else rc = glu ? matmul_launch<float, true>(ctx, a) : matmul_launch<float, false>(ctx, a);
     if (rc != WR_OK) return rc;
     WR_CHECK_LAUNCH();
   }

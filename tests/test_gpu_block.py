@@ -467,6 +467,43 @@ def test_matmul_i8_extreme_sums_and_scales(wr, ctx):
     assert not bool(y[1].any()) and bool(torch.isnan(y[2]).all())
 
 
+# Tokens and weight rows for which each of the largest shared tiles takes the fewest rounds; odd strides and a last slice
+# that passes n.  The sums are exact in fp64 too.
+@pytest.mark.parametrize("swiglu", [False, True], ids=["plain", "swiglu"])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("batch,rows,n,padx,padw", [(3000, 4090, 300, 4, 4), (4090, 4092, 150, 10, 10), (5100, 4090, 520, 8, 8),
+                                                    (4090, 5100, 300, 4, 4), (5101, 4090, 131, 0, 3), (4090, 5102, 263, 0, 0)])
+def test_matmul_i8_largest_tiles(wr, ctx, batch, rows, n, padx, padw, dtype, swiglu):
+    x, xs, w, ws, b = mm_inputs(batch + rows + n, batch, rows, n, padx, padw)
+    if swiglu:
+        xs, ws = xs * (40 / n ** 0.5), ws * (10 / n ** 0.5)
+    y = Padded(batch, rows // 2 if swiglu else rows, dtype, 1)
+    wr.wr_matmul_i8(ctx, x, xs, w, ws, y.view, bias=b, swiglu=swiglu)
+    z0 = (x.double() @ w.double().t().contiguous()) * xs.double()[:, None] * ws.double()
+    ez = E32 * (4 * z0.abs() + 2 * b.double().abs())  # the int32 sum to fp32, two scales, the bias
+    ref, err = z0 + b.double(), ez
+    if swiglu:
+        (g, u), (eg, eu) = ref.chunk(2, 1), ez.chunk(2, 1)
+        sg = g / (1 + torch.exp(-g))
+        ref = sg * u
+        err = 1.1 * u.abs() * eg + sg.abs() * eu + 1.1 * eg * eu + 12 * E32 * ref.abs()
+    assert bool(((y.view.double() - ref).abs() <= err + (ref.abs() + err) * round_err(dtype)).all())
+    assert y.untouched()
+
+
+def test_matmul_i8_rows_far_apart(wr, ctx):
+    """Rows 8 MiB and more apart: offsets in a tile pass 32 bits."""
+    n, far = 200, (1 << 23) + 5
+    x, w = (torch.zeros(k * far, dtype=torch.int8, device="cuda").view(k, far)[:, :n] for k in (3, 40))
+    x.copy_(torch.randint(-128, 128, (3, n)))
+    w.copy_(torch.randint(-128, 128, (40, n)))
+    one = torch.ones(40, device="cuda")
+    for a, c in ((x, w), (x.contiguous(), w), (x, w.contiguous())):
+        y = torch.empty(3, 40, device="cuda")
+        wr.wr_matmul_i8(ctx, a, one[:3], c, one, y)
+        assert torch.equal(y.double(), x.double() @ w.double().t().contiguous())
+
+
 def test_matmul_i8_empty(wr, ctx):
     z8 = lambda *s: torch.zeros(*s, dtype=torch.int8, device="cuda")  # noqa: E731
     b = torch.randn(6, device="cuda")
