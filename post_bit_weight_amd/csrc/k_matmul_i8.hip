@@ -141,12 +141,9 @@ __global__ __launch_bounds__(256) void matmul_i8_short_kernel(const I8Args a) {
 }
 
 // ---- LDS DMA.  Sixteen-byte chunk c of row r of a slice lies at chunk c ^ swizzle(r), so that the sixteen rows an
-// operand read touches at once lie on different banks (rows of 128 bytes: two, of 64 bytes: four fill the banks).
+// operand read touches at once lie on different banks (two rows of 128 bytes fill the banks once).
 typedef __attribute__((address_space(3))) char lds_char;
-template <int ROW>
-__device__ __forceinline__ int swizzle(int row) {
-  return ROW == 128 ? row >> 1 & 7 : row >> 2 & 3;
-}
+__device__ __forceinline__ int swizzle(int row) { return row >> 1 & 7; }
 // Wave-wide LDS DMA: lane l copies the 16 bytes at base + off to LDS byte m0 + 16 l.  In assembly so that the compiler
 // does not wait for it before every LDS read; vm_wait awaits it.  The M0 write needs one wait state before the DMA.
 // Global addresses may have any alignment, as for every other load (rows of odd strides come this way too).
@@ -163,6 +160,10 @@ __device__ __forceinline__ void vm_wait() {
 // of NS slots of its own, eight rows of 128 bytes (whole cache lines) per copy instruction; the waves share nothing
 // before their sums are added at the end, so the loop has no barrier.  The copies go to LDS directly, NS slices ahead
 // and without registers.  Rows and tokens past the end repeat the last one and are not stored.
+//
+// Bound by the weights' bytes and, with so few of them, by latency: one token 9728 -> 2560 (25 MB) 6.2 us, 4.0 TB/s; 48
+// tokens 2560 -> 4096 5.2 us; 777 tokens 2531 -> 1023 with odd strides 12.9 us.  Loading the operands straight into
+// registers, without LDS, took twice as long: 16 rows a load, each a quarter of a cache line.
 template <typename TY, bool GLU, int RF, int NT, int NW, int NS>
 __global__ __launch_bounds__(64 * NW) void matmul_i8_stream_kernel(const I8Args a) {
   constexpr int F = RF + NT, OF = GLU ? RF / 2 : RF;  // blocks of 16 rows; of 16 outputs
@@ -181,7 +182,7 @@ __global__ __launch_bounds__(64 * NW) void matmul_i8_stream_kernel(const I8Args 
   uint32_t off[2 * F];
   int col[2];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) col[h] = 16 * ((lane & 7) ^ swizzle<128>(8 * h + (lane >> 3)));
+  for (int h = 0; h < 2; ++h) col[h] = 16 * ((lane & 7) ^ swizzle(8 * h + (lane >> 3)));
 #pragma unroll
   for (int i = 0; i < 2 * F; ++i) {
     const int f = i >> 1, r = 8 * (i & 1) + (lane >> 3);
@@ -205,7 +206,7 @@ __global__ __launch_bounds__(64 * NW) void matmul_i8_stream_kernel(const I8Args 
   const int r = lane & 15;
   uint32_t rd[2];  // where this lane reads in a block, for either half of a slice
 #pragma unroll
-  for (int u = 0; u < 2; ++u) rd[u] = r * 128 + (((4 * u + (lane >> 4)) ^ swizzle<128>(r)) << 4);
+  for (int u = 0; u < 2; ++u) rd[u] = r * 128 + (((4 * u + (lane >> 4)) ^ swizzle(r)) << 4);
 
   i32x4 acc[RF][NT] = {};
 #pragma unroll
@@ -238,13 +239,17 @@ __global__ __launch_bounds__(64 * NW) void matmul_i8_stream_kernel(const I8Args 
 }
 
 // Large products: WI x WJ waves share a tile of 32 FI WI tokens x 32 FJ WJ weight rows, each with 32 FI x 32 FJ of it
-// in registers (32x32x32 MFMAs).  Slices of BK bytes of the tile's rows are copied into a ring of NS slots by LDS
+// in registers (32x32x32 MFMAs).  Slices of 128 bytes of the tile's rows are copied into a ring of NS slots by LDS
 // DMA, NS slices ahead; the operands of the next 32 bytes are read while the present ones are multiplied.  Chunk c
-// of row r lies at chunk c ^ f(r) (see the stream kernel; with 64-byte rows f(r) = r / 2 % 4).
-template <typename TY, bool GLU, int FI, int FJ, int WI, int WJ, int BK, int NS, bool LATE>
+// of row r lies at chunk c ^ swizzle(r), without which half of the LDS cycles were bank conflicts.
+//
+// Bound by the matrix cores at the clock that they leave: 16384 tokens 4096 -> 2560 166 us (2071 TOPS; a library's product
+// without scales 160 us), 8192 tokens 2560 -> 2 x 9728 with SwiGLU 420 us (1944 TOPS; product alone 404 us).  Slower:
+// copies issued between the MFMAs, five slots of 64 bytes, eight waves for 128 x 128, raised wave priority.
+template <typename TY, bool GLU, int FI, int FJ, int WI, int WJ, int NS, bool LATE>
 __global__ __launch_bounds__(64 * WI * WJ, 1) void matmul_i8_big_kernel(const I8Args a, int tiles_t, int tiles_o) {
   constexpr int NW = WI * WJ, TM = 32 * FI * WI, TN = 32 * FJ * WJ;
-  constexpr int CPR = BK / 16, RPI = 64 / CPR;       // chunks per row, rows per copy instruction
+  constexpr int BK = 128, CPR = BK / 16, RPI = 64 / CPR;  // bytes of a slice, chunks per row, rows per copy instruction
   constexpr int kSlot = (TM + TN) * BK;
   constexpr int kCopies = (TM + TN) / RPI / NW;      // copy instructions per wave and slice
   constexpr int KS = BK / 32;                        // MFMA steps per slice
@@ -277,7 +282,7 @@ __global__ __launch_bounds__(64 * WI * WJ, 1) void matmul_i8_big_kernel(const I8
   const int8_t* base[kCopies];  // the same for all lanes
   uint32_t off[kCopies];
   // the same for every i: NW RPI rows are a multiple of the rows after which the swizzle repeats
-  const int col = 16 * ((lane % CPR) ^ swizzle<BK>(wave * RPI + crow));
+  const int col = 16 * ((lane % CPR) ^ swizzle(wave * RPI + crow));
 #pragma unroll
   for (int i = 0; i < kCopies; ++i) {
     const int r0 = (i * NW + wave) * RPI, r = r0 + crow;
@@ -306,7 +311,7 @@ __global__ __launch_bounds__(64 * WI * WJ, 1) void matmul_i8_big_kernel(const I8
 
   uint32_t rd[KS];  // this lane's place in a block of 32 rows for each MFMA step of a slice
 #pragma unroll
-  for (int u = 0; u < KS; ++u) rd[u] = (lane & 31) * BK + (((2 * u + (lane >> 5)) ^ swizzle<BK>(lane & 31)) << 4);
+  for (int u = 0; u < KS; ++u) rd[u] = (lane & 31) * BK + (((2 * u + (lane >> 5)) ^ swizzle(lane & 31)) << 4);
   i32x4 fw[2][FJ], fx[2][FI];
   auto read = [&](int slot, int u, int set) {
     const lds_char* st = lds + slot * kSlot + rd[u];
@@ -327,6 +332,11 @@ __global__ __launch_bounds__(64 * WI * WJ, 1) void matmul_i8_big_kernel(const I8
       for (int j = 0; j < FJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[set][j], fx[set][i], acc[i][j], 0, 0, 0);
   };
 
+  // The tile's scales and biases, in registers until LDS has room for them.
+  static_assert(TN <= 64 * NW && TM <= 64 * NW, "a thread loads one scale");
+  const int r = threadIdx.x, own_t = std::min(t0 + r, a.batch - 1);
+  const int own_r = std::min(o0 + (GLU ? (r >> 6) * 32 + (r & 31) : r), outs - 1) + (GLU ? (r >> 5 & 1) * outs : 0);
+  const float own_xs = a.xs[own_t], own_ws = a.ws[own_r], own_bias = a.bias ? a.bias[own_r] : 0.0f;
 #pragma unroll
   for (int p = 0; p < NS; ++p)
     if (p < slices) issue(p, p);
@@ -366,24 +376,36 @@ __global__ __launch_bounds__(64 * WI * WJ, 1) void matmul_i8_big_kernel(const I8
   constexpr int WO = GLU ? 16 * FJ : 32 * FJ;               // outputs of a wave
   constexpr int RB = WO * (int)sizeof(TY), LS = RB + 16;    // bytes of a token's outputs, and in LDS
   constexpr int LPR = RB / 16, kPer = 16 / (int)sizeof(TY);  // lanes that store a row, outputs of one of them
-  static_assert(NW * 32 * LS <= NS * kSlot, "the turned outputs take the ring's place");
+  static_assert(NW * 32 * LS + 4 * (TM + 2 * TN) <= NS * kSlot, "the turned outputs and the scales take the ring's place");
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // no wave reads the ring any more
   lds_char* const turn = lds + wave * 32 * LS;
+  typedef __attribute__((address_space(3))) float lds_float;
+  lds_float* const ws_lds = (lds_float*)(lds + NW * 32 * LS);
+  lds_float* const bias_lds = ws_lds + TN;
+  lds_float* const xs_lds = bias_lds + TN;
+  if (r < TN) {
+    ws_lds[r] = own_ws;
+    bias_lds[r] = own_bias;
+  }
+  if (r < TM) xs_lds[r] = own_xs;
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   const int ow = o0 + wj * WO;
 #pragma unroll
   for (int i = 0; i < FI; ++i) {
     const int tw = t0 + (wi * FI + i) * 32;
-    const float xs = a.xs[std::min(tw + (lane & 31), a.batch - 1)];
+    const float xs = xs_lds[(wi * FI + i) * 32 + (lane & 31)];
 #pragma unroll
     for (int j = 0; j < FJ; j += GLU ? 2 : 1)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int o = ow + (GLU ? j / 2 : j) * 32 + 8 * q + 4 * (lane >> 5);
-        const f32x4 ws = load_outputs(a.ws, outs, o), bs = load_outputs(a.bias, outs, o);
+        auto scale4 = [&](const lds_float* v, int j) {
+          return *(const __attribute__((address_space(3))) f32x4*)(v + (wj * FJ + j) * 32 + 8 * q + 4 * (lane >> 5));
+        };
+        const f32x4 ws = scale4(ws_lds, j), bs = scale4(bias_lds, j);
         f32x4 wu = {}, bu = {};
         if constexpr (GLU) {
-          wu = load_outputs(a.ws + outs, outs, o);
-          bu = load_outputs(a.bias ? a.bias + outs : nullptr, outs, o);
+          wu = scale4(ws_lds, j + 1);
+          bu = scale4(bias_lds, j + 1);
         }
         float z[4];
 #pragma unroll
@@ -437,14 +459,14 @@ static int stream_launch(wr_ctx* ctx, const I8Args& a) {
   return WR_OK;
 }
 
-template <typename TY, bool GLU, int FI, int FJ, int WI, int WJ, int BK, int NS, bool LATE>
+template <typename TY, bool GLU, int FI, int FJ, int WI, int WJ, int NS, bool LATE>
 static int big_launch(wr_ctx* ctx, const I8Args& a) {
   constexpr int TM = 32 * FI * WI, TN = 32 * FJ * WJ, kOuts = GLU ? TN / 2 : TN;
-  constexpr int lds = NS * (TM + TN) * BK;
+  constexpr int lds = NS * (TM + TN) * 128;
   static_assert(lds <= 160 * 1024, "LDS");
   const int outs = GLU ? a.rows / 2 : a.rows;
   const int tt = (a.batch + TM - 1) / TM, to = (outs + kOuts - 1) / kOuts;
-  auto* kernel = matmul_i8_big_kernel<TY, GLU, FI, FJ, WI, WJ, BK, NS, LATE>;
+  auto* kernel = matmul_i8_big_kernel<TY, GLU, FI, FJ, WI, WJ, NS, LATE>;
   if (!lds_limit((const void*)kernel, lds)) return WR_EHIP;
   hipLaunchKernelGGL(kernel, dim3((unsigned)((tt * to + 7) / 8 * 8)), dim3(64 * WI * WJ), lds, ctx->stream, a, tt, to);
   return WR_OK;
@@ -471,10 +493,10 @@ static int matmul_launch(wr_ctx* ctx, const I8Args& a) {
   if (tiles(64, 32) <= cu) return stream_launch<TY, GLU, 4, 2, 4, 3>(ctx, a);
   if (a.batch <= 16) return stream_launch<TY, GLU, R, 1, 8, 2>(ctx, a);
   if (tiles(32, 64) <= cu) return stream_launch<TY, GLU, 2, 4, 4, 2>(ctx, a);
-  // Two rounds of 64 x 64 beat shared tiles where the sum is long (512 tokens, 9728 -> 2560: 32.5 us against 38.5).
-  if (tiles(64, 64) <= (!GLU && a.n >= 4096 ? 2 : 1) * cu) return stream_launch<TY, GLU, 4, 4, 4, 2>(ctx, a);
+  if (tiles(64, 64) <= cu) return stream_launch<TY, GLU, 4, 4, 4, 2>(ctx, a);
+  // From here on shared tiles: a second round of 64 x 64 takes 51 us for 770 tokens 9664 -> 1672, one of 64 x 128 35.
   if (tiles(128, 64) <= 2 * cu)
-    return big_launch<TY, GLU, 1, 2, 2, 2, 128, 3, false>(ctx, a);
+    return big_launch<TY, GLU, 1, 2, 2, 2, 3, false>(ctx, a);
   // Shared tiles: the least number of rounds over the CUs times the time of one round, measured in hundredths of that of
   // 256 x 256 (n = 2560: 45 us, 4096: 68): the larger tile wins by the bytes it reads from LDS, the other by
   // a last round that is nearly empty.  8192 tokens 2560 -> 2 x 9728: 527, 455, 451 and 420 us in this order; 16384
@@ -491,12 +513,12 @@ static int matmul_launch(wr_ctx* ctx, const I8Args& a) {
     if (t < least) best = i, least = t;
   }
   switch (best) {
-    case 0: return big_launch<TY, GLU, 2, 2, 2, 2, 128, 2, false>(ctx, a);
-    case 1: return big_launch<TY, GLU, 3, 2, 2, 4, 128, 2, true>(ctx, a);
-    case 2: return big_launch<TY, GLU, 4, 2, 2, 4, 128, 2, true>(ctx, a);
-    case 3: return big_launch<TY, GLU, 5, 2, 2, 4, 128, 2, true>(ctx, a);
+    case 0: return big_launch<TY, GLU, 2, 2, 2, 2, 2, false>(ctx, a);
+    case 1: return big_launch<TY, GLU, 3, 2, 2, 4, 2, true>(ctx, a);
+    case 2: return big_launch<TY, GLU, 4, 2, 2, 4, 2, true>(ctx, a);
+    case 3: return big_launch<TY, GLU, 5, 2, 2, 4, 2, true>(ctx, a);
   }
-  if constexpr (kWide == 5) return big_launch<TY, GLU, 2, 5, 4, 2, 128, 2, true>(ctx, a);
+  if constexpr (kWide == 5) return big_launch<TY, GLU, 2, 5, 4, 2, 2, true>(ctx, a);
   return WR_EINVAL;
 }
 

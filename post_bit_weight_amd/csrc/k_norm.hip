@@ -7,6 +7,10 @@
 // the maximum are reductions over the lanes that share the row.  Rows of up to 512 values take 16, 32 or
 // 64 lanes of a wave (no barrier); wider rows take a workgroup of up to 1024 threads with one or two
 // chunks of eight values per thread.
+//
+// Bound by memory.  16384 x 2560 bf16 with both norms, gate and residual (335 MB) take 64 us and 131072 x 128 bf16 with
+// one norm (67 MB) 13 us, both at the 5.2 TB/s of a large copy; 1013 x 9727 fp32 (158 MB) 41 us, 3.9 TB/s: two rows a
+// workgroup, and nothing hides the first one's loads; one token 3.3 us, a launch's latency.
 #include "rowops.hpp"
 
 namespace wr {
@@ -151,6 +155,8 @@ __global__ __launch_bounds__(MAXT) void block_norm_kernel(const NormArgs a) {
   }
 }
 
+// One pass: the row's maximum, its scale max / 127, and the codes from the values still in registers.  Bound by memory (3
+// bytes a bf16 value): 16384 x 4096 take 40 us, 5.0 TB/s.
 template <typename T, int CH, int LANES, int MAXT>
 __global__ __launch_bounds__(MAXT) void quant_rows_kernel(const T* __restrict__ x, int64_t ldx, int rows, int n,
                                                           int8_t* __restrict__ q, int64_t ldq,
