@@ -2,7 +2,8 @@
 GPTQ/LDLQ sweep, joint fp16 scales and the wring, bit packing.
 
 The compute lives in ``libwringer.so`` (HIP, C ABI declared in ``include/wringer.h``);
-``_lib`` is its ctypes binding and ``pipeline`` sequences the calls for one module.
+``_lib`` is its ctypes binding and ``pipeline`` sequences the calls for one module; ``int8`` runs a block's gated MLP
+in 8-bit integers on the container's modules.
 """
 
 from . import _lib  # noqa: F401

@@ -243,8 +243,9 @@ __global__ __launch_bounds__(64 * NW) void matmul_i8_stream_kernel(const I8Args 
 // DMA, NS slices ahead; the operands of the next 32 bytes are read while the present ones are multiplied.  Chunk c
 // of row r lies at chunk c ^ swizzle(r), without which half of the LDS cycles were bank conflicts.
 //
-// Bound by the matrix cores at the clock that they leave: 16384 tokens 4096 -> 2560 166 us (2071 TOPS; a library's product
-// without scales 160 us), 8192 tokens 2560 -> 2 x 9728 with SwiGLU 420 us (1944 TOPS; product alone 404 us).  Slower:
+// Bound by the matrix cores, half busy at the 1.9 GHz that they leave: 16384 tokens 4096 -> 2560 160 us (2149 TOPS; a library's product
+// without scales 160 us), 8192 tokens 2560 -> 2 x 9728 with SwiGLU 401 us (2034 TOPS; product alone 404 us).  Short
+// sums are bound by the outputs: 8192 tokens 256 -> 4096 25 us, 2.7 TB/s.  Slower:
 // copies issued between the MFMAs, five slots of 64 bytes, eight waves for 128 x 128, raised wave priority.
 template <typename TY, bool GLU, int FI, int FJ, int WI, int WJ, int NS, bool LATE>
 __global__ __launch_bounds__(64 * WI * WJ, 1) void matmul_i8_big_kernel(const I8Args a, int tiles_t, int tiles_o) {
@@ -498,9 +499,9 @@ static int matmul_launch(wr_ctx* ctx, const I8Args& a) {
   if (tiles(128, 64) <= 2 * cu)
     return big_launch<TY, GLU, 1, 2, 2, 2, 3, false>(ctx, a);
   // Shared tiles: the least number of rounds over the CUs times the time of one round, measured in hundredths of that of
-  // 256 x 256 (n = 2560: 45 us, 4096: 68): the larger tile wins by the bytes it reads from LDS, the other by
-  // a last round that is nearly empty.  8192 tokens 2560 -> 2 x 9728: 527, 455, 451 and 420 us in this order; 16384
-  // tokens 4096 -> 2560: 210, 208, 203, 234 and 166; 4096 tokens 9728 -> 2560: 130, 101, 109, 128 and 121.
+  // 256 x 256 (n = 2560: 44 us, 4096: 62): the larger tile wins by the bytes it reads from LDS, the other by
+  // a last round that is nearly empty.  8192 tokens 2560 -> 2 x 9728: 497, 461, 436 and 401 us in this order; 16384
+  // tokens 4096 -> 2560: 196, 193, 187, 205 and 160; 4096 tokens 9728 -> 2560: 134, 107, 117, 131 and 128.
   struct Tile {
     int64_t tokens, rows, per_cu, time;
   };
