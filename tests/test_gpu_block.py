@@ -533,6 +533,49 @@ def test_tensors_on_the_contexts_stream(wr):
     assert np.allclose(f64(z), v @ v.T, rtol=1e-5, atol=1e-5)
 
 
+def test_replayed_graph_equals_eager(wr):
+    """The calls recorded in a graph read their inputs anew at each replay, with other work between the replays."""
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        c = wr.Context(0, stream)
+        g = torch.Generator(device="cuda").manual_seed(5)
+        b, x, dy = (torch.randn(200, 640, generator=g, device="cuda").to(BF16) for _ in range(3))
+        w, gate = (torch.randn(640, generator=g, device="cuda").to(BF16) for _ in range(2))
+        codes = torch.randint(-127, 128, (1500, 640), generator=g, device="cuda", dtype=torch.int8)
+        ws = torch.rand(1500, generator=g, device="cuda") * 0.01
+
+        def outputs():
+            return dict(xo=torch.zeros_like(x), q=torch.zeros(200, 640, dtype=torch.int8, device="cuda"),
+                        qs=torch.zeros(200, device="cuda"), st=torch.zeros(200, 2, device="cuda"),
+                        h=torch.zeros(200, 750, device="cuda"), hq=torch.zeros(200, 750, dtype=torch.int8, device="cuda"),
+                        hs=torch.zeros(200, device="cuda"), db=torch.zeros_like(b), dw=torch.zeros(640, device="cuda"),
+                        dg=torch.zeros(1, 640, device="cuda"))
+
+        def calls(o):
+            wr.wr_block_norm(c, 1e-6, branch=b, resid=x, w_post=w, gate=gate[None], w_pre=w, resid_out=o["xo"], q=o["q"],
+                             q_scales=o["qs"], stats=o["st"])
+            wr.wr_matmul_i8(c, o["q"], o["qs"], codes, ws, o["h"], swiglu=True)
+            wr.wr_quant_rows_i8(c, o["h"], o["hq"], o["hs"])
+            wr.wr_block_norm_backward(c, o["st"], branch=b, resid=x, w_post=w, gate=gate[None], w_pre=w, dy=dy,
+                                      dbranch=o["db"], dw_pre=o["dw"], dgate=o["dg"])
+
+        eager, replayed = outputs(), outputs()
+        calls(eager)  # also registers the workspace
+        stream.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            calls(replayed)
+        for _ in range(4):
+            b.copy_(torch.randn(200, 640, generator=g, device="cuda"))
+            for t in replayed.values():
+                t.zero_()
+            graph.replay()
+            calls(eager)
+            stream.synchronize()
+            for name in eager:
+                assert torch.equal(eager[name], replayed[name]), name
+
+
 # ---------------------------------------------------------------- refusals
 
 def test_refusals(wr, ctx):
