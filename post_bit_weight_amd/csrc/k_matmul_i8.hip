@@ -241,14 +241,15 @@ __global__ __launch_bounds__(64 * NW) void matmul_i8_stream_kernel(const I8Args 
 // Large products: WI x WJ waves share a tile of 32 FI WI tokens x 32 FJ WJ weight rows, each with 32 FI x 32 FJ of it
 // in registers (32x32x32 MFMAs).  Slices of 128 bytes of the tile's rows are copied into a ring of NS slots by LDS
 // DMA, NS slices ahead; the operands of the next 32 bytes are read while the present ones are multiplied.  Chunk c
-// of row r lies at chunk c ^ swizzle(r), without which half of the LDS cycles were bank conflicts.
+// of row r lies at chunk c ^ swizzle(r), without which half of the LDS cycles were bank conflicts.  KG such groups of
+// waves, each with a ring of its own, take every KG-th slice of the same tile; their sums meet in LDS at the end.
 //
-// Bound by the matrix cores, half busy at the 1.9 GHz that they leave: 16384 tokens 4096 -> 2560 160 us (2149 TOPS; a library's product
-// without scales 160 us), 8192 tokens 2560 -> 2 x 9728 with SwiGLU 401 us (2034 TOPS; product alone 404 us).  Short
-// sums are bound by the outputs: 8192 tokens 256 -> 4096 25 us, 2.7 TB/s.  Slower:
-// copies issued between the MFMAs, five slots of 64 bytes, eight waves for 128 x 128, raised wave priority.
-template <typename TY, bool GLU, int FI, int FJ, int WI, int WJ, int NS, bool LATE>
-__global__ __launch_bounds__(64 * WI * WJ, 1) void matmul_i8_big_kernel(const I8Args a, int tiles_t, int tiles_o) {
+// Bound by the matrix cores, half busy at the 1.9 GHz that they leave: 16384 tokens 4096 -> 2560 160 us (2149 TOPS; a
+// library's product without scales 160 us), 8192 tokens 2560 -> 2 x 9728 with SwiGLU 401 us (2034 TOPS; product alone
+// 404 us).  Short sums are bound by the outputs: 8192 tokens 256 -> 4096 25 us, 2.7 TB/s.  Slower: copies issued
+// between the MFMAs, five slots of 64 bytes, eight waves for 128 x 128, raised wave priority.
+template <typename TY, bool GLU, int FI, int FJ, int WI, int WJ, int NS, bool LATE, int KG>
+__global__ __launch_bounds__(64 * WI * WJ * KG, 1) void matmul_i8_big_kernel(const I8Args a, int tiles_t, int tiles_o) {
   constexpr int NW = WI * WJ, TM = 32 * FI * WI, TN = 32 * FJ * WJ;
   constexpr int BK = 128, CPR = BK / 16, RPI = 64 / CPR;  // bytes of a slice, chunks per row, rows per copy instruction
   constexpr int kSlot = (TM + TN) * BK;
@@ -257,9 +258,10 @@ __global__ __launch_bounds__(64 * WI * WJ, 1) void matmul_i8_big_kernel(const I8
   constexpr int kOuts = GLU ? TN / 2 : TN;
   static_assert((TM + TN) % (RPI * NW) == 0 && KS % 2 == 0 && NW * RPI % 16 == 0 && (!GLU || FJ % 2 == 0), "tile shape");
   extern __shared__ __attribute__((aligned(1024))) char i8_lds[];
-  lds_char* const lds = (lds_char*)i8_lds;
+  const int lane = threadIdx.x & 63, wave_of_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = KG > 1 ? wave_of_all / NW : 0, wave = KG > 1 ? wave_of_all % NW : wave_of_all;
+  lds_char* const lds = (lds_char*)i8_lds + group * NS * kSlot;
   const uint32_t lds_at = (uint32_t)(uintptr_t)lds;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wi = wave / WJ, wj = wave % WJ;
   const int outs = GLU ? a.rows / 2 : a.rows;
 
@@ -292,19 +294,20 @@ __global__ __launch_bounds__(64 * WI * WJ, 1) void matmul_i8_big_kernel(const I8
     off[i] = r >= TN ? (uint32_t)std::min(r - TN, a.batch - 1 - t0) * (uint32_t)a.ldx
                      : (uint32_t)std::min(GLU ? (r >> 6) * 32 + (r & 31) : r, outs - 1 - o0) * (uint32_t)a.ldw;
   }
-  const int slices = (a.n + BK - 1) / BK, whole = a.n / BK;  // a last slice beyond the whole ones passes n
+  // This group's slices are KG s + group; those from `whole` on pass n, or lie beyond it (zeros).
+  const int slices = (a.n + BK * KG - 1) / (BK * KG), whole = (a.n / BK + KG - 1 - group) / KG;
   auto issue = [&](int s, int slot) {
     if (s < whole) {
       const uint32_t at = __builtin_amdgcn_readfirstlane(lds_at + slot * kSlot + wave * 1024);
 #pragma unroll
-      for (int i = 0; i < kCopies; ++i) lds_dma16(base[i] + BK * s, off[i] + col, at + i * NW * 1024);
+      for (int i = 0; i < kCopies; ++i) lds_dma16(base[i] + BK * (KG * s + group), off[i] + col, at + i * NW * 1024);
     } else {  // through registers, with zeros past n
 #pragma unroll
       for (int i = 0; i < kCopies; ++i) {
         // The accumulators leave few registers: no full addresses kept for this one slice, three loads in flight.
         uint32_t from = off[i];
         asm volatile("" : "+v"(from));
-        *(__attribute__((address_space(3))) u32x4*)(lds + slot * kSlot + (i * NW + wave) * 1024 + 16 * lane) = load16(base[i] + from, BK * s + col, a.n);
+        *(__attribute__((address_space(3))) u32x4*)(lds + slot * kSlot + (i * NW + wave) * 1024 + 16 * lane) = load16(base[i] + from, BK * (KG * s + group) + col, a.n);
         if (i % 3 == 2) asm volatile("" ::: "memory");
       }
     }
@@ -377,11 +380,12 @@ __global__ __launch_bounds__(64 * WI * WJ, 1) void matmul_i8_big_kernel(const I8
   constexpr int WO = GLU ? 16 * FJ : 32 * FJ;               // outputs of a wave
   constexpr int RB = WO * (int)sizeof(TY), LS = RB + 16;    // bytes of a token's outputs, and in LDS
   constexpr int LPR = RB / 16, kPer = 16 / (int)sizeof(TY);  // lanes that store a row, outputs of one of them
-  static_assert(NW * 32 * LS + 4 * (TM + 2 * TN) <= NS * kSlot, "the turned outputs and the scales take the ring's place");
+  constexpr int kShared = NW * 32 * LS + 4 * (TM + 2 * TN), kAcc = KG > 1 ? NW * FI * FJ * 4096 : 0;
+  static_assert(kShared % 16 == 0 && kShared + kAcc <= KG * NS * kSlot, "outputs, scales and sums take the rings' place");
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // no wave reads the ring any more
-  lds_char* const turn = lds + wave * 32 * LS;
+  lds_char* const turn = (lds_char*)i8_lds + wave * 32 * LS;
   typedef __attribute__((address_space(3))) float lds_float;
-  lds_float* const ws_lds = (lds_float*)(lds + NW * 32 * LS);
+  lds_float* const ws_lds = (lds_float*)((lds_char*)i8_lds + NW * 32 * LS);
   lds_float* const bias_lds = ws_lds + TN;
   lds_float* const xs_lds = bias_lds + TN;
   if (r < TN) {
@@ -389,7 +393,30 @@ __global__ __launch_bounds__(64 * WI * WJ, 1) void matmul_i8_big_kernel(const I8
     bias_lds[r] = own_bias;
   }
   if (r < TM) xs_lds[r] = own_xs;
+  // The second group hands its sums to the first, which stores.
+  auto sum_at = [&](int f, int q) {
+    return (__attribute__((address_space(3))) i32x4*)((lds_char*)i8_lds + kShared + ((wave * FI * FJ + f) * 4 + q) * 1024 + 16 * lane);
+  };
+  if (KG > 1 && group)
+#pragma unroll
+    for (int f = 0; f < FI * FJ; ++f)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const i32x16& v = acc[f / FJ][f % FJ];
+        *sum_at(f, q) = i32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+      }
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  if constexpr (KG > 1) {
+    if (group) return;
+#pragma unroll
+    for (int f = 0; f < FI * FJ; ++f)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const i32x4 v = *sum_at(f, q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[f / FJ][f % FJ][4 * q + e] += v[e];
+      }
+  }
   const int ow = o0 + wj * WO;
 #pragma unroll
   for (int i = 0; i < FI; ++i) {
@@ -460,16 +487,16 @@ static int stream_launch(wr_ctx* ctx, const I8Args& a) {
   return WR_OK;
 }
 
-template <typename TY, bool GLU, int FI, int FJ, int WI, int WJ, int NS, bool LATE>
+template <typename TY, bool GLU, int FI, int FJ, int WI, int WJ, int NS, bool LATE, int KG = 1>
 static int big_launch(wr_ctx* ctx, const I8Args& a) {
   constexpr int TM = 32 * FI * WI, TN = 32 * FJ * WJ, kOuts = GLU ? TN / 2 : TN;
-  constexpr int lds = NS * (TM + TN) * 128;
+  constexpr int lds = KG * NS * (TM + TN) * 128;
   static_assert(lds <= 160 * 1024, "LDS");
   const int outs = GLU ? a.rows / 2 : a.rows;
   const int tt = (a.batch + TM - 1) / TM, to = (outs + kOuts - 1) / kOuts;
-  auto* kernel = matmul_i8_big_kernel<TY, GLU, FI, FJ, WI, WJ, NS, LATE>;
+  auto* kernel = matmul_i8_big_kernel<TY, GLU, FI, FJ, WI, WJ, NS, LATE, KG>;
   if (!lds_limit((const void*)kernel, lds)) return WR_EHIP;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)((tt * to + 7) / 8 * 8)), dim3(64 * WI * WJ), lds, ctx->stream, a, tt, to);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)((tt * to + 7) / 8 * 8)), dim3(64 * WI * WJ * KG), lds, ctx->stream, a, tt, to);
   return WR_OK;
 }
 
@@ -496,8 +523,10 @@ static int matmul_launch(wr_ctx* ctx, const I8Args& a) {
   if (tiles(32, 64) <= cu) return stream_launch<TY, GLU, 2, 4, 4, 2>(ctx, a);
   if (tiles(64, 64) <= cu) return stream_launch<TY, GLU, 4, 4, 4, 2>(ctx, a);
   // From here on shared tiles: a second round of 64 x 64 takes 51 us for 770 tokens 9664 -> 1672, one of 64 x 128 35.
-  if (tiles(128, 64) <= 2 * cu)
-    return big_launch<TY, GLU, 1, 2, 2, 2, 3, false>(ctx, a);
+  // With one workgroup a CU, two groups of waves cut the sum: 512 tokens 9728 -> 2560 26.4 us against 33.7, 512 tokens
+  // 4096 -> 2 x 2048 14.5 against 18.3, 64 tokens 2560 -> 2 x 9728 11.8 against 12.8; with two, one covers the other's waits.
+  if (tiles(128, 64) <= cu) return big_launch<TY, GLU, 1, 2, 2, 2, 3, false, 2>(ctx, a);
+  if (tiles(128, 64) <= 2 * cu) return big_launch<TY, GLU, 1, 2, 2, 2, 3, false>(ctx, a);
   // Shared tiles: the least number of rounds over the CUs times the time of one round, measured in hundredths of that of
   // 256 x 256 (n = 2560: 44 us, 4096: 62): the larger tile wins by the bytes it reads from LDS, the other by
   // a last round that is nearly empty.  8192 tokens 2560 -> 2 x 9728: 497, 461, 436 and 401 us in this order; 16384
