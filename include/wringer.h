@@ -398,7 +398,8 @@ int wr_block_norm(wr_ctx* ctx, int64_t rows, int64_t n, const void* branch, int 
  * dbranch (b_dtype, ld lddb), dresid (r_dtype, ld lddr) and the fp32 dw_post (n), dw_pre (n) and dgate
  * (gate rows x n, contiguous) may each be null; each needs its input.  With rows 0 the sums
  * are written as 0 (dgate if gate_rows is 0).  The sums over tokens are fp32 in a
- * fixed order (deterministic, no atomics).  x' is formed again from branch and resid.  dbranch may be
+ * fixed order (deterministic, no atomics).  x' is formed again from branch and resid; without dy no
+ * gradient depends on it, resid is not read and non-finite values in x' change nothing.  dbranch may be
  * dy or branch, and dresid may be dresid_out or resid, with the same type and leading dimension.
  * Workspace: WR_OP_NORM_BWD (rows, n, gate_rows).
  */

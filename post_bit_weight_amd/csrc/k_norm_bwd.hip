@@ -86,7 +86,8 @@ struct BwdArgs {
   float* dgate;      // gates x n (segs == 0), or null
 };
 
-// One value's share of a row: bn, x' without the residual (along), xn, dres + r2 d (t) and bscale g (cg).
+// One value's share of a row: bn, x' without the residual (along), xn, dres + r2 d (t) and bscale g (cg).  Without dy
+// nothing depends on x': xn is 0 then, and not x' times 0, which an infinity in x' would turn to NaN.
 struct NormTerms {
   float bn, along, xn, t, cg;
   NormTerms() = default;
@@ -95,7 +96,7 @@ struct NormTerms {
     bn = b * ib;
     cg = a.bscale * g;
     along = cg * wp * bn;
-    xn = fmaf(a.rscale, x, along) * ix;
+    xn = a.dy ? fmaf(a.rscale, x, along) * ix : 0.0f;
     t = fmaf(ix, dy * wq, dr);
   }
   // Adds the value's terms to the row's three sums.
@@ -541,7 +542,7 @@ int wr_block_norm_backward_impl(wr_ctx* ctx, int64_t rows, int64_t n, const void
   a.gate = gate;
   a.ldg = ldg;
   a.bscale = branch_scale;
-  a.resid = resid;
+  a.resid = dy ? resid : nullptr;  // read for xn alone
   a.ldr = ldr;
   a.rscale = resid_scale;
   a.w_pre = w_pre;
