@@ -121,11 +121,12 @@ __global__ __launch_bounds__(MAXT) void block_norm_kernel(const NormArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = fmaf(t[e], t[e], ss);
     }
+    // Where resid_out is resid, x' is stored once all waves have read x.  The reduction for the pre norm waits for that; the
+    // one for the post norm waits for b alone, so without a pre norm every wave awaits its loads and meets the others.
+    if (LANES == 0 && !a.w_pre && a.resid_out == a.resid) asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
     // the next row's loads are in flight during the rest of this one
     if (row + walk.step < a.rows) load_row(row + walk.step);
-    // Stored after a reduction, by which the whole row has been read: resid_out may be resid.
     if (a.w_pre) r2 = 1.0f / sqrtf(grp.sum(ss) * inv_n + a.eps);
-    else if (LANES == 0 && !a.w_post) __syncthreads();
     if (a.resid_out)
 #pragma unroll
       for (int k = 0; k < CH; ++k) map.store((TR*)a.resid_out + row * a.ldo, k, v[k]);
