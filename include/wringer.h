@@ -87,7 +87,9 @@ int wr_destroy(wr_ctx* ctx);
 /* Device scratch bytes an operation needs for the given problem size. */
 size_t wr_workspace_bytes(int op, int64_t rows, int64_t n, int32_t group, int32_t rank, int32_t lazy_batch);
 
-/* Register caller-owned device scratch memory (256-byte aligned) for later calls. */
+/* Register caller-owned device scratch memory (256-byte aligned) for later calls.  A call recorded in a HIP graph
+ * keeps the address of the memory registered then: that memory has to live as long as the graph, also where a
+ * larger one is registered later. */
 int wr_set_workspace(wr_ctx* ctx, void* dev_ptr, size_t bytes);
 
 /*

@@ -143,11 +143,20 @@ class Context:
         _check("wr_create", lib.wr_create(ctypes.byref(h), self.device.index or 0, ctypes.c_void_p(self.stream.cuda_stream)))
         self.handle = h
         self.workspace = None
+        self.replaced = []
 
     def ensure_workspace(self, nbytes):
-        if self.workspace is None or self.workspace.numel() < nbytes:
-            self.workspace = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=self.device)
-            _check("wr_set_workspace", load().wr_set_workspace(self.handle, _ptr(self.workspace), self.workspace.numel()))
+        """Registers a workspace of at least nbytes.  A call recorded in a graph keeps the address of the one it was recorded
+        with, so the workspaces that a larger one replaces live as long as the context.  Each is at least half as large
+        again as the one before it, so that those replaced stay below twice the last."""
+        old = 0 if self.workspace is None else self.workspace.numel()
+        if old < nbytes or not old:
+            size = max(int(nbytes), old + old // 2, 256)
+            workspace = torch.empty(size, dtype=torch.uint8, device=self.device)
+            _check("wr_set_workspace", load().wr_set_workspace(self.handle, _ptr(workspace), size))
+            if old:
+                self.replaced.append(self.workspace)
+            self.workspace = workspace
 
     def close(self):
         if self.handle:
