@@ -152,7 +152,8 @@ class Context:
         old = 0 if self.workspace is None else self.workspace.numel()
         if old < nbytes or not old:
             size = max(int(nbytes), old + old // 2, 256)
-            workspace = torch.empty(size, dtype=torch.uint8, device=self.device)
+            with torch.cuda.stream(self.stream):  # the allocator may hand it on in the order of the stream that uses it
+                workspace = torch.empty(size, dtype=torch.uint8, device=self.device)
             _check("wr_set_workspace", load().wr_set_workspace(self.handle, _ptr(workspace), size))
             if old:
                 self.replaced.append(self.workspace)

@@ -28,8 +28,16 @@ class Library:
 @pytest.fixture
 def library(monkeypatch):
     lib = Library()
+    lib.current = []  # the streams made current, the innermost last
+
+    @contextlib.contextmanager
+    def on(stream):
+        lib.current.append(stream)
+        yield
+        lib.current.pop()
+
     monkeypatch.setattr(_lib, "load", lambda: lib)
-    monkeypatch.setattr(torch.cuda, "stream", lambda stream: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "stream", on)
     return lib
 
 
@@ -67,3 +75,14 @@ def test_the_first_workspace_is_what_was_asked_for(library):
     ctx.ensure_workspace(100)
     ctx.ensure_workspace(5000)
     assert [size for _, size in library.registered] == [256, 5000] and ctx.workspace.numel() == 5000
+
+
+def test_a_workspace_belongs_to_the_contexts_stream(library, monkeypatch):
+    """The allocator orders a block's next use after its last one on the stream that was current when it was allocated."""
+    ctx = context()
+    made_on = []
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: made_on.append(library.current[-1:]) or empty(*a, **k))
+    ctx.ensure_workspace(1 << 20)
+    ctx.ensure_workspace(4 << 20)
+    assert made_on == [[ctx.stream], [ctx.stream]]
