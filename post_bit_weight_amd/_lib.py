@@ -132,8 +132,45 @@ def _wdtype(t):
 FLOATS = (torch.float32, torch.bfloat16)
 
 
+class _Behind:
+    """See Context.behind_caller."""
+
+    def __init__(self, stream, caller, tensors):
+        self.stream, self.caller, self.tensors, self.made = stream, caller, tensors, []
+
+    def __enter__(self):
+        self.stream.wait_stream(self.caller)
+        self.current = torch.cuda.stream(self.stream)
+        self.current.__enter__()
+        return self.made
+
+    def __exit__(self, *error):
+        self.current.__exit__(*error)
+        for t in self.tensors:
+            if t is not None:
+                t.record_stream(self.stream)
+        for t in self.made:
+            t.record_stream(self.caller)
+        self.caller.wait_stream(self.stream)
+
+
+class _Same:
+    """Where the caller's stream is the context's: nothing to do."""
+
+    def __enter__(self):
+        return []
+
+    def __exit__(self, *error):
+        pass
+
+
+_SAME = _Same()
+_raw_stream = torch._C._cuda_getCurrentRawStream  # a tenth of a microsecond, torch.cuda.current_stream takes two
+
+
 class Context:
-    """One library context bound to a device and a HIP stream, plus its workspace tensor."""
+    """One library context bound to a device and a HIP stream, plus its workspace tensor.  Calls are queued on that stream, not
+    on torch's current one: where the two differ, the caller orders the tensors' use between them (behind_caller)."""
 
     def __init__(self, device=0, stream=None):
         lib = load()
@@ -144,6 +181,14 @@ class Context:
         self.handle = h
         self.workspace = None
         self.replaced = []
+
+    def behind_caller(self, *tensors):
+        """A block whose work is queued on the context's stream, behind the caller's work so far and before its later work.
+        tensors (or None) come from the caller and are read in the block; what the block allocates and the caller gets is
+        appended to the list that `with` gives.  Where the caller's stream is the context's, nothing is done."""
+        if _raw_stream(self.device.index or 0) == self.stream.cuda_stream:
+            return _SAME
+        return _Behind(self.stream, torch.cuda.current_stream(self.device), tensors)
 
     def ensure_workspace(self, nbytes):
         """Registers a workspace of at least nbytes.  A call recorded in a graph keeps the address of the one it was recorded

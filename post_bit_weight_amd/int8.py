@@ -10,7 +10,8 @@ one scale per output channel, once, and every pass multiplies them with tokens t
     out = qh D^T                                       wr_matmul_i8
 
 ``out`` is the next block's ``branch``: its residual add, gate and post norm happen in that block's norm.  Every step
-runs in libwringer.so; torch only allocates.  Run on synthetic modules of the container's format:
+runs in libwringer.so; torch only allocates.  The context may be on another stream than the caller: each call here is queued
+behind the caller's work so far, and the caller's later work waits for it.  Run on synthetic modules of the container's format:
 python -m post_bit_weight_amd.int8 [--tokens 64] [--hidden 2560] [--inner 9728]
 """
 
@@ -30,9 +31,11 @@ class Int8Linear:
 
     def __init__(self, ctx, weights):
         rows, n = weights.shape
-        self.codes = torch.empty(rows, n + -n % 16, dtype=torch.int8, device=weights.device)[:, :n]
-        self.scales = torch.empty(rows, dtype=torch.float32, device=weights.device)
-        wr.wr_quant_rows_i8(ctx, weights, self.codes, self.scales)
+        with ctx.behind_caller(weights) as made:
+            self.codes = torch.empty(rows, n + -n % 16, dtype=torch.int8, device=weights.device)[:, :n]
+            self.scales = torch.empty(rows, dtype=torch.float32, device=weights.device)
+            made += [self.codes, self.scales]
+            wr.wr_quant_rows_i8(ctx, weights, self.codes, self.scales)
 
     @classmethod
     def from_packed(cls, ctx, modules):
@@ -41,13 +44,16 @@ class Int8Linear:
         n = modules[0]["n_out"]
         if any(m["n_out"] != n for m in modules):
             raise ValueError("the modules must have one n_out")
-        weights = torch.empty(sum(m["rows"] for m in modules), n, dtype=torch.bfloat16, device=ctx.device)
-        row = 0
-        for m in modules:
-            wr.wr_materialize(ctx, m["buf"], m["rows"], m["n_store"], m["bits"], m["group"], weights[row:row + m["rows"]],
-                              m.get("had_block", 0), m.get("signs"))
-            row += m["rows"]
-        return cls(ctx, weights)
+        with ctx.behind_caller(*[m.get(k) for m in modules for k in ("buf", "signs")]) as made:
+            weights = torch.empty(sum(m["rows"] for m in modules), n, dtype=torch.bfloat16, device=ctx.device)
+            row = 0
+            for m in modules:
+                wr.wr_materialize(ctx, m["buf"], m["rows"], m["n_store"], m["bits"], m["group"], weights[row:row + m["rows"]],
+                                  m.get("had_block", 0), m.get("signs"))
+                row += m["rows"]
+            layer = cls(ctx, weights)
+            made += [layer.codes, layer.scales]
+        return layer
 
 
 class Tokens:
@@ -72,34 +78,40 @@ class Int8Mlp:
         if self.gate_up.codes.shape[0] != 2 * inner or self.down.codes.shape[0] != n:
             raise ValueError("gate_up must be 2 h x n and down n x h")
         self.most = most_tokens
-        self.tokens, self.inner = Tokens(most_tokens, n, ctx.device), Tokens(most_tokens, inner, ctx.device)
-        self.hidden = torch.empty(most_tokens, inner, dtype=torch.bfloat16, device=ctx.device)
+        with ctx.behind_caller(w_pre, w_post, gate, gate_up.codes, gate_up.scales, down.codes, down.scales):
+            self.tokens, self.inner = Tokens(most_tokens, n, ctx.device), Tokens(most_tokens, inner, ctx.device)
+            self.hidden = torch.empty(most_tokens, inner, dtype=torch.bfloat16, device=ctx.device)
 
     def __call__(self, resid, branch):
         """(x', the block's output) for tokens x n of the residual stream and the branch that is added to it."""
         rows = branch.shape[0]
         if rows > self.most:
             raise ValueError(f"{rows} tokens, but space for {self.most}")
-        out = torch.empty_like(branch, memory_format=torch.contiguous_format)
-        resid_out = torch.empty_like(resid, memory_format=torch.contiguous_format)
-        q, scales = self.tokens.of(rows)
-        wr.wr_block_norm(self.ctx, self.eps, branch=branch, resid=resid, w_post=self.w_post, gate=self.gate,
-                         w_pre=self.w_pre, resid_out=resid_out, q=q, q_scales=scales)
-        hidden = self.hidden[:rows]
-        wr.wr_matmul_i8(self.ctx, q, scales, self.gate_up.codes, self.gate_up.scales, hidden, swiglu=True)
-        qh, hscales = self.inner.of(rows)
-        wr.wr_quant_rows_i8(self.ctx, hidden, qh, hscales)
-        wr.wr_matmul_i8(self.ctx, qh, hscales, self.down.codes, self.down.scales, out)
+        with self.ctx.behind_caller(resid, branch) as made:
+            out = torch.empty_like(branch, memory_format=torch.contiguous_format)
+            resid_out = torch.empty_like(resid, memory_format=torch.contiguous_format)
+            q, scales = self.tokens.of(rows)
+            wr.wr_block_norm(self.ctx, self.eps, branch=branch, resid=resid, w_post=self.w_post, gate=self.gate,
+                             w_pre=self.w_pre, resid_out=resid_out, q=q, q_scales=scales)
+            hidden = self.hidden[:rows]
+            wr.wr_matmul_i8(self.ctx, q, scales, self.gate_up.codes, self.gate_up.scales, hidden, swiglu=True)
+            qh, hscales = self.inner.of(rows)
+            wr.wr_quant_rows_i8(self.ctx, hidden, qh, hscales)
+            wr.wr_matmul_i8(self.ctx, qh, hscales, self.down.codes, self.down.scales, out)
+            made += [resid_out, out]
         return resid_out, out
 
 
 def synthetic_module(ctx, rows, n, bits, group, seed):
     """A packed module of random codes whose weights have a standard deviation near 0.02."""
-    g = torch.Generator(device=ctx.device).manual_seed(seed)
-    codes = torch.randint(0, 1 << bits, (rows, n), dtype=torch.uint8, device=ctx.device, generator=g)
-    spread = 0.02 / (((1 << (2 * bits)) - 1) / 3.0) ** 0.5
-    scales = ((0.75 + 0.5 * torch.rand(rows, n // group, device=ctx.device, generator=g)) * spread).to(torch.float16)
-    return dict(buf=pipeline.pack(ctx, codes, scales, bits, group), rows=rows, n_store=n, bits=bits, group=group, n_out=n)
+    with ctx.behind_caller() as made:
+        g = torch.Generator(device=ctx.device).manual_seed(seed)
+        codes = torch.randint(0, 1 << bits, (rows, n), dtype=torch.uint8, device=ctx.device, generator=g)
+        spread = 0.02 / (((1 << (2 * bits)) - 1) / 3.0) ** 0.5
+        scales = ((0.75 + 0.5 * torch.rand(rows, n // group, device=ctx.device, generator=g)) * spread).to(torch.float16)
+        buf = pipeline.pack(ctx, codes, scales, bits, group)
+        made.append(buf)
+    return dict(buf=buf, rows=rows, n_store=n, bits=bits, group=group, n_out=n)
 
 
 def main(argv=None):

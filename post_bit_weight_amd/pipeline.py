@@ -5,7 +5,9 @@ H accumulation and damping -> optional Hadamard rotation -> GPTQ codes and
 scales -> joint scales against the weights -> wring against
 W_hat + (alpha / r) B A (nearest-point codes, joint scales) -> packing.
 Every step runs in libwringer.so; torch only allocates device memory and pads
-the weights into the stored (rotated) dimension.
+the weights into the stored (rotated) dimension.  Tensors are allocated on
+torch's current stream: with a context on another one, call these inside
+``with torch.cuda.stream(ctx.stream)``.
 """
 
 import torch

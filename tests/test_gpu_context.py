@@ -54,3 +54,46 @@ def test_a_recorded_graph_keeps_its_workspace(wr):
             stream.synchronize()
             assert all(torch.equal(eager[name], replayed[name]) for name in eager)
             assert all(bool((t == 77).all()) for t in others)
+
+
+def test_mlp_on_a_stream_of_its_own(wr):
+    """Modules loaded, run and dropped from the caller's stream with the context on another: the bits of a context on the
+    caller's, while the caller's stream keeps allocating."""
+    from post_bit_weight_amd import int8
+
+    def run(ctx):
+        mods = [int8.synthetic_module(ctx, r, k, b, 64, s) for r, k, b, s in ((4096, 1024, 2, 1), (4096, 1024, 2, 2), (1024, 4096, 3, 3))]
+        up, down = int8.Int8Linear.from_packed(ctx, mods[:2]), int8.Int8Linear.from_packed(ctx, mods[2:])
+        del mods
+        noise = [torch.full((8192, 1024), 3.0, device="cuda").to(BF16) for _ in range(4)]  # the size of dropped weights
+        g = torch.Generator(device="cuda").manual_seed(6)
+        w = (1 + 0.1 * torch.randn(1024, generator=g, device="cuda")).to(BF16)
+        mlp = int8.Int8Mlp(ctx, up, down, w, w.clone(), most_tokens=600)
+        outs = []
+        for _ in range(5):
+            resid, branch = (torch.randn(600, 1024, generator=g, device="cuda").to(BF16) for _ in range(2))
+            outs += [t.float().sum(1) for t in mlp(resid, branch)]
+            del resid, branch
+            noise.append(torch.full((600, 1024), 5.0, device="cuda").to(BF16))
+        torch.cuda.synchronize()
+        return up.codes.clone(), up.scales.clone(), *outs
+
+    here = run(wr.Context(0))
+    apart = run(wr.Context(0, torch.cuda.Stream()))
+    assert all(torch.equal(a, b) for a, b in zip(here, apart))
+
+
+def test_workspace_that_grows_on_a_stream_of_its_own(wr):
+    """Gradients of more and more tokens are right while the caller's stream allocates what the workspaces leave."""
+    stream = torch.cuda.Stream()
+    here, apart = wr.Context(0), wr.Context(0, stream)
+    for rows, n in ((40, 640), (300, 2560), (2000, 5120)):
+        inp, up, stats = gradient_inputs(rows, n, 7, rows)
+        a, b = gradient_outputs(inp), gradient_outputs(inp)
+        wr.wr_block_norm_backward(here, stats, **inp, **up, **a)
+        with apart.behind_caller(stats, *up.values(), *(t for t in inp.values() if torch.is_tensor(t))) as made:
+            wr.wr_block_norm_backward(apart, stats, **inp, **up, **b)
+            made += b.values()
+        noise = [torch.full((here.workspace.numel() // 4,), 7.0, device="cuda") for _ in range(3)]
+        assert all(torch.equal(a[k], b[k]) for k in a)
+        assert all(bool((t == 7).all()) for t in noise)
