@@ -471,9 +471,6 @@ __global__ __launch_bounds__(64 * WI * WJ * KG, 1) void matmul_i8_big_kernel(con
 
 using namespace wr;
 
-template <int N>
-using Int = std::integral_constant<int, N>;
-
 template <typename TY, bool GLU, int RF, int NT, int NW, int NS>
 static int stream_launch(wr_ctx* ctx, const I8Args& a) {
   constexpr int OF = GLU ? RF / 2 : RF;
