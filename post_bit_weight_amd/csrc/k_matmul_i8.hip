@@ -244,9 +244,10 @@ __global__ __launch_bounds__(64 * NW) void matmul_i8_stream_kernel(const I8Args 
 // of row r lies at chunk c ^ swizzle(r), without which half of the LDS cycles were bank conflicts.  KG such groups of
 // waves, each with a ring of its own, take every KG-th slice of the same tile; their sums meet in LDS at the end.
 //
-// Bound by the matrix cores, half busy at the 1.9 GHz that they leave: 16384 tokens 4096 -> 2560 160 us (2149 TOPS; a
-// library's product without scales 160 us), 8192 tokens 2560 -> 2 x 9728 with SwiGLU 401 us (2034 TOPS; product alone
-// 404 us).  Short sums are bound by the outputs: 8192 tokens 256 -> 4096 25 us, 2.7 TB/s.  Slower: copies issued
+// 16384 tokens 4096 -> 2560 take 149 us (2309 TOPS), 8192 tokens 2560 -> 2 x 9728 with SwiGLU 374 us (2184 TOPS), timed in
+// turn with a library's product of the same sizes without scales (168 and 414 us).  By the counters no unit is full: the matrix cores
+// are busy for 53 % of the cycles (at 1.9 GHz), LDS reads for 25 %, HBM gives 1.4 to 1.8 TB/s; the waves, two a SIMD, wait for 35 %
+// of theirs.  Short sums are bound by the outputs: 8192 tokens 256 -> 4096 25 us, 2.7 TB/s.  Slower: copies issued
 // between the MFMAs, five slots of 64 bytes, eight waves for 128 x 128, raised wave priority.
 template <typename TY, bool GLU, int FI, int FJ, int WI, int WJ, int NS, bool LATE, int KG>
 __global__ __launch_bounds__(64 * WI * WJ * KG, 1) void matmul_i8_big_kernel(const I8Args a, int tiles_t, int tiles_o) {

