@@ -69,12 +69,16 @@ enum wr_op {             /* operations that need workspace, for wr_workspace_byt
   WR_OP_TRELLIS = 6,     /* rows, n, group = number of trellis states: wr_trellis_quantize */
   WR_OP_GEMV = 7,        /* rows = number of input vectors, n = n_store: wr_packed_gemv */
   WR_OP_STATS = 8,       /* rows: wr_quant_stats */
-  WR_OP_NORM_BWD = 9     /* rows, n, group = gate_rows (0 when at least rows): wr_block_norm_backward */
+  WR_OP_NORM_BWD = 9,    /* rows, n, group = gate_rows (0 when at least rows): wr_block_norm_backward */
+  WR_OP_KV_ATTENTION = 10, /* rows = rows of q, n = query heads * head dim, group = head dim: wr_kv_attention */
+  WR_OP_ADAPTERS = 11    /* rows, n = most of the inputs and outputs, rank: wr_adapters */
 };
 
 enum wr_hessian_flags { WR_H_ZERO = 1 };               /* zero S before accumulating */
 enum wr_rotate_mode { WR_ROT_ROWS = 0, WR_ROT_ROWS_INVERSE = 1, WR_ROT_SYM = 2 };
 enum wr_i8_flags { WR_I8_SWIGLU = 1 };                 /* silu(first half of the rows) * second half */
+enum wr_rotary_flags { WR_ROTARY_INTERLEAVED = 1, WR_ROTARY_INVERSE = 2 };
+enum wr_attention_flags { WR_ATTENTION_CAUSAL = 1 };
 enum wr_wring_flags { WR_RECODE_NEAREST = 1, WR_RECODE_GPTQ = 2, WR_RECODE_SEARCH = 4 };
 
 typedef struct wr_ctx wr_ctx;
@@ -411,6 +415,113 @@ int wr_block_norm_backward(wr_ctx* ctx, int64_t rows, int64_t n, const void* bra
                            int w_dtype, const float* stats, const void* dy, int64_t lddy, const void* dresid_out,
                            int64_t lddo, void* dbranch, int64_t lddb, void* dresid, int64_t lddr, float* dw_post,
                            float* dgate, float* dw_pre);
+
+/*
+ * (i) The attention half of a block: rotary positions, a paged cache of keys and values in 4 bits,
+ * attention over it, and low-rank adapters of many requests beside the shared projections.
+ *
+ * wr_rotary: every head of every row turns by its position.  x: rows x (heads * dim), `dtype`, ld ldx.
+ * Pair i (0 <= i < pairs, 2 pairs <= dim) of a head is (x[i], x[pairs + i]), or (x[2 i], x[2 i + 1])
+ * with WR_ROTARY_INTERLEAVED; with the angle a = positions[axis_of[i]][row] * freqs[i] it becomes
+ *   (x0 cos a - x1 sin a, x0 sin a + x1 cos a),
+ * or with WR_ROTARY_INVERSE the same with -a, which is also the gradient of the forward form.
+ * Values behind the pairs are copied.  positions: axes x rows int32 (row stride ldp); axis_of: pairs int32,
+ * or null when axes is 1; a pair whose axis is outside 0 .. axes - 1 is copied.  freqs: pairs fp64,
+ * in radians per position.  Angles are formed and reduced in fp64, everything else is fp32, and y (as x, ld
+ * ldy) is rounded once.  y may be x with the same ld; other overlaps are not allowed.  pairs may be 0; dim <= 1024
+ * and axes <= 8 (WR_EUNSUPPORTED above); rows may be 0.  Any alignment to the type.  No workspace.
+ */
+int wr_rotary(wr_ctx* ctx, const void* x, int dtype, int64_t rows, int32_t heads, int32_t dim, int64_t ldx,
+              int32_t pairs, const int32_t* positions, int32_t axes, int64_t ldp, const int32_t* axis_of,
+              const double* freqs, int flags, void* y, int64_t ldy);
+
+/*
+ * The cache: `count` pages, each with the keys and values of `page_tokens` consecutive positions of one
+ * sequence, `heads` heads of `dim` values.  `group` values of a head of a token share a scale and an offset,
+ * both fp16.  dim is 64, 128 or 256; group 32, 64 or 128 and divides dim; page_tokens 16, 32, 64, 128
+ * or 256.  pages: 16-byte aligned device memory of count * wr_kv_page_bytes(heads, dim, page_tokens, group)
+ * bytes, which need not be cleared.  In a page, for each head one after the other:
+ *   keys' codes     page_tokens x dim / 2 bytes; a token's dword s of part g (bytes g dim / 8 + 4 s) holds
+ *                   dims 32 s + 8 g + n in its bits 4 n .. 4 n + 3
+ *   values' codes   for every 16 tokens 8 dim bytes: byte ((g * 16 + l) * dim / 32 + m) * 4 + i holds token
+ *                   4 g + i of the 16, dim 16 m + l in its low and dim / 2 + 16 m + l in its high half
+ *   keys' groups    dim / group x page_tokens pairs of fp16: scale, offset
+ *   values' groups  the same.
+ * The first operand of a matrix product is read from it in whole 16-byte loads, and no byte holds values of two
+ * tokens: rows that are written at the same time never share one.
+ */
+typedef struct {
+  void* pages;
+  int64_t count;
+  int32_t heads, dim, page_tokens, group;
+} wr_kv_cache;
+
+/*
+ * The sequences of a call.  Sequence i owns rows starts[i] .. starts[i + 1] - 1 of the call's row matrices (new_i
+ * of them), which are its last positions: its row j is position lengths[i] - new_i + j.  Position p lives in
+ * page table[i * ldt + p / page_tokens].  starts (n + 1), lengths (n) and table (n x width) are int32 device
+ * memory that the kernels read; most_new and most_tokens are what the host knows of them.
+ * A sequence is left out - nothing of it is read or written - unless 0 <= starts[i] <= starts[i + 1] <= rows,
+ * new_i <= most_new and 0 <= lengths[i] <= min(most_tokens, width * page_tokens).  A position below 0
+ * (new_i > lengths[i]), and one in a page outside 0 .. count - 1, is absent.
+ */
+typedef struct {
+  const int32_t* starts;
+  const int32_t* lengths;
+  const int32_t* table;
+  int64_t ldt;
+  int32_t n, width, most_new, most_tokens;
+} wr_kv_seqs;
+
+/* Bytes of a page, 0 for a form of the cache that the library does not have. */
+size_t wr_kv_page_bytes(int32_t heads, int32_t dim, int32_t page_tokens, int32_t group);
+
+/*
+ * wr_kv_write: the sequences' rows of k and v (rows x heads * dim, `dtype`, ld ldk and ldv) go into the cache.  For
+ * each group x of a head of a token, with values saturated at +-65024 and f16() to nearest:
+ *   offset = f16(min x)     scale = f16((max x - offset) / 15)     code = rint((x - offset) / scale) in 0 .. 15,
+ * every difference and quotient a correctly rounded fp32 one, ties of rint to even, code 0 where scale is 0; it
+ * stands for offset + scale * code.  A group that holds an infinity or a NaN gets scale and offset NaN and
+ * codes 0.  Rows of absent positions are not written.  k or v may be null.  Where sequences share a page, at most
+ * one of them writes to a position.  Any alignment to the type.  No workspace.
+ */
+int wr_kv_write(wr_ctx* ctx, const wr_kv_cache* cache, const wr_kv_seqs* seqs, const void* k, int64_t ldk, const void* v,
+                int64_t ldv, int dtype, int64_t rows);
+
+/* wr_kv_read: the mirror of wr_kv_write: rows of k and v (either may be null) become what the cache holds, offset +
+ * scale * code, rounded once to `dtype`; 0 at absent positions. */
+int wr_kv_read(wr_ctx* ctx, const wr_kv_cache* cache, const wr_kv_seqs* seqs, void* k, int64_t ldk, void* v, int64_t ldv,
+               int dtype, int64_t rows);
+
+/*
+ * wr_kv_attention: out = softmax(scale * q k^T) v.  q and out: rows x heads * dim bf16 (ld ldq, ldo); query
+ * head h reads head h / (heads / cache heads) of the cache; heads is a multiple of the cache's, up to 64 times.  Row j
+ * of sequence i, at position p = lengths[i] - new_i + j, sees positions 0 .. lengths[i] - 1, with
+ * WR_ATTENTION_CAUSAL only those up to p, and with window > 0 only those above p - window (and, without
+ * the flag, below p + window).  Absent positions are not seen, whatever the cache holds.  A row that sees nothing, or
+ * whose scores are all -infinity, becomes 0.  scale is finite.  Sums, scores and the softmax are fp32; the matrix
+ * cores take the cache's values and the weights rounded to fp16 (2^-11 relative).  Outputs of left-out sequences and of no sequence stay as they were.
+ * out may not overlap q.  Workspace: WR_OP_KV_ATTENTION (rows, heads * dim, dim).
+ */
+int wr_kv_attention(wr_ctx* ctx, const wr_kv_cache* cache, const wr_kv_seqs* seqs, const void* q, int64_t ldq,
+                    int64_t rows, int32_t heads, float scale, int flags, int32_t window, void* out, int64_t ldo);
+
+/*
+ * wr_adapters: y = base + scales[a] * B_a (A_a x) for rows of n_seqs requests, each with an adapter of its own.  Request i
+ * owns rows starts[i] .. starts[i + 1] - 1 and uses adapter a = ids[i]; outside 0 .. adapters - 1 it uses none
+ * (y = base).  x: rows x n (x_dtype, ld ldx); A: adapters x rank x n bf16, B: adapters x outs x rank bf16, both
+ * contiguous; scales: adapters fp32 (alpha / rank); ranks: adapters int32, or null: adapter a has ranks[a] <= rank
+ * rows of A and columns of B, the others are not read (a value outside 0 .. rank counts as the nearest of these).  base
+ * and y: rows x outs (y_dtype, ld ldb and ldy); base may be null (0) or y itself with the same ld, y overlaps
+ * nothing else.  A request is left out, its rows of y unchanged, unless 0 <= starts[i] <= starts[i + 1] <= rows and it has at
+ * most `most` rows; rows of no request are unchanged as well.  A x is kept in fp32 and multiplied with B
+ * in three bf16 parts, x in fp32 likewise: products are exact, sums fp32, y is rounded once.  rank <= 256
+ * (WR_EUNSUPPORTED above); n >= 1.  Any alignment to the type.  Workspace: WR_OP_ADAPTERS (rows, max(n, outs), rank).
+ */
+int wr_adapters(wr_ctx* ctx, const void* x, int x_dtype, int64_t rows, int64_t n, int64_t ldx, const void* A, const void* B,
+                int32_t adapters, int32_t rank, int64_t outs, const float* scales, const int32_t* ranks,
+                const int32_t* starts, const int32_t* ids, int32_t n_seqs, int64_t most, const void* base, int64_t ldb,
+                void* y, int y_dtype, int64_t ldy);
 
 /* Static description of a status code. */
 const char* wr_strerror(int status);

@@ -43,6 +43,7 @@ from .materialize import bf16_rne_bits, bf16_bits_to_f64, materialize, materiali
 from .trellis import viterbi as trellis_viterbi, greedy as trellis_greedy, decode as trellis_decode
 from .gemv import packed_gemv
 from .block import block_norm, block_norm_backward, gate_per_token, quant_rows_i8, matmul_i8
+from .attention import rotary, kv_codes, kv_values, kv_page, attend, sees, adapters
 
 __all__ = [
     "second_moment", "second_moment_chunks", "sum_of_products", "pad_square", "damp",
@@ -59,4 +60,5 @@ __all__ = [
     "trellis_viterbi", "trellis_greedy", "trellis_decode",
     "packed_gemv",
     "block_norm", "block_norm_backward", "gate_per_token", "quant_rows_i8", "matmul_i8",
+    "rotary", "kv_codes", "kv_values", "kv_page", "attend", "sees", "adapters",
 ]

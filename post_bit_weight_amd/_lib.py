@@ -18,10 +18,12 @@ WR_OK, WR_EINVAL, WR_EWORKSPACE, WR_EHIP, WR_EUNSUPPORTED, WR_ESCRATCH = 0, 1, 2
 WR_STATIC_SCRATCH_BYTES = 64 << 20
 WR_F32, WR_BF16 = 0, 1
 (WR_OP_HESSIAN, WR_OP_GPTQ, WR_OP_WRING, WR_OP_ROTATE, WR_OP_FINALIZE, WR_OP_WRING_GPTQ, WR_OP_TRELLIS,
- WR_OP_GEMV, WR_OP_STATS, WR_OP_NORM_BWD) = range(10)
+ WR_OP_GEMV, WR_OP_STATS, WR_OP_NORM_BWD, WR_OP_KV_ATTENTION, WR_OP_ADAPTERS) = range(12)
 WR_H_ZERO = 1
 WR_ROT_ROWS, WR_ROT_ROWS_INVERSE, WR_ROT_SYM = 0, 1, 2
 WR_I8_SWIGLU = 1
+WR_ROTARY_INTERLEAVED, WR_ROTARY_INVERSE = 1, 2
+WR_ATTENTION_CAUSAL = 1
 WR_RECODE_NEAREST = 1
 WR_RECODE_GPTQ = 2
 WR_RECODE_SEARCH = 4
@@ -31,7 +33,8 @@ EXPORTED = (
     "wr_hessian_accumulate", "wr_hessian_accumulate_noalloc", "wr_hessian_finalize", "wr_hadamard_rotate",
     "wr_gptq_sweep", "wr_wring_solve", "wr_pack", "wr_unpack", "wr_materialize", "wr_trellis_quantize",
     "wr_packed_gemv", "wr_set_scale_trace", "wr_wring_target", "wr_quant_stats",
-    "wr_quant_rows_i8", "wr_matmul_i8", "wr_block_norm", "wr_block_norm_backward", "wr_strerror",
+    "wr_quant_rows_i8", "wr_matmul_i8", "wr_block_norm", "wr_block_norm_backward", "wr_rotary", "wr_kv_page_bytes",
+    "wr_kv_write", "wr_kv_read", "wr_kv_attention", "wr_adapters", "wr_strerror",
 )
 
 
@@ -84,6 +87,13 @@ def load():
                               P, P]),
         "wr_block_norm_backward": (I, [P, I64, I64, P, I, I64, P, P, I64, I64, F, P, I, I64, F, P, I, P, P, I64, P, I64,
                                        P, I64, P, I64, P, P, P]),
+        "wr_rotary": (I, [P, P, I, I64, c.c_int32, c.c_int32, I64, c.c_int32, P, c.c_int32, I64, P, P, I, P, I64]),
+        "wr_kv_page_bytes": (SZ, [c.c_int32] * 4),
+        "wr_kv_write": (I, [P, P, P, P, I64, P, I64, I, I64]),
+        "wr_kv_read": (I, [P, P, P, P, I64, P, I64, I, I64]),
+        "wr_kv_attention": (I, [P, P, P, P, I64, I64, c.c_int32, F, I, c.c_int32, P, I64]),
+        "wr_adapters": (I, [P, P, I, I64, I64, I64, P, P, c.c_int32, c.c_int32, I64, P, P, P, P, c.c_int32, I64, P, I64, P, I,
+                            I64]),
         "wr_strerror": (c.c_char_p, [I]),
     }
     for name, (res, args) in sig.items():
@@ -635,3 +645,155 @@ def wr_block_norm_backward(ctx, stats, branch=None, resid=None, w_post=None, gat
         status = load().wr_block_norm_backward(*args)
     if status:
         _check("wr_block_norm_backward", status)
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("count", ctypes.c_int64), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("group", ctypes.c_int32)]
+
+
+class _KvSeqs(ctypes.Structure):
+    _fields_ = [("starts", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("table", ctypes.c_void_p), ("ldt", ctypes.c_int64),
+                ("n", ctypes.c_int32), ("width", ctypes.c_int32), ("most_new", ctypes.c_int32), ("most_tokens", ctypes.c_int32)]
+
+
+class KvCache:
+    """A paged cache of keys and values in 4 bits: `pages` pages of page_tokens positions for `heads` heads of `dim` values
+    (64, 128 or 256), with a scale and an offset for each `group` values.  buf (uint8) holds the pages; it may be given."""
+
+    def __init__(self, pages, heads, dim, page_tokens=64, group=64, device="cuda", buf=None):
+        self.pages, self.heads, self.dim, self.page_tokens, self.group = pages, heads, dim, page_tokens, group
+        self.page_bytes = int(load().wr_kv_page_bytes(heads, dim, page_tokens, group))
+        if not self.page_bytes:
+            raise WringerError("wr_kv_page_bytes", WR_EUNSUPPORTED)
+        if buf is None:
+            buf = torch.empty(pages * self.page_bytes, dtype=torch.uint8, device=device)
+        _dev(buf, "buf", (torch.uint8,))
+        if buf.numel() != pages * self.page_bytes or not buf.is_contiguous():
+            raise ValueError(f"buf must hold {pages * self.page_bytes} contiguous bytes")
+        self.buf, self.width = buf, heads * dim
+        self.c = _KvCache(buf.data_ptr(), pages, heads, dim, page_tokens, group)
+        self.ref = ctypes.addressof(self.c)
+
+
+class Sequences:
+    """The sequences of calls on a cache: int32 GPU tensors starts (n + 1: the first row of each), lengths (n: positions with
+    the new rows) and table (n x width: the page of every page_tokens positions), and what the host knows of them: the most
+    new rows and the most positions of any.  The tensors' values may change between calls, in place."""
+
+    def __init__(self, starts, lengths, table, most_new, most_tokens):
+        for t, name in ((starts, "starts"), (lengths, "lengths"), (table, "table")):
+            _dev(t, name, (torch.int32,))
+        n = lengths.numel()
+        if starts.numel() != n + 1 or not starts.is_contiguous() or not lengths.is_contiguous():
+            raise ValueError("starts must hold one contiguous value more than lengths")
+        if table.dim() != 2 or table.shape[0] != n:
+            raise ValueError("table must have a row for each sequence")
+        if table.shape[1] > 1 and table.stride(1) != 1:
+            raise ValueError("table must be row-major")
+        if most_new < 0 or most_tokens < 0:
+            raise ValueError("most_new and most_tokens must not be negative")
+        self.starts, self.lengths, self.table = starts, lengths, table
+        self.most_new, self.most_tokens = int(most_new), int(most_tokens)
+        self.c = _KvSeqs(starts.data_ptr(), lengths.data_ptr(), table.data_ptr(), table.stride(0), n, table.shape[1],
+                         min(self.most_new, 2147483647), min(self.most_tokens, 2147483647))
+        self.ref = ctypes.addressof(self.c)
+
+
+def wr_rotary(ctx, x, y, positions, freqs, head_dim, axis_of=None, interleaved=False, inverse=False):
+    """y = x (rows x heads * head_dim, bf16 or fp32) with every pair i of every head turned by positions[axis_of[i]] *
+    freqs[i], back with inverse.  positions: int32, rows or axes x rows; freqs: fp64, one for each pair; axis_of: int32, None
+    for one axis.  Pairs are (i, pairs + i) or, interleaved, (2 i, 2 i + 1).  y may be x."""
+    shape = x.shape
+    if len(shape) != 2 or head_dim <= 0 or shape[1] % head_dim or not shape[1]:
+        raise ValueError("x must be rows x heads * head_dim")
+    rows, n = shape
+    code = _type_code(x, "x")
+    px, ldx = _matrix(x, "x", x.dtype, shape)
+    py, ldy = _matrix(y, "y", x.dtype, shape)
+    pairs = freqs.numel()
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    pp, ldp = _matrix(positions if positions.dim() == 2 else positions.unsqueeze(0), "positions", torch.int32, (axes, rows))
+    status = load().wr_rotary(
+        ctx.handle, px, code, rows, n // head_dim, head_dim, ldx, pairs, pp, axes, ldp,
+        None if axis_of is None else _vector(axis_of, "axis_of", torch.int32, pairs),
+        _vector(freqs, "freqs", torch.float64, pairs),
+        (WR_ROTARY_INTERLEAVED if interleaved else 0) | (WR_ROTARY_INVERSE if inverse else 0), py, ldy)
+    if status:
+        _check("wr_rotary", status)
+
+
+def _kv_rows(cache, k, v):
+    """(rows, type code, address and row stride of k and of v); either may be None."""
+    some = k if k is not None else v
+    if some is None:
+        raise ValueError("k or v must be given")
+    shape = (some.shape[0], cache.width)
+    code = _type_code(some, "k" if k is not None else "v")
+    pk, ldk = (None, cache.width) if k is None else _matrix(k, "k", some.dtype, shape)
+    pv, ldv = (None, cache.width) if v is None else _matrix(v, "v", some.dtype, shape)
+    return shape[0], code, pk, ldk, pv, ldv
+
+
+def wr_kv_write(ctx, cache, seqs, k, v):
+    """Puts the sequences' rows of k and v (rows x heads * dim, bf16 or fp32; either may be None) into the cache."""
+    rows, code, pk, ldk, pv, ldv = _kv_rows(cache, k, v)
+    status = load().wr_kv_write(ctx.handle, cache.ref, seqs.ref, pk, ldk, pv, ldv, code, rows)
+    if status:
+        _check("wr_kv_write", status)
+
+
+def wr_kv_read(ctx, cache, seqs, k, v):
+    """Fills the sequences' rows of k and v (either may be None) with what the cache holds."""
+    rows, code, pk, ldk, pv, ldv = _kv_rows(cache, k, v)
+    status = load().wr_kv_read(ctx.handle, cache.ref, seqs.ref, pk, ldk, pv, ldv, code, rows)
+    if status:
+        _check("wr_kv_read", status)
+
+
+def wr_kv_attention(ctx, cache, seqs, q, out, scale, causal=True, window=0):
+    """out = softmax(scale * q k^T) v for the sequences' rows of q (rows x heads * dim, bf16) over the cache."""
+    shape = q.shape
+    if len(shape) != 2 or shape[1] % cache.dim or not shape[1]:
+        raise ValueError("q must be rows x heads * dim")
+    rows, n = shape
+    pq, ldq = _matrix(q, "q", torch.bfloat16, shape)
+    po, ldo = _matrix(out, "out", torch.bfloat16, shape)
+    args = (ctx.handle, cache.ref, seqs.ref, pq, ldq, rows, n // cache.dim, scale, WR_ATTENTION_CAUSAL if causal else 0, window,
+            po, ldo)
+    status = load().wr_kv_attention(*args)
+    if status == WR_EWORKSPACE:  # refused before any launch: register what it needs and call again
+        ctx.ensure_workspace(wr_workspace_bytes(WR_OP_KV_ATTENTION, rows, n, cache.dim))
+        status = load().wr_kv_attention(*args)
+    if status:
+        _check("wr_kv_attention", status)
+
+
+def wr_adapters(ctx, x, A, B, scales, starts, ids, most, y, base=None, ranks=None):
+    """y = base + scales[a] * B_a (A_a x) for the rows starts[i] .. starts[i + 1] - 1 (at most `most` of them) of request i with
+    adapter a = ids[i], or base (0 where it is None) for an id outside the adapters.  A: adapters x rank x n and B: adapters x
+    outs x rank, bf16, contiguous; scales: fp32; ranks: int32 or None; starts, ids: int32.  y may be base."""
+    xshape, ashape, bshape = x.shape, A.shape, B.shape
+    if len(xshape) != 2 or len(ashape) != 3 or len(bshape) != 3 or ashape[2] != xshape[1]:
+        raise ValueError("x must be rows x n, A adapters x rank x n, B adapters x outs x rank")
+    rows, n = xshape
+    adapters, rank = ashape[:2]
+    if bshape[0] != adapters or bshape[2] != rank:
+        raise ValueError("A must be adapters x rank x n and B adapters x outs x rank")
+    outs, seqs = bshape[1], ids.numel()
+    xcode, ycode = _type_code(x, "x"), _type_code(y, "y")
+    px, ldx = _matrix(x, "x", x.dtype, xshape)
+    py, ldy = _matrix(y, "y", y.dtype, (rows, outs))
+    pb, ldb = (None, outs) if base is None else _matrix(base, "base", y.dtype, (rows, outs))
+    args = (ctx.handle, px, xcode, rows, n, ldx, _vector(A, "A", torch.bfloat16, adapters * rank * n),
+            _vector(B, "B", torch.bfloat16, adapters * outs * rank), adapters, rank, outs,
+            _vector(scales, "scales", torch.float32, adapters),
+            None if ranks is None else _vector(ranks, "ranks", torch.int32, adapters),
+            _vector(starts, "starts", torch.int32, seqs + 1), _vector(ids, "ids", torch.int32, seqs), seqs, most, pb, ldb, py,
+            ycode, ldy)
+    status = load().wr_adapters(*args)
+    if status == WR_EWORKSPACE:
+        ctx.ensure_workspace(wr_workspace_bytes(WR_OP_ADAPTERS, rows, max(n, outs), 0, rank))
+        status = load().wr_adapters(*args)
+    if status:
+        _check("wr_adapters", status)

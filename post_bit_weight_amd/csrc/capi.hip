@@ -44,6 +44,18 @@ int wr_block_norm_backward_impl(wr_ctx*, int64_t, int64_t, const void*, int, int
                                 int64_t, float, const void*, int, int64_t, float, const void*, int, const float*,
                                 const void*, int64_t, const void*, int64_t, void*, int64_t, void*, int64_t, float*,
                                 float*, float*);
+int wr_rotary_impl(wr_ctx*, const void*, int, int64_t, int32_t, int32_t, int64_t, int32_t, const int32_t*, int32_t, int64_t,
+                   const int32_t*, const double*, int, void*, int64_t);
+int64_t wr_kv_blocks(const wr_kv_cache&, const wr_kv_seqs&);
+int wr_kv_write_impl(wr_ctx*, const wr_kv_cache&, const wr_kv_seqs&, const void*, int64_t, const void*, int64_t, int, int64_t);
+int wr_kv_read_impl(wr_ctx*, const wr_kv_cache&, const wr_kv_seqs&, void*, int64_t, void*, int64_t, int, int64_t);
+size_t wr_kv_attention_ws_bytes(int64_t rows, int64_t n, int32_t dim);
+int wr_kv_attention_impl(wr_ctx*, const wr_kv_cache&, const wr_kv_seqs&, const void*, int64_t, int64_t, int32_t, float, int,
+                         int32_t, void*, int64_t);
+size_t wr_adapters_ws_bytes(int64_t rows, int64_t n, int32_t rank);
+int wr_adapters_impl(wr_ctx*, const void*, int, int64_t, int64_t, int64_t, const void*, const void*, int32_t, int32_t, int64_t,
+                     const float*, const int32_t*, const int32_t*, const int32_t*, int32_t, int64_t, const void*, int64_t,
+                     void*, int, int64_t);
 
 namespace {
 
@@ -53,6 +65,10 @@ constexpr int64_t kNormMax = 16384;   // widest row of the block norm (a workgro
 constexpr int64_t kI8Max = 131071;    // longest exact int32 sum of 8-bit products: 131071 * 2^14 < 2^31
 constexpr int64_t kI8Rows = 1 << 26;   // weight rows of an 8-bit product (its grid)
 constexpr int64_t kRowsMax = 2147483647;
+constexpr int32_t kRotaryDim = 1024;   // widest head (the angles in a workgroup's LDS)
+constexpr int32_t kRotaryAxes = 8;
+constexpr int32_t kShareMax = 64;      // query heads of a head of the cache
+constexpr int32_t kRankMax = 256;      // widest adapter
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 bool valid_dtype(int d) { return d == WR_F32 || d == WR_BF16; }
@@ -130,6 +146,8 @@ size_t wr_workspace_bytes(int op, int64_t rows, int64_t n, int32_t group, int32_
     case WR_OP_GEMV: return rows >= 1 && rows <= 8 ? wr_gemv_ws_bytes(n, (int32_t)rows) : 0;
     case WR_OP_NORM_BWD: return n <= kNormMax && group >= 0 ? wr_norm_bwd_ws_bytes(rows, n, group) : 0;
     case WR_OP_STATS: return wr_stats_ws_bytes(rows > 0 ? rows : 1);
+    case WR_OP_KV_ATTENTION: return group > 0 ? wr_kv_attention_ws_bytes(rows, n, group) : 0;
+    case WR_OP_ADAPTERS: return rank > 0 && rank <= kRankMax ? wr_adapters_ws_bytes(rows, n, rank) : 0;
     default: return 0;
   }
 }
@@ -433,6 +451,114 @@ int wr_block_norm_backward(wr_ctx* ctx, int64_t rows, int64_t n, const void* bra
   return wr_block_norm_backward_impl(ctx, rows, n, branch, b_dtype, ldb, w_post, gate, ldg, gate_rows, branch_scale,
                                      resid, r_dtype, ldr, resid_scale, w_pre, w_dtype, stats, dy, lddy, dresid_out,
                                      lddo, dbranch, lddb, dresid, lddr, dw_post, dgate, dw_pre);
+}
+
+int wr_rotary(wr_ctx* ctx, const void* x, int dtype, int64_t rows, int32_t heads, int32_t dim, int64_t ldx,
+              int32_t pairs, const int32_t* positions, int32_t axes, int64_t ldp, const int32_t* axis_of,
+              const double* freqs, int flags, void* y, int64_t ldy) {
+  if (!ctx || !valid_dtype(dtype) || rows < 0 || rows > kRowsMax || heads <= 0 || dim <= 0 || pairs < 0 || pairs > dim / 2 ||
+      axes <= 0 || (flags & ~(WR_ROTARY_INTERLEAVED | WR_ROTARY_INVERSE)))
+    return WR_EINVAL;
+  if (dim > kRotaryDim || axes > kRotaryAxes) return WR_EUNSUPPORTED;
+  if (rows == 0) return WR_OK;
+  const int64_t n = (int64_t)heads * dim;
+  if (!x || !y || !rows_ok(x, dtype, rows, n, ldx) || !rows_ok(y, dtype, rows, n, ldy) || (x == y && ldx != ldy && rows > 1))
+    return WR_EINVAL;
+  if (pairs > 0 && (!positions || !freqs || (!axis_of && axes > 1) || (ldp < rows && axes > 1) || !aligned(positions, 4) ||
+                    !aligned(freqs, 8) || !aligned(axis_of, 4)))
+    return WR_EINVAL;
+  DeviceScope ds(ctx->device);
+  if (!ds.ok) return WR_EHIP;
+  return wr_rotary_impl(ctx, x, dtype, rows, heads, dim, ldx, pairs, positions, axes, ldp, axis_of, freqs, flags, y, ldy);
+}
+
+size_t wr_kv_page_bytes(int32_t heads, int32_t dim, int32_t page_tokens, int32_t group) {
+  if (heads <= 0 || heads > 65536 || (dim != 64 && dim != 128 && dim != 256) || (group != 32 && group != 64 && group != 128) ||
+      dim % group != 0 || page_tokens < 16 || page_tokens > 256 || !pow2(page_tokens))
+    return 0;
+  return (size_t)heads * page_tokens * (dim + 8 * (dim / group));
+}
+
+// What the calls on a cache check alike.  nothing: there is no row or no sequence.
+static int kv_args_ok(wr_ctx* ctx, const wr_kv_cache* c, const wr_kv_seqs* s, int64_t rows, bool& nothing) {
+  if (!ctx || !c || !s || rows < 0 || rows > kRowsMax || c->count < 0 || s->n < 0 || s->width < 0 || s->most_new < 0 ||
+      s->most_tokens < 0)
+    return WR_EINVAL;
+  if (wr_kv_page_bytes(c->heads, c->dim, c->page_tokens, c->group) == 0) return WR_EUNSUPPORTED;
+  nothing = rows == 0 || s->n == 0 || s->most_new == 0;
+  if (nothing) return WR_OK;
+  if (!c->pages || c->count == 0 || !aligned(c->pages, 16) || !s->starts || !s->lengths || !aligned(s->starts, 4) ||
+      !aligned(s->lengths, 4) || !aligned(s->table, 4) || (s->width > 0 && !s->table) || (s->ldt < s->width && s->n > 1))
+    return WR_EINVAL;
+  return WR_OK;
+}
+
+static int kv_rows_args(wr_ctx* ctx, const wr_kv_cache* cache, const wr_kv_seqs* seqs, const void* k, int64_t ldk, const void* v,
+                        int64_t ldv, int dtype, int64_t rows, bool& nothing) {
+  if (!valid_dtype(dtype)) return WR_EINVAL;
+  const int rc = kv_args_ok(ctx, cache, seqs, rows, nothing);
+  if (rc != WR_OK || nothing) return rc;
+  const int64_t n = (int64_t)cache->heads * cache->dim;
+  if ((!k && !v) || !rows_ok(k, dtype, rows, n, ldk) || !rows_ok(v, dtype, rows, n, ldv)) return WR_EINVAL;
+  return wr_kv_blocks(*cache, *seqs) > kRowsMax ? WR_EUNSUPPORTED : WR_OK;
+}
+
+int wr_kv_write(wr_ctx* ctx, const wr_kv_cache* cache, const wr_kv_seqs* seqs, const void* k, int64_t ldk, const void* v,
+                int64_t ldv, int dtype, int64_t rows) {
+  bool nothing = false;
+  const int rc = kv_rows_args(ctx, cache, seqs, k, ldk, v, ldv, dtype, rows, nothing);
+  if (rc != WR_OK || nothing) return rc;
+  DeviceScope ds(ctx->device);
+  if (!ds.ok) return WR_EHIP;
+  return wr_kv_write_impl(ctx, *cache, *seqs, k, ldk, v, ldv, dtype, rows);
+}
+
+int wr_kv_read(wr_ctx* ctx, const wr_kv_cache* cache, const wr_kv_seqs* seqs, void* k, int64_t ldk, void* v, int64_t ldv,
+               int dtype, int64_t rows) {
+  bool nothing = false;
+  const int rc = kv_rows_args(ctx, cache, seqs, k, ldk, v, ldv, dtype, rows, nothing);
+  if (rc != WR_OK || nothing) return rc;
+  DeviceScope ds(ctx->device);
+  if (!ds.ok) return WR_EHIP;
+  return wr_kv_read_impl(ctx, *cache, *seqs, k, ldk, v, ldv, dtype, rows);
+}
+
+int wr_kv_attention(wr_ctx* ctx, const wr_kv_cache* cache, const wr_kv_seqs* seqs, const void* q, int64_t ldq,
+                    int64_t rows, int32_t heads, float scale, int flags, int32_t window, void* out, int64_t ldo) {
+  if ((flags & ~WR_ATTENTION_CAUSAL) || window < 0 || heads <= 0 || !std::isfinite(scale)) return WR_EINVAL;
+  bool nothing = false;
+  const int rc = kv_args_ok(ctx, cache, seqs, rows, nothing);
+  if (rc != WR_OK) return rc;
+  if (heads % cache->heads != 0) return WR_EINVAL;
+  const int32_t share = heads / cache->heads;
+  if (share > kShareMax || (int64_t)seqs->most_new * share > 1 << 30) return WR_EUNSUPPORTED;
+  if (nothing) return WR_OK;
+  const int64_t n = (int64_t)heads * cache->dim;
+  if (!q || !out || !rows_ok(q, WR_BF16, rows, n, ldq) || !rows_ok(out, WR_BF16, rows, n, ldo)) return WR_EINVAL;
+  DeviceScope ds(ctx->device);
+  if (!ds.ok) return WR_EHIP;
+  return wr_kv_attention_impl(ctx, *cache, *seqs, q, ldq, rows, heads, scale, flags, window, out, ldo);
+}
+
+int wr_adapters(wr_ctx* ctx, const void* x, int x_dtype, int64_t rows, int64_t n, int64_t ldx, const void* A, const void* B,
+                int32_t adapters, int32_t rank, int64_t outs, const float* scales, const int32_t* ranks,
+                const int32_t* starts, const int32_t* ids, int32_t n_seqs, int64_t most, const void* base, int64_t ldb,
+                void* y, int y_dtype, int64_t ldy) {
+  if (!ctx || !valid_dtype(x_dtype) || !valid_dtype(y_dtype) || rows < 0 || rows > kRowsMax || n <= 0 || adapters < 0 ||
+      rank < 0 || outs < 0 || n_seqs < 0 || most < 0)
+    return WR_EINVAL;
+  if (rank > kRankMax || n > kRowsMax || outs > kRowsMax) return WR_EUNSUPPORTED;
+  if (rows == 0 || n_seqs == 0 || most == 0 || outs == 0) return WR_OK;
+  const bool some = adapters > 0 && rank > 0;
+  if (!starts || !ids || !y || (some && (!x || !A || !B || !scales)) || !rows_ok(x, x_dtype, rows, n, ldx) ||
+      !rows_ok(base, y_dtype, rows, outs, ldb) || !rows_ok(y, y_dtype, rows, outs, ldy) ||
+      (base == y && ldb != ldy && rows > 1) || !aligned(A, 2) || !aligned(B, 2) || !aligned(scales, 4) ||
+      !aligned(ranks, 4) || !aligned(starts, 4) || !aligned(ids, 4))
+    return WR_EINVAL;
+  DeviceScope ds(ctx->device);
+  if (!ds.ok) return WR_EHIP;
+  return wr_adapters_impl(ctx, x, x_dtype, rows, n, ldx, A, B, adapters, rank, outs, scales, ranks, starts, ids, n_seqs, most,
+                          base, ldb, y, y_dtype, ldy);
 }
 
 const char* wr_strerror(int status) {

@@ -1,0 +1,251 @@
+// Writing rows of keys and values into the 4-bit cache and reading them back.
+//
+// Both stream: a value is 2 or 4 bytes on the row side and half a byte (plus 4 bytes a group) in the cache, so the
+// bound is memory.  A workgroup takes 16 consecutive positions of one head that start at a multiple of 16, which is a
+// tile of the values' layout: it alone writes the tile's dwords, and no two workgroups share a byte.
+#include "kv_cache.hpp"
+
+namespace wr {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// One of the 16-token tiles that a sequence's rows touch, for one head.
+struct Tile {
+  int row0;        // row of the tile's first position (below the first row for positions that are not rows)
+  int from, to;    // tokens of the tile that are rows
+  int page;        // outside 0 .. count - 1: absent
+  int at;          // the tile's first token in its page
+};
+
+// Blocks are numbered head fastest, then tile, then sequence.
+__device__ __forceinline__ bool tile_of(const KvArgs& a, int tiles, uint32_t block, int& head, Tile& t) {
+  const uint32_t rest = block / (uint32_t)a.heads;
+  head = block % (uint32_t)a.heads;
+  const int i = rest / (uint32_t)tiles, nth = rest % (uint32_t)tiles;
+  const KvSeq s = kv_seq(a, i);
+  if (s.fresh <= 0) return false;
+  const int first = s.length - s.fresh;             // position of the first row; below 0 where rows have none
+  const int tile = (first >= 0 ? first / 16 : -((15 - first) / 16)) + nth;  // floor
+  const int p0 = 16 * tile;
+  if (p0 >= s.length) return false;
+  t.row0 = s.row + p0 - first;
+  t.from = max(first - p0, 0);
+  t.to = min(s.length - p0, 16);
+  t.page = -1;
+  if (tile >= 0) {  // a whole tile is on one side of position 0
+    t.page = a.table[(int64_t)i * a.ldt + (p0 >> a.page_shift)];
+    t.at = p0 & ((1 << a.page_shift) - 1);
+  }
+  return true;
+}
+
+template <typename T>
+__device__ __forceinline__ void group_codes(const Raw8<T>& x, int lanes, uint32_t& codes, uint32_t& meta) {
+  float lo = x.get(0), hi = lo;
+  bool bad = false;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float f = x.get(e);
+    lo = fminf(lo, f);
+    hi = fmaxf(hi, f);
+    bad |= !(fabsf(f) <= 3.402823466e38f);
+  }
+  int any = bad;
+  for (int m = 1; m < lanes; m <<= 1) {
+    lo = fminf(lo, __shfl_xor(lo, m));
+    hi = fmaxf(hi, __shfl_xor(hi, m));
+    any |= __shfl_xor(any, m);
+  }
+  lo = fminf(fmaxf(lo, -kKvMost), kKvMost);
+  hi = fminf(fmaxf(hi, -kKvMost), kKvMost);
+  const uint16_t off_bits = f32_to_f16_bits_clamped(lo);
+  const float off = f16_bits_to_f32(off_bits);
+  const uint16_t scale_bits = f32_to_f16_bits_clamped(__fdiv_rn(hi - off, 15.0f));
+  const float scale = f16_bits_to_f32(scale_bits);
+  codes = 0;
+  if (any) {
+    meta = 0x7e007e00u;
+    return;
+  }
+  meta = scale_bits | (uint32_t)off_bits << 16;
+  if (!(scale > 0.0f)) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float c = fminf(fmaxf(rintf(__fdiv_rn(fminf(fmaxf(x.get(e), -kKvMost), kKvMost) - off, scale)), 0.0f), 15.0f);
+    codes |= (uint32_t)c << (4 * e);
+  }
+}
+
+template <int DIM, int GROUP, typename T>
+__global__ __launch_bounds__(kThreads) void kv_write_kernel(KvArgs a, int tiles, const T* __restrict__ k, int64_t ldk,
+                                                            const T* __restrict__ v, int64_t ldv) {
+  constexpr int UNITS = DIM / 8;  // of eight values a token
+  __shared__ uint32_t vcodes[16][UNITS + 1];
+  Tile t;
+  int head;
+  if (!tile_of(a, tiles, blockIdx.x, head, t) || t.page < 0 || t.page >= a.count) return;
+  const KvLayout<DIM, GROUP> at{1 << a.page_shift};
+  uint8_t* base = a.pages + (int64_t)t.page * ((int64_t)a.heads * at.head_bytes()) + head * at.head_bytes();
+  for (int u = threadIdx.x; u < 2 * 16 * UNITS; u += kThreads) {  // a wave has units of either k or v
+    const bool values = u >= 16 * UNITS;
+    const int token = u / UNITS % 16, c = u % UNITS;
+    const T* src = values ? v : k;
+    if (!src) continue;
+    const bool live = token >= t.from && token < t.to;
+    if (__builtin_amdgcn_ballot_w64(live) == 0) continue;
+    Raw8<T> x;
+    x.load(src + (int64_t)(t.row0 + (live ? token : t.from)) * (values ? ldv : ldk) + head * DIM + 8 * c);
+    uint32_t codes, meta;
+    group_codes(x, GROUP / 8, codes, meta);
+    if (!live) continue;
+    const int in_page = t.at + token;
+    if (values)
+      vcodes[token][c] = codes;
+    else
+      *reinterpret_cast<uint32_t*>(base + in_page * (DIM / 2) + (c % 4) * (DIM / 8) + (c / 4) * 4) = codes;
+    if (c % (GROUP / 8) == 0)
+      *reinterpret_cast<uint32_t*>(base + (values ? at.v_meta() : at.k_meta()) +
+                                   ((c / (GROUP / 8)) * at.page_tokens + in_page) * 4) = meta;
+  }
+  if (!v) return;
+  __syncthreads();
+  uint8_t* tile = base + at.v_codes() + t.at * (DIM / 2);
+  for (int w = threadIdx.x; w < 2 * DIM; w += kThreads) {  // the tile's dwords
+    const int m = w % (DIM / 32), l = w / (DIM / 32) % 16, g = w / (DIM / 2);
+    const int d = 16 * m + l;
+    uint32_t word = 0;
+    int live = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int token = 4 * g + i;
+      if (token >= t.from && token < t.to) {
+        const uint32_t lo = vcodes[token][d / 8] >> (4 * (d % 8)) & 15u;
+        const uint32_t hi = vcodes[token][(DIM / 2 + d) / 8] >> (4 * (d % 8)) & 15u;
+        word |= (lo | hi << 4) << (8 * i);
+        live |= 1 << i;
+      }
+    }
+    if (live == 15) {
+      *reinterpret_cast<uint32_t*>(tile + 4 * w) = word;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (live >> i & 1) tile[4 * w + i] = (uint8_t)(word >> (8 * i));
+    }
+  }
+}
+
+template <int DIM, int GROUP, typename T>
+__global__ __launch_bounds__(kThreads) void kv_read_kernel(KvArgs a, int tiles, T* __restrict__ k, int64_t ldk,
+                                                           T* __restrict__ v, int64_t ldv) {
+  constexpr int UNITS = DIM / 8;
+  __shared__ uint32_t vtile[2 * DIM];
+  Tile t;
+  int head;
+  if (!tile_of(a, tiles, blockIdx.x, head, t)) return;
+  const bool there = t.page >= 0 && t.page < a.count;
+  const KvLayout<DIM, GROUP> at{1 << a.page_shift};
+  const uint8_t* base = a.pages + (int64_t)(there ? t.page : 0) * ((int64_t)a.heads * at.head_bytes()) + head * at.head_bytes();
+  if (v) {
+    const uint8_t* tile = base + at.v_codes() + t.at * (DIM / 2);
+    if (there)
+      for (int w = threadIdx.x; w < 2 * DIM; w += kThreads) vtile[w] = *reinterpret_cast<const uint32_t*>(tile + 4 * w);
+    __syncthreads();
+  }
+  for (int u = threadIdx.x; u < 2 * 16 * UNITS; u += kThreads) {
+    const bool values = u >= 16 * UNITS;
+    const int token = u / UNITS % 16, c = u % UNITS;
+    T* dst = values ? v : k;
+    if (!dst || token < t.from || token >= t.to) continue;
+    float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (there) {
+      const int in_page = t.at + token;
+      const uint32_t meta = *reinterpret_cast<const uint32_t*>(base + (values ? at.v_meta() : at.k_meta()) +
+                                                               ((c / (GROUP / 8)) * at.page_tokens + in_page) * 4);
+      const float scale = f16_bits_to_f32((uint16_t)meta), off = f16_bits_to_f32((uint16_t)(meta >> 16));
+      uint32_t codes;
+      if (values) {
+        codes = 0;
+        const int cc = c % (UNITS / 2), shift = 8 * (token % 4) + (c >= UNITS / 2 ? 4 : 0);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int d = 8 * cc + e;
+          codes |= (vtile[((token / 4) * 16 + d % 16) * (DIM / 32) + d / 16] >> shift & 15u) << (4 * e);
+        }
+      } else {
+        codes = *reinterpret_cast<const uint32_t*>(base + in_page * (DIM / 2) + (c % 4) * (DIM / 8) + (c / 4) * 4);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = fmaf((float)(codes >> (4 * e) & 15u), scale, off);  // the product is exact
+    }
+    Raw8<T> r;
+    r.round(f);
+    r.store(dst + (int64_t)(t.row0 + token) * (values ? ldv : ldk) + head * DIM + 8 * c);
+  }
+}
+
+}  // namespace
+
+KvArgs kv_args(const wr_kv_cache& c, const wr_kv_seqs& s, int64_t rows) {
+  KvArgs a;
+  a.pages = static_cast<uint8_t*>(c.pages);
+  a.starts = s.starts;
+  a.lengths = s.lengths;
+  a.table = s.table;
+  a.ldt = s.ldt;
+  a.rows = rows;
+  a.count = (int32_t)std::min<int64_t>(c.count, 2147483647);
+  a.heads = c.heads;
+  a.page_shift = __builtin_ctz((unsigned)c.page_tokens);
+  a.n = s.n;
+  a.most_new = s.most_new;
+  a.most_tokens = (int32_t)std::min<int64_t>(s.most_tokens, (int64_t)s.width * c.page_tokens);
+  return a;
+}
+
+}  // namespace wr
+
+using namespace wr;
+
+// Tiles that most_new consecutive positions can touch.
+static int64_t tiles_of(const wr_kv_seqs& s) { return ((int64_t)s.most_new + 14) / 16 + 1; }
+
+int64_t wr_kv_blocks(const wr_kv_cache& c, const wr_kv_seqs& s) { return (int64_t)c.heads * s.n * tiles_of(s); }
+
+int wr_kv_write_impl(wr_ctx* ctx, const wr_kv_cache& c, const wr_kv_seqs& s, const void* k, int64_t ldk, const void* v,
+                     int64_t ldv, int dtype, int64_t rows) {
+  const KvArgs a = kv_args(c, s, rows);
+  const bool there = kv_form(c.dim, c.group, [&](auto d, auto g) {
+    constexpr int D = decltype(d)::value, G = decltype(g)::value;
+    const dim3 grid((uint32_t)wr_kv_blocks(c, s));
+    if (dtype == WR_BF16)
+      hipLaunchKernelGGL((kv_write_kernel<D, G, uint16_t>), grid, dim3(kThreads), 0, ctx->stream, a, (int)tiles_of(s),
+                         static_cast<const uint16_t*>(k), ldk, static_cast<const uint16_t*>(v), ldv);
+    else
+      hipLaunchKernelGGL((kv_write_kernel<D, G, float>), grid, dim3(kThreads), 0, ctx->stream, a, (int)tiles_of(s),
+                         static_cast<const float*>(k), ldk, static_cast<const float*>(v), ldv);
+  });
+  if (!there) return WR_EUNSUPPORTED;
+  WR_CHECK_LAUNCH();
+  return WR_OK;
+}
+
+int wr_kv_read_impl(wr_ctx* ctx, const wr_kv_cache& c, const wr_kv_seqs& s, void* k, int64_t ldk, void* v, int64_t ldv,
+                    int dtype, int64_t rows) {
+  const KvArgs a = kv_args(c, s, rows);
+  const bool there = kv_form(c.dim, c.group, [&](auto d, auto g) {
+    constexpr int D = decltype(d)::value, G = decltype(g)::value;
+    const dim3 grid((uint32_t)wr_kv_blocks(c, s));
+    if (dtype == WR_BF16)
+      hipLaunchKernelGGL((kv_read_kernel<D, G, uint16_t>), grid, dim3(kThreads), 0, ctx->stream, a, (int)tiles_of(s),
+                         static_cast<uint16_t*>(k), ldk, static_cast<uint16_t*>(v), ldv);
+    else
+      hipLaunchKernelGGL((kv_read_kernel<D, G, float>), grid, dim3(kThreads), 0, ctx->stream, a, (int)tiles_of(s),
+                         static_cast<float*>(k), ldk, static_cast<float*>(v), ldv);
+  });
+  if (!there) return WR_EUNSUPPORTED;
+  WR_CHECK_LAUNCH();
+  return WR_OK;
+}
