@@ -1,11 +1,17 @@
 // Low-rank adapters of many requests beside a shared projection: y = base + s B (A x).
+//
+// Two launches.  The first forms t = A x (rows x rank, fp32, in the workspace): x is read once, a workgroup takes 16
+// or 32 rows of a request and up to 64 rows of A, and its eight waves cut the sum over n, which is what fills the card when
+// there are few rows.  The second forms y: a wave keeps its rows of t as matrix operands and walks the outputs 64 at a
+// time; the matrix product's rows are dealt to outputs so that a lane ends up with 16 neighbouring ones, and base
+// is read and y written in whole 16-byte accesses, 128 bytes of a row in a wave.  One token is bound by
+// the two launches and the latency of a few dependent loads, long prompts by the bytes of x, base and y: the products, three
+// of bf16 parts for each of fp32 (x = x0 + x1 + x2 exactly, t likewise), stay below a tenth of the matrix cores' rate.
 #include "rowops.hpp"
 
 namespace wr {
 
 namespace {
-
-constexpr int kThreads = 256;
 
 struct AdapterArgs {
   const int32_t* starts;
@@ -17,68 +23,228 @@ struct AdapterArgs {
   float* t;        // rows x rank
   int64_t rows, n, outs, most;
   int64_t ldx, ldb, ldy;
-  int32_t adapters, rank, n_seqs;
+  int32_t adapters, rank;
+  uint32_t tiles;  // row tiles of a request
 };
 
 struct Request {
-  int64_t row, count;  // count 0: nothing to do
+  int64_t row, count;  // rows left in the tile: count <= 0: nothing to do
   int adapter, rank;   // adapter -1: none
 };
 
-__device__ __forceinline__ Request request_of(const AdapterArgs& a, int i) {
+// The rows of a request from its row `first`.
+__device__ __forceinline__ Request request_of(const AdapterArgs& a, int i, int64_t first) {
   const int64_t b = a.starts[i], e = a.starts[i + 1];
   const bool ok = b >= 0 && e >= b && e <= a.rows && e - b <= a.most;
   int id = a.ids[i];
   if (id < 0 || id >= a.adapters) id = -1;
   int rank = a.rank;
   if (id >= 0 && a.ranks) rank = min(max(a.ranks[id], 0), a.rank);
-  return Request{b, ok ? e - b : 0, id, id >= 0 ? rank : 0};
+  return Request{b + first, ok ? e - b - first : 0, id, id >= 0 ? rank : 0};
 }
 
+__device__ __forceinline__ f32x4 mfma16x16x32_bf16(const u32x4& a, const u32x4& b, const f32x4& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
+}
+
+// Eight values from place k of a row of n, zeros behind its end.
 template <typename T>
-__device__ __forceinline__ float value(T v) {
-  if constexpr (sizeof(T) == 2) return bf16_bits_to_f32(v);
-  else return v;
+__device__ __forceinline__ void load8(Raw8<T>& r, const T* row, int64_t k, int64_t n) {
+  if (k + 8 <= n) {
+    r.load(row + k);
+  } else {
+    r.fill(0.0f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (k + e < n) r.set(e, row[k + e]);
+  }
 }
 
-// t = A x: a workgroup a row.
+// f = p[0] + p[1] + p[2] in bf16, exactly; an infinity or NaN is p[0].
+__device__ __forceinline__ void three_parts(const float (&f)[8], u32x4 (&p)[3]) {
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    float a = f[2 * d], b = f[2 * d + 1];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const uint32_t h = pack_bf16(a, b);
+      p[i][d] = h;
+      a = (h & 0x7f80u) == 0x7f80u ? 0.0f : a - __uint_as_float(h << 16);
+      b = (h & 0x7f800000u) == 0x7f800000u ? 0.0f : b - __uint_as_float(h & 0xffff0000u);
+    }
+  }
+}
+
 template <typename X>
-__global__ __launch_bounds__(kThreads) void adapters_in_kernel(AdapterArgs a, const X* __restrict__ x) {
-  const Request q = request_of(a, blockIdx.y);
-  if (q.adapter < 0) return;
+struct Parts {  // a matrix operand of x
+  static constexpr int N = sizeof(X) == 2 ? 1 : 3;
+  u32x4 p[N];
+  __device__ __forceinline__ explicit Parts(const Raw8<X>& r) {
+    if constexpr (N == 1) {
+      p[0] = r.v;
+    } else {
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = r.get(e);
+      three_parts(f, p);
+    }
+  }
+};
+
+// t = A x: 16 MT rows, 16 NT ranks.
+template <typename X, int MT, int NT>
+__global__ __launch_bounds__(512) void adapters_in_kernel(AdapterArgs a, const X* __restrict__ x, uint32_t rank_tiles) {
+  constexpr int WAVES = 8;
+  __shared__ f32x4 part[WAVES][MT][NT][kWave];
+  const uint32_t rt = blockIdx.x % rank_tiles, rest = blockIdx.x / rank_tiles;
+  const Request q = request_of(a, rest / a.tiles, (int64_t)(rest % a.tiles) * 16 * MT);
+  const int r0 = rt * 16 * NT;
+  if (q.count <= 0 || r0 >= q.rank) return;
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  for (int64_t j = blockIdx.x; j < q.count; j += gridDim.x) {
-    const X* xr = x + (q.row + j) * a.ldx;
-    for (int r = wave; r < q.rank; r += kThreads / kWave) {
-      const uint16_t* ar = a.A + ((int64_t)q.adapter * a.rank + r) * a.n;
-      float sum = 0.0f;
-      for (int64_t c = lane; c < a.n; c += kWave) sum = fmaf(bf16_bits_to_f32(ar[c]), value(xr[c]), sum);
-      for (int m = 1; m < kWave; m <<= 1) sum += __shfl_xor(sum, m);
-      if (lane == 0) a.t[(q.row + j) * a.rank + r] = sum;
+  const int low = lane % 16, g = lane / 16;
+  const X* xr[MT];
+  const uint16_t* ar[NT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) xr[m] = x + (q.row + min((int64_t)(16 * m + low), q.count - 1)) * a.ldx;
+#pragma unroll
+  for (int c = 0; c < NT; ++c) ar[c] = a.A + ((int64_t)q.adapter * a.rank + min(r0 + 16 * c + low, q.rank - 1)) * a.n;
+  f32x4 acc[MT][NT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int c = 0; c < NT; ++c) acc[m][c] = f32x4{0, 0, 0, 0};
+  auto step = [&](int64_t k, auto whole) {  // 64 values of n
+    Raw8<X> xv[2][MT];
+    Raw8<uint16_t> av[2][NT];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int c = 0; c < NT; ++c) {
+        if constexpr (decltype(whole)::value) av[h][c].load(ar[c] + k + 32 * h + 8 * g);
+        else load8(av[h][c], ar[c], k + 32 * h + 8 * g, a.n);
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        if constexpr (decltype(whole)::value) xv[h][m].load(xr[m] + k + 32 * h + 8 * g);
+        else load8(xv[h][m], xr[m], k + 32 * h + 8 * g, a.n);
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const Parts<X> p(xv[h][m]);
+#pragma unroll
+        for (int i = 0; i < Parts<X>::N; ++i)
+#pragma unroll
+          for (int c = 0; c < NT; ++c) acc[m][c] = mfma16x16x32_bf16(av[h][c].v, p.p[i], acc[m][c]);
+      }
+  };
+  const int64_t whole = a.n / 64 * 64;
+#pragma unroll 2
+  for (int64_t k = 64 * wave; k < whole; k += 64 * WAVES) step(k, std::true_type{});
+  if (whole < a.n && (a.n / 64) % WAVES == wave) step(whole, std::false_type{});
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int c = 0; c < NT; ++c) part[wave][m][c][lane] = acc[m][c];
+  __syncthreads();
+  // a lane of a tile holds ranks 4 g .. 4 g + 3 of row `low`; the waves' sums in their order
+  for (int u = threadIdx.x; u < MT * NT * kWave; u += 512) {
+    const int m = u / (NT * kWave), c = u / kWave % NT, l = u % kWave;
+    f32x4 sum = part[0][m][c][l];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) sum += part[w][m][c][l];
+    const int row = 16 * m + l % 16, r = r0 + 16 * c + 4 * (l / 16);
+    if (row < q.count) {
+      float* t = a.t + (q.row + row) * a.rank + r;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (r + i < q.rank) t[i] = sum[i];
     }
   }
 }
 
-// y = base + s B t: a workgroup a row.
-template <typename Y>
-__global__ __launch_bounds__(kThreads) void adapters_out_kernel(AdapterArgs a, const Y* base, Y* y) {
-  const Request q = request_of(a, blockIdx.y);
-  const float s = q.adapter >= 0 ? a.scales[q.adapter] : 0.0f;
-  for (int64_t j = blockIdx.x; j < q.count; j += gridDim.x) {
-    const int64_t row = q.row + j;
-    for (int64_t o = threadIdx.x; o < a.outs; o += kThreads) {
-      float sum = 0.0f;
-      if (q.adapter >= 0) {
-        const uint16_t* br = a.B + ((int64_t)q.adapter * a.outs + o) * a.rank;
-        for (int r = 0; r < q.rank; ++r) sum = fmaf(bf16_bits_to_f32(br[r]), a.t[row * a.rank + r], sum);
-        sum *= s;
+// y = base + s B t: 16 MT rows and some of the outputs, 64 at a time, KS slices of 32 ranks.
+template <typename Y, int MT, int KS>
+__global__ __launch_bounds__(256) void adapters_out_kernel(AdapterArgs a, const Y* base, Y* y, uint32_t out_parts) {
+  constexpr int WAVES = 4;
+  const uint32_t nth = blockIdx.x % out_parts, rest = blockIdx.x / out_parts;
+  const Request q = request_of(a, rest / a.tiles, (int64_t)(rest % a.tiles) * 16 * MT);
+  if (q.count <= 0 || (q.rank == 0 && base == y)) return;
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int low = lane % 16, g = lane / 16;
+  const float s = q.rank > 0 ? a.scales[q.adapter] : 0.0f;
+  u32x4 t[MT][KS][3];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const float* tr = a.t + (q.row + min((int64_t)(16 * m + low), q.count - 1)) * a.rank;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int r = 32 * ks + 8 * g + e;
+        f[e] = r < q.rank ? tr[r] : 0.0f;
       }
-      if (base) sum += value(base[row * a.ldb + o]);
-      if constexpr (sizeof(Y) == 2) y[row * a.ldy + o] = (Y)f32_to_bf16_bits(sum);
-      else y[row * a.ldy + o] = sum;
+      three_parts(f, t[m][ks]);
+    }
+  }
+  const uint16_t* bp = a.B + (int64_t)max(q.adapter, 0) * a.outs * a.rank;
+  for (int64_t o0 = ((int64_t)nth * WAVES + wave) * 64; o0 < a.outs; o0 += (int64_t)out_parts * WAVES * 64) {
+    f32x4 acc[MT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[m][j] = f32x4{0, 0, 0, 0};
+    if (q.rank > 0) {
+      // row `low` of product j is output 16 (low / 4) + 4 j + low % 4
+      Raw8<uint16_t> b[4][KS];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint16_t* br = bp + min(o0 + 16 * (low / 4) + 4 * j + low % 4, a.outs - 1) * a.rank;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) load8(b[j][ks], br, 32 * ks + 8 * g, q.rank);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int i = 0; i < 3; ++i)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) acc[m][j] = mfma16x16x32_bf16(b[j][ks].v, t[m][ks][i], acc[m][j]);
+    }
+    const int64_t o = o0 + 16 * g;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int row = 16 * m + low;
+      if (row >= q.count) continue;
+      const Y* b = base ? base + (q.row + row) * a.ldb : nullptr;
+      Y* out = y + (q.row + row) * a.ldy;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t at = o + 8 * h;
+        if (at >= a.outs) continue;
+        Raw8<Y> v;
+        v.fill(0.0f);
+        if (b) load8(v, b, at, a.outs);
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = fmaf(acc[m][2 * h + e / 4][e % 4], s, v.get(e));
+        if (q.rank > 0) v.round(f);
+        if (at + 8 <= a.outs) {
+          v.store(out + at);
+        } else {
+          for (int e = 0; e < 8; ++e)
+            if (at + e < a.outs) out[at + e] = v.at(e);
+        }
+      }
     }
   }
 }
+
+constexpr int64_t kMostBlocks = 1 << 30;
 
 }  // namespace
 
@@ -95,23 +261,59 @@ int wr_adapters_impl(wr_ctx* ctx, const void* x, int x_dtype, int64_t rows, int6
                      const void* B, int32_t adapters, int32_t rank, int64_t outs, const float* scales,
                      const int32_t* ranks, const int32_t* starts, const int32_t* ids, int32_t n_seqs, int64_t most,
                      const void* base, int64_t ldb, void* y, int y_dtype, int64_t ldy) {
-  const AdapterArgs a{starts, ids, ranks, scales, static_cast<const uint16_t*>(A), static_cast<const uint16_t*>(B),
-                      static_cast<float*>(ctx->ws), rows, n, outs, most, ldx, ldb, ldy, adapters, rank, n_seqs};
-  if (ctx->ws_bytes < wr_adapters_ws_bytes(rows, n, rank)) return WR_EWORKSPACE;
-  const dim3 grid((uint32_t)std::min<int64_t>(std::max<int64_t>(std::min(most, rows), 1), 4096), (uint32_t)n_seqs);
-  if (adapters > 0 && rank > 0) {
-    if (x_dtype == WR_BF16)
-      hipLaunchKernelGGL(adapters_in_kernel<uint16_t>, grid, dim3(kThreads), 0, ctx->stream, a, static_cast<const uint16_t*>(x));
-    else
-      hipLaunchKernelGGL(adapters_in_kernel<float>, grid, dim3(kThreads), 0, ctx->stream, a, static_cast<const float*>(x));
+  AdapterArgs a{starts, ids, ranks, scales, static_cast<const uint16_t*>(A), static_cast<const uint16_t*>(B),
+                static_cast<float*>(ctx->ws), rows, n, outs, most, ldx, ldb, ldy, rank > 0 ? adapters : 0, rank, 1};
+  if (a.adapters > 0 && ctx->ws_bytes < wr_adapters_ws_bytes(rows, n, rank)) return WR_EWORKSPACE;
+  most = std::min(most, rows);
+  // 16 rows a tile where that leaves none of it empty or the card is not full, else 32
+  const int64_t mt = most <= 16 ? 1 : 2;
+  const int64_t tiles = (most + 16 * mt - 1) / (16 * mt);
+  const int nt = rank <= 16 ? 1 : rank <= 32 ? 2 : 4;
+  const int64_t rank_tiles = (rank + 16 * nt - 1) / (16 * nt);
+  const int64_t out_steps = (outs + 255) / 256;
+  // waves enough for eight on each SIMD; a wave that walks several steps reads its rows of t once
+  const int64_t row_tiles = std::min<int64_t>(tiles * n_seqs, rows / (16 * mt) + n_seqs);
+  const int64_t out_parts = std::max<int64_t>(1, std::min(out_steps, (8 * (int64_t)ctx->num_cu + row_tiles - 1) / row_tiles));
+  if (tiles * n_seqs > kMostBlocks / std::max<int64_t>(rank_tiles, out_parts)) return WR_EUNSUPPORTED;
+  a.tiles = (uint32_t)tiles;
+  auto with_rows = [&](auto type, auto&& f) {
+    using T = decltype(type);
+    if (mt == 1) f(type, std::integral_constant<int, 1>{});
+    else f(type, std::integral_constant<int, 2>{});
+    (void)sizeof(T);
+  };
+  if (a.adapters > 0) {
+    const dim3 grid((uint32_t)(tiles * n_seqs * rank_tiles));
+    auto go = [&](auto type, auto m) {
+      using X = decltype(type);
+      constexpr int MT = decltype(m)::value;
+      const X* xp = static_cast<const X*>(x);
+      if (nt == 1) hipLaunchKernelGGL((adapters_in_kernel<X, MT, 1>), grid, dim3(512), 0, ctx->stream, a, xp, (uint32_t)rank_tiles);
+      else if (nt == 2) hipLaunchKernelGGL((adapters_in_kernel<X, MT, 2>), grid, dim3(512), 0, ctx->stream, a, xp, (uint32_t)rank_tiles);
+      else hipLaunchKernelGGL((adapters_in_kernel<X, MT, 4>), grid, dim3(512), 0, ctx->stream, a, xp, (uint32_t)rank_tiles);
+    };
+    if (x_dtype == WR_BF16) with_rows(uint16_t{}, go);
+    else with_rows(float{}, go);
     WR_CHECK_LAUNCH();
   }
-  if (y_dtype == WR_BF16)
-    hipLaunchKernelGGL(adapters_out_kernel<uint16_t>, grid, dim3(kThreads), 0, ctx->stream, a,
-                       static_cast<const uint16_t*>(base), static_cast<uint16_t*>(y));
-  else
-    hipLaunchKernelGGL(adapters_out_kernel<float>, grid, dim3(kThreads), 0, ctx->stream, a, static_cast<const float*>(base),
-                       static_cast<float*>(y));
-  WR_CHECK_LAUNCH();
+  {
+    const dim3 grid((uint32_t)(tiles * n_seqs * out_parts));
+    auto go = [&](auto type, auto m) {
+      using Y = decltype(type);
+      constexpr int MT = decltype(m)::value;
+      const Y* bp = static_cast<const Y*>(base);
+      Y* yp = static_cast<Y*>(y);
+      auto run = [&](auto ks) {
+        hipLaunchKernelGGL((adapters_out_kernel<Y, MT, decltype(ks)::value>), grid, dim3(256), 0, ctx->stream, a, bp, yp, (uint32_t)out_parts);
+      };
+      if (rank <= 32) run(std::integral_constant<int, 1>{});
+      else if (rank <= 64) run(std::integral_constant<int, 2>{});
+      else if (rank <= 128) run(std::integral_constant<int, 4>{});
+      else run(std::integral_constant<int, 8>{});
+    };
+    if (y_dtype == WR_BF16) with_rows(uint16_t{}, go);
+    else with_rows(float{}, go);
+    WR_CHECK_LAUNCH();
+  }
   return WR_OK;
 }
