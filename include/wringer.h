@@ -446,7 +446,8 @@ int wr_rotary(wr_ctx* ctx, const void* x, int dtype, int64_t rows, int32_t heads
  *   values' codes   for every 16 tokens 8 dim bytes: byte ((g * 16 + l) * dim / 32 + m) * 4 + i holds token
  *                   4 g + i of the 16, dim 16 m + l in its low and dim / 2 + 16 m + l in its high half
  *   keys' groups    dim / group x page_tokens pairs of fp16: scale, offset
- *   values' groups  the same.
+ *   values' groups  as many bytes, for every four tokens of a group: scale 0, scale 2, offset 0, offset 2, scale 1,
+ *                   scale 3, offset 1, offset 3.
  * The first operand of a matrix product is read from it in whole 16-byte loads, and no byte holds values of two
  * tokens: rows that are written at the same time never share one.
  */

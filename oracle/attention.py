@@ -58,8 +58,11 @@ def kv_page(k, v, group, page):
         for t in range(page):
             for d in range(dim):
                 values[t // 16, t % 16 // 4, d % 16, d % (dim // 2) // 16, t % 4] |= vc[t, d] << (4 * (d // (dim // 2)))
-        meta = [np.stack([s.T, o.T], -1).view(np.uint8) for s, o in ((ks, ko), (vs, vo))]
-        out += [keys.ravel(), values.ravel(), meta[0].ravel(), meta[1].ravel()]
+        kmeta = np.stack([ks.T, ko.T], -1)
+        vmeta = np.zeros((dim // group, page // 4, 2, 2, 2), np.float16)  # odd token, scale or offset, later pair
+        for t in range(page):
+            vmeta[:, t // 4, t % 2, 0, t % 4 // 2], vmeta[:, t // 4, t % 2, 1, t % 4 // 2] = vs[t], vo[t]
+        out += [keys.ravel(), values.ravel(), kmeta.view(np.uint8).ravel(), vmeta.view(np.uint8).ravel()]
     return np.concatenate(out)
 
 

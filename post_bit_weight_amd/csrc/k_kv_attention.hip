@@ -1,143 +1,238 @@
-// Attention over the 4-bit cache.
+// Attention over the 4-bit cache for few rows: 16 or 32 (query, head) pairs of a sequence and head of the cache, which is
+// what a step of one or some new tokens has.
 //
-// A value s c + o (code c, scale s and offset o of its group) becomes an fp16 number, rounded once, on its way to
-// the matrix cores: the code OR-ed into the mantissa of 1024 is the fp16 number 1024 + c, less 1024 is c, and one packed
-// fused multiply-add makes two values.  All of that is exact up to the one rounding (2^-11 relative; s and o are fp16,
-// so that small values are exact multiples of 2^-24, and the cache holds nothing beyond fp16's range), an eighth of what bf16 would lose.
-// Queries are scaled by a power of two each, which the scores give back, and fit fp16 exactly.  Weights are kept
-// as 2^15 times what they are relative to the row's largest: fp16 then holds those down to 2^-39 of it.
-// The scores come out transposed (a lane holds four tokens of one query), which is the layout in which the second product
-// takes its weights: nothing crosses lanes but the maximum.
-#include "kv_cache.hpp"
+// A wave reads 32 tokens at a time straight into operands of the matrix cores.  The scores come out transposed (a lane holds four
+// tokens of one row), which is the layout in which the second product takes its weights: nothing crosses lanes but the maximum.
+#include "kv_attention.hpp"
 
 namespace wr {
 
 namespace {
 
-constexpr float kLowest = -3.402823466e38f;
 constexpr int kPaged = 1024;  // tokens whose pages a wave holds: one of 64 tiles of 16 a lane
+constexpr int kUnit = 128;     // tokens of a round of a workgroup's four waves
 
-constexpr float kLift = 15.0f;   // log2 of what a row's largest weight is held as
-
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-
-__device__ __forceinline__ f32x4 mfma16x16x32_f16(const u32x4& a, const u32x4& b, const f32x4& c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-}
-__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
-__device__ __forceinline__ uint32_t pack_f16(float a, float b) {  // round to nearest even
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, f16x2));
-}
-// The values of the codes in bits 0..3 and 16..19, with a scale and an offset for each.
-__device__ __forceinline__ uint32_t two_values(uint32_t w, f16x2 scale, f16x2 off) {
-  const f16x2 lifted = __builtin_bit_cast(f16x2, (w & 0x000f000fu) | 0x64006400u);
-  const f16x2 c = lifted - f16x2{(_Float16)1024.0f, (_Float16)1024.0f};
-  return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(c, scale, off));
-}
-__device__ __forceinline__ f16x2 low_halves(uint32_t a, uint32_t b) {
-  return __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(b, a, 0x05040100u));
-}
-__device__ __forceinline__ f16x2 high_halves(uint32_t a, uint32_t b) {
-  return __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(b, a, 0x07060302u));
-}
-
-struct AttentionArgs {
-  KvArgs kv;
-  const uint16_t* q;
-  uint16_t* out;
-  float* part;   // unnormalised outputs of the chunks: (row, head, chunk, dim)
-  f32x2* stats;  // their maximum (of log2 weights) and sum: (row, head, chunk)
-  int64_t ldq, ldo;
-  int heads, share;  // query heads, and how many of them share a head of the cache
-  float scale;       // times log2(e)
-  int window;
-  bool causal;
-  int chunk, splits;  // tokens a workgroup takes, chunks of a row at most
+// What a lane holds of 32 tokens in two tiles of 16.
+template <int DIM, int GROUP>
+struct Step {
+  static constexpr int SL = DIM / 32, NG = DIM / GROUP;
+  uint32_t kc[2][SL], vc[2][SL];
+  uint32_t km[2][NG];  // scale and offset of the lane's own token, lane % 16
+  uint32_t vm[2][NG];  // dword lane % 4 of the scales and offsets of tokens 4 (lane / 16) .. + 3
+  bool there[2];
 };
 
-// The positions that queries first .. last of a sequence see: lo .. hi - 1.
-struct Span {
-  int lo, hi;
+// Where a lane's loads lie behind the tile's first codes, and behind a group's first scale of the tile.
+template <int DIM, int GROUP>
+struct StepOffsets {
+  uint32_t kc, vc, km, vm;
+  __device__ __forceinline__ explicit StepOffsets(int lane)
+      : kc(lane % 16 * (DIM / 2) + lane / 16 * (DIM / 8)), vc(lane * (DIM / 8)), km(lane % 16 * 4),
+        vm((lane / 16 * 4 + lane % 4) * 4) {}
 };
-__device__ __forceinline__ Span seen(const AttentionArgs& a, const KvSeq& s, int first, int last) {
-  const int64_t p0 = (int64_t)s.length - s.fresh + first, p1 = (int64_t)s.length - s.fresh + last;
-  int64_t hi = a.causal ? p1 + 1 : a.window ? p1 + a.window : s.length;
-  if (hi > s.length) hi = s.length;
-  int64_t lo = a.window ? p0 - a.window + 1 : 0;
-  if (lo < 0) lo = 0;
-  if (hi < lo) hi = lo;
-  return Span{(int)lo, (int)hi};
+
+template <int DIM, int GROUP>
+__device__ __forceinline__ void load_tile(Step<DIM, GROUP>& f, int tt, const uint8_t* base, const KvLayout<DIM, GROUP>& at,
+                                          int in_page, const StepOffsets<DIM, GROUP>& off) {
+  constexpr int kAlign = DIM / 8 < 16 ? DIM / 8 : 16;
+  const uint8_t* codes = base + in_page * (DIM / 2);
+  __builtin_memcpy(f.kc[tt], __builtin_assume_aligned(codes + off.kc, kAlign), DIM / 8);
+  __builtin_memcpy(f.vc[tt], __builtin_assume_aligned(codes + at.v_codes() + off.vc, kAlign), DIM / 8);
+#pragma unroll
+  for (int k = 0; k < DIM / GROUP; ++k) {
+    f.km[tt][k] = *reinterpret_cast<const uint32_t*>(base + at.k_meta() + (k * at.page_tokens + in_page) * 4 + off.km);
+    f.vm[tt][k] = *reinterpret_cast<const uint32_t*>(base + at.v_meta() + (k * at.page_tokens + in_page) * 4 + off.vm);
+  }
 }
 
-// The queries of a tile of rows (query, head of the share), numbered query first.
-struct RowTile {
-  int first, last;
-};
-__device__ __forceinline__ RowTile row_tile(const AttentionArgs& a, const KvSeq& s, int tile, int rows) {
-  const uint32_t m0 = tile * rows, m1 = min(m0 + rows, (uint32_t)(s.fresh * a.share)) - 1;
-  return RowTile{(int)(m0 / (uint32_t)a.share), (int)(m1 / (uint32_t)a.share)};
+// Lane N of each row of 16, for the whole row.
+template <int N>
+__device__ __forceinline__ uint32_t row_lane(uint32_t v) {
+  return __builtin_amdgcn_update_dpp(0, v, 0x150 + N, 0xf, 0xf, true);
 }
 
-// ---------------------------------------------------------------- few rows: 16 NT of them against one chunk
+// ---------------------------------------------------------------- who does what
+// The work is cut into units of kUnit tokens of a sequence and head, numbered sequence first, then head, then unit; every
+// workgroup gets an equal run of them, whatever the lengths are, and so takes the end of one (sequence, head), whole ones and
+// the start of another.  Only the device knows the lengths: each workgroup sums the sequences' units itself.
+
+// Units of a sequence and head; 1 for rows that see nothing, which get their zeros, and 0 for a sequence without rows.
+__device__ __forceinline__ uint32_t units_of(const AttentionArgs& a, const KvSeq& s) {
+  if (s.fresh <= 0) return 0;
+  const Span all = seen(a, s, 0, s.fresh - 1);
+  return max(1u, (uint32_t)(all.hi - (all.lo & ~15) + kUnit - 1) / kUnit);
+}
+
+struct Found {
+  uint32_t total;   // units of all
+  uint32_t seq;     // of unit x
+  uint32_t before;  // units of the sequences before it
+};
+struct FoundShared {
+  uint32_t waves[4], seq, before;
+};
+// The sequence of unit at(total), or, with sequence >= 0, what comes before that sequence.  For all 256 threads.
+template <typename F>
+__device__ __forceinline__ Found find_units(const AttentionArgs& a, FoundShared& f, int sequence, F&& at) {
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  if (a.kv.n <= kWave) {  // each wave by itself
+    const uint32_t mine = lane < a.kv.n ? units_of(a, kv_seq(a.kv, lane)) * a.kv.heads : 0;
+    uint32_t upto = mine;
+    for (int m = 1; m < a.kv.n; m <<= 1) {
+      const uint32_t below = __shfl_up(upto, m);
+      if (lane >= m) upto += below;
+    }
+    const uint32_t total = __builtin_amdgcn_readlane(upto, a.kv.n - 1);
+    if (sequence < 0) {  // the first that reaches past x
+      const uint64_t past = __builtin_amdgcn_ballot_w64(upto > at(total));
+      sequence = past ? __builtin_ctzll(past) : 0;
+    }
+    sequence = __builtin_amdgcn_readfirstlane(sequence);
+    return Found{total, (uint32_t)sequence, (uint32_t)__builtin_amdgcn_readlane(upto - mine, sequence)};
+  }
+  const int per = (a.kv.n + 255) / 256;
+  const int begin = min((int)threadIdx.x * per, a.kv.n), end = min(begin + per, a.kv.n);
+  uint32_t mine = 0;
+  for (int i = begin; i < end; ++i) mine += units_of(a, kv_seq(a.kv, i)) * a.kv.heads;
+  uint32_t upto = mine;  // of this and the lanes below
+#pragma unroll
+  for (int m = 1; m < kWave; m <<= 1) {
+    const uint32_t below = __shfl_up(upto, m);
+    if (lane >= m) upto += below;
+  }
+  if (lane == kWave - 1) f.waves[wave] = upto;
+  __syncthreads();
+  uint32_t total = 0, before = upto - mine;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    total += f.waves[w];
+    if (w < wave) before += f.waves[w];
+  }
+  const uint32_t x = at(total);
+  if (sequence >= 0 ? sequence >= begin && sequence < end : x >= before && x < before + mine) {
+    int i = begin;
+    for (; i + 1 < end; ++i) {
+      const uint32_t u = units_of(a, kv_seq(a.kv, i)) * a.kv.heads;
+      if (sequence >= 0 ? i == sequence : x < before + u) break;
+      before += u;
+    }
+    f.seq = i;
+    f.before = before;
+  }
+  __syncthreads();
+  return Found{total, f.seq, f.before};
+}
+// Unit where a workgroup begins; those beyond one for each unit have nothing.
+__device__ __forceinline__ uint32_t first_unit(uint32_t total, uint32_t group, uint32_t groups) {
+  groups = min(groups, total);
+  return group >= groups ? total : (uint32_t)((uint64_t)total * group / groups);
+}
+__device__ __forceinline__ uint32_t group_of(uint32_t total, uint32_t unit, uint32_t groups) {
+  return (uint32_t)((((uint64_t)unit + 1) * min(groups, total) - 1) / total);
+}
+
+// ---------------------------------------------------------------- the rows of a step
+// Workgroups that a compute unit holds at once, by the registers they take; as many are launched, since more would wait
+// and leave the end uneven.
+constexpr int groups_per_cu(int dim, int nt) { return dim == 64 ? 5 - nt : dim * nt == 128 ? 3 : dim * nt == 256 ? 2 : 1; }
+
 template <int DIM, int GROUP, int NT>
-__global__ __launch_bounds__(256) void attend_rows_kernel(AttentionArgs a, int tiles) {
+__global__ __launch_bounds__(256, groups_per_cu(DIM, NT)) void attend_rows_kernel(AttentionArgs a) {
   constexpr int SL = DIM / 32;      // slices of 32 dims: dwords a lane loads of a tile
   constexpr int NG = DIM / GROUP;
   constexpr int WAVES = 4;
   __shared__ __attribute__((aligned(16))) float sums[16 * NT][DIM + 4];
   __shared__ float tops[WAVES][16 * NT], dens[WAVES][16 * NT];
-
-  uint32_t block = blockIdx.x;
-  const int head = block % (uint32_t)a.kv.heads;
-  block /= (uint32_t)a.kv.heads;
-  const int tile = block % (uint32_t)tiles;
-  block /= (uint32_t)tiles;
-  const int split = block % (uint32_t)a.splits;
-  const int seq = block / (uint32_t)a.splits;
-
-  const KvSeq s = kv_seq(a.kv, seq);
-  if (s.fresh <= 0 || tile * 16 * NT >= s.fresh * a.share) return;
-  const RowTile rt = row_tile(a, s, tile, 16 * NT);
-  const Span all = seen(a, s, rt.first, rt.last);
-  const int begin = (all.lo & ~15) + split * a.chunk;
-  const int end = min(all.hi, begin + a.chunk);
-  if (split > 0 && begin >= end) return;  // the first chunk of rows that see nothing writes their zeros
-
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  __shared__ FoundShared found;
+  const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int col = lane % 16, g = lane / 16;
+  const uint32_t groups = gridDim.x;
+  const Found f0 = find_units(a, found, -1, [&](uint32_t total) { return first_unit(total, blockIdx.x, groups); });
+  uint32_t x = __builtin_amdgcn_readfirstlane(first_unit(f0.total, blockIdx.x, groups));
+  const uint32_t x1 = __builtin_amdgcn_readfirstlane(first_unit(f0.total, blockIdx.x + 1, groups));
+  int seq = __builtin_amdgcn_readfirstlane(f0.seq);
+  uint32_t y = x - __builtin_amdgcn_readfirstlane(f0.before);  // the unit's number in its sequence
+  while (x < x1 && seq < a.kv.n) {
+  const KvSeq s = kv_seq(a.kv, seq);
+  const uint32_t units = units_of(a, s);
+  if (y >= units * a.kv.heads) {  // on to the next one
+    ++seq;
+    y = 0;
+    continue;
+  }
+  const int head = y / units, unit0 = y % units;
+  const int taken = min(units - unit0, x1 - x);
+  x += taken;
+  y += taken;
+  const Span all = seen(a, s, 0, s.fresh - 1);
+  const int begin = (all.lo & ~15) + unit0 * kUnit;
+  const int end = min(all.hi, begin + taken * kUnit);
+  const int32_t* table = a.kv.table + (int64_t)seq * a.kv.ldt;
+  int pages = -1;
 
-  // queries, as fp16 times 2^-e each; unit: what turns a product into log2 of a weight
-  u32x4 qr[NT][SL];
-  float unit[NT];
+  const KvLayout<DIM, GROUP> at{1 << a.kv.page_shift};
+  const int64_t page_bytes = (int64_t)a.kv.heads * at.head_bytes();
+  const uint8_t* cache = a.kv.pages + (int64_t)head * at.head_bytes();
+  // queries, as fp16 times +-2^-e each; unit >= 0: what turns a product into log2 of a weight
   Span mine[NT];
-  const Span first = seen(a, s, rt.first, rt.first), last = seen(a, s, rt.last, rt.last);
+  const int every_lo = seen(a, s, s.fresh - 1, s.fresh - 1).lo, every_hi = seen(a, s, 0, 0).hi;  // seen by every row
+  Raw8<uint16_t> raw[NT][SL];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const uint32_t m = tile * 16 * NT + 16 * n + col;
+    const uint32_t m = 16 * n + col;
     const bool live = m < (uint32_t)(s.fresh * a.share);
     const int j = m / (uint32_t)a.share, h = head * a.share + m % (uint32_t)a.share;
     mine[n] = live ? seen(a, s, j, j) : Span{0, 0};
     const uint16_t* qp = a.q + (int64_t)(s.row + (live ? j : 0)) * a.ldq + (int64_t)(live ? h : 0) * DIM + 8 * g;
-    Raw8<uint16_t> x[SL];
+#pragma unroll
+    for (int sl = 0; sl < SL; ++sl) raw[n][sl].load(qp + 32 * sl);
+  }
+
+  const Unpack unpack;
+  const StepOffsets<DIM, GROUP> lanes(lane);
+  // the loads of the 32 tokens from t0, which may be past the end
+  auto fetch = [&](Step<DIM, GROUP>& f, int t0) {
+    StepOffsets<DIM, GROUP> off = lanes;
+    asm("" : "+v"(off.kc), "+v"(off.vc), "+v"(off.km), "+v"(off.vm));  // 32 bits beside a scalar address, not 64 hoisted
+    const int nth0 = (t0 - begin) % kPaged / 16;
+    if (nth0 < 2 * WAVES) {
+      const int t = t0 + 16 * (lane - nth0);
+      pages = t < end ? table[t >> a.kv.page_shift] : -1;
+      asm volatile("" : "+v"(pages));  // waited for here, not in every step with all that is on its way
+    }
+#pragma unroll
+    for (int tt = 0; tt < 2; ++tt) {
+      const int t = t0 + 16 * tt;
+      int page = __builtin_amdgcn_readlane(pages, nth0 + tt);
+      f.there[tt] = t < end && page >= 0 && page < a.kv.count;
+      if (!f.there[tt]) page = 0;
+      load_tile(f, tt, cache + page * page_bytes, at, t & (at.page_tokens - 1), off);
+    }
+  };
+  // two steps in turn, each loaded while the other is worked on; the first comes before the queries are looked at
+  constexpr int kRound = 32 * WAVES;
+  Step<DIM, GROUP> even, odd;
+  int t0 = begin + 32 * wave;
+  fetch(even, t0);
+  u32x4 qr[NT][SL];
+  float unit[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
     float big = 0.0f;
 #pragma unroll
-    for (int sl = 0; sl < SL; ++sl) {
-      x[sl].load(qp + 32 * sl);
+    for (int sl = 0; sl < SL; ++sl)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[sl].get(e)));
-    }
-    big = fmaxf(big, __shfl_xor(big, 16));
-    big = fmaxf(big, __shfl_xor(big, 32));
+      for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(raw[n][sl].get(e)));
+    big = max_of_four(big);
     // 2^e <= big < 2^(e + 1), within what has a reciprocal in fp32
     const int e = min(max((int)(__float_as_uint(big) >> 23) - 127, -120), 120);
-    const float down = live ? __uint_as_float((uint32_t)(127 - e) << 23) : 0.0f;
-    unit[n] = a.scale * __uint_as_float((uint32_t)(127 + e) << 23);
+    const float down = copysignf(__uint_as_float((uint32_t)(127 - e) << 23), a.scale);
+    unit[n] = fabsf(a.scale) * __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
     for (int sl = 0; sl < SL; ++sl)
 #pragma unroll
       for (int i = 0; i < 4; ++i)  // codes i and 4 + i of a dword go together
-        qr[n][sl][i] = live ? pack_f16(x[sl].get(i) * down, x[sl].get(4 + i) * down) : 0u;
+        qr[n][sl][i] = pack_f16(raw[n][sl].get(i) * down, raw[n][sl].get(4 + i) * down);
   }
 
   f32x4 acc[NT][2][SL];  // [half][m]: dims half * DIM / 2 + 16 m + 4 g + r
@@ -151,43 +246,12 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttentionArgs a, int t
     for (int m = 0; m < SL; ++m) acc[n][0][m] = acc[n][1][m] = zero;
   }
 
-  const KvLayout<DIM, GROUP> at{1 << a.kv.page_shift};
-  const int64_t page_bytes = (int64_t)a.kv.heads * at.head_bytes();
-  const uint8_t* cache = a.kv.pages + (int64_t)head * at.head_bytes();
-  const int32_t* table = a.kv.table + (int64_t)seq * a.kv.ldt;
-  int pages = -1;
-
-  for (int t0 = begin + 32 * wave; t0 < end; t0 += 32 * WAVES) {
-    const int nth0 = (t0 - begin) % kPaged / 16;
-    if (nth0 < 2 * WAVES) {
-      const int t = t0 + 16 * (lane - nth0);
-      pages = t < end ? table[t >> a.kv.page_shift] : -1;
-    }
-    uint32_t kc[2][SL], vc[2][SL];
-    uint32_t km[2][NG];
-    u32x4 vm[2][NG];
-    bool there[2];
-#pragma unroll
-    for (int tt = 0; tt < 2; ++tt) {
-      const int t = t0 + 16 * tt;
-      int page = __builtin_amdgcn_readlane(pages, nth0 + tt);
-      there[tt] = t < end && page >= 0 && page < a.kv.count;
-      if (!there[tt]) page = 0;
-      const int in_page = t & (at.page_tokens - 1);
-      const uint8_t* base = cache + page * page_bytes;
-      const uint8_t* kp = base + in_page * (DIM / 2) + col * (DIM / 2) + g * (DIM / 8);
-      const uint8_t* vp = base + at.v_codes() + in_page * (DIM / 2) + lane * (DIM / 8);
-      __builtin_memcpy(kc[tt], __builtin_assume_aligned(kp, DIM / 8 < 16 ? DIM / 8 : 16), SL * 4);
-      __builtin_memcpy(vc[tt], __builtin_assume_aligned(vp, DIM / 8 < 16 ? DIM / 8 : 16), SL * 4);
-#pragma unroll
-      for (int k = 0; k < NG; ++k) {
-        km[tt][k] = *reinterpret_cast<const uint32_t*>(base + at.k_meta() + (k * at.page_tokens + in_page + col) * 4);
-        vm[tt][k] = *reinterpret_cast<const u32x4*>(base + at.v_meta() + (k * at.page_tokens + in_page + 4 * g) * 4);
-      }
-    }
+  auto attend = [&](Step<DIM, GROUP>& f, int t0) {
     // every row sees all of these 32 tokens
-    const bool whole = there[0] && there[1] && t0 + 32 <= min(first.hi, last.hi) && t0 >= max(first.lo, last.lo);
-
+    const bool whole = f.there[0] && f.there[1] && t0 + 32 <= every_hi && t0 >= every_lo;
+    const uint32_t(&kc)[2][SL] = f.kc, (&vc)[2][SL] = f.vc, (&km)[2][NG] = f.km;
+    uint32_t(&vm)[2][NG] = f.vm;
+    const bool(&there)[2] = f.there;
     f32x4 score[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) score[n][0] = score[n][1] = zero;
@@ -196,8 +260,8 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttentionArgs a, int t
 #pragma unroll
       for (int sl = 0; sl < SL; ++sl) {
         const uint32_t meta = km[tt][sl * 32 / GROUP], w = kc[tt][sl];
-        const f16x2 sc = low_halves(meta, meta), of = high_halves(meta, meta);
-        const u32x4 keys{two_values(w, sc, of), two_values(w >> 4, sc, of), two_values(w >> 8, sc, of), two_values(w >> 12, sc, of)};
+        const f16x2 both = __builtin_bit_cast(f16x2, meta), sc = both.xx, of = both.yy;
+        const u32x4 keys{unpack.two<0>(w, sc, of), unpack.two<4>(w, sc, of), unpack.two<0>(w >> 8, sc, of), unpack.two<4>(w >> 8, sc, of)};
 #pragma unroll
         for (int n = 0; n < NT; ++n) score[n][tt] = mfma16x16x32_f16(keys, qr[n][sl], score[n][tt]);
       }
@@ -206,20 +270,28 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttentionArgs a, int t
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float p[2][4];
-      float high = kLowest;
+      int ok = 255;
 #pragma unroll
       for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          p[tt][i] = score[n][tt][i] * unit[n];
-          if (!whole) {
+        for (int i = 0; i < 4; ++i) p[tt][i] = score[n][tt][i];
+      if (!whole) {
+        asm volatile("");  // a branch, not selects in every step
+        ok = 0;
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
             const int t = t0 + 16 * tt + 4 * g + i;
-            if (!(there[tt] && t >= mine[n].lo && t < mine[n].hi)) p[tt][i] = -INFINITY;
+            const bool in = there[tt] && t >= mine[n].lo && t < mine[n].hi;
+            ok |= in << (4 * tt + i);
+            if (!in) p[tt][i] = -INFINITY;
           }
-          high = fmaxf(high, p[tt][i]);
-        }
-      high = fmaxf(high, __shfl_xor(high, 16));
-      high = fmaxf(high, __shfl_xor(high, 32));
+      }
+      float high = fmaxf(fmaxf(fmaxf(p[0][0], p[0][1]), fmaxf(p[0][2], p[0][3])),
+                         fmaxf(fmaxf(p[1][0], p[1][1]), fmaxf(p[1][2], p[1][3])));
+      high = max_of_four(high);
+      high = high == -INFINITY ? kLowest : high * unit[n];
       if (__builtin_amdgcn_ballot_w64(high > top[n]) != 0) {
         const float now = fmaxf(high, top[n]);
         const float keep = exp2_fast(top[n] - now);
@@ -235,67 +307,86 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttentionArgs a, int t
 #pragma unroll
       for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          p[tt][i] = exp2_fast(p[tt][i] - less);
-          den[n] += p[tt][i];
-        }
+        for (int i = 0; i < 4; ++i) p[tt][i] = exp2_fast(fmaf(p[tt][i], unit[n], -less));
+      if (!whole) {
+        asm volatile("");
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!(ok >> (4 * tt + i) & 1)) p[tt][i] = 0.0f;
+      }
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) den[n] += p[tt][i];
       weights[n] = u32x4{pack_f16(p[0][0], p[0][2]), pack_f16(p[0][1], p[0][3]), pack_f16(p[1][0], p[1][2]),
                          pack_f16(p[1][1], p[1][3])};
     }
-    if (!whole) {
-      // A token that a row does not see may hold NaNs or anything, which its weight of 0 would not hide: what no row
-      // sees becomes 0, and a NaN goes to the rows that see it by itself.
-      int poison[NT] = {};
-#pragma unroll
-      for (int tt = 0; tt < 2; ++tt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = t0 + 16 * tt + 4 * g + i;
-#pragma unroll
-          for (int k = 0; k < NG; ++k) {
-            if (!(there[tt] && t >= all.lo && t < all.hi)) vm[tt][k][i] = 0;
-            if ((vm[tt][k][i] & 0x7fffu) <= 0x7c00u) continue;
-            vm[tt][k][i] = 0;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-              if (t >= mine[n].lo && t < mine[n].hi) poison[n] |= 1 << k;
-          }
-        }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if (__builtin_amdgcn_ballot_w64(poison[n] != 0) == 0) continue;
-        poison[n] |= __shfl_xor(poison[n], 16);
-        poison[n] |= __shfl_xor(poison[n], 32);
-#pragma unroll
-        for (int m = 0; m < SL; ++m)
-#pragma unroll
-          for (int half = 0; half < 2; ++half)
-            if (poison[n] >> ((half * (DIM / 2) + 16 * m) / GROUP) & 1)
-              acc[n][half][m] = f32x4{NAN, NAN, NAN, NAN};
-      }
-    }
 #pragma unroll
     for (int k = 0; k < NG; ++k) {
-      f16x2 sc[2][2], of[2][2];  // tokens 0 and 2, 1 and 3
+      uint32_t sc[2][2], of[2][2];  // tokens 0 and 2, 1 and 3
 #pragma unroll
-      for (int tt = 0; tt < 2; ++tt)
+      for (int tt = 0; tt < 2; ++tt) {
+        sc[tt][0] = row_lane<0>(vm[tt][k]);
+        of[tt][0] = row_lane<1>(vm[tt][k]);
+        sc[tt][1] = row_lane<2>(vm[tt][k]);
+        of[tt][1] = row_lane<3>(vm[tt][k]);
+      }
+      if (!whole) {
+        asm volatile("");
+        // A token that a row does not see may hold NaNs or anything, which its weight of 0 would not hide: what no row
+        // sees becomes 0, and a NaN goes to the rows that see it by itself.
+        int bad[NT] = {};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          sc[tt][i] = low_halves(vm[tt][k][i], vm[tt][k][i + 2]);
-          of[tt][i] = high_halves(vm[tt][k][i], vm[tt][k][i + 2]);
+        for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = t0 + 16 * tt + 4 * g + i;
+            const bool in = there[tt] && t >= all.lo && t < all.hi;
+            const bool nan = in && (sc[tt][i % 2] >> (16 * (i / 2)) & 0x7fffu) > 0x7c00u;
+            if (!in || nan) {
+              sc[tt][i % 2] &= i / 2 ? 0x0000ffffu : 0xffff0000u;
+              of[tt][i % 2] &= i / 2 ? 0x0000ffffu : 0xffff0000u;
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) bad[n] |= nan && t >= mine[n].lo && t < mine[n].hi;
+          }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (__builtin_amdgcn_ballot_w64(bad[n] != 0) == 0) continue;
+          bad[n] |= __shfl_xor(bad[n], 16);
+          bad[n] |= __shfl_xor(bad[n], 32);
+          if (bad[n])
+#pragma unroll
+            for (int m = 0; m < SL; ++m)
+#pragma unroll
+              for (int half = 0; half < 2; ++half)
+                if ((half * (DIM / 2) + 16 * m) / GROUP == k) acc[n][half][m] = f32x4{NAN, NAN, NAN, NAN};
         }
+      }
 #pragma unroll
       for (int m = 0; m < SL; ++m)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           if ((half * (DIM / 2) + 16 * m) / GROUP != k) continue;
-          const int sh = 4 * half;
-          const u32x4 values{two_values(vc[0][m] >> sh, sc[0][0], of[0][0]), two_values(vc[0][m] >> (8 + sh), sc[0][1], of[0][1]),
-                             two_values(vc[1][m] >> sh, sc[1][0], of[1][0]), two_values(vc[1][m] >> (8 + sh), sc[1][1], of[1][1])};
+          auto two = [&](uint32_t w, int tt, int i) {
+            const f16x2 x = __builtin_bit_cast(f16x2, sc[tt][i]), y = __builtin_bit_cast(f16x2, of[tt][i]);
+            return half ? unpack.two<4>(w, x, y) : unpack.two<0>(w, x, y);
+          };
+          const u32x4 values{two(vc[0][m], 0, 0), two(vc[0][m] >> 8, 0, 1), two(vc[1][m], 1, 0), two(vc[1][m] >> 8, 1, 1)};
 #pragma unroll
           for (int n = 0; n < NT; ++n) acc[n][half][m] = mfma16x16x32_f16(values, weights[n], acc[n][half][m]);
         }
     }
+  };
+  while (t0 < end) {
+    fetch(odd, t0 + kRound);
+    attend(even, t0);
+    if (t0 + kRound >= end) break;
+    fetch(even, t0 + 2 * kRound);
+    attend(odd, t0 + kRound);
+    t0 += 2 * kRound;
   }
 
   // the waves' parts: one maximum, then the sums in the waves' order
@@ -335,7 +426,7 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttentionArgs a, int t
   }
   for (int u = threadIdx.x; u < 16 * NT * (DIM / 4); u += 256) {
     const int r = u / (DIM / 4), d = u % (DIM / 4) * 4;
-    const uint32_t m = tile * 16 * NT + r;
+    const uint32_t m = r;
     if (m >= (uint32_t)(s.fresh * a.share)) break;
     const int64_t row = s.row + m / (uint32_t)a.share;
     const int h = head * a.share + m % (uint32_t)a.share;
@@ -345,82 +436,100 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttentionArgs a, int t
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) total += dens[w][r] * exp2_fast(tops[w][r] - now);
     const f32x4 v = *reinterpret_cast<const f32x4*>(&sums[r][d]);
-    if (a.splits == 1) {
+    if ((uint32_t)taken == units) {
       const float inv = total == 0.0f ? 0.0f : 1.0f / total;
       u32x2_any o;
       o[0] = pack_bf16(v[0] * inv, v[1] * inv);
       o[1] = pack_bf16(v[2] * inv, v[3] * inv);
       *reinterpret_cast<u32x2_any*>(a.out + row * a.ldo + (int64_t)h * DIM + d) = o;
-    } else {
-      const int64_t slot = (row * a.heads + h) * a.splits + split;
+    } else {  // a workgroup has at most one part that others began and one that others go on with
+      const int64_t slot = ((int64_t)blockIdx.x * 2 + (unit0 == 0)) * (16 * NT) + r;
       *reinterpret_cast<f32x4*>(a.part + slot * DIM + d) = v;
       if (d == 0) a.stats[slot] = f32x2{now, total};
     }
   }
+  __syncthreads();
+  }
 }
 
-// The chunks' parts of a row, added in the chunks' order: a wave a row and head.
+// The parts of a row and head that went to several workgroups: a workgroup each, of 4 waves that take every fourth part.
 template <int DIM>
-__global__ __launch_bounds__(256) void attend_join_kernel(AttentionArgs a, int tile_rows) {
-  constexpr int PER = DIM / kWave;
-  const int lane = threadIdx.x % kWave;
-  const uint32_t unit = blockIdx.x * 4 + threadIdx.x / kWave;
-  const int h = unit % (uint32_t)a.heads;
-  const uint32_t rest = unit / (uint32_t)a.heads;
+__global__ __launch_bounds__(256) void attend_join_kernel(AttentionArgs a, int rows, uint32_t groups) {
+  constexpr int PER = DIM / kWave, WAVES = 4;
+  __shared__ float sums[WAVES][DIM], dens[WAVES], tops[WAVES];
+  __shared__ FoundShared found;
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int h = blockIdx.x % (uint32_t)a.heads;
+  const uint32_t rest = blockIdx.x / (uint32_t)a.heads;
   const int j = rest % (uint32_t)a.kv.most_new;
   const int seq = rest / (uint32_t)a.kv.most_new;
-  if (seq >= a.kv.n) return;
+  const Found f = find_units(a, found, seq, [](uint32_t) { return 0u; });
   const KvSeq s = kv_seq(a.kv, seq);
   if (j >= s.fresh) return;
-  const int m = j * a.share + h % a.share;
-  const RowTile rt = row_tile(a, s, m / tile_rows, tile_rows);
-  const Span all = seen(a, s, rt.first, rt.last);
-  const int parts = min(a.splits, max(1, (all.hi - (all.lo & ~15) + a.chunk - 1) / a.chunk));
-  const int64_t slot = ((int64_t)(s.row + j) * a.heads + h) * a.splits;
-  float top = kLowest;
-  for (int c = lane; c < parts; c += kWave) top = fmaxf(top, a.stats[slot + c].x);
-  for (int x = 1; x < kWave; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
-  float sum[PER], total = 0.0f;
+  const uint32_t units = units_of(a, s), first = f.before + h / a.share * units;
+  const uint32_t b0 = group_of(f.total, first, groups), b1 = group_of(f.total, first + units - 1, groups);
+  if (b0 == b1) return;  // it has written the row
+  const int m = j * a.share + h % a.share, parts = b1 - b0 + 1;
+  float top = kLowest, total = 0.0f, sum[PER];
 #pragma unroll
   for (int e = 0; e < PER; ++e) sum[e] = 0.0f;
-#pragma unroll 4
-  for (int c = 0; c < parts; ++c) {
-    const f32x2 st = a.stats[slot + c];
-    const float keep = exp2_fast(st.x - top);
-    total = fmaf(st.y, keep, total);
+  for (int c0 = wave; c0 < parts; c0 += WAVES * 8) {  // eight parts at a time
+    f32x2 st[8];
+    float v[8][PER];
 #pragma unroll
-    for (int e = 0; e < PER; ++e) sum[e] = fmaf(a.part[(slot + c) * DIM + e * kWave + lane], keep, sum[e]);
+    for (int i = 0; i < 8; ++i) {
+      const int c = min(c0 + WAVES * i, parts - 1);
+      const int64_t slot = ((int64_t)(b0 + c) * 2 + (c == 0)) * rows + m;
+      st[i] = a.stats[slot];
+      if (c0 + WAVES * i >= parts) st[i] = f32x2{kLowest, 0.0f};
+#pragma unroll
+      for (int e = 0; e < PER; ++e) v[i][e] = a.part[slot * DIM + e * kWave + lane];
+    }
+    float now = top;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) now = fmaxf(now, st[i].x);
+    float keep = exp2_fast(top - now);
+    top = now;
+    total *= keep;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) sum[e] *= keep;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (c0 + WAVES * i >= parts) break;
+      keep = exp2_fast(st[i].x - now);
+      total = fmaf(st[i].y, keep, total);
+#pragma unroll
+      for (int e = 0; e < PER; ++e) sum[e] = fmaf(v[i][e], keep, sum[e]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < PER; ++e) sums[wave][e * kWave + lane] = sum[e];
+  if (lane == 0) {
+    dens[wave] = total;
+    tops[wave] = top;
+  }
+  __syncthreads();
+  float now = kLowest;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) now = fmaxf(now, tops[w]);
+  total = 0.0f;
+  float keep[WAVES];
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    keep[w] = exp2_fast(tops[w] - now);
+    total = fmaf(dens[w], keep[w], total);
   }
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   uint16_t* o = a.out + (int64_t)(s.row + j) * a.ldo + (int64_t)h * DIM;
+  for (int d = threadIdx.x; d < DIM; d += 256) {
+    float v = 0.0f;
 #pragma unroll
-  for (int e = 0; e < PER; ++e) o[e * kWave + lane] = (uint16_t)f32_to_bf16_bits(sum[e] * inv);
+    for (int w = 0; w < WAVES; ++w) v = fmaf(sums[w][d], keep[w], v);
+    o[d] = (uint16_t)f32_to_bf16_bits(v * inv);
+  }
 }
 
-struct Plan {
-  int chunk, splits;
-  int64_t tiles;  // row tiles of a sequence and head
-};
-
-constexpr int kTileRows = 16;
-constexpr int kWanted = 2048;  // workgroups: eight for every compute unit
-
-Plan plan_of(const wr_kv_cache& c, const wr_kv_seqs& s, int heads, int flags, int window) {
-  const int share = heads / c.heads;
-  Plan p;
-  p.tiles = ((int64_t)s.most_new * share + kTileRows - 1) / kTileRows;
-  // positions that a tile's rows can see, from a multiple of 16
-  const int64_t queries = std::min<int64_t>(s.most_new, (kTileRows + share - 2) / share + 1);
-  int64_t span = std::min<int64_t>(s.most_tokens, (int64_t)s.width * c.page_tokens);
-  if (window > 0) span = std::min(span, (int64_t)window * (flags & WR_ATTENTION_CAUSAL ? 1 : 2) + queries + 15);
-  const int64_t groups = std::max<int64_t>(1, s.n * p.tiles * c.heads);
-  const int64_t most_splits = std::max<int64_t>(1, kWanted / groups);
-  int64_t chunk = std::max<int64_t>(128, (span + most_splits - 1) / most_splits);
-  chunk = (chunk + 127) / 128 * 128;
-  p.chunk = (int)std::min<int64_t>(chunk, 1 << 30);
-  p.splits = (int)std::max<int64_t>(1, (span + chunk - 1) / chunk);
-  return p;
-}
+constexpr int kMostCUs = 256;  // what the workspace is sized for
 
 }  // namespace
 
@@ -428,25 +537,23 @@ Plan plan_of(const wr_kv_cache& c, const wr_kv_seqs& s, int heads, int flags, in
 
 using namespace wr;
 
-// The chunks are split off only up to kWanted workgroups, each with kTileRows rows at most.
+size_t wr_kv_many_ws_bytes(int64_t rows, int64_t n, int32_t dim);
+int wr_kv_many_impl(wr_ctx* ctx, const wr_kv_cache& c, const wr_kv_seqs& s, AttentionArgs a, int flags);
+
 size_t wr_kv_attention_ws_bytes(int64_t rows, int64_t n, int32_t dim) {
-  const int64_t parts = kWanted * std::min<int64_t>(kTileRows, rows * (n / dim));
-  return (size_t)parts * (dim + 2) * sizeof(float);
+  size_t parts = 0;
+  for (int r : {16, 32}) parts = std::max(parts, (size_t)groups_per_cu(dim, r / 16) * kMostCUs * 2 * r);
+  return std::max(parts * (dim + 2) * sizeof(float), wr_kv_many_ws_bytes(rows, n, dim));
 }
 
 int wr_kv_attention_impl(wr_ctx* ctx, const wr_kv_cache& c, const wr_kv_seqs& s, const void* q, int64_t ldq, int64_t rows,
                          int32_t heads, float scale, int flags, int32_t window, void* out, int64_t ldo) {
-  const Plan p = plan_of(c, s, heads, flags, window);
-  const int64_t blocks = (int64_t)s.n * p.splits * p.tiles * c.heads;
-  const int64_t joins = ((int64_t)s.n * s.most_new * heads + 3) / 4;
-  if (blocks > 1 << 30 || joins > 1 << 29) return WR_EUNSUPPORTED;
-  if (p.splits > 1 && ctx->ws_bytes < (size_t)rows * heads * p.splits * (c.dim + 2) * sizeof(float)) return WR_EWORKSPACE;
   AttentionArgs a;
   a.kv = kv_args(c, s, rows);
   a.q = static_cast<const uint16_t*>(q);
   a.out = static_cast<uint16_t*>(out);
   a.part = static_cast<float*>(ctx->ws);
-  a.stats = reinterpret_cast<f32x2*>(a.part + (size_t)rows * heads * p.splits * c.dim);
+  a.stats = nullptr;
   a.ldq = ldq;
   a.ldo = ldo;
   a.heads = heads;
@@ -454,13 +561,25 @@ int wr_kv_attention_impl(wr_ctx* ctx, const wr_kv_cache& c, const wr_kv_seqs& s,
   a.scale = scale * 1.4426950408889634f;
   a.window = window;
   a.causal = flags & WR_ATTENTION_CAUSAL;
-  a.chunk = p.chunk;
-  a.splits = p.splits;
+  a.chunk = a.splits = 0;
+  const int64_t most_rows = (int64_t)s.most_new * a.share;
+  if (most_rows > 32) return wr_kv_many_impl(ctx, c, s, a, flags);
+
+  const int tile = most_rows <= 16 ? 16 : 32;
+  const int64_t most_units = (int64_t)s.n * c.heads * ((a.kv.most_tokens + 15 + kUnit) / kUnit + 1);
+  const int64_t joins = (int64_t)s.n * s.most_new * heads;
+  if (most_units > 1 << 30 || joins > 1 << 30) return WR_EUNSUPPORTED;
+  const int groups = (int)std::min<int64_t>(groups_per_cu(c.dim, tile / 16) * std::min(ctx->num_cu, kMostCUs), most_units);
+  const size_t parts = (size_t)groups * 2 * tile;
+  if (ctx->ws_bytes < parts * (c.dim + 2) * sizeof(float)) return WR_EWORKSPACE;
+  a.stats = reinterpret_cast<f32x2*>(a.part + parts * c.dim);
   const bool there = kv_form(c.dim, c.group, [&](auto d, auto g) {
     constexpr int D = decltype(d)::value, G = decltype(g)::value;
-    hipLaunchKernelGGL((attend_rows_kernel<D, G, 1>), dim3((uint32_t)blocks), dim3(256), 0, ctx->stream, a, (int)p.tiles);
-    if (p.splits > 1)
-      hipLaunchKernelGGL(attend_join_kernel<D>, dim3((uint32_t)joins), dim3(256), 0, ctx->stream, a, kTileRows);
+    if (tile == 16)
+      hipLaunchKernelGGL((attend_rows_kernel<D, G, 1>), dim3(groups), dim3(256), 0, ctx->stream, a);
+    else
+      hipLaunchKernelGGL((attend_rows_kernel<D, G, 2>), dim3(groups), dim3(256), 0, ctx->stream, a);
+    hipLaunchKernelGGL(attend_join_kernel<D>, dim3((uint32_t)joins), dim3(256), 0, ctx->stream, a, tile, (uint32_t)groups);
   });
   if (!there) return WR_EUNSUPPORTED;
   WR_CHECK_LAUNCH();

@@ -105,9 +105,16 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvArgs a, int tiles,
       vcodes[token][c] = codes;
     else
       *reinterpret_cast<uint32_t*>(base + in_page * (DIM / 2) + (c % 4) * (DIM / 8) + (c / 4) * 4) = codes;
-    if (c % (GROUP / 8) == 0)
-      *reinterpret_cast<uint32_t*>(base + (values ? at.v_meta() : at.k_meta()) +
-                                   ((c / (GROUP / 8)) * at.page_tokens + in_page) * 4) = meta;
+    if (c % (GROUP / 8) == 0) {
+      const int first = (c / (GROUP / 8)) * at.page_tokens;
+      if (values) {
+        uint16_t* m = reinterpret_cast<uint16_t*>(base + at.v_meta()) + at.v_scale(first, in_page);
+        m[0] = (uint16_t)meta;
+        m[2] = (uint16_t)(meta >> 16);
+      } else {
+        *reinterpret_cast<uint32_t*>(base + at.k_meta() + (first + in_page) * 4) = meta;
+      }
+    }
   }
   if (!v) return;
   __syncthreads();
@@ -162,9 +169,10 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvArgs a, int tiles, 
     float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (there) {
       const int in_page = t.at + token;
-      const uint32_t meta = *reinterpret_cast<const uint32_t*>(base + (values ? at.v_meta() : at.k_meta()) +
-                                                               ((c / (GROUP / 8)) * at.page_tokens + in_page) * 4);
-      const float scale = f16_bits_to_f32((uint16_t)meta), off = f16_bits_to_f32((uint16_t)(meta >> 16));
+      const int first = (c / (GROUP / 8)) * at.page_tokens;
+      const uint16_t* m = values ? reinterpret_cast<const uint16_t*>(base + at.v_meta()) + at.v_scale(first, in_page)
+                                 : reinterpret_cast<const uint16_t*>(base + at.k_meta()) + 2 * (first + in_page);
+      const float scale = f16_bits_to_f32(m[0]), off = f16_bits_to_f32(m[values ? 2 : 1]);
       uint32_t codes;
       if (values) {
         codes = 0;

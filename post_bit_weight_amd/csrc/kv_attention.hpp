@@ -1,0 +1,88 @@
+// What the kernels of attention over the 4-bit cache share: their arguments, what rows see, and how codes become values.
+//
+// A value s c + o (code c, scale s and offset o of its group) becomes an fp16 number, rounded once, on its way to
+// the matrix cores: the code OR-ed into the mantissa of 1024 is the fp16 number 1024 + c, less 1024 is c, and one packed
+// fused multiply-add makes two values.  All of that is exact up to the one rounding (2^-11 relative; s and o are fp16,
+// so that small values are exact multiples of 2^-24, and the cache holds nothing beyond fp16's range), an eighth of what bf16 would lose.
+// Queries are scaled by a power of two each, which the scores give back, and fit fp16 exactly.  Weights are kept
+// as 2^15 times what they are relative to the row's largest: fp16 then holds those down to 2^-39 of it.
+#pragma once
+#include "kv_cache.hpp"
+
+namespace wr {
+
+constexpr float kLowest = -3.402823466e38f;
+
+constexpr float kLift = 15.0f;   // log2 of what a row's largest weight is held as
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ f32x4 mfma16x16x32_f16(const u32x4& a, const u32x4& b, const f32x4& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {  // round to nearest even
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, f16x2));
+}
+// The values of the codes in bits 0..3 and 16..19 (AT 0) or 4..7 and 20..23 (AT 4), with a scale and an offset for each.
+// In the mantissa of 1024 the last four bits count ones, in that of 64 the four above them.
+struct Unpack {
+  uint32_t mask[2], over[2];  // in registers, so that one instruction can take both
+  __device__ __forceinline__ Unpack() : mask{0x000f000fu, 0x00f000f0u}, over{0x64006400u, 0x54005400u} {
+    asm("" : "+s"(mask[0]), "+s"(mask[1]));
+    asm("" : "+v"(over[0]), "+v"(over[1]));
+  }
+  template <int AT>
+  __device__ __forceinline__ uint32_t two(uint32_t w, f16x2 scale, f16x2 off) const {
+    constexpr int i = AT / 4;
+    const f16x2 c = __builtin_bit_cast(f16x2, (w & mask[i]) | over[i]) - __builtin_bit_cast(f16x2, over[i]);
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(c, scale, off));
+  }
+};
+// The largest of the four lanes that differ in bits 4 and 5.
+__device__ __forceinline__ float max_of_four(float v) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+
+struct AttentionArgs {
+  KvArgs kv;
+  const uint16_t* q;
+  uint16_t* out;
+  float* part;   // unnormalised outputs of parts of a row's positions
+  f32x2* stats;  // their maximum (of log2 weights) and sum
+  int64_t ldq, ldo;
+  int heads, share;  // query heads, and how many of them share a head of the cache
+  float scale;       // times log2(e)
+  int window;
+  bool causal;
+  int chunk, splits;  // many rows: tokens that a workgroup takes, chunks of a row at most
+};
+
+// The positions that queries first .. last of a sequence see: lo .. hi - 1.
+struct Span {
+  int lo, hi;
+};
+__device__ __forceinline__ Span seen(const AttentionArgs& a, const KvSeq& s, int first, int last) {
+  const int64_t p0 = (int64_t)s.length - s.fresh + first, p1 = (int64_t)s.length - s.fresh + last;
+  int64_t hi = a.causal ? p1 + 1 : a.window ? p1 + a.window : s.length;
+  if (hi > s.length) hi = s.length;
+  int64_t lo = a.window ? p0 - a.window + 1 : 0;
+  if (lo < 0) lo = 0;
+  if (hi < lo) hi = lo;
+  return Span{(int)lo, (int)hi};
+}
+
+// The queries of a tile of rows (query, head of the share), numbered query first.
+struct RowTile {
+  int first, last;
+};
+__device__ __forceinline__ RowTile row_tile(const AttentionArgs& a, const KvSeq& s, int tile, int rows) {
+  const uint32_t m0 = tile * rows, m1 = min(m0 + rows, (uint32_t)(s.fresh * a.share)) - 1;
+  return RowTile{(int)(m0 / (uint32_t)a.share), (int)(m1 / (uint32_t)a.share)};
+}
+
+}  // namespace wr

@@ -22,6 +22,10 @@ struct KvLayout {
   __device__ __forceinline__ int v_codes() const { return codes(); }
   __device__ __forceinline__ int k_meta() const { return 2 * codes(); }
   __device__ __forceinline__ int v_meta() const { return 2 * codes() + metas(); }
+  // Among the values' fp16 numbers: the scale of a token; its offset is two behind it.
+  __device__ __forceinline__ int v_scale(int first, int token) const {
+    return 2 * (first + (token & ~3)) + 4 * (token & 1) + (token >> 1 & 1);
+  }
 };
 
 // What a kernel gets of wr_kv_cache and wr_kv_seqs.
