@@ -45,12 +45,6 @@ __device__ __forceinline__ void load_tile(Step<DIM, GROUP>& f, int tt, const uin
   }
 }
 
-// Lane N of each row of 16, for the whole row.
-template <int N>
-__device__ __forceinline__ uint32_t row_lane(uint32_t v) {
-  return __builtin_amdgcn_update_dpp(0, v, 0x150 + N, 0xf, 0xf, true);
-}
-
 // ---------------------------------------------------------------- who does what
 // The work is cut into units of kUnit tokens of a sequence and head, numbered sequence first, then head, then unit; every
 // workgroup gets an equal run of them, whatever the lengths are, and so takes the end of one (sequence, head), whole ones and

@@ -1,17 +1,18 @@
 // Attention over the 4-bit cache for many rows: prompts and chunks of prompts.
 //
-// A workgroup of four waves takes 128 RT rows (query, head of the share) of a sequence and head of the cache, a wave 32 RT
-// of them.  The workgroup turns the codes of a tile of tokens into fp16 values in LDS once, in the order in which the
-// matrix cores take them, while it works on the tile before; every wave reads all of them.  Per 32 x 32 scores a wave
-// reads 8 KB of keys and as much of values for each 32 tokens (128 dims): with RT = 1 that alone would keep LDS as busy
-// as the matrix cores, so RT is 2 where registers allow.  Three tiles lie in LDS, so that one barrier a tile is enough.
-// Scores are formed for the next 32 tokens while the weights of the present ones are: both are in one stretch of
-// code, and the matrix cores have something to do beside the exponentials.
+// A workgroup of eight waves takes 256 rows (query, head of the share) of a sequence and head of the cache, a wave 32 of
+// them.  The workgroup turns the codes of a tile of tokens into fp16 values in LDS once, in the order in which the
+// matrix cores take them, while it works on the tile before; every wave reads all of them.  Three tiles lie in LDS, so that one
+// barrier a tile is enough.  Scores are formed for the next 32 tokens while the weights of the present ones are: both are in
+// one stretch of code, and the matrix cores have something to do beside the exponentials.
 #include "kv_attention.hpp"
 
 namespace wr {
 
 namespace {
+
+constexpr int kThreads = 512;
+constexpr int kRows = 256;
 
 __device__ __forceinline__ f32x16 mfma32x32x16_f16(const u32x4& a, const u32x4& b, const f32x16& c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
@@ -24,21 +25,19 @@ __device__ __forceinline__ float max_of_two(float v) {  // lanes that differ in 
 // The token of accumulator register v of half h in 32 scores, and the dim of an output likewise.
 __device__ __forceinline__ int at_reg(int v, int h) { return 8 * (v >> 2) + 4 * h + (v & 3); }
 
-template <int DIM, int GROUP>
+template <int DIM>
 struct Tile {
-  static constexpr int TOKENS = DIM == 256 ? 32 : 64;
-  static constexpr int SL = DIM / 32;
+  static constexpr int TOKENS = 8192 / DIM;
   // keys: [block of 32][step of 16 dims][half][token]; values: [16 tokens][32 dims][half][dim], 16 bytes each
   u32x4 keys[TOKENS / 32][DIM / 16][2][32];
   u32x4 values[TOKENS / 16][DIM / 32][2][32];
-  int bad[4];  // a wave has met a NaN among the values
+  int bad[kThreads / kWave];  // a wave has met a NaN among the values
 };
 
-template <int DIM, int GROUP, int RT>
-__global__ __launch_bounds__(256, 1) void attend_many_kernel(AttentionArgs a, uint32_t tiles) {
-  using T = Tile<DIM, GROUP>;
-  constexpr int TOKENS = T::TOKENS, NB = TOKENS / 32, KS = DIM / 16, SL = DIM / 32, ROWS = 128 * RT;
-  constexpr int XT = DIM / 32;                 // tiles of 32 dims
+template <int DIM, int GROUP>
+__global__ __launch_bounds__(kThreads, 1) void attend_many_kernel(AttentionArgs a, uint32_t tiles) {
+  using T = Tile<DIM>;
+  constexpr int TOKENS = T::TOKENS, N16 = TOKENS / 16, NB = TOKENS / 32, KS = DIM / 16, SL = DIM / 32;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   T* buf = reinterpret_cast<T*>(lds);
 
@@ -51,8 +50,8 @@ __global__ __launch_bounds__(256, 1) void attend_many_kernel(AttentionArgs a, ui
   const int tile = tiles - 1 - block / (uint32_t)a.splits;  // those that see most first
 
   const KvSeq s = kv_seq(a.kv, seq);
-  if (s.fresh <= 0 || tile * ROWS >= s.fresh * a.share) return;
-  const RowTile rt = row_tile(a, s, tile, ROWS);
+  if (s.fresh <= 0 || tile * kRows >= s.fresh * a.share) return;
+  const RowTile rt = row_tile(a, s, tile, kRows);
   const Span all = seen(a, s, rt.first, rt.last);
   const int begin = (all.lo & ~15) + split * a.chunk;
   const int end = min(all.hi, begin + a.chunk);
@@ -67,175 +66,126 @@ __global__ __launch_bounds__(256, 1) void attend_many_kernel(AttentionArgs a, ui
   const Unpack unpack;
 
   // ---- codes of a tile on their way from memory to LDS
-  // keys: a thread has part g (DIM / 8 bytes) of a token; values: 2 M dims m .. of the quads h and 2 + h of 16 tokens
-  constexpr int KT = TOKENS * 4 / 256 > 0 ? 256 : TOKENS * 4;  // threads with keys
-  constexpr int VM = SL * TOKENS / 16 * 2 * 16 / 256;           // neighbouring m a thread takes
-  static_assert(KT == TOKENS * 4 && VM * 256 == SL * TOKENS * 2, "a thread has one unit of keys and one of values");
-  const int k_token = threadIdx.x % TOKENS, k_part = threadIdx.x / TOKENS;
-  const int v_l = threadIdx.x % 16, v_h = threadIdx.x / 16 % 2, v_m = threadIdx.x / 32 % (SL / VM) * VM,
-            v_16 = threadIdx.x / 32 / (SL / VM);
+  // keys: a thread has two dwords of part g of a token.  values: it has the dwords of dims 16 m + l (and DIM / 2 more) of the quads
+  // h and 2 + h of 16 tokens; their scales and offsets are eight dwords for each half of the dims, one a lane of 16.
+  const int k_token = threadIdx.x % TOKENS, k_part = threadIdx.x / TOKENS % 4, k_slice = threadIdx.x / TOKENS / 4 * 2;
+  const int v_l = threadIdx.x % 16, v_h = threadIdx.x / 16 % 2, v_m = threadIdx.x / 32 % SL, v_16 = threadIdx.x / 32 / SL;
+  const uint32_t k_at = k_part * (DIM / 8) + k_slice * 4;
+  const uint32_t v_at = ((v_h * 16 + v_l) * SL + v_m) * 4;
+  const int v_group = ((v_l / 8) * (DIM / 2) + 16 * v_m) / GROUP;
+  const uint32_t vm_at = (v_h + v_l / 4 % 2 * 2) * 16 + v_l % 4 * 4;
+  constexpr int KM = GROUP == 32 ? 2 : 1;
   struct Raw {
-    uint32_t k[SL], km[DIM / GROUP], v[2][VM];
-    u32x4 vm[2][2];  // quad; low or high half of the dims
-    int there;       // bit i: tokens 16 i .. of the tile are in the cache
+    uint32_t k[2], km[KM], v[2], vm;
+    int there;  // bit i: tokens 16 i .. of the tile are in the cache
   } raw;
   auto pages_of = [&](int t0) {  // lane i: the page of 16 tokens i
-    const int t = t0 + 16 * (lane % (TOKENS / 16));
-    return t >= 0 && t < end ? table[t >> a.kv.page_shift] : -1;
+    const int t = t0 + 16 * (lane % N16);
+    return t < end ? table[t >> a.kv.page_shift] : -1;
   };
   auto load = [&](int t0, int pages) {
-    raw.there = 0;
-    const uint8_t* base[TOKENS / 16];
-#pragma unroll
-    for (int i = 0; i < TOKENS / 16; ++i) {
-      const int page = __builtin_amdgcn_readlane(pages, i);
-      const bool ok = page >= 0 && page < a.kv.count;
-      raw.there |= ok << i;
-      base[i] = cache + (ok ? page : 0) * page_bytes;
-    }
-    auto pick = [&](int i) {
-      const uint8_t* p = base[0];
-#pragma unroll
-      for (int j = 1; j < TOKENS / 16; ++j) p = i == j ? base[j] : p;
-      return p;
-    };
-    if (KT == 256 || k_part < 4) {
-      const uint8_t* p = pick(k_token / 16);
+    const bool there = pages >= 0 && pages < a.kv.count;
+    raw.there = (int)__builtin_amdgcn_ballot_w64(there) & ((1 << N16) - 1);
+    const int mapped = there ? pages : 0;
+    {
+      const uint8_t* p = cache + __shfl(mapped, k_token / 16) * page_bytes;
       const int in_page = (t0 + k_token) & (at.page_tokens - 1);
-      __builtin_memcpy(raw.k, __builtin_assume_aligned(p + in_page * (DIM / 2) + k_part * (DIM / 8), 8), DIM / 8);
+      __builtin_memcpy(raw.k, __builtin_assume_aligned(p + in_page * (DIM / 2) + k_at, 8), 8);
 #pragma unroll
-      for (int k = 0; k < DIM / GROUP; ++k)
-        raw.km[k] = *reinterpret_cast<const uint32_t*>(p + at.k_meta() + (k * at.page_tokens + in_page) * 4);
+      for (int k = 0; k < KM; ++k)
+        raw.km[k] = *reinterpret_cast<const uint32_t*>(p + at.k_meta() + ((k_slice * 32 / GROUP + k) * at.page_tokens + in_page) * 4);
     }
-    const uint8_t* p = pick(v_16);
+    const uint8_t* p = cache + __shfl(mapped, v_16) * page_bytes;
     const int in_page = (t0 + 16 * v_16) & (at.page_tokens - 1);
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int g = v_h + 2 * q;
-      const uint8_t* c = p + at.v_codes() + in_page * (DIM / 2) + ((g * 16 + v_l) * SL + v_m) * 4;
-      __builtin_memcpy(raw.v[q], __builtin_assume_aligned(c, 4 * VM), 4 * VM);
-#pragma unroll
-      for (int half = 0; half < 2; ++half)
-        raw.vm[q][half] = *reinterpret_cast<const u32x4*>(
-            p + at.v_meta() + (((half * (DIM / 2) + 16 * v_m) / GROUP) * at.page_tokens + in_page + 4 * g) * 4);
-    }
+    for (int q = 0; q < 2; ++q)
+      raw.v[q] = *reinterpret_cast<const uint32_t*>(p + at.v_codes() + in_page * (DIM / 2) + q * (32 * SL * 4) + v_at);
+    raw.vm = *reinterpret_cast<const uint32_t*>(p + at.v_meta() + (v_group * at.page_tokens + in_page) * 4 + vm_at);
   };
   auto store = [&](T& to) {
-    if (KT == 256 || k_part < 4) {
-      const bool ok = raw.there >> (k_token / 16) & 1;
+    const bool k_there = raw.there >> (k_token / 16) & 1, v_there = raw.there >> v_16 & 1;
 #pragma unroll
-      for (int sl = 0; sl < SL; ++sl) {
-        const f16x2 both = __builtin_bit_cast(f16x2, ok ? raw.km[sl * 32 / GROUP] : 0u), sc = both.xx, of = both.yy;
-        const uint32_t w = raw.k[sl];
-        to.keys[k_token / 32][2 * sl + k_part / 2][k_part % 2][k_token % 32] =
-            u32x4{unpack.two<0>(w, sc, of), unpack.two<4>(w, sc, of), unpack.two<0>(w >> 8, sc, of), unpack.two<4>(w >> 8, sc, of)};
+    for (int i = 0; i < 2; ++i) {
+      const f16x2 both = __builtin_bit_cast(f16x2, k_there ? raw.km[i % KM] : 0u), sc = both.xx, of = both.yy;
+      const uint32_t w = raw.k[i];
+      to.keys[k_token / 32][2 * (k_slice + i) + k_part / 2][k_part % 2][k_token % 32] =
+          u32x4{unpack.two<0>(w, sc, of), unpack.two<4>(w, sc, of), unpack.two<0>(w >> 8, sc, of), unpack.two<4>(w >> 8, sc, of)};
+    }
+    const uint32_t vm = v_there ? raw.vm : 0u;
+    const f16x2 scale = __builtin_bit_cast(f16x2, vm);
+    const bool nan = __builtin_amdgcn_ballot_w64(v_l % 2 == 0 && (scale.x != scale.x || scale.y != scale.y)) != 0;
+    if (lane == 0) to.bad[wave] = nan;
+    uint32_t meta[16];  // [half of the dims][quad][scales 0 and 2, offsets, scales 1 and 3, offsets]
+    static_for<0, 16>([&](auto i) { meta[i] = row_lane<decltype(i)::value>(vm); });
+    if (nan) {  // the rows that see it get their NaN by themselves: 0 times NaN would reach the others
+      asm volatile("");
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const f16x2 x = __builtin_bit_cast(f16x2, meta[i]);
+        const uint32_t keep = (x.x == x.x ? 0x0000ffffu : 0u) | (x.y == x.y ? 0xffff0000u : 0u);
+        meta[i] &= keep;
+        meta[i + 1] &= keep;
       }
     }
-    bool nan = false;
-    f16x2 sc[2][2][2], of[2][2][2];  // [quad][half][0: tokens 0 and 2, 1: tokens 1 and 3]
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
+    for (int half = 0; half < 2; ++half) {
+      u32x4 out;
 #pragma unroll
-      for (int half = 0; half < 2; ++half)
+      for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int o = 0; o < 2; ++o) {
-          const bool ok = raw.there >> v_16 & 1;
-          f16x2 x = __builtin_bit_cast(f16x2, ok ? raw.vm[q][half][2 * o] : 0u);
-          f16x2 y = __builtin_bit_cast(f16x2, ok ? raw.vm[q][half][2 * o + 1] : 0u);
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (x[e] != x[e]) {  // its rows get their NaN by themselves (0 times NaN would reach the others)
-              nan = true;
-              x[e] = y[e] = (_Float16)0.0f;
-            }
-          sc[q][half][o] = x;
-          of[q][half][o] = y;
+          const uint32_t w = o ? raw.v[q] >> 8 : raw.v[q];
+          const f16x2 sc = __builtin_bit_cast(f16x2, meta[8 * half + 4 * q + 2 * o]);
+          const f16x2 of = __builtin_bit_cast(f16x2, meta[8 * half + 4 * q + 2 * o + 1]);
+          out[2 * q + o] = half ? unpack.two<4>(w, sc, of) : unpack.two<0>(w, sc, of);
         }
-#pragma unroll
-    for (int i = 0; i < VM; ++i)
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        u32x4 out;
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-          for (int o = 0; o < 2; ++o) {
-            const uint32_t w = o ? raw.v[q][i] >> 8 : raw.v[q][i];
-            out[2 * q + o] = half ? unpack.two<4>(w, sc[q][half][o], of[q][half][o]) : unpack.two<0>(w, sc[q][half][o], of[q][half][o]);
-          }
-        const int d = half * (DIM / 2) + 16 * (v_m + i) + v_l;
-        to.values[v_16][d / 32][v_h][d % 32] = out;
-      }
-    const bool any = __builtin_amdgcn_ballot_w64(nan) != 0;
-    if (lane == 0) to.bad[wave] = any;
+      const int d = half * (DIM / 2) + 16 * v_m + v_l;
+      to.values[v_16][d / 32][v_h][d % 32] = out;
+    }
   };
 
   // ---- the wave's rows
-  u32x4 q[RT][KS];
-  float unit[RT];
-  Span mine[RT];
+  u32x4 q[KS];
+  float unit;
+  const uint32_t rows = s.fresh * a.share, m = tile * kRows + wave * 32 + col;
+  const bool live = m < rows;
+  const int query = live ? m / (uint32_t)a.share : 0, out_head = head * a.share + (live ? m % (uint32_t)a.share : 0);
+  const Span mine = live ? seen(a, s, query, query) : Span{0, 2147483647};
   int every_lo = 0, every_hi = 2147483647;  // seen by every row of the wave
-  int64_t out_row[RT];
-  int out_head[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const uint32_t m = tile * ROWS + (wave * RT + r) * 32 + col;
-    const bool live = m < (uint32_t)(s.fresh * a.share);
-    const int j = m / (uint32_t)a.share, hd = head * a.share + m % (uint32_t)a.share;
-    mine[r] = live ? seen(a, s, j, j) : Span{0, 2147483647};
-    out_row[r] = live ? s.row + j : -1;
-    out_head[r] = hd;
-    const uint16_t* qp = a.q + (int64_t)(s.row + (live ? j : 0)) * a.ldq + (int64_t)(live ? hd : 0) * DIM;
-    Raw8<uint16_t> x[SL][2];
+  {
+    const uint32_t m0 = tile * kRows + wave * 32;
+    if (m0 < rows) {
+      const int j0 = m0 / (uint32_t)a.share, j1 = (min(m0 + 32, rows) - 1) / (uint32_t)a.share;
+      every_hi = seen(a, s, j0, j0).hi;
+      every_lo = seen(a, s, j1, j1).lo;
+    }
+    const uint16_t* qp = a.q + (int64_t)(s.row + query) * a.ldq + (int64_t)out_head * DIM;
+    Raw8<uint16_t> x[KS];
     float big = 0.0f;
 #pragma unroll
-    for (int sl = 0; sl < SL; ++sl)
+    for (int ks = 0; ks < KS; ++ks) {  // step 2 sl + o of 16 dims: parts 2 o + h of the slice
+      x[ks].load(qp + 16 * ks + 8 * h);
 #pragma unroll
-      for (int o = 0; o < 2; ++o) {  // step 2 sl + o of 16 dims: parts 2 o + h of the slice
-        x[sl][o].load(qp + 32 * sl + 8 * (2 * o + h));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[sl][o].get(e)));
-      }
+      for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[ks].get(e)));
+    }
     big = max_of_two(big);
     const int e = min(max((int)(__float_as_uint(big) >> 23) - 127, -120), 120);
     const float down = copysignf(__uint_as_float((uint32_t)(127 - e) << 23), a.scale);
-    unit[r] = fabsf(a.scale) * __uint_as_float((uint32_t)(127 + e) << 23);
+    unit = fabsf(a.scale) * __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
-    for (int sl = 0; sl < SL; ++sl)
+    for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-      for (int o = 0; o < 2; ++o)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          q[r][2 * sl + o][i] = live ? pack_f16(x[sl][o].get(i) * down, x[sl][o].get(4 + i) * down) : 0u;
+      for (int i = 0; i < 4; ++i) q[ks][i] = pack_f16(x[ks].get(i) * down, x[ks].get(4 + i) * down);
   }
-  {
-    const uint32_t m0 = tile * ROWS + wave * RT * 32, most = s.fresh * a.share;
-    if (m0 < most) {
-      const int j0 = m0 / (uint32_t)a.share, j1 = min(m0 + RT * 32, most) - 1;
-      every_hi = seen(a, s, j0, j0).hi;
-      every_lo = seen(a, s, j1 / (uint32_t)a.share, j1 / (uint32_t)a.share).lo;
-    }
-  }
-  f32x16 acc[RT][XT];
-  float top[RT], den[RT];
+  f32x16 acc[SL], score;
+  float top = kLowest, den = 0.0f;
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    top[r] = kLowest;
-    den[r] = 0.0f;
+  for (int x = 0; x < SL; ++x) acc[x] = f32x16{};
+  auto scores = [&](const T& from, int b) {
+    f32x16 sc{};
 #pragma unroll
-    for (int x = 0; x < XT; ++x) acc[r][x] = f32x16{};
-  }
-
-  f32x16 score[RT];
-  auto scores = [&](const T& from, int b, f32x16 (&sc)[RT]) {
-#pragma unroll
-    for (int r = 0; r < RT; ++r) sc[r] = f32x16{};
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const u32x4 k = from.keys[b][ks][h][col];
-#pragma unroll
-      for (int r = 0; r < RT; ++r) sc[r] = mfma32x32x16_f16(k, q[r][ks], sc[r]);
-    }
+    for (int ks = 0; ks < KS; ++ks) sc = mfma32x32x16_f16(from.keys[b][ks][h][col], q[ks], sc);
+    return sc;
   };
 
   int pages = pages_of(begin);
@@ -246,85 +196,77 @@ __global__ __launch_bounds__(256, 1) void attend_many_kernel(AttentionArgs a, ui
   load(begin + TOKENS, pages);
   pages = pages_of(begin + 2 * TOKENS);
   __syncthreads();
-  scores(buf[0], 0, score);
+  score = scores(buf[0], 0);
   int which = 0;
   for (int t0 = begin; t0 < end; t0 += TOKENS) {
-    const int next = which == 2 ? 0 : which + 1;
+    const int after = which == 2 ? 0 : which + 1;
     const T& now = buf[which];
-    int there_next = 0;
+    T& next = buf[after];
+    // every row of the wave sees all of the tile
+    const bool whole = there == (1 << N16) - 1 && t0 + TOKENS <= every_hi && t0 >= every_lo;
+    const int there_now = there;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       const int tb = t0 + 32 * b;
-      const bool whole = (there >> (2 * b) & 3) == 3 && tb + 32 <= every_hi && tb >= every_lo;
-      float less[RT];
+      int see = 65535;
+      if (!whole) {
+        asm volatile("");  // a branch, not selects in every tile
+        see = 0;
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        if (!whole) {
-          asm volatile("");
-#pragma unroll
-          for (int v = 0; v < 16; ++v) {
-            const int t = tb + at_reg(v, h);
-            if (!((there >> (2 * b + v / 8) & 1) && t >= mine[r].lo && t < mine[r].hi)) score[r][v] = -INFINITY;
-          }
+        for (int v = 0; v < 16; ++v) {
+          const int t = tb + at_reg(v, h);
+          const bool in = (there_now >> (2 * b + v / 8) & 1) && t >= mine.lo && t < mine.hi;
+          see |= in << v;
+          if (!in) score[v] = -INFINITY;
         }
-        float high = score[r][0];
-#pragma unroll
-        for (int v = 1; v < 16; ++v) high = fmaxf(high, score[r][v]);
-        high = max_of_two(high);
-        high = high == -INFINITY ? kLowest : high * unit[r];
-        if (__builtin_amdgcn_ballot_w64(high > top[r]) != 0) {
-          const float t = fmaxf(high, top[r]);
-          const float keep = exp2_fast(top[r] - t);
-          top[r] = t;
-          den[r] *= keep;
-#pragma unroll
-          for (int x = 0; x < XT; ++x) acc[r][x] *= keep;
-        }
-        less[r] = top[r] - kLift;
       }
+      float high = score[0];
+#pragma unroll
+      for (int v = 1; v < 16; ++v) high = fmaxf(high, score[v]);
+      high = max_of_two(high);
+      high = high == -INFINITY ? kLowest : high * unit;
+      if (__builtin_amdgcn_ballot_w64(high > top) != 0) {
+        const float t = fmaxf(high, top);
+        const float keep = exp2_fast(top - t);
+        top = t;
+        den *= keep;
+#pragma unroll
+        for (int x = 0; x < SL; ++x) acc[x] *= keep;
+      }
+      const float less = top - kLift;
       if (b == 0) {
-        there_next = raw.there;
-        store(buf[next]);
+        there = raw.there;
+        store(next);
         load(t0 + 2 * TOKENS, pages);
         pages = pages_of(t0 + 3 * TOKENS);
       }
       if (b == NB - 1) __syncthreads();
-      f32x16 ahead[RT];
-      scores(b == NB - 1 ? buf[next] : now, b == NB - 1 ? 0 : b + 1, ahead);
-      u32x4 w[RT][2];
+      const f32x16 ahead = scores(b == NB - 1 ? next : now, b == NB - 1 ? 0 : b + 1);
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
+      for (int v = 0; v < 16; ++v) score[v] = exp2_fast(fmaf(score[v], unit, -less));
+      if (!whole) {
+        asm volatile("");
 #pragma unroll
-        for (int v = 0; v < 16; ++v) {
-          score[r][v] = exp2_fast(fmaf(score[r][v], unit[r], -less[r]));
-        }
-        if (!whole) {
-          asm volatile("");
-#pragma unroll
-          for (int v = 0; v < 16; ++v) {
-            const int t = tb + at_reg(v, h);
-            if (!((there >> (2 * b + v / 8) & 1) && t >= mine[r].lo && t < mine[r].hi)) score[r][v] = 0.0f;
-          }
-        }
-#pragma unroll
-        for (int v = 0; v < 16; ++v) den[r] += score[r][v];
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          w[r][j] = u32x4{pack_f16(score[r][8 * j], score[r][8 * j + 2]), pack_f16(score[r][8 * j + 1], score[r][8 * j + 3]),
-                          pack_f16(score[r][8 * j + 4], score[r][8 * j + 6]), pack_f16(score[r][8 * j + 5], score[r][8 * j + 7])};
+        for (int v = 0; v < 16; ++v)
+          if (!(see >> v & 1)) score[v] = 0.0f;
       }
+#pragma unroll
+      for (int v = 0; v < 16; ++v) den += score[v];
+      u32x4 w[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        w[j] = u32x4{pack_f16(score[8 * j], score[8 * j + 2]), pack_f16(score[8 * j + 1], score[8 * j + 3]),
+                     pack_f16(score[8 * j + 4], score[8 * j + 6]), pack_f16(score[8 * j + 5], score[8 * j + 7])};
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int x = 0; x < XT; ++x) {
-          const u32x4 v = now.values[2 * b + j][x][h][col];
-#pragma unroll
-          for (int r = 0; r < RT; ++r) acc[r][x] = mfma32x32x16_f16(v, w[r][j], acc[r][x]);
-        }
-#pragma unroll
-      for (int r = 0; r < RT; ++r) score[r] = ahead[r];
+        for (int x = 0; x < SL; ++x) acc[x] = mfma32x32x16_f16(now.values[2 * b + j][x][h][col], w[j], acc[x]);
+      score = ahead;
     }
-    if (now.bad[0] | now.bad[1] | now.bad[2] | now.bad[3]) {  // NaNs go to the rows that see them, group by group
+    int bad = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / kWave; ++w) bad |= now.bad[w];
+    if (__builtin_amdgcn_readfirstlane(bad)) {  // NaNs go to the rows that see them, group by group
       for (int t = t0; t < min(t0 + TOKENS, end); ++t) {
         const int page = table[t >> a.kv.page_shift];
         if (page < 0 || page >= a.kv.count) continue;
@@ -332,50 +274,43 @@ __global__ __launch_bounds__(256, 1) void attend_many_kernel(AttentionArgs a, ui
 #pragma unroll
         for (int k = 0; k < DIM / GROUP; ++k) {
           const uint16_t scale = reinterpret_cast<const uint16_t*>(p + at.v_meta())[at.v_scale(k * at.page_tokens, t & (at.page_tokens - 1))];
-          if ((scale & 0x7fffu) <= 0x7c00u) continue;
+          if ((scale & 0x7fffu) <= 0x7c00u || t < mine.lo || t >= mine.hi) continue;
 #pragma unroll
-          for (int r = 0; r < RT; ++r)
-            if (t >= mine[r].lo && t < mine[r].hi)
+          for (int x = 0; x < SL; ++x)
+            if (x * 32 / GROUP == k)
 #pragma unroll
-              for (int x = 0; x < XT; ++x)
-                if (x * 32 / GROUP == k)
-#pragma unroll
-                  for (int v = 0; v < 16; ++v) acc[r][x][v] = NAN;
+              for (int v = 0; v < 16; ++v) acc[x][v] = NAN;
         }
       }
     }
-    there = there_next;
-    which = next;
+    which = after;
   }
 
+  den += __shfl_xor(den, 32);
+  if (!live) return;
+  const float inv = den == 0.0f ? 0.0f : 1.0f / den;
+  const int64_t row = s.row + query, slot = (row * a.heads + out_head) * a.splits + split;
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    den[r] += __shfl_xor(den[r], 32);
-    if (out_row[r] < 0) continue;
-    const float inv = den[r] == 0.0f ? 0.0f : 1.0f / den[r];
-    const int64_t slot = (out_row[r] * a.heads + out_head[r]) * a.splits + split;
+  for (int x = 0; x < SL; ++x)
 #pragma unroll
-    for (int x = 0; x < XT; ++x)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int d = 32 * x + 8 * i + 4 * h;
-        f32x4 v{acc[r][x][4 * i], acc[r][x][4 * i + 1], acc[r][x][4 * i + 2], acc[r][x][4 * i + 3]};
-        if (a.splits == 1) {
-          u32x2_any o;
-          o[0] = pack_bf16(v[0] * inv, v[1] * inv);
-          o[1] = pack_bf16(v[2] * inv, v[3] * inv);
-          *reinterpret_cast<u32x2_any*>(a.out + out_row[r] * a.ldo + (int64_t)out_head[r] * DIM + d) = o;
-        } else {
-          *reinterpret_cast<f32x4*>(a.part + slot * DIM + d) = v;
-        }
+    for (int i = 0; i < 4; ++i) {
+      const int d = 32 * x + 8 * i + 4 * h;
+      const f32x4 v{acc[x][4 * i], acc[x][4 * i + 1], acc[x][4 * i + 2], acc[x][4 * i + 3]};
+      if (a.splits == 1) {
+        u32x2_any o;
+        o[0] = pack_bf16(v[0] * inv, v[1] * inv);
+        o[1] = pack_bf16(v[2] * inv, v[3] * inv);
+        *reinterpret_cast<u32x2_any*>(a.out + row * a.ldo + (int64_t)out_head * DIM + d) = o;
+      } else {
+        *reinterpret_cast<f32x4*>(a.part + slot * DIM + d) = v;
       }
-    if (a.splits > 1 && h == 0) a.stats[slot] = f32x2{top[r], den[r]};
-  }
+    }
+  if (a.splits > 1 && h == 0) a.stats[slot] = f32x2{top, den};
 }
 
 // The chunks' parts of a row and head, in the chunks' order: a wave each.
 template <int DIM>
-__global__ __launch_bounds__(256) void attend_chunks_kernel(AttentionArgs a, int tile_rows) {
+__global__ __launch_bounds__(256) void attend_chunks_kernel(AttentionArgs a) {
   constexpr int PER = DIM / kWave;
   const int lane = threadIdx.x % kWave;
   const uint32_t unit = blockIdx.x * 4 + threadIdx.x / kWave;
@@ -386,7 +321,7 @@ __global__ __launch_bounds__(256) void attend_chunks_kernel(AttentionArgs a, int
   if (seq >= a.kv.n) return;
   const KvSeq s = kv_seq(a.kv, seq);
   if (j >= s.fresh) return;
-  const RowTile rt = row_tile(a, s, (j * a.share + h % a.share) / tile_rows, tile_rows);
+  const RowTile rt = row_tile(a, s, (j * a.share + h % a.share) / kRows, kRows);
   const Span all = seen(a, s, rt.first, rt.last);
   const int parts = min(a.splits, max(1, (all.hi - (all.lo & ~15) + a.chunk - 1) / a.chunk));
   const int64_t slot = ((int64_t)(s.row + j) * a.heads + h) * a.splits;
@@ -410,7 +345,6 @@ __global__ __launch_bounds__(256) void attend_chunks_kernel(AttentionArgs a, int
 }
 
 constexpr int kWanted = 512;  // workgroups, two for every compute unit, below which the positions are split as well
-constexpr int most_rows_of(int dim) { return dim == 256 ? 128 : 256; }
 
 }  // namespace
 
@@ -420,16 +354,15 @@ using namespace wr;
 
 // rows * heads * splits stays below kWanted workgroups' rows.
 size_t wr_kv_many_ws_bytes(int64_t rows, int64_t n, int32_t dim) {
-  return (size_t)std::min<int64_t>(rows * (n / dim), most_rows_of(dim)) * kWanted * (dim + 2) * sizeof(float);
+  return (size_t)std::min<int64_t>(rows * (n / dim), kRows) * kWanted * (dim + 2) * sizeof(float);
 }
 
 int wr_kv_many_impl(wr_ctx* ctx, const wr_kv_cache& c, const wr_kv_seqs& s, AttentionArgs a, int flags) {
   const int64_t most = (int64_t)s.most_new * a.share;
-  const int rows = most <= 128 ? 128 : most_rows_of(c.dim);
-  const int64_t tiles = (most + rows - 1) / rows;
+  const int64_t tiles = (most + kRows - 1) / kRows;
   // positions that a tile's rows can see, from a multiple of 16
   int64_t span = a.kv.most_tokens;
-  const int64_t queries = std::min<int64_t>(s.most_new, (rows + a.share - 2) / a.share + 1);
+  const int64_t queries = std::min<int64_t>(s.most_new, (kRows + a.share - 2) / a.share + 1);
   if (a.window > 0) span = std::min(span, (int64_t)a.window * (flags & WR_ATTENTION_CAUSAL ? 1 : 2) + queries + 15);
   const int64_t groups = std::max<int64_t>(1, s.n * tiles * c.heads);
   const int64_t splits = std::max<int64_t>(1, std::min((span + 511) / 512, kWanted / groups));
@@ -442,16 +375,11 @@ int wr_kv_many_impl(wr_ctx* ctx, const wr_kv_cache& c, const wr_kv_seqs& s, Atte
   bool limits = true;
   const bool there = kv_form(c.dim, c.group, [&](auto d, auto g) {
     constexpr int D = decltype(d)::value, G = decltype(g)::value;
-    constexpr int bytes = 3 * sizeof(Tile<D, G>);
-    auto go = [&](auto rt) {
-      constexpr int RT = decltype(rt)::value;
-      limits = lds_limit(reinterpret_cast<const void*>(&attend_many_kernel<D, G, RT>), bytes);
-      if (limits) hipLaunchKernelGGL((attend_many_kernel<D, G, RT>), dim3((uint32_t)blocks), dim3(256), bytes, ctx->stream, a, (uint32_t)tiles);
-    };
-    if (rows == 128) go(std::integral_constant<int, 1>{});
-    else if constexpr (D < 256) go(std::integral_constant<int, 2>{});
-    if (limits && a.splits > 1)
-      hipLaunchKernelGGL(attend_chunks_kernel<D>, dim3((uint32_t)joins), dim3(256), 0, ctx->stream, a, rows);
+    constexpr int bytes = 3 * sizeof(Tile<D>);
+    limits = lds_limit(reinterpret_cast<const void*>(&attend_many_kernel<D, G>), bytes);
+    if (!limits) return;
+    hipLaunchKernelGGL((attend_many_kernel<D, G>), dim3((uint32_t)blocks), dim3(kThreads), bytes, ctx->stream, a, (uint32_t)tiles);
+    if (a.splits > 1) hipLaunchKernelGGL(attend_chunks_kernel<D>, dim3((uint32_t)joins), dim3(256), 0, ctx->stream, a);
   });
   if (!there) return WR_EUNSUPPORTED;
   if (!limits) return WR_EHIP;

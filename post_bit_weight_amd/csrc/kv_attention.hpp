@@ -48,6 +48,12 @@ __device__ __forceinline__ float max_of_four(float v) {
   return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 
+// Lane N of each row of 16, for the whole row.
+template <int N>
+__device__ __forceinline__ uint32_t row_lane(uint32_t v) {
+  return __builtin_amdgcn_update_dpp(0, v, 0x150 + N, 0xf, 0xf, true);
+}
+
 struct AttentionArgs {
   KvArgs kv;
   const uint16_t* q;
