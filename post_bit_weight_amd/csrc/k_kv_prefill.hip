@@ -66,15 +66,18 @@ __global__ __launch_bounds__(kThreads, 1) void attend_many_kernel(AttentionArgs 
   const Unpack unpack;
 
   // ---- codes of a tile on their way from memory to LDS
-  // keys: a thread has two dwords of part g of a token.  values: it has the dwords of dims 16 m + l (and DIM / 2 more) of the quads
-  // h and 2 + h of 16 tokens; their scales and offsets are eight dwords for each half of the dims, one a lane of 16.
-  const int k_token = threadIdx.x % TOKENS, k_part = threadIdx.x / TOKENS % 4, k_slice = threadIdx.x / TOKENS / 4 * 2;
-  const int v_l = threadIdx.x % 16, v_h = threadIdx.x / 16 % 2, v_m = threadIdx.x / 32 % SL, v_16 = threadIdx.x / 32 / SL;
-  const uint32_t k_at = k_part * (DIM / 8) + k_slice * 4;
-  const uint32_t v_at = ((v_h * 16 + v_l) * SL + v_m) * 4;
+  // keys: a wave has two dwords of each part of 16 tokens.  values: a thread has the dwords of dims 16 m + l (and DIM / 2 more) of
+  // the quads h and 2 + h of 16 tokens; their scales and offsets are eight dwords for each half of the dims, one a lane of 16.
+  const int k_16 = wave % N16, k_slice = wave / N16 * 2, k_part = lane / 16, k_token = 16 * k_16 + lane % 16;
+  const int v_l = threadIdx.x % 16, v_h = threadIdx.x / 16 % 2, v_m = threadIdx.x / 32 % SL, v_16 = wave / (SL / 2);
   const int v_group = ((v_l / 8) * (DIM / 2) + 16 * v_m) / GROUP;
-  const uint32_t vm_at = (v_h + v_l / 4 % 2 * 2) * 16 + v_l % 4 * 4;
   constexpr int KM = GROUP == 32 ? 2 : 1;
+  struct Offsets {  // of a lane behind a uniform place
+    uint32_t k, km, v, vm;
+  };
+  const Offsets lanes{(uint32_t)(lane % 16 * (DIM / 2) + k_part * (DIM / 8)), (uint32_t)(lane % 16 * 4),
+                      (uint32_t)(((v_h * 16 + v_l) * SL + v_m) * 4),
+                      (uint32_t)(v_group * at.page_tokens * 4 + (v_h + v_l / 4 % 2 * 2) * 16 + v_l % 4 * 4)};
   struct Raw {
     uint32_t k[2], km[KM], v[2], vm;
     int there;  // bit i: tokens 16 i .. of the tile are in the cache
@@ -84,26 +87,29 @@ __global__ __launch_bounds__(kThreads, 1) void attend_many_kernel(AttentionArgs 
     return t < end ? table[t >> a.kv.page_shift] : -1;
   };
   auto load = [&](int t0, int pages) {
+    Offsets off = lanes;
+    asm("" : "+v"(off.k), "+v"(off.km), "+v"(off.v), "+v"(off.vm));  // 32 bits beside a scalar address, not 64 hoisted
     const bool there = pages >= 0 && pages < a.kv.count;
     raw.there = (int)__builtin_amdgcn_ballot_w64(there) & ((1 << N16) - 1);
     const int mapped = there ? pages : 0;
     {
-      const uint8_t* p = cache + __shfl(mapped, k_token / 16) * page_bytes;
-      const int in_page = (t0 + k_token) & (at.page_tokens - 1);
-      __builtin_memcpy(raw.k, __builtin_assume_aligned(p + in_page * (DIM / 2) + k_at, 8), 8);
+      const int in_page = (t0 + 16 * k_16) & (at.page_tokens - 1);
+      const uint8_t* p = cache + __builtin_amdgcn_readlane(mapped, k_16) * page_bytes;
+      const uint8_t* codes = p + in_page * (DIM / 2) + k_slice * 4;
+      __builtin_memcpy(raw.k, __builtin_assume_aligned(codes + off.k, 8), 8);
 #pragma unroll
       for (int k = 0; k < KM; ++k)
-        raw.km[k] = *reinterpret_cast<const uint32_t*>(p + at.k_meta() + ((k_slice * 32 / GROUP + k) * at.page_tokens + in_page) * 4);
+        raw.km[k] = *reinterpret_cast<const uint32_t*>(p + at.k_meta() + ((k_slice * 32 / GROUP + k) * at.page_tokens + in_page) * 4 + off.km);
     }
-    const uint8_t* p = cache + __shfl(mapped, v_16) * page_bytes;
     const int in_page = (t0 + 16 * v_16) & (at.page_tokens - 1);
+    const uint8_t* p = cache + __builtin_amdgcn_readlane(mapped, v_16) * page_bytes;
 #pragma unroll
     for (int q = 0; q < 2; ++q)
-      raw.v[q] = *reinterpret_cast<const uint32_t*>(p + at.v_codes() + in_page * (DIM / 2) + q * (32 * SL * 4) + v_at);
-    raw.vm = *reinterpret_cast<const uint32_t*>(p + at.v_meta() + (v_group * at.page_tokens + in_page) * 4 + vm_at);
+      raw.v[q] = *reinterpret_cast<const uint32_t*>(p + at.v_codes() + in_page * (DIM / 2) + q * (32 * SL * 4) + off.v);
+    raw.vm = *reinterpret_cast<const uint32_t*>(p + at.v_meta() + in_page * 4 + off.vm);
   };
-  auto store = [&](T& to) {
-    const bool k_there = raw.there >> (k_token / 16) & 1, v_there = raw.there >> v_16 & 1;
+  auto store = [&](T& to, int t0) {
+    const bool k_there = raw.there >> k_16 & 1, v_there = raw.there >> v_16 & 1;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const f16x2 both = __builtin_bit_cast(f16x2, k_there ? raw.km[i % KM] : 0u), sc = both.xx, of = both.yy;
@@ -111,22 +117,22 @@ __global__ __launch_bounds__(kThreads, 1) void attend_many_kernel(AttentionArgs 
       to.keys[k_token / 32][2 * (k_slice + i) + k_part / 2][k_part % 2][k_token % 32] =
           u32x4{unpack.two<0>(w, sc, of), unpack.two<4>(w, sc, of), unpack.two<0>(w >> 8, sc, of), unpack.two<4>(w >> 8, sc, of)};
     }
-    const uint32_t vm = v_there ? raw.vm : 0u;
-    const f16x2 scale = __builtin_bit_cast(f16x2, vm);
-    const bool nan = __builtin_amdgcn_ballot_w64(v_l % 2 == 0 && (scale.x != scale.x || scale.y != scale.y)) != 0;
-    if (lane == 0) to.bad[wave] = nan;
-    uint32_t meta[16];  // [half of the dims][quad][scales 0 and 2, offsets, scales 1 and 3, offsets]
-    static_for<0, 16>([&](auto i) { meta[i] = row_lane<decltype(i)::value>(vm); });
-    if (nan) {  // the rows that see it get their NaN by themselves: 0 times NaN would reach the others
+    f16x2 vm = __builtin_bit_cast(f16x2, v_there ? raw.vm : 0u);
+    if (t0 < all.lo || t0 + TOKENS > all.hi) {  // what no row sees may hold anything, which a weight of 0 would not hide
       asm volatile("");
-#pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        const f16x2 x = __builtin_bit_cast(f16x2, meta[i]);
-        const uint32_t keep = (x.x == x.x ? 0x0000ffffu : 0u) | (x.y == x.y ? 0xffff0000u : 0u);
-        meta[i] &= keep;
-        meta[i + 1] &= keep;
-      }
+      const int t = t0 + 16 * v_16 + 4 * (v_h + v_l / 4 % 2 * 2) + v_l % 4 / 2;
+      if (t < all.lo || t >= all.hi) vm.x = (_Float16)0.0f;
+      if (t + 2 < all.lo || t + 2 >= all.hi) vm.y = (_Float16)0.0f;
     }
+    // The rows that see a NaN get it by themselves; here it becomes 0, since 0 times NaN would reach the others.
+    const bool nx = vm.x != vm.x, ny = vm.y != vm.y;
+    const bool nan = __builtin_amdgcn_ballot_w64(nx || ny) != 0;
+    if (lane == 0) to.bad[wave] = nan;
+    if (nx) vm.x = (_Float16)0.0f;
+    if (ny) vm.y = (_Float16)0.0f;
+    const uint32_t finite = __builtin_bit_cast(uint32_t, vm);
+    uint32_t meta[16];  // [half of the dims][quad][scales 0 and 2, offsets, scales 1 and 3, offsets]
+    static_for<0, 16>([&](auto i) { meta[i] = row_lane<decltype(i)::value>(finite); });
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       u32x4 out;
@@ -192,7 +198,7 @@ __global__ __launch_bounds__(kThreads, 1) void attend_many_kernel(AttentionArgs 
   load(begin, pages);
   pages = pages_of(begin + TOKENS);
   int there = raw.there;
-  store(buf[0]);
+  store(buf[0], begin);
   load(begin + TOKENS, pages);
   pages = pages_of(begin + 2 * TOKENS);
   __syncthreads();
@@ -234,12 +240,13 @@ __global__ __launch_bounds__(kThreads, 1) void attend_many_kernel(AttentionArgs 
         for (int x = 0; x < SL; ++x) acc[x] *= keep;
       }
       const float less = top - kLift;
-      if (b == 0) {
+      auto turn = [&] {
         there = raw.there;
-        store(next);
+        store(next, t0 + TOKENS);
         load(t0 + 2 * TOKENS, pages);
         pages = pages_of(t0 + 3 * TOKENS);
-      }
+      };
+      if (NB == 1) turn();
       if (b == NB - 1) __syncthreads();
       const f32x16 ahead = scores(b == NB - 1 ? next : now, b == NB - 1 ? 0 : b + 1);
 #pragma unroll
@@ -250,17 +257,20 @@ __global__ __launch_bounds__(kThreads, 1) void attend_many_kernel(AttentionArgs 
         for (int v = 0; v < 16; ++v)
           if (!(see >> v & 1)) score[v] = 0.0f;
       }
-#pragma unroll
-      for (int v = 0; v < 16; ++v) den += score[v];
       u32x4 w[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j)
         w[j] = u32x4{pack_f16(score[8 * j], score[8 * j + 2]), pack_f16(score[8 * j + 1], score[8 * j + 3]),
                      pack_f16(score[8 * j + 4], score[8 * j + 6]), pack_f16(score[8 * j + 5], score[8 * j + 7])};
+      const f16x2 one{(_Float16)1.0f, (_Float16)1.0f};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)  // the weights as they are used
+        den = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, (uint32_t)w[i / 4][i % 4]), one, den, false);
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int x = 0; x < SL; ++x) acc[x] = mfma32x32x16_f16(now.values[2 * b + j][x][h][col], w[j], acc[x]);
+      if (NB > 1 && b == 0) turn();
       score = ahead;
     }
     int bad = 0;
