@@ -31,7 +31,11 @@ struct Tile {
   // keys: [block of 32][step of 16 dims][half][token]; values: [16 tokens][32 dims][half][dim], 16 bytes each
   u32x4 keys[TOKENS / 32][DIM / 16][2][32];
   u32x4 values[TOKENS / 16][DIM / 32][2][32];
-  int bad[kThreads / kWave];  // a wave has met a NaN among the values
+};
+template <int DIM>
+struct Shared {
+  Tile<DIM> tile[3];
+  int bad;  // the last tile among whose values a NaN was met, -1: none
 };
 
 template <int DIM, int GROUP>
@@ -39,7 +43,8 @@ __global__ __launch_bounds__(kThreads, 1) void attend_many_kernel(AttentionArgs 
   using T = Tile<DIM>;
   constexpr int TOKENS = T::TOKENS, N16 = TOKENS / 16, NB = TOKENS / 32, KS = DIM / 16, SL = DIM / 32;
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  T* buf = reinterpret_cast<T*>(lds);
+  Shared<DIM>& shared = *reinterpret_cast<Shared<DIM>*>(lds);
+  T* buf = shared.tile;
 
   uint32_t block = blockIdx.x;
   const int head = block % (uint32_t)a.kv.heads;
@@ -66,20 +71,27 @@ __global__ __launch_bounds__(kThreads, 1) void attend_many_kernel(AttentionArgs 
   const Unpack unpack;
 
   // ---- codes of a tile on their way from memory to LDS
-  // keys: a wave has two dwords of each part of 16 tokens.  values: a thread has the dwords of dims 16 m + l (and DIM / 2 more) of
-  // the quads h and 2 + h of 16 tokens; their scales and offsets are eight dwords for each half of the dims, one a lane of 16.
-  const int k_16 = wave % N16, k_slice = wave / N16 * 2, k_part = lane / 16, k_token = 16 * k_16 + lane % 16;
-  const int v_l = threadIdx.x % 16, v_h = threadIdx.x / 16 % 2, v_m = threadIdx.x / 32 % SL, v_16 = wave / (SL / 2);
-  const int v_group = ((v_l / 8) * (DIM / 2) + 16 * v_m) / GROUP;
-  constexpr int KM = GROUP == 32 ? 2 : 1;
-  struct Offsets {  // of a lane behind a uniform place
-    uint32_t k, km, v, vm;
-  };
-  const Offsets lanes{(uint32_t)(lane % 16 * (DIM / 2) + k_part * (DIM / 8)), (uint32_t)(lane % 16 * 4),
-                      (uint32_t)(((v_h * 16 + v_l) * SL + v_m) * 4),
-                      (uint32_t)(v_group * at.page_tokens * 4 + (v_h + v_l / 4 % 2 * 2) * 16 + v_l % 4 * 4)};
+  // Four waves take the keys, a lane KD dwords of a part of a token; four the values, a lane the dwords of VM neighbouring m (and so dims
+  // 16 m + l and DIM / 2 + 16 m + l) of the quads h and 2 + h of 16 tokens.  The values' scales and offsets are eight dwords for
+  // each half of the dims, one a lane of 16.  A wave has PIECES pieces of 16 tokens.
+  constexpr int PIECES = N16 > 4 ? N16 / 4 : 1, KD = SL * N16 / 4 / PIECES, VM = KD / 2;
+  constexpr int KM = (KD * 32 + GROUP - 1) / GROUP;  // groups of a lane's keys
+  const bool keys = wave < 4;
+  const int part = wave % 4, first16 = part * PIECES % N16;
+  const int slice = part * PIECES / N16 * KD;           // of the keys' dwords
+  const int v_l = lane % 16, v_h = lane / 16 % 2, v_m = part * PIECES / N16 * KD + lane / 32 * VM;
+  struct Offsets {  // of a lane behind the codes and the scales of 16 tokens
+    uint32_t codes, meta;
+  } lanes;
+  if (keys) {
+    lanes.codes = lane % 16 * (DIM / 2) + lane / 16 * (DIM / 8) + slice * 4;
+    lanes.meta = at.k_meta() + slice * 32 / GROUP * at.page_tokens * 4 + lane % 16 * 4;
+  } else {
+    lanes.codes = at.v_codes() + ((v_h * 16 + v_l) * SL + v_m) * 4;
+    lanes.meta = at.v_meta() + ((v_l / 8) * (DIM / 2) + 16 * v_m) / GROUP * at.page_tokens * 4 + (v_h + v_l / 4 % 2 * 2) * 16 + v_l % 4 * 4;
+  }
   struct Raw {
-    uint32_t k[2], km[KM], v[2], vm;
+    uint32_t codes[PIECES][KD], meta[PIECES][KM];
     int there;  // bit i: tokens 16 i .. of the tile are in the cache
   } raw;
   auto pages_of = [&](int t0) {  // lane i: the page of 16 tokens i
@@ -88,65 +100,77 @@ __global__ __launch_bounds__(kThreads, 1) void attend_many_kernel(AttentionArgs 
   };
   auto load = [&](int t0, int pages) {
     Offsets off = lanes;
-    asm("" : "+v"(off.k), "+v"(off.km), "+v"(off.v), "+v"(off.vm));  // 32 bits beside a scalar address, not 64 hoisted
+    asm("" : "+v"(off.codes), "+v"(off.meta));  // 32 bits beside a scalar address, not 64 hoisted
     const bool there = pages >= 0 && pages < a.kv.count;
     raw.there = (int)__builtin_amdgcn_ballot_w64(there) & ((1 << N16) - 1);
-    const int mapped = there ? pages : 0;
-    {
-      const int in_page = (t0 + 16 * k_16) & (at.page_tokens - 1);
-      const uint8_t* p = cache + __builtin_amdgcn_readlane(mapped, k_16) * page_bytes;
-      const uint8_t* codes = p + in_page * (DIM / 2) + k_slice * 4;
-      __builtin_memcpy(raw.k, __builtin_assume_aligned(codes + off.k, 8), 8);
+    const int64_t where = (there ? pages : 0) * page_bytes;
 #pragma unroll
-      for (int k = 0; k < KM; ++k)
-        raw.km[k] = *reinterpret_cast<const uint32_t*>(p + at.k_meta() + ((k_slice * 32 / GROUP + k) * at.page_tokens + in_page) * 4 + off.km);
+    for (int i = 0; i < PIECES; ++i) {
+      const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)where, first16 + i), hi = __builtin_amdgcn_readlane((uint32_t)(where >> 32), first16 + i);
+      const int in_page = (t0 + 16 * (first16 + i)) & (at.page_tokens - 1);
+      const uint8_t* p = cache + ((uint64_t)hi << 32 | lo);
+      const uint8_t *codes = p + in_page * (DIM / 2), *meta = p + in_page * 4;
+      if (keys) {
+        __builtin_memcpy(raw.codes[i], __builtin_assume_aligned(codes + off.codes, KD * 4), KD * 4);
+#pragma unroll
+        for (int k = 0; k < KM; ++k)
+          raw.meta[i][k] = *reinterpret_cast<const uint32_t*>(meta + k * at.page_tokens * 4 + off.meta);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          __builtin_memcpy(&raw.codes[i][q * VM], __builtin_assume_aligned(codes + q * (32 * SL * 4) + off.codes, VM * 4), VM * 4);
+        raw.meta[i][0] = *reinterpret_cast<const uint32_t*>(meta + off.meta);
+      }
     }
-    const int in_page = (t0 + 16 * v_16) & (at.page_tokens - 1);
-    const uint8_t* p = cache + __builtin_amdgcn_readlane(mapped, v_16) * page_bytes;
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-      raw.v[q] = *reinterpret_cast<const uint32_t*>(p + at.v_codes() + in_page * (DIM / 2) + q * (32 * SL * 4) + off.v);
-    raw.vm = *reinterpret_cast<const uint32_t*>(p + at.v_meta() + in_page * 4 + off.vm);
   };
-  auto store = [&](T& to, int t0) {
-    const bool k_there = raw.there >> k_16 & 1, v_there = raw.there >> v_16 & 1;
+  auto store = [&](T& to, int t0, int nth) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const f16x2 both = __builtin_bit_cast(f16x2, k_there ? raw.km[i % KM] : 0u), sc = both.xx, of = both.yy;
-      const uint32_t w = raw.k[i];
-      to.keys[k_token / 32][2 * (k_slice + i) + k_part / 2][k_part % 2][k_token % 32] =
-          u32x4{unpack.two<0>(w, sc, of), unpack.two<4>(w, sc, of), unpack.two<0>(w >> 8, sc, of), unpack.two<4>(w >> 8, sc, of)};
-    }
-    f16x2 vm = __builtin_bit_cast(f16x2, v_there ? raw.vm : 0u);
-    if (t0 < all.lo || t0 + TOKENS > all.hi) {  // what no row sees may hold anything, which a weight of 0 would not hide
-      asm volatile("");
-      const int t = t0 + 16 * v_16 + 4 * (v_h + v_l / 4 % 2 * 2) + v_l % 4 / 2;
-      if (t < all.lo || t >= all.hi) vm.x = (_Float16)0.0f;
-      if (t + 2 < all.lo || t + 2 >= all.hi) vm.y = (_Float16)0.0f;
-    }
-    // The rows that see a NaN get it by themselves; here it becomes 0, since 0 times NaN would reach the others.
-    const bool nx = vm.x != vm.x, ny = vm.y != vm.y;
-    const bool nan = __builtin_amdgcn_ballot_w64(nx || ny) != 0;
-    if (lane == 0) to.bad[wave] = nan;
-    if (nx) vm.x = (_Float16)0.0f;
-    if (ny) vm.y = (_Float16)0.0f;
-    const uint32_t finite = __builtin_bit_cast(uint32_t, vm);
-    uint32_t meta[16];  // [half of the dims][quad][scales 0 and 2, offsets, scales 1 and 3, offsets]
-    static_for<0, 16>([&](auto i) { meta[i] = row_lane<decltype(i)::value>(finite); });
+    for (int i = 0; i < PIECES; ++i) {
+      const int p16 = first16 + i;
+      const bool there = raw.there >> p16 & 1;
+      if (keys) {
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      u32x4 out;
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-#pragma unroll
-        for (int o = 0; o < 2; ++o) {
-          const uint32_t w = o ? raw.v[q] >> 8 : raw.v[q];
-          const f16x2 sc = __builtin_bit_cast(f16x2, meta[8 * half + 4 * q + 2 * o]);
-          const f16x2 of = __builtin_bit_cast(f16x2, meta[8 * half + 4 * q + 2 * o + 1]);
-          out[2 * q + o] = half ? unpack.two<4>(w, sc, of) : unpack.two<0>(w, sc, of);
+        for (int k = 0; k < KD; ++k) {
+          const f16x2 both = __builtin_bit_cast(f16x2, there ? raw.meta[i][k * 32 / GROUP] : 0u), sc = both.xx, of = both.yy;
+          const uint32_t w = raw.codes[i][k];
+          to.keys[p16 / 2][2 * (slice + k) + lane / 32][lane / 16 % 2][p16 % 2 * 16 + lane % 16] =
+              u32x4{unpack.two<0>(w, sc, of), unpack.two<4>(w, sc, of), unpack.two<0>(w >> 8, sc, of), unpack.two<4>(w >> 8, sc, of)};
         }
-      const int d = half * (DIM / 2) + 16 * v_m + v_l;
-      to.values[v_16][d / 32][v_h][d % 32] = out;
+        continue;
+      }
+      f16x2 vm = __builtin_bit_cast(f16x2, there ? raw.meta[i][0] : 0u);
+      if (t0 < all.lo || t0 + TOKENS > all.hi) {  // what no row sees may hold anything, which a weight of 0 would not hide
+        asm volatile("");
+        const int t = t0 + 16 * p16 + 4 * (v_h + v_l / 4 % 2 * 2) + v_l % 4 / 2;
+        if (t < all.lo || t >= all.hi) vm.x = (_Float16)0.0f;
+        if (t + 2 < all.lo || t + 2 >= all.hi) vm.y = (_Float16)0.0f;
+      }
+      if (__builtin_amdgcn_ballot_w64(vm.x != vm.x || vm.y != vm.y)) {
+        // The rows that see a NaN get it by themselves; here it becomes 0, since 0 times NaN would reach the others.
+        asm volatile("");
+        if (vm.x != vm.x) vm.x = (_Float16)0.0f;
+        if (vm.y != vm.y) vm.y = (_Float16)0.0f;
+        atomicMax(&shared.bad, nth);
+      }
+      const uint32_t finite = __builtin_bit_cast(uint32_t, vm);
+      uint32_t meta[16];  // [half of the dims][quad][scales 0 and 2, offsets, scales 1 and 3, offsets]
+      static_for<0, 16>([&](auto n) { meta[n] = row_lane<decltype(n)::value>(finite); });
+#pragma unroll
+      for (int n = 0; n < VM; ++n)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          u32x4 out;
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+              const uint32_t w = o ? raw.codes[i][q * VM + n] >> 8 : raw.codes[i][q * VM + n];
+              const f16x2 sc = __builtin_bit_cast(f16x2, meta[8 * half + 4 * q + 2 * o]);
+              const f16x2 of = __builtin_bit_cast(f16x2, meta[8 * half + 4 * q + 2 * o + 1]);
+              out[2 * q + o] = half ? unpack.two<4>(w, sc, of) : unpack.two<0>(w, sc, of);
+            }
+          to.values[p16][half * (SL / 2) + (v_m + n) / 2][v_h][(v_m + n) % 2 * 16 + v_l] = out;
+        }
     }
   };
 
@@ -194,16 +218,18 @@ __global__ __launch_bounds__(kThreads, 1) void attend_many_kernel(AttentionArgs 
     return sc;
   };
 
+  if (threadIdx.x == 0) shared.bad = -1;
+  __syncthreads();
   int pages = pages_of(begin);
   load(begin, pages);
   pages = pages_of(begin + TOKENS);
   int there = raw.there;
-  store(buf[0], begin);
+  store(buf[0], begin, 0);
   load(begin + TOKENS, pages);
   pages = pages_of(begin + 2 * TOKENS);
   __syncthreads();
   score = scores(buf[0], 0);
-  int which = 0;
+  int which = 0, nth = 0;
   for (int t0 = begin; t0 < end; t0 += TOKENS) {
     const int after = which == 2 ? 0 : which + 1;
     const T& now = buf[which];
@@ -230,7 +256,7 @@ __global__ __launch_bounds__(kThreads, 1) void attend_many_kernel(AttentionArgs 
 #pragma unroll
       for (int v = 1; v < 16; ++v) high = fmaxf(high, score[v]);
       high = max_of_two(high);
-      high = high == -INFINITY ? kLowest : high * unit;
+      high = fmaxf(high * unit, kLowest);  // also where 0 times -infinity is a NaN
       if (__builtin_amdgcn_ballot_w64(high > top) != 0) {
         const float t = fmaxf(high, top);
         const float keep = exp2_fast(top - t);
@@ -242,7 +268,7 @@ __global__ __launch_bounds__(kThreads, 1) void attend_many_kernel(AttentionArgs 
       const float less = top - kLift;
       auto turn = [&] {
         there = raw.there;
-        store(next, t0 + TOKENS);
+        store(next, t0 + TOKENS, nth + 1);
         load(t0 + 2 * TOKENS, pages);
         pages = pages_of(t0 + 3 * TOKENS);
       };
@@ -273,10 +299,7 @@ __global__ __launch_bounds__(kThreads, 1) void attend_many_kernel(AttentionArgs 
       if (NB > 1 && b == 0) turn();
       score = ahead;
     }
-    int bad = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / kWave; ++w) bad |= now.bad[w];
-    if (__builtin_amdgcn_readfirstlane(bad)) {  // NaNs go to the rows that see them, group by group
+    if (__builtin_amdgcn_readfirstlane(shared.bad) >= nth) {  // NaNs go to the rows that see them, group by group
       for (int t = t0; t < min(t0 + TOKENS, end); ++t) {
         const int page = table[t >> a.kv.page_shift];
         if (page < 0 || page >= a.kv.count) continue;
@@ -294,6 +317,7 @@ __global__ __launch_bounds__(kThreads, 1) void attend_many_kernel(AttentionArgs 
       }
     }
     which = after;
+    ++nth;
   }
 
   den += __shfl_xor(den, 32);
@@ -385,7 +409,7 @@ int wr_kv_many_impl(wr_ctx* ctx, const wr_kv_cache& c, const wr_kv_seqs& s, Atte
   bool limits = true;
   const bool there = kv_form(c.dim, c.group, [&](auto d, auto g) {
     constexpr int D = decltype(d)::value, G = decltype(g)::value;
-    constexpr int bytes = 3 * sizeof(Tile<D>);
+    constexpr int bytes = sizeof(Shared<D>);
     limits = lds_limit(reinterpret_cast<const void*>(&attend_many_kernel<D, G>), bytes);
     if (!limits) return;
     hipLaunchKernelGGL((attend_many_kernel<D, G>), dim3((uint32_t)blocks), dim3(kThreads), bytes, ctx->stream, a, (uint32_t)tiles);
