@@ -41,41 +41,58 @@ __device__ __forceinline__ bool tile_of(const KvArgs& a, int tiles, uint32_t blo
   return true;
 }
 
-template <typename T>
-__device__ __forceinline__ void group_codes(const Raw8<T>& x, int lanes, uint32_t& codes, uint32_t& meta) {
-  float lo = x.get(0), hi = lo;
-  bool bad = false;
+// The value of the lane that differs in the bit STEP (1, 2, 4 or 8) of a row of 16; for 4 and 8 some lane of the other half, which is the
+// same where the lanes of each half agree already.
+template <int STEP>
+__device__ __forceinline__ float across(float v) {
+  constexpr int ctrl = STEP == 1 ? 0xb1 : STEP == 2 ? 0x4e : STEP == 4 ? 0x141 : 0x140;  // quad_perm, half mirror, mirror
+  return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), ctrl, 0xf, 0xf, true));
+}
+
+// The codes of a lane's eight values and the scale and offset of the LANES lanes that share a group.
+template <int LANES, typename T>
+__device__ __forceinline__ void group_codes(const Raw8<T>& raw, uint32_t& codes, uint32_t& meta) {
+  float x[8];
+  float lo = INFINITY, hi = -INFINITY, size = 0.0f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float f = x.get(e);
-    lo = fminf(lo, f);
-    hi = fmaxf(hi, f);
-    bad |= !(fabsf(f) <= 3.402823466e38f);
+    x[e] = raw.get(e);
+    lo = fminf(lo, x[e]);
+    hi = fmaxf(hi, x[e]);
+    size = fmaf(0.0f, x[e], size);  // 0, or NaN where a value is not finite
   }
-  int any = bad;
-  for (int m = 1; m < lanes; m <<= 1) {
-    lo = fminf(lo, __shfl_xor(lo, m));
-    hi = fmaxf(hi, __shfl_xor(hi, m));
-    any |= __shfl_xor(any, m);
+  static_for<0, LANES == 4 ? 2 : LANES == 8 ? 3 : 4>([&](auto n) {
+    constexpr int step = 1 << decltype(n)::value;
+    lo = fminf(lo, across<step>(lo));
+    hi = fmaxf(hi, across<step>(hi));
+    size += across<step>(size);
+  });
+  const bool finite = size == 0.0f;
+  if (__builtin_amdgcn_ballot_w64(lo < -kKvMost || hi > kKvMost)) {
+    asm volatile("");
+    lo = fminf(fmaxf(lo, -kKvMost), kKvMost);
+    hi = fminf(fmaxf(hi, -kKvMost), kKvMost);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = fminf(fmaxf(x[e], -kKvMost), kKvMost);
   }
-  lo = fminf(fmaxf(lo, -kKvMost), kKvMost);
-  hi = fminf(fmaxf(hi, -kKvMost), kKvMost);
-  const uint16_t off_bits = f32_to_f16_bits_clamped(lo);
+  const uint16_t off_bits = __builtin_bit_cast(uint16_t, (_Float16)lo);
   const float off = f16_bits_to_f32(off_bits);
-  const uint16_t scale_bits = f32_to_f16_bits_clamped(__fdiv_rn(hi - off, 15.0f));
+  const uint16_t scale_bits = __builtin_bit_cast(uint16_t, (_Float16)__fdiv_rn(hi - off, 15.0f));
   const float scale = f16_bits_to_f32(scale_bits);
-  codes = 0;
-  if (any) {
-    meta = 0x7e007e00u;
-    return;
-  }
-  meta = scale_bits | (uint32_t)off_bits << 16;
-  if (!(scale > 0.0f)) return;
+  meta = finite ? scale_bits | (uint32_t)off_bits << 16 : 0x7e007e00u;
+  const bool some = finite && scale > 0.0f;
+  // The quotient correctly rounded, by Markstein's theorem: with y the correctly rounded reciprocal, q = d y and the
+  // exact rest r = d - q scale, q + r y rounds to the quotient.
+  const float y = __fdiv_rn(1.0f, some ? scale : 1.0f);
+  float c[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float c = fminf(fmaxf(rintf(__fdiv_rn(fminf(fmaxf(x.get(e), -kKvMost), kKvMost) - off, scale)), 0.0f), 15.0f);
-    codes |= (uint32_t)c << (4 * e);
+    const float d = x[e] - off, q = d * y, r = fmaf(-q, scale, d);
+    c[e] = rintf(__builtin_amdgcn_fmed3f(fmaf(r, y, q), 0.0f, 15.0f));
   }
+  const uint32_t low = (uint32_t)fmaf(4096.0f, c[3], fmaf(256.0f, c[2], fmaf(16.0f, c[1], c[0])));
+  const uint32_t high = (uint32_t)fmaf(4096.0f, c[7], fmaf(256.0f, c[6], fmaf(16.0f, c[5], c[4])));
+  codes = some ? low | high << 16 : 0u;
 }
 
 template <int DIM, int GROUP, typename T>
@@ -98,7 +115,7 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvArgs a, int tiles,
     Raw8<T> x;
     x.load(src + (int64_t)(t.row0 + (live ? token : t.from)) * (values ? ldv : ldk) + head * DIM + 8 * c);
     uint32_t codes, meta;
-    group_codes(x, GROUP / 8, codes, meta);
+    group_codes<GROUP / 8>(x, codes, meta);
     if (!live) continue;
     const int in_page = t.at + token;
     if (values)

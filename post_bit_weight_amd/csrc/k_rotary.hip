@@ -39,37 +39,85 @@ __device__ __forceinline__ void row_turns(const RotaryArgs& a, int64_t row, f32x
   }
 }
 
-// One value or pair at a time, for any pairs and dim.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void rotary_any_kernel(RotaryArgs a, const T* x, T* y) {
-  __shared__ f32x2 turn[kPairs];
-  auto get = [](T v) {
-    if constexpr (sizeof(T) == 2) return bf16_bits_to_f32(v);
-    else return v;
-  };
-  auto put = [](float f) {
-    if constexpr (sizeof(T) == 2) return (T)f32_to_bf16_bits(f);
-    else return f;
-  };
-  const int units = a.dim - a.pairs;  // pairs, then the values behind them
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    __syncthreads();
-    row_turns(a, row, turn, threadIdx.x, kThreads);
-    __syncthreads();
-    const T* xr = x + row * a.ldx;
-    T* yr = y + row * a.ldy;
-    for (int64_t u = threadIdx.x; u < (int64_t)a.heads * units; u += kThreads) {
-      const int64_t h = u / units * a.dim;
-      const int i = (int)(u % units);
-      if (i < a.pairs) {
-        const int64_t p = h + (a.interleaved ? 2 * i : i), q = h + (a.interleaved ? 2 * i + 1 : a.pairs + i);
-        const float v0 = get(xr[p]), v1 = get(xr[q]);
-        const f32x2 t = turn[i];
-        yr[p] = put(v0 * t.x - v1 * t.y);
-        yr[q] = put(v0 * t.y + v1 * t.x);
-      } else if (!a.in_place) {
-        yr[h + a.pairs + i] = xr[h + a.pairs + i];
+// VEC neighbouring values of a row.
+template <typename T, int VEC>
+struct Values {
+  T v[VEC];
+  __device__ __forceinline__ void load(const T* p) { __builtin_memcpy(v, p, sizeof(v)); }
+  __device__ __forceinline__ void store(T* p) const { __builtin_memcpy(p, v, sizeof(v)); }
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (sizeof(T) == 2) return bf16_bits_to_f32(v[e]);
+    else return v[e];
+  }
+  __device__ __forceinline__ void set(int e, float a, float b) {  // values e and e + 1
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t w = pack_bf16(a, b);
+      v[e] = (T)w;
+      if (e + 1 < VEC) v[e + 1] = (T)(w >> 16);
+    } else {
+      v[e] = a;
+      if (e + 1 < VEC) v[e + 1] = b;
+    }
+  }
+};
+
+// A workgroup has `block_rows` rows of `heads` heads from head blockIdx.y * heads on.  Its units are VEC pairs, or VEC values
+// behind the pairs; VEC divides pairs and dim.  A thread asks for the UNROLL units of a round at once.
+template <typename T, int VEC, bool INTERLEAVED>
+__global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, int block_rows, int heads, const T* x, T* y) {
+  constexpr int UNROLL = 4;
+  extern __shared__ f32x2 turn[];  // block_rows x pairs
+  const int64_t row0 = (int64_t)blockIdx.x * block_rows;
+  const int rows = (int)min((int64_t)block_rows, a.rows - row0);
+  const int head0 = blockIdx.y * heads, mine = min(heads, a.heads - head0);
+  for (int r = 0; r < rows; ++r) row_turns(a, row0 + r, turn + r * a.pairs, threadIdx.x, kThreads);
+  __syncthreads();
+  const uint32_t turning = a.pairs / VEC, per_head = turning + (a.in_place ? 0 : (a.dim - 2 * a.pairs) / VEC);
+  const uint32_t units = (uint32_t)rows * mine * per_head;
+  for (uint32_t u0 = threadIdx.x; u0 < units; u0 += kThreads * UNROLL) {
+    Values<T, VEC> p[UNROLL], q[UNROLL];
+    int64_t at[UNROLL];
+    uint32_t i[UNROLL], row[UNROLL];
+#pragma unroll
+    for (int k = 0; k < UNROLL; ++k) {
+      const uint32_t u = u0 + k * kThreads;
+      if (u >= units) break;
+      const uint32_t rest = u / per_head;
+      i[k] = u - rest * per_head;
+      row[k] = rest / (uint32_t)mine;
+      const uint32_t place = (rest - row[k] * mine + head0) * a.dim;
+      const bool turns = i[k] < turning;
+      at[k] = place + (turns ? (INTERLEAVED ? 2 : 1) * i[k] * VEC : 2 * a.pairs + (i[k] - turning) * VEC);
+      const T* src = x + (row0 + row[k]) * a.ldx + at[k];
+      p[k].load(src);
+      if (turns) q[k].load(src + (INTERLEAVED ? VEC : a.pairs));
+    }
+#pragma unroll
+    for (int k = 0; k < UNROLL; ++k) {
+      if (u0 + k * kThreads >= units) break;
+      T* dst = y + (row0 + row[k]) * a.ldy + at[k];
+      if (i[k] >= turning) {
+        p[k].store(dst);
+        continue;
       }
+      const f32x2* t = turn + row[k] * a.pairs + i[k] * VEC;
+      float c[2 * VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const int m = 2 * e, n = 2 * e + 1;
+        const float v0 = INTERLEAVED ? (m < VEC ? p[k].get(m % VEC) : q[k].get(m % VEC)) : p[k].get(e);
+        const float v1 = INTERLEAVED ? (n < VEC ? p[k].get(n % VEC) : q[k].get(n % VEC)) : q[k].get(e);
+        const f32x2 w = t[e];
+        c[INTERLEAVED ? m : e] = v0 * w.x - v1 * w.y;
+        c[INTERLEAVED ? n : VEC + e] = v0 * w.y + v1 * w.x;
+      }
+#pragma unroll
+      for (int e = 0; e < VEC; e += 2) {
+        p[k].set(e, c[e], c[e + 1]);
+        q[k].set(e, c[VEC + e], VEC + e + 1 < 2 * VEC ? c[VEC + e + 1] : 0.0f);
+      }
+      p[k].store(dst);
+      q[k].store(dst + (INTERLEAVED ? VEC : a.pairs));
     }
   }
 }
@@ -82,9 +130,29 @@ using namespace wr;
 
 template <typename T>
 static void rotary_launch(wr_ctx* ctx, const RotaryArgs& a, const void* x, void* y) {
-  const uint32_t blocks = (uint32_t)std::min<int64_t>(a.rows, 1 << 20);
-  hipLaunchKernelGGL(rotary_any_kernel<T>, dim3(blocks), dim3(kThreads), 0, ctx->stream, a, static_cast<const T*>(x),
-                     static_cast<T*>(y));
+  const int vec = a.pairs % 8 == 0 && a.dim % 8 == 0 ? 8 : a.pairs % 4 == 0 && a.dim % 4 == 0 ? 4 : 1;
+  // Rows enough for five units a thread share a workgroup and its latency of forming angles; a workgroup of one row has about
+  // 256 units of it, so that few rows still go to many compute units.
+  const int64_t per_head = std::max<int64_t>(1, (a.pairs + (a.in_place ? 0 : a.dim - 2 * a.pairs)) / vec);
+  const int64_t per_row = per_head * a.heads;
+  int64_t rows = std::max<int64_t>(1, std::min<int64_t>({kThreads * 5 / per_row, a.rows, 16 * kPairs / std::max(a.pairs, 1) / 4}));
+  rows = std::max<int64_t>(1, std::min(rows, a.rows / (4 * (int64_t)ctx->num_cu)));
+  const int64_t heads = rows > 1 ? a.heads : std::min<int64_t>(a.heads, std::max<int64_t>(1, kThreads / per_head));
+  const int64_t blocks = (a.rows + rows - 1) / rows, parts = (a.heads + heads - 1) / heads;
+  const size_t lds = (size_t)rows * std::max(a.pairs, 1) * sizeof(f32x2);
+  auto go = [&](auto v, auto inter) {
+    constexpr int VEC = decltype(v)::value;
+    constexpr bool INTERLEAVED = decltype(inter)::value;
+    hipLaunchKernelGGL((rotary_kernel<T, VEC, INTERLEAVED>), dim3((uint32_t)blocks, (uint32_t)parts), dim3(kThreads), lds, ctx->stream,
+                       a, (int)rows, (int)heads, static_cast<const T*>(x), static_cast<T*>(y));
+  };
+  auto with = [&](auto inter) {
+    if (vec == 8) go(std::integral_constant<int, 8>{}, inter);
+    else if (vec == 4) go(std::integral_constant<int, 4>{}, inter);
+    else go(std::integral_constant<int, 1>{}, inter);
+  };
+  if (a.interleaved) with(std::true_type{});
+  else with(std::false_type{});
 }
 
 int wr_rotary_impl(wr_ctx* ctx, const void* x, int dtype, int64_t rows, int32_t heads, int32_t dim, int64_t ldx,
