@@ -53,21 +53,24 @@ __device__ __forceinline__ float across(float v) {
 template <int LANES, typename T>
 __device__ __forceinline__ void group_codes(const Raw8<T>& raw, uint32_t& codes, uint32_t& meta) {
   float x[8];
-  float lo = INFINITY, hi = -INFINITY, size = 0.0f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    x[e] = raw.get(e);
-    lo = fminf(lo, x[e]);
-    hi = fmaxf(hi, x[e]);
-    size = fmaf(0.0f, x[e], size);  // 0, or NaN where a value is not finite
+  for (int e = 0; e < 8; ++e) x[e] = raw.get(e);
+  auto least = [](float a, float b) { return __builtin_elementwise_minimum(a, b); };  // NaN where there is one
+  auto most = [](float a, float b) { return __builtin_elementwise_maximum(a, b); };
+  float lo = least(least(x[0], x[1]), x[2]), hi = most(most(x[0], x[1]), x[2]);
+#pragma unroll
+  for (int e = 3; e < 7; e += 2) {
+    lo = least(least(lo, x[e]), x[e + 1]);
+    hi = most(most(hi, x[e]), x[e + 1]);
   }
+  lo = least(lo, x[7]);
+  hi = most(hi, x[7]);
   static_for<0, LANES == 4 ? 2 : LANES == 8 ? 3 : 4>([&](auto n) {
     constexpr int step = 1 << decltype(n)::value;
-    lo = fminf(lo, across<step>(lo));
-    hi = fmaxf(hi, across<step>(hi));
-    size += across<step>(size);
+    lo = least(lo, across<step>(lo));
+    hi = most(hi, across<step>(hi));
   });
-  const bool finite = size == 0.0f;
+  const bool finite = fabsf(lo) < INFINITY && fabsf(hi) < INFINITY;
   if (__builtin_amdgcn_ballot_w64(lo < -kKvMost || hi > kKvMost)) {
     asm volatile("");
     lo = fminf(fmaxf(lo, -kKvMost), kKvMost);
@@ -75,20 +78,27 @@ __device__ __forceinline__ void group_codes(const Raw8<T>& raw, uint32_t& codes,
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = fminf(fmaxf(x[e], -kKvMost), kKvMost);
   }
+  // Quotients correctly rounded, by Markstein's theorem: with y the correctly rounded reciprocal of the divisor, q = d y and the
+  // exact rest r = d - q divisor, q + r y rounds to the quotient.  One Newton step makes y out of a reciprocal that is
+  // off by up to two units in the last place, for every divisor of eleven bits.
+  auto quotient = [](float d, float divisor, float y) {
+    const float q = d * y;
+    return fmaf(fmaf(-q, divisor, d), y, q);
+  };
   const uint16_t off_bits = __builtin_bit_cast(uint16_t, (_Float16)lo);
   const float off = f16_bits_to_f32(off_bits);
-  const uint16_t scale_bits = __builtin_bit_cast(uint16_t, (_Float16)__fdiv_rn(hi - off, 15.0f));
+  float step = quotient(hi - off, 15.0f, 1.0f / 15.0f);
+  asm("" : "+v"(step));  // rounded to fp32 first: an instruction that rounds the last product and sum straight to fp16 differs at ties
+  const uint16_t scale_bits = __builtin_bit_cast(uint16_t, (_Float16)step);
   const float scale = f16_bits_to_f32(scale_bits);
   meta = finite ? scale_bits | (uint32_t)off_bits << 16 : 0x7e007e00u;
   const bool some = finite && scale > 0.0f;
-  // The quotient correctly rounded, by Markstein's theorem: with y the correctly rounded reciprocal, q = d y and the
-  // exact rest r = d - q scale, q + r y rounds to the quotient.
-  const float y = __fdiv_rn(1.0f, some ? scale : 1.0f);
+  const float divisor = some ? scale : 1.0f, y0 = __builtin_amdgcn_rcpf(divisor);
+  const float y = fmaf(fmaf(-divisor, y0, 1.0f), y0, y0);
   float c[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float d = x[e] - off, q = d * y, r = fmaf(-q, scale, d);
-    c[e] = rintf(__builtin_amdgcn_fmed3f(fmaf(r, y, q), 0.0f, 15.0f));
+    c[e] = rintf(__builtin_amdgcn_fmed3f(quotient(x[e] - off, divisor, y), 0.0f, 15.0f));
   }
   const uint32_t low = (uint32_t)fmaf(4096.0f, c[3], fmaf(256.0f, c[2], fmaf(16.0f, c[1], c[0])));
   const uint32_t high = (uint32_t)fmaf(4096.0f, c[7], fmaf(256.0f, c[6], fmaf(16.0f, c[5], c[4])));
@@ -100,23 +110,34 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvArgs a, int tiles,
                                                             const T* __restrict__ v, int64_t ldv) {
   constexpr int UNITS = DIM / 8;  // of eight values a token
   __shared__ uint32_t vcodes[16][UNITS + 1];
+  constexpr int ITERS = 2 * 16 * UNITS / kThreads;  // a wave has units of either k or v
   Tile t;
   int head;
-  if (!tile_of(a, tiles, blockIdx.x, head, t) || t.page < 0 || t.page >= a.count) return;
-  const KvLayout<DIM, GROUP> at{1 << a.page_shift};
-  uint8_t* base = a.pages + (int64_t)t.page * ((int64_t)a.heads * at.head_bytes()) + head * at.head_bytes();
-  for (int u = threadIdx.x; u < 2 * 16 * UNITS; u += kThreads) {  // a wave has units of either k or v
+  if (!tile_of(a, tiles, blockIdx.x, head, t)) return;
+  Raw8<T> x[ITERS];
+  bool live[ITERS];
+#pragma unroll
+  for (int n = 0; n < ITERS; ++n) {
+    const int u = threadIdx.x + n * kThreads;
     const bool values = u >= 16 * UNITS;
     const int token = u / UNITS % 16, c = u % UNITS;
     const T* src = values ? v : k;
-    if (!src) continue;
-    const bool live = token >= t.from && token < t.to;
-    if (__builtin_amdgcn_ballot_w64(live) == 0) continue;
-    Raw8<T> x;
-    x.load(src + (int64_t)(t.row0 + (live ? token : t.from)) * (values ? ldv : ldk) + head * DIM + 8 * c);
+    live[n] = src && token >= t.from && token < t.to;
+    if (live[n]) x[n].load(src + (int64_t)(t.row0 + token) * (values ? ldv : ldk) + head * DIM + 8 * c);
+    else x[n].fill(0.0f);
+  }
+  if (t.page < 0 || t.page >= a.count) return;
+  const KvLayout<DIM, GROUP> at{1 << a.page_shift};
+  uint8_t* base = a.pages + (int64_t)t.page * ((int64_t)a.heads * at.head_bytes()) + head * at.head_bytes();
+#pragma unroll
+  for (int n = 0; n < ITERS; ++n) {
+    const int u = threadIdx.x + n * kThreads;
+    const bool values = u >= 16 * UNITS;
+    const int token = u / UNITS % 16, c = u % UNITS;
+    if (__builtin_amdgcn_ballot_w64(live[n]) == 0) continue;
     uint32_t codes, meta;
-    group_codes<GROUP / 8>(x, codes, meta);
-    if (!live) continue;
+    group_codes<GROUP / 8>(x[n], codes, meta);
+    if (!live[n]) continue;
     const int in_page = t.at + token;
     if (values)
       vcodes[token][c] = codes;

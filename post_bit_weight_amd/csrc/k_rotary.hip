@@ -62,10 +62,10 @@ struct Values {
 };
 
 // A workgroup has `block_rows` rows of `heads` heads from head blockIdx.y * heads on.  Its units are VEC pairs, or VEC values
-// behind the pairs; VEC divides pairs and dim.  A thread asks for the UNROLL units of a round at once.
+// behind the pairs; VEC divides pairs and dim.  One unit at a time a thread: the waves that few registers leave room for hide memory better
+// than more units in flight (8192 rows of 40 heads of 128: 37 us with one, 44 with two or three, 48 with four).
 template <typename T, int VEC, bool INTERLEAVED>
 __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, int block_rows, int heads, const T* x, T* y) {
-  constexpr int UNROLL = 4;
   extern __shared__ f32x2 turn[];  // block_rows x pairs
   const int64_t row0 = (int64_t)blockIdx.x * block_rows;
   const int rows = (int)min((int64_t)block_rows, a.rows - row0);
@@ -74,51 +74,39 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, int bloc
   __syncthreads();
   const uint32_t turning = a.pairs / VEC, per_head = turning + (a.in_place ? 0 : (a.dim - 2 * a.pairs) / VEC);
   const uint32_t units = (uint32_t)rows * mine * per_head;
-  for (uint32_t u0 = threadIdx.x; u0 < units; u0 += kThreads * UNROLL) {
-    Values<T, VEC> p[UNROLL], q[UNROLL];
-    int64_t at[UNROLL];
-    uint32_t i[UNROLL], row[UNROLL];
+  for (uint32_t u = threadIdx.x; u < units; u += kThreads) {
+    const uint32_t rest = u / per_head, i = u - rest * per_head, row = rest / (uint32_t)mine;
+    const int64_t place = (int64_t)(rest - row * mine + head0) * a.dim;
+    const T* src = x + (row0 + row) * a.ldx + place;
+    T* dst = y + (row0 + row) * a.ldy + place;
+    Values<T, VEC> p, q;
+    if (i >= turning) {
+      const uint32_t at = 2 * a.pairs + (i - turning) * VEC;
+      p.load(src + at);
+      p.store(dst + at);
+      continue;
+    }
+    const uint32_t at = (INTERLEAVED ? 2 : 1) * i * VEC, to = at + (INTERLEAVED ? VEC : a.pairs);
+    p.load(src + at);
+    q.load(src + to);
+    const f32x2* t = turn + row * a.pairs + i * VEC;
+    float c[2 * VEC];
 #pragma unroll
-    for (int k = 0; k < UNROLL; ++k) {
-      const uint32_t u = u0 + k * kThreads;
-      if (u >= units) break;
-      const uint32_t rest = u / per_head;
-      i[k] = u - rest * per_head;
-      row[k] = rest / (uint32_t)mine;
-      const uint32_t place = (rest - row[k] * mine + head0) * a.dim;
-      const bool turns = i[k] < turning;
-      at[k] = place + (turns ? (INTERLEAVED ? 2 : 1) * i[k] * VEC : 2 * a.pairs + (i[k] - turning) * VEC);
-      const T* src = x + (row0 + row[k]) * a.ldx + at[k];
-      p[k].load(src);
-      if (turns) q[k].load(src + (INTERLEAVED ? VEC : a.pairs));
+    for (int e = 0; e < VEC; ++e) {
+      const int m = 2 * e, n = 2 * e + 1;
+      const float v0 = INTERLEAVED ? (m < VEC ? p.get(m % VEC) : q.get(m % VEC)) : p.get(e);
+      const float v1 = INTERLEAVED ? (n < VEC ? p.get(n % VEC) : q.get(n % VEC)) : q.get(e);
+      const f32x2 w = t[e];
+      c[INTERLEAVED ? m : e] = v0 * w.x - v1 * w.y;
+      c[INTERLEAVED ? n : VEC + e] = v0 * w.y + v1 * w.x;
     }
 #pragma unroll
-    for (int k = 0; k < UNROLL; ++k) {
-      if (u0 + k * kThreads >= units) break;
-      T* dst = y + (row0 + row[k]) * a.ldy + at[k];
-      if (i[k] >= turning) {
-        p[k].store(dst);
-        continue;
-      }
-      const f32x2* t = turn + row[k] * a.pairs + i[k] * VEC;
-      float c[2 * VEC];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const int m = 2 * e, n = 2 * e + 1;
-        const float v0 = INTERLEAVED ? (m < VEC ? p[k].get(m % VEC) : q[k].get(m % VEC)) : p[k].get(e);
-        const float v1 = INTERLEAVED ? (n < VEC ? p[k].get(n % VEC) : q[k].get(n % VEC)) : q[k].get(e);
-        const f32x2 w = t[e];
-        c[INTERLEAVED ? m : e] = v0 * w.x - v1 * w.y;
-        c[INTERLEAVED ? n : VEC + e] = v0 * w.y + v1 * w.x;
-      }
-#pragma unroll
-      for (int e = 0; e < VEC; e += 2) {
-        p[k].set(e, c[e], c[e + 1]);
-        q[k].set(e, c[VEC + e], VEC + e + 1 < 2 * VEC ? c[VEC + e + 1] : 0.0f);
-      }
-      p[k].store(dst);
-      q[k].store(dst + (INTERLEAVED ? VEC : a.pairs));
+    for (int e = 0; e < VEC; e += 2) {
+      p.set(e, c[e], c[e + 1]);
+      q.set(e, c[VEC + e], VEC > 1 ? c[VEC + (e + 1) % VEC] : 0.0f);
     }
+    p.store(dst + at);
+    q.store(dst + to);
   }
 }
 
