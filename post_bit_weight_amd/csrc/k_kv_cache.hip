@@ -19,11 +19,15 @@ struct Tile {
   int at;          // the tile's first token in its page
 };
 
-// Blocks are numbered head fastest, then tile, then sequence.
-__device__ __forceinline__ bool tile_of(const KvArgs& a, int tiles, uint32_t block, int& head, Tile& t) {
-  const uint32_t rest = block / (uint32_t)a.heads;
-  head = block % (uint32_t)a.heads;
-  const int i = rest / (uint32_t)tiles, nth = rest % (uint32_t)tiles;
+// Blocks take `per` heads of a tile, so that many of them share the latency of finding it; they are numbered heads fastest, then tile,
+// then sequence.
+struct Work {
+  int tiles, per;  // tiles of a sequence, heads of a block
+};
+__device__ __forceinline__ bool tile_of(const KvArgs& a, const Work& w, uint32_t block, int& head, Tile& t) {
+  const uint32_t parts = (a.heads + w.per - 1) / (uint32_t)w.per, rest = block / parts;
+  head = (block - rest * parts) * w.per;
+  const int i = rest / (uint32_t)w.tiles, nth = rest - (uint32_t)i * w.tiles;
   const KvSeq s = kv_seq(a, i);
   if (s.fresh <= 0) return false;
   const int first = s.length - s.fresh;             // position of the first row; below 0 where rows have none
@@ -106,129 +110,140 @@ __device__ __forceinline__ void group_codes(const Raw8<T>& raw, uint32_t& codes,
 }
 
 template <int DIM, int GROUP, typename T>
-__global__ __launch_bounds__(kThreads) void kv_write_kernel(KvArgs a, int tiles, const T* __restrict__ k, int64_t ldk,
+__global__ __launch_bounds__(kThreads) void kv_write_kernel(KvArgs a, Work work, const T* __restrict__ k, int64_t ldk,
                                                             const T* __restrict__ v, int64_t ldv) {
   constexpr int UNITS = DIM / 8;  // of eight values a token
-  __shared__ uint32_t vcodes[16][UNITS + 1];
+  __shared__ uint32_t vcodes[2][16][UNITS + 1];
   constexpr int ITERS = 2 * 16 * UNITS / kThreads;  // a wave has units of either k or v
   Tile t;
   int head;
-  if (!tile_of(a, tiles, blockIdx.x, head, t)) return;
+  if (!tile_of(a, work, blockIdx.x, head, t)) return;
+  const int end = min(head + work.per, a.heads);
   Raw8<T> x[ITERS];
   bool live[ITERS];
+  auto load = [&](int h) {
 #pragma unroll
-  for (int n = 0; n < ITERS; ++n) {
-    const int u = threadIdx.x + n * kThreads;
-    const bool values = u >= 16 * UNITS;
-    const int token = u / UNITS % 16, c = u % UNITS;
-    const T* src = values ? v : k;
-    live[n] = src && token >= t.from && token < t.to;
-    if (live[n]) x[n].load(src + (int64_t)(t.row0 + token) * (values ? ldv : ldk) + head * DIM + 8 * c);
-    else x[n].fill(0.0f);
-  }
+    for (int n = 0; n < ITERS; ++n) {
+      const int u = threadIdx.x + n * kThreads;
+      const bool values = u >= 16 * UNITS;
+      const int token = u / UNITS % 16, c = u % UNITS;
+      const T* src = values ? v : k;
+      live[n] = src && token >= t.from && token < t.to;
+      if (live[n]) x[n].load(src + (int64_t)(t.row0 + token) * (values ? ldv : ldk) + h * DIM + 8 * c);
+    }
+  };
+  load(head);
   if (t.page < 0 || t.page >= a.count) return;
   const KvLayout<DIM, GROUP> at{1 << a.page_shift};
   uint8_t* base = a.pages + (int64_t)t.page * ((int64_t)a.heads * at.head_bytes()) + head * at.head_bytes();
+  for (int which = 0; head < end; ++head, which ^= 1, base += at.head_bytes()) {
+    uint32_t codes[ITERS], meta[ITERS];
 #pragma unroll
-  for (int n = 0; n < ITERS; ++n) {
-    const int u = threadIdx.x + n * kThreads;
-    const bool values = u >= 16 * UNITS;
-    const int token = u / UNITS % 16, c = u % UNITS;
-    if (__builtin_amdgcn_ballot_w64(live[n]) == 0) continue;
-    uint32_t codes, meta;
-    group_codes<GROUP / 8>(x[n], codes, meta);
-    if (!live[n]) continue;
-    const int in_page = t.at + token;
-    if (values)
-      vcodes[token][c] = codes;
-    else
-      *reinterpret_cast<uint32_t*>(base + in_page * (DIM / 2) + (c % 4) * (DIM / 8) + (c / 4) * 4) = codes;
-    if (c % (GROUP / 8) == 0) {
-      const int first = (c / (GROUP / 8)) * at.page_tokens;
-      if (values) {
-        uint16_t* m = reinterpret_cast<uint16_t*>(base + at.v_meta()) + at.v_scale(first, in_page);
-        m[0] = (uint16_t)meta;
-        m[2] = (uint16_t)(meta >> 16);
+    for (int n = 0; n < ITERS; ++n) {
+      codes[n] = meta[n] = 0;
+      if (__builtin_amdgcn_ballot_w64(live[n])) group_codes<GROUP / 8>(x[n], codes[n], meta[n]);
+    }
+    if (head + 1 < end) load(head + 1);  // on its way while these are stored
+#pragma unroll
+    for (int n = 0; n < ITERS; ++n) {
+      if (!live[n]) continue;
+      const int u = threadIdx.x + n * kThreads;
+      const bool values = u >= 16 * UNITS;
+      const int token = u / UNITS % 16, c = u % UNITS, in_page = t.at + token;
+      if (values)
+        vcodes[which][token][c] = codes[n];
+      else
+        *reinterpret_cast<uint32_t*>(base + in_page * (DIM / 2) + (c % 4) * (DIM / 8) + (c / 4) * 4) = codes[n];
+      if (c % (GROUP / 8) == 0) {
+        const int first = (c / (GROUP / 8)) * at.page_tokens;
+        if (values) {
+          uint16_t* m = reinterpret_cast<uint16_t*>(base + at.v_meta()) + at.v_scale(first, in_page);
+          m[0] = (uint16_t)meta[n];
+          m[2] = (uint16_t)(meta[n] >> 16);
+        } else {
+          *reinterpret_cast<uint32_t*>(base + at.k_meta() + (first + in_page) * 4) = meta[n];
+        }
+      }
+    }
+    if (!v) continue;
+    __syncthreads();
+    uint8_t* tile = base + at.v_codes() + t.at * (DIM / 2);
+    for (int w = threadIdx.x; w < 2 * DIM; w += kThreads) {  // the tile's dwords
+      const int m = w % (DIM / 32), l = w / (DIM / 32) % 16, g = w / (DIM / 2);
+      const int d = 16 * m + l;
+      uint32_t word = 0;
+      int there = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int token = 4 * g + i;
+        if (token >= t.from && token < t.to) {
+          const uint32_t lo = vcodes[which][token][d / 8] >> (4 * (d % 8)) & 15u;
+          const uint32_t hi = vcodes[which][token][(DIM / 2 + d) / 8] >> (4 * (d % 8)) & 15u;
+          word |= (lo | hi << 4) << (8 * i);
+          there |= 1 << i;
+        }
+      }
+      if (there == 15) {
+        *reinterpret_cast<uint32_t*>(tile + 4 * w) = word;
       } else {
-        *reinterpret_cast<uint32_t*>(base + at.k_meta() + (first + in_page) * 4) = meta;
-      }
-    }
-  }
-  if (!v) return;
-  __syncthreads();
-  uint8_t* tile = base + at.v_codes() + t.at * (DIM / 2);
-  for (int w = threadIdx.x; w < 2 * DIM; w += kThreads) {  // the tile's dwords
-    const int m = w % (DIM / 32), l = w / (DIM / 32) % 16, g = w / (DIM / 2);
-    const int d = 16 * m + l;
-    uint32_t word = 0;
-    int live = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int token = 4 * g + i;
-      if (token >= t.from && token < t.to) {
-        const uint32_t lo = vcodes[token][d / 8] >> (4 * (d % 8)) & 15u;
-        const uint32_t hi = vcodes[token][(DIM / 2 + d) / 8] >> (4 * (d % 8)) & 15u;
-        word |= (lo | hi << 4) << (8 * i);
-        live |= 1 << i;
+        for (int i = 0; i < 4; ++i)
+          if (there >> i & 1) tile[4 * w + i] = (uint8_t)(word >> (8 * i));
       }
-    }
-    if (live == 15) {
-      *reinterpret_cast<uint32_t*>(tile + 4 * w) = word;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (live >> i & 1) tile[4 * w + i] = (uint8_t)(word >> (8 * i));
     }
   }
 }
 
 template <int DIM, int GROUP, typename T>
-__global__ __launch_bounds__(kThreads) void kv_read_kernel(KvArgs a, int tiles, T* __restrict__ k, int64_t ldk,
+__global__ __launch_bounds__(kThreads) void kv_read_kernel(KvArgs a, Work work, T* __restrict__ k, int64_t ldk,
                                                            T* __restrict__ v, int64_t ldv) {
   constexpr int UNITS = DIM / 8;
-  __shared__ uint32_t vtile[2 * DIM];
+  __shared__ uint32_t vtile[2][2 * DIM];
   Tile t;
   int head;
-  if (!tile_of(a, tiles, blockIdx.x, head, t)) return;
+  if (!tile_of(a, work, blockIdx.x, head, t)) return;
+  const int end = min(head + work.per, a.heads);
   const bool there = t.page >= 0 && t.page < a.count;
   const KvLayout<DIM, GROUP> at{1 << a.page_shift};
   const uint8_t* base = a.pages + (int64_t)(there ? t.page : 0) * ((int64_t)a.heads * at.head_bytes()) + head * at.head_bytes();
-  if (v) {
-    const uint8_t* tile = base + at.v_codes() + t.at * (DIM / 2);
-    if (there)
-      for (int w = threadIdx.x; w < 2 * DIM; w += kThreads) vtile[w] = *reinterpret_cast<const uint32_t*>(tile + 4 * w);
-    __syncthreads();
-  }
-  for (int u = threadIdx.x; u < 2 * 16 * UNITS; u += kThreads) {
-    const bool values = u >= 16 * UNITS;
-    const int token = u / UNITS % 16, c = u % UNITS;
-    T* dst = values ? v : k;
-    if (!dst || token < t.from || token >= t.to) continue;
-    float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (there) {
-      const int in_page = t.at + token;
-      const int first = (c / (GROUP / 8)) * at.page_tokens;
-      const uint16_t* m = values ? reinterpret_cast<const uint16_t*>(base + at.v_meta()) + at.v_scale(first, in_page)
-                                 : reinterpret_cast<const uint16_t*>(base + at.k_meta()) + 2 * (first + in_page);
-      const float scale = f16_bits_to_f32(m[0]), off = f16_bits_to_f32(m[values ? 2 : 1]);
-      uint32_t codes;
-      if (values) {
-        codes = 0;
-        const int cc = c % (UNITS / 2), shift = 8 * (token % 4) + (c >= UNITS / 2 ? 4 : 0);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int d = 8 * cc + e;
-          codes |= (vtile[((token / 4) * 16 + d % 16) * (DIM / 32) + d / 16] >> shift & 15u) << (4 * e);
-        }
-      } else {
-        codes = *reinterpret_cast<const uint32_t*>(base + in_page * (DIM / 2) + (c % 4) * (DIM / 8) + (c / 4) * 4);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = fmaf((float)(codes >> (4 * e) & 15u), scale, off);  // the product is exact
+  for (int which = 0; head < end; ++head, which ^= 1, base += at.head_bytes()) {
+    if (v) {
+      const uint8_t* tile = base + at.v_codes() + t.at * (DIM / 2);
+      if (there)
+        for (int w = threadIdx.x; w < 2 * DIM; w += kThreads) vtile[which][w] = *reinterpret_cast<const uint32_t*>(tile + 4 * w);
+      __syncthreads();
     }
-    Raw8<T> r;
-    r.round(f);
-    r.store(dst + (int64_t)(t.row0 + token) * (values ? ldv : ldk) + head * DIM + 8 * c);
+    for (int u = threadIdx.x; u < 2 * 16 * UNITS; u += kThreads) {
+      const bool values = u >= 16 * UNITS;
+      const int token = u / UNITS % 16, c = u % UNITS;
+      T* dst = values ? v : k;
+      if (!dst || token < t.from || token >= t.to) continue;
+      float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      if (there) {
+        const int in_page = t.at + token;
+        const int first = (c / (GROUP / 8)) * at.page_tokens;
+        const uint16_t* m = values ? reinterpret_cast<const uint16_t*>(base + at.v_meta()) + at.v_scale(first, in_page)
+                                   : reinterpret_cast<const uint16_t*>(base + at.k_meta()) + 2 * (first + in_page);
+        const float scale = f16_bits_to_f32(m[0]), off = f16_bits_to_f32(m[values ? 2 : 1]);
+        uint32_t codes;
+        if (values) {
+          codes = 0;
+          const int cc = c % (UNITS / 2), shift = 8 * (token % 4) + (c >= UNITS / 2 ? 4 : 0);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int d = 8 * cc + e;
+            codes |= (vtile[which][((token / 4) * 16 + d % 16) * (DIM / 32) + d / 16] >> shift & 15u) << (4 * e);
+          }
+        } else {
+          codes = *reinterpret_cast<const uint32_t*>(base + in_page * (DIM / 2) + (c % 4) * (DIM / 8) + (c / 4) * 4);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = fmaf((float)(codes >> (4 * e) & 15u), scale, off);  // the product is exact
+      }
+      Raw8<T> r;
+      r.round(f);
+      r.store(dst + (int64_t)(t.row0 + token) * (values ? ldv : ldk) + head * DIM + 8 * c);
+    }
   }
 }
 
@@ -260,17 +275,26 @@ static int64_t tiles_of(const wr_kv_seqs& s) { return ((int64_t)s.most_new + 14)
 
 int64_t wr_kv_blocks(const wr_kv_cache& c, const wr_kv_seqs& s) { return (int64_t)c.heads * s.n * tiles_of(s); }
 
+// One head a block until the card is full eight times over, then as many as leave it that.
+static Work work_of(wr_ctx* ctx, const wr_kv_cache& c, const wr_kv_seqs& s, dim3& grid) {
+  const int64_t full = 8 * (int64_t)ctx->num_cu, tiles = s.n * tiles_of(s);
+  const int per = (int)std::min<int64_t>(c.heads, std::max<int64_t>(1, c.heads * tiles / full));
+  grid = dim3((uint32_t)(tiles * ((c.heads + per - 1) / per)));
+  return Work{(int)tiles_of(s), per};
+}
+
 int wr_kv_write_impl(wr_ctx* ctx, const wr_kv_cache& c, const wr_kv_seqs& s, const void* k, int64_t ldk, const void* v,
                      int64_t ldv, int dtype, int64_t rows) {
   const KvArgs a = kv_args(c, s, rows);
   const bool there = kv_form(c.dim, c.group, [&](auto d, auto g) {
     constexpr int D = decltype(d)::value, G = decltype(g)::value;
-    const dim3 grid((uint32_t)wr_kv_blocks(c, s));
+    dim3 grid;
+    const Work work = work_of(ctx, c, s, grid);
     if (dtype == WR_BF16)
-      hipLaunchKernelGGL((kv_write_kernel<D, G, uint16_t>), grid, dim3(kThreads), 0, ctx->stream, a, (int)tiles_of(s),
+      hipLaunchKernelGGL((kv_write_kernel<D, G, uint16_t>), grid, dim3(kThreads), 0, ctx->stream, a, work,
                          static_cast<const uint16_t*>(k), ldk, static_cast<const uint16_t*>(v), ldv);
     else
-      hipLaunchKernelGGL((kv_write_kernel<D, G, float>), grid, dim3(kThreads), 0, ctx->stream, a, (int)tiles_of(s),
+      hipLaunchKernelGGL((kv_write_kernel<D, G, float>), grid, dim3(kThreads), 0, ctx->stream, a, work,
                          static_cast<const float*>(k), ldk, static_cast<const float*>(v), ldv);
   });
   if (!there) return WR_EUNSUPPORTED;
@@ -283,12 +307,13 @@ int wr_kv_read_impl(wr_ctx* ctx, const wr_kv_cache& c, const wr_kv_seqs& s, void
   const KvArgs a = kv_args(c, s, rows);
   const bool there = kv_form(c.dim, c.group, [&](auto d, auto g) {
     constexpr int D = decltype(d)::value, G = decltype(g)::value;
-    const dim3 grid((uint32_t)wr_kv_blocks(c, s));
+    dim3 grid;
+    const Work work = work_of(ctx, c, s, grid);
     if (dtype == WR_BF16)
-      hipLaunchKernelGGL((kv_read_kernel<D, G, uint16_t>), grid, dim3(kThreads), 0, ctx->stream, a, (int)tiles_of(s),
+      hipLaunchKernelGGL((kv_read_kernel<D, G, uint16_t>), grid, dim3(kThreads), 0, ctx->stream, a, work,
                          static_cast<uint16_t*>(k), ldk, static_cast<uint16_t*>(v), ldv);
     else
-      hipLaunchKernelGGL((kv_read_kernel<D, G, float>), grid, dim3(kThreads), 0, ctx->stream, a, (int)tiles_of(s),
+      hipLaunchKernelGGL((kv_read_kernel<D, G, float>), grid, dim3(kThreads), 0, ctx->stream, a, work,
                          static_cast<float*>(k), ldk, static_cast<float*>(v), ldv);
   });
   if (!there) return WR_EUNSUPPORTED;
