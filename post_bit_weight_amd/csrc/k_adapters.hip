@@ -1,6 +1,6 @@
 // Low-rank adapters of many requests beside a shared projection: y = base + s B (A x).
 //
-// Two launches.  The first forms t = A x (rows x rank, fp32, in the workspace): x is read once, a workgroup takes 16
+// Two launches.  The first forms t = A x (rows x rank, as three bf16 parts, in the workspace): x is read once, a workgroup takes 16
 // or 32 rows of a request and up to 64 rows of A, and its eight waves cut the sum over n, which is what fills the card when
 // there are few rows.  The second forms y: a wave keeps its rows of t as matrix operands and walks the outputs 64 at a
 // time; the matrix product's rows are dealt to outputs so that a lane ends up with 16 neighbouring ones, and base
@@ -20,10 +20,10 @@ struct AdapterArgs {
   const float* scales;
   const uint16_t* A;
   const uint16_t* B;
-  float* t;        // rows x rank
+  uint16_t* t;     // rows x 3 x wide: A x as the sum of three bf16 parts
   int64_t rows, n, outs, most;
   int64_t ldx, ldb, ldy;
-  int32_t adapters, rank;
+  int32_t adapters, rank, wide;  // wide: rank, up to a multiple of 8
   uint32_t tiles;  // row tiles of a request
 };
 
@@ -60,19 +60,21 @@ __device__ __forceinline__ void load8(Raw8<T>& r, const T* row, int64_t k, int64
   }
 }
 
-// f = p[0] + p[1] + p[2] in bf16, exactly; an infinity or NaN is p[0].
-__device__ __forceinline__ void three_parts(const float (&f)[8], u32x4 (&p)[3]) {
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// The values rounded to bf16, and what is left of them.  Three times makes any fp32 value exactly; of an infinity or NaN
+// nothing is left.
+__device__ __forceinline__ uint32_t bf16_part(float& a, float& b) {
+  const uint32_t h = pack_bf16(a, b);
+  a = (h & 0x7f80u) == 0x7f80u ? 0.0f : a - __uint_as_float(h << 16);
+  b = (h & 0x7f800000u) == 0x7f800000u ? 0.0f : b - __uint_as_float(h & 0xffff0000u);
+  return h;
+}
+__device__ __forceinline__ void three_parts(float (&f)[8], u32x4 (&p)[3]) {
 #pragma unroll
-  for (int d = 0; d < 4; ++d) {
-    float a = f[2 * d], b = f[2 * d + 1];
+  for (int i = 0; i < 3; ++i)
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      const uint32_t h = pack_bf16(a, b);
-      p[i][d] = h;
-      a = (h & 0x7f80u) == 0x7f80u ? 0.0f : a - __uint_as_float(h << 16);
-      b = (h & 0x7f800000u) == 0x7f800000u ? 0.0f : b - __uint_as_float(h & 0xffff0000u);
-    }
-  }
+    for (int d = 0; d < 4; ++d) p[i][d] = bf16_part(f[2 * d], f[2 * d + 1]);
 }
 
 template <typename X>
@@ -113,37 +115,55 @@ __global__ __launch_bounds__(512) void adapters_in_kernel(AdapterArgs a, const X
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int c = 0; c < NT; ++c) acc[m][c] = f32x4{0, 0, 0, 0};
-  auto step = [&](int64_t k, auto whole) {  // 64 values of n
-    Raw8<X> xv[2][MT];
-    Raw8<uint16_t> av[2][NT];
+  struct Step {  // 64 values of n
+    Raw8<X> x[2][MT];
+    Raw8<uint16_t> a[2][NT];
+  } even, odd;
+  auto fetch = [&](Step& f, int64_t k, bool whole) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int c = 0; c < NT; ++c) {
-        if constexpr (decltype(whole)::value) av[h][c].load(ar[c] + k + 32 * h + 8 * g);
-        else load8(av[h][c], ar[c], k + 32 * h + 8 * g, a.n);
-      }
+      const int64_t at = k + 32 * h + 8 * g;
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        if constexpr (decltype(whole)::value) xv[h][m].load(xr[m] + k + 32 * h + 8 * g);
-        else load8(xv[h][m], xr[m], k + 32 * h + 8 * g, a.n);
+        if (whole) f.x[h][m].load(xr[m] + at);
+        else load8(f.x[h][m], xr[m], at, a.n);
+      }
+#pragma unroll
+      for (int c = 0; c < NT; ++c) {
+        if (whole) f.a[h][c].load(ar[c] + at);
+        else load8(f.a[h][c], ar[c], at, a.n);
       }
     }
+  };
+  auto multiply = [&](const Step& f) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const Parts<X> p(xv[h][m]);
+        const Parts<X> p(f.x[h][m]);
 #pragma unroll
         for (int i = 0; i < Parts<X>::N; ++i)
 #pragma unroll
-          for (int c = 0; c < NT; ++c) acc[m][c] = mfma16x16x32_bf16(av[h][c].v, p.p[i], acc[m][c]);
+          for (int c = 0; c < NT; ++c) acc[m][c] = mfma16x16x32_bf16(f.a[h][c].v, p.p[i], acc[m][c]);
       }
   };
+  // two steps in turn, each loaded while the other is worked on
+  constexpr int64_t kRound = 64 * WAVES;
   const int64_t whole = a.n / 64 * 64;
-#pragma unroll 2
-  for (int64_t k = 64 * wave; k < whole; k += 64 * WAVES) step(k, std::true_type{});
-  if (whole < a.n && (a.n / 64) % WAVES == wave) step(whole, std::false_type{});
+  int64_t k = 64 * wave;
+  if (k < whole) fetch(even, k, true);
+  while (k < whole) {
+    if (k + kRound < whole) fetch(odd, k + kRound, true);
+    multiply(even);
+    if (k + kRound >= whole) break;
+    if (k + 2 * kRound < whole) fetch(even, k + 2 * kRound, true);
+    multiply(odd);
+    k += 2 * kRound;
+  }
+  if (whole < a.n && (a.n / 64) % WAVES == wave) {
+    fetch(even, whole, false);
+    multiply(even);
+  }
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -156,11 +176,16 @@ __global__ __launch_bounds__(512) void adapters_in_kernel(AdapterArgs a, const X
 #pragma unroll
     for (int w = 1; w < WAVES; ++w) sum += part[w][m][c][l];
     const int row = 16 * m + l % 16, r = r0 + 16 * c + 4 * (l / 16);
-    if (row < q.count) {
-      float* t = a.t + (q.row + row) * a.rank + r;
+    if (row < q.count && r < a.wide) {  // zeros behind the rank, in the last eight of it
+      uint16_t* t = a.t + (q.row + row) * 3 * a.wide + r;
+      float f[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (r + i < q.rank) t[i] = sum[i];
+      for (int e = 0; e < 4; ++e) f[e] = r + e < q.rank ? sum[e] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const uint32_t low = bf16_part(f[0], f[1]), high = bf16_part(f[2], f[3]);
+        *reinterpret_cast<u32x2*>(t + i * a.wide) = u32x2{low, high};
+      }
     }
   }
 }
@@ -178,34 +203,44 @@ __global__ __launch_bounds__(256) void adapters_out_kernel(AdapterArgs a, const 
   u32x4 t[MT][KS][3];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    const float* tr = a.t + (q.row + min((int64_t)(16 * m + low), q.count - 1)) * a.rank;
+    const uint16_t* tr = a.t + (q.row + min((int64_t)(16 * m + low), q.count - 1)) * 3 * a.wide;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      float f[8];
+    for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int r = 32 * ks + 8 * g + e;
-        f[e] = r < q.rank ? tr[r] : 0.0f;
+      for (int i = 0; i < 3; ++i) {
+        const int r = 32 * ks + 8 * g;
+        t[m][ks][i] = r < q.rank ? *reinterpret_cast<const u32x4*>(tr + i * a.wide + r) : u32x4{0, 0, 0, 0};
       }
-      three_parts(f, t[m][ks]);
-    }
   }
   const uint16_t* bp = a.B + (int64_t)max(q.adapter, 0) * a.outs * a.rank;
   for (int64_t o0 = ((int64_t)nth * WAVES + wave) * 64; o0 < a.outs; o0 += (int64_t)out_parts * WAVES * 64) {
-    f32x4 acc[MT][4];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[m][j] = f32x4{0, 0, 0, 0};
+    // everything that this step reads is asked for first
+    Raw8<uint16_t> b[4][KS];
     if (q.rank > 0) {
       // row `low` of product j is output 16 (low / 4) + 4 j + low % 4
-      Raw8<uint16_t> b[4][KS];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint16_t* br = bp + min(o0 + 16 * (low / 4) + 4 * j + low % 4, a.outs - 1) * a.rank;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) load8(b[j][ks], br, 32 * ks + 8 * g, q.rank);
       }
+    }
+    const int64_t o = o0 + 16 * g;
+    Raw8<Y> v[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = 16 * m + low;
+        if (base && row < q.count && o + 8 * h < a.outs) load8(v[m][h], base + (q.row + row) * a.ldb, o + 8 * h, a.outs);
+        else v[m][h].fill(0.0f);
+      }
+    f32x4 acc[MT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[m][j] = f32x4{0, 0, 0, 0};
+    if (q.rank > 0) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -215,29 +250,24 @@ __global__ __launch_bounds__(256) void adapters_out_kernel(AdapterArgs a, const 
 #pragma unroll
             for (int m = 0; m < MT; ++m) acc[m][j] = mfma16x16x32_bf16(b[j][ks].v, t[m][ks][i], acc[m][j]);
     }
-    const int64_t o = o0 + 16 * g;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const int row = 16 * m + low;
       if (row >= q.count) continue;
-      const Y* b = base ? base + (q.row + row) * a.ldb : nullptr;
       Y* out = y + (q.row + row) * a.ldy;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int64_t at = o + 8 * h;
         if (at >= a.outs) continue;
-        Raw8<Y> v;
-        v.fill(0.0f);
-        if (b) load8(v, b, at, a.outs);
         float f[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = fmaf(acc[m][2 * h + e / 4][e % 4], s, v.get(e));
-        if (q.rank > 0) v.round(f);
+        for (int e = 0; e < 8; ++e) f[e] = fmaf(acc[m][2 * h + e / 4][e % 4], s, v[m][h].get(e));
+        if (q.rank > 0) v[m][h].round(f);
         if (at + 8 <= a.outs) {
-          v.store(out + at);
+          v[m][h].store(out + at);
         } else {
           for (int e = 0; e < 8; ++e)
-            if (at + e < a.outs) out[at + e] = v.at(e);
+            if (at + e < a.outs) out[at + e] = v[m][h].at(e);
         }
       }
     }
@@ -254,7 +284,7 @@ using namespace wr;
 
 size_t wr_adapters_ws_bytes(int64_t rows, int64_t n, int32_t rank) {
   (void)n;
-  return (size_t)rows * rank * sizeof(float);
+  return (size_t)rows * ((rank + 7) / 8 * 8) * 3 * sizeof(uint16_t);
 }
 
 int wr_adapters_impl(wr_ctx* ctx, const void* x, int x_dtype, int64_t rows, int64_t n, int64_t ldx, const void* A,
@@ -262,7 +292,7 @@ int wr_adapters_impl(wr_ctx* ctx, const void* x, int x_dtype, int64_t rows, int6
                      const int32_t* ranks, const int32_t* starts, const int32_t* ids, int32_t n_seqs, int64_t most,
                      const void* base, int64_t ldb, void* y, int y_dtype, int64_t ldy) {
   AdapterArgs a{starts, ids, ranks, scales, static_cast<const uint16_t*>(A), static_cast<const uint16_t*>(B),
-                static_cast<float*>(ctx->ws), rows, n, outs, most, ldx, ldb, ldy, rank > 0 ? adapters : 0, rank, 1};
+                static_cast<uint16_t*>(ctx->ws), rows, n, outs, most, ldx, ldb, ldy, rank > 0 ? adapters : 0, rank, (rank + 7) / 8 * 8, 1};
   if (a.adapters > 0 && ctx->ws_bytes < wr_adapters_ws_bytes(rows, n, rank)) return WR_EWORKSPACE;
   most = std::min(most, rows);
   // 16 rows a tile where that leaves none of it empty or the card is not full, else 32
