@@ -3,8 +3,8 @@
 // Two launches.  The first forms t = A x (rows x rank, as three bf16 parts, in the workspace): x is read once, a workgroup takes 16
 // or 32 rows of a request and up to 64 rows of A, and its eight waves cut the sum over n, which is what fills the card when
 // there are few rows.  The second forms y: a wave keeps its rows of t as matrix operands and walks the outputs 64 at a
-// time; the matrix product's rows are dealt to outputs so that a lane ends up with 16 neighbouring ones, and base
-// is read and y written in whole 16-byte accesses, 128 bytes of a row in a wave.  One token is bound by
+// time; the matrix product's rows are dealt to outputs so that a lane ends up with 8 neighbouring ones, and base
+// is read and y written in whole 16-byte accesses, 64 neighbouring bytes of a row each.  One token is bound by
 // the two launches and the latency of a few dependent loads, long prompts by the bytes of x, base and y: the products, three
 // of bf16 parts for each of fp32 (x = x0 + x1 + x2 exactly, t likewise), stay below a tenth of the matrix cores' rate.
 #include "rowops.hpp"
@@ -190,15 +190,16 @@ __global__ __launch_bounds__(512) void adapters_in_kernel(AdapterArgs a, const X
   }
 }
 
-// y = base + s B t: 16 MT rows and some of the outputs, 64 at a time, KS slices of 32 ranks.
-template <typename Y, int MT, int KS>
-__global__ __launch_bounds__(256) void adapters_out_kernel(AdapterArgs a, const Y* base, Y* y, uint32_t out_parts) {
+// y = base + s B t: 16 MT rows a wave and some of the outputs, 64 at a time, KS slices of 32 ranks.  The four waves have different outputs
+// of the same rows (ROWS false), or different rows and walk the same outputs together, so that B comes from L2 once for them.
+template <typename Y, int MT, int KS, bool ROWS>
+__global__ __launch_bounds__(256, KS <= 4 ? 2 : 1) void adapters_out_kernel(AdapterArgs a, const Y* base, Y* y, uint32_t out_parts) {
   constexpr int WAVES = 4;
-  const uint32_t nth = blockIdx.x % out_parts, rest = blockIdx.x / out_parts;
-  const Request q = request_of(a, rest / a.tiles, (int64_t)(rest % a.tiles) * 16 * MT);
-  if (q.count <= 0 || (q.rank == 0 && base == y)) return;
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int low = lane % 16, g = lane / 16;
+  const uint32_t nth = blockIdx.x % out_parts, rest = blockIdx.x / out_parts;
+  const Request q = request_of(a, rest / a.tiles, (int64_t)(ROWS ? rest % a.tiles * WAVES + wave : rest % a.tiles) * 16 * MT);
+  if (q.count <= 0 || (q.rank == 0 && base == y)) return;
   const float s = q.rank > 0 ? a.scales[q.adapter] : 0.0f;
   u32x4 t[MT][KS][3];
 #pragma unroll
@@ -213,28 +214,13 @@ __global__ __launch_bounds__(256) void adapters_out_kernel(AdapterArgs a, const 
       }
   }
   const uint16_t* bp = a.B + (int64_t)max(q.adapter, 0) * a.outs * a.rank;
-  for (int64_t o0 = ((int64_t)nth * WAVES + wave) * 64; o0 < a.outs; o0 += (int64_t)out_parts * WAVES * 64) {
-    // everything that this step reads is asked for first
+  struct Step {  // what 64 outputs read
     Raw8<uint16_t> b[4][KS];
-    if (q.rank > 0) {
-      // row `low` of product j is output 16 (low / 4) + 4 j + low % 4
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint16_t* br = bp + min(o0 + 16 * (low / 4) + 4 * j + low % 4, a.outs - 1) * a.rank;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) load8(b[j][ks], br, 32 * ks + 8 * g, q.rank);
-      }
-    }
-    const int64_t o = o0 + 16 * g;
     Raw8<Y> v[MT][2];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = 16 * m + low;
-        if (base && row < q.count && o + 8 * h < a.outs) load8(v[m][h], base + (q.row + row) * a.ldb, o + 8 * h, a.outs);
-        else v[m][h].fill(0.0f);
-      }
+  };
+  // row `low` of product j is output 32 (j / 2) + 8 (low / 4) + 4 (j % 2) + low % 4, so that a lane gets outputs 8 g .. 8 g + 7 and
+  // 32 more of row `low`, and four lanes 64 neighbouring bytes of bf16
+  auto multiply = [&](Step& f, int64_t o0, auto whole) {
     f32x4 acc[MT][4];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -248,7 +234,7 @@ __global__ __launch_bounds__(256) void adapters_out_kernel(AdapterArgs a, const 
 #pragma unroll
           for (int i = 0; i < 3; ++i)
 #pragma unroll
-            for (int m = 0; m < MT; ++m) acc[m][j] = mfma16x16x32_bf16(b[j][ks].v, t[m][ks][i], acc[m][j]);
+            for (int m = 0; m < MT; ++m) acc[m][j] = mfma16x16x32_bf16(f.b[j][ks].v, t[m][ks][i], acc[m][j]);
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -257,20 +243,77 @@ __global__ __launch_bounds__(256) void adapters_out_kernel(AdapterArgs a, const 
       Y* out = y + (q.row + row) * a.ldy;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int64_t at = o + 8 * h;
-        if (at >= a.outs) continue;
-        float f[8];
+        const int64_t at = o0 + 32 * h + 8 * g;
+        if (!decltype(whole)::value && at >= a.outs) continue;
+        Raw8<Y>& v = f.v[m][h];
+        if (!base) v.fill(0.0f);
+        float r[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = fmaf(acc[m][2 * h + e / 4][e % 4], s, v[m][h].get(e));
-        if (q.rank > 0) v[m][h].round(f);
-        if (at + 8 <= a.outs) {
-          v[m][h].store(out + at);
+        for (int e = 0; e < 8; ++e) r[e] = fmaf(acc[m][2 * h + e / 4][e % 4], s, v.get(e));
+        if (q.rank > 0) v.round(r);
+        if (decltype(whole)::value || at + 8 <= a.outs) {
+          v.store(out + at);
         } else {
           for (int e = 0; e < 8; ++e)
-            if (at + e < a.outs) out[at + e] = v[m][h].at(e);
+            if (at + e < a.outs) out[at + e] = v.at(e);
         }
       }
     }
+  };
+  const int64_t stride = (int64_t)out_parts * (ROWS ? 64 : WAVES * 64);
+  int64_t o0 = ROWS ? (int64_t)nth * 64 : ((int64_t)nth * WAVES + wave) * 64;
+  const Y* from = base ? base : y;  // what is read without a base is not used
+  const int64_t ldf = base ? a.ldb : a.ldy;
+  if constexpr (KS <= 2) {
+    // Whole steps, each loaded while the one before it is worked on.  The loads are not conditional, or waiting for one step
+    // would mean waiting for the next as well; past the end they repeat the last one.
+    const int64_t last = a.outs / 64 * 64 - 64;
+    if (q.rank == 32 * KS && o0 <= last) {
+      auto fetch = [&](Step& f, int64_t at) {
+        at = min(at, last);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) f.b[j][ks].load(bp + (at + 32 * (j / 2) + 8 * (low / 4) + 4 * (j % 2) + low % 4) * a.rank + 32 * ks + 8 * g);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            f.v[m][h].load(from + (q.row + min((int64_t)(16 * m + low), q.count - 1)) * ldf + at + 32 * h + 8 * g);
+      };
+      Step even, odd;
+      fetch(even, o0);
+      for (;;) {
+        fetch(odd, o0 + stride);
+        multiply(even, o0, std::true_type{});
+        o0 += stride;
+        if (o0 > last) break;
+        fetch(even, o0 + stride);
+        multiply(odd, o0, std::true_type{});
+        o0 += stride;
+        if (o0 > last) break;
+      }
+    }
+  }
+  for (; o0 < a.outs; o0 += stride) {
+    Step f;
+    if (q.rank > 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint16_t* br = bp + min(o0 + 32 * (j / 2) + 8 * (low / 4) + 4 * (j % 2) + low % 4, a.outs - 1) * a.rank;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) load8(f.b[j][ks], br, 32 * ks + 8 * g, q.rank);
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = 16 * m + low;
+        const int64_t at = o0 + 32 * h + 8 * g;
+        if (base && row < q.count && at < a.outs) load8(f.v[m][h], base + (q.row + row) * a.ldb, at, a.outs);
+      }
+    multiply(f, o0, std::false_type{});
   }
 }
 
@@ -295,25 +338,22 @@ int wr_adapters_impl(wr_ctx* ctx, const void* x, int x_dtype, int64_t rows, int6
                 static_cast<uint16_t*>(ctx->ws), rows, n, outs, most, ldx, ldb, ldy, rank > 0 ? adapters : 0, rank, (rank + 7) / 8 * 8, 1};
   if (a.adapters > 0 && ctx->ws_bytes < wr_adapters_ws_bytes(rows, n, rank)) return WR_EWORKSPACE;
   most = std::min(most, rows);
-  // 16 rows a tile where that leaves none of it empty or the card is not full, else 32
-  const int64_t mt = most <= 16 ? 1 : 2;
-  const int64_t tiles = (most + 16 * mt - 1) / (16 * mt);
+  // single tokens and steps of a few: 16 rows a tile; else 32 for the first product and four times 32 (16 of wide adapters, whose
+  // parts fill the registers) for the second
+  const bool many = most > 16;
+  const int64_t in_rows = many ? 32 : 16, out_rows = !many ? 16 : rank > 64 ? 64 : 128;
+  const int64_t in_tiles = (most + in_rows - 1) / in_rows, out_tiles = (most + out_rows - 1) / out_rows;
   const int nt = rank <= 16 ? 1 : rank <= 32 ? 2 : 4;
   const int64_t rank_tiles = (rank + 16 * nt - 1) / (16 * nt);
-  const int64_t out_steps = (outs + 255) / 256;
-  // waves enough for eight on each SIMD; a wave that walks several steps reads its rows of t once
-  const int64_t row_tiles = std::min<int64_t>(tiles * n_seqs, rows / (16 * mt) + n_seqs);
-  const int64_t out_parts = std::max<int64_t>(1, std::min(out_steps, (8 * (int64_t)ctx->num_cu + row_tiles - 1) / row_tiles));
-  if (tiles * n_seqs > kMostBlocks / std::max<int64_t>(rank_tiles, out_parts)) return WR_EUNSUPPORTED;
-  a.tiles = (uint32_t)tiles;
-  auto with_rows = [&](auto type, auto&& f) {
-    using T = decltype(type);
-    if (mt == 1) f(type, std::integral_constant<int, 1>{});
-    else f(type, std::integral_constant<int, 2>{});
-    (void)sizeof(T);
-  };
+  const int64_t out_steps = (outs + (many ? 63 : 255)) / (many ? 64 : 256);
+  // Many rows: as many workgroups as two on each compute unit, which is what registers leave room for; more would be a second, mostly
+  // empty round.  Few: up to four on each.
+  const int64_t row_tiles = std::min<int64_t>(out_tiles * n_seqs, rows / out_rows + n_seqs);
+  const int64_t out_parts = std::max<int64_t>(1, std::min(out_steps, (many ? 2 : 4) * (int64_t)ctx->num_cu / row_tiles));
+  if (std::max(in_tiles * std::max<int64_t>(1, rank_tiles), out_tiles * out_parts) * n_seqs > kMostBlocks) return WR_EUNSUPPORTED;
   if (a.adapters > 0) {
-    const dim3 grid((uint32_t)(tiles * n_seqs * rank_tiles));
+    a.tiles = (uint32_t)in_tiles;
+    const dim3 grid((uint32_t)(in_tiles * n_seqs * rank_tiles));
     auto go = [&](auto type, auto m) {
       using X = decltype(type);
       constexpr int MT = decltype(m)::value;
@@ -322,28 +362,34 @@ int wr_adapters_impl(wr_ctx* ctx, const void* x, int x_dtype, int64_t rows, int6
       else if (nt == 2) hipLaunchKernelGGL((adapters_in_kernel<X, MT, 2>), grid, dim3(512), 0, ctx->stream, a, xp, (uint32_t)rank_tiles);
       else hipLaunchKernelGGL((adapters_in_kernel<X, MT, 4>), grid, dim3(512), 0, ctx->stream, a, xp, (uint32_t)rank_tiles);
     };
-    if (x_dtype == WR_BF16) with_rows(uint16_t{}, go);
-    else with_rows(float{}, go);
-    WR_CHECK_LAUNCH();
-  }
-  {
-    const dim3 grid((uint32_t)(tiles * n_seqs * out_parts));
-    auto go = [&](auto type, auto m) {
-      using Y = decltype(type);
-      constexpr int MT = decltype(m)::value;
-      const Y* bp = static_cast<const Y*>(base);
-      Y* yp = static_cast<Y*>(y);
-      auto run = [&](auto ks) {
-        hipLaunchKernelGGL((adapters_out_kernel<Y, MT, decltype(ks)::value>), grid, dim3(256), 0, ctx->stream, a, bp, yp, (uint32_t)out_parts);
-      };
-      if (rank <= 32) run(std::integral_constant<int, 1>{});
-      else if (rank <= 64) run(std::integral_constant<int, 2>{});
-      else if (rank <= 128) run(std::integral_constant<int, 4>{});
-      else run(std::integral_constant<int, 8>{});
+    auto with_rows = [&](auto type) {
+      if (many) go(type, std::integral_constant<int, 2>{});
+      else go(type, std::integral_constant<int, 1>{});
     };
-    if (y_dtype == WR_BF16) with_rows(uint16_t{}, go);
-    else with_rows(float{}, go);
+    if (x_dtype == WR_BF16) with_rows(uint16_t{});
+    else with_rows(float{});
     WR_CHECK_LAUNCH();
   }
+  a.tiles = (uint32_t)out_tiles;
+  const dim3 grid((uint32_t)(out_tiles * n_seqs * out_parts));
+  auto go = [&](auto type, auto m, auto ks, auto by_rows) {
+    using Y = decltype(type);
+    hipLaunchKernelGGL((adapters_out_kernel<Y, decltype(m)::value, decltype(ks)::value, decltype(by_rows)::value>), grid, dim3(256), 0,
+                       ctx->stream, a, static_cast<const Y*>(base), static_cast<Y*>(y), (uint32_t)out_parts);
+  };
+  auto with_rank = [&](auto type) {
+    auto run = [&](auto ks) {
+      constexpr int MT = decltype(ks)::value <= 2 ? 2 : 1;
+      if (many) go(type, std::integral_constant<int, MT>{}, ks, std::true_type{});
+      else go(type, std::integral_constant<int, 1>{}, ks, std::false_type{});
+    };
+    if (rank <= 32) run(std::integral_constant<int, 1>{});
+    else if (rank <= 64) run(std::integral_constant<int, 2>{});
+    else if (rank <= 128) run(std::integral_constant<int, 4>{});
+    else run(std::integral_constant<int, 8>{});
+  };
+  if (y_dtype == WR_BF16) with_rank(uint16_t{});
+  else with_rank(float{});
+  WR_CHECK_LAUNCH();
   return WR_OK;
 }
