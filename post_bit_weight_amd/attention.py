@@ -1,0 +1,197 @@
+"""Run a block's attention in 8-bit integers over a 4-bit cache on the weights of the container.
+
+The counterpart of ``int8.Int8Mlp`` for the other half of a block.  For the new tokens of any number of sequences:
+
+    x'      = resid + gate * post_norm(branch)                    wr_block_norm: one pass, which also writes
+    q8      = 8-bit tokens of pre_norm(x')                        the 8-bit tokens (and pre_norm(x') for adapters)
+    q, k, v = q8 Wq^T, q8 Wk^T, q8 Wv^T                           wr_matmul_i8
+              + each request's adapter                            wr_adapters
+    q, k    = rotary(head_norm(q)), rotary(head_norm(k))          wr_block_norm, wr_rotary
+    cache  <- k, v in 4 bits                                      wr_kv_write
+    a       = softmax(scale q k^T) v over the cache               wr_kv_attention
+    out     = (8-bit tokens of a) Wo^T + adapter                  wr_quant_rows_i8, wr_matmul_i8, wr_adapters
+
+``out`` is the ``branch`` of the block's MLP.  Every step runs in libwringer.so; torch only allocates.  The context may be on
+another stream than the caller: each call here is queued behind the caller's work so far, and the caller's later work waits for
+it.  Run on synthetic modules of the container's format, a prompt and then single tokens:
+python -m post_bit_weight_amd.attention [--sequences 4] [--prompt 512] [--steps 32] [--adapters 3]
+"""
+
+import argparse
+import json
+import time
+
+import torch
+
+from . import _lib as wr
+from . import int8
+
+
+class Adapters:
+    """Low-rank adapters beside one projection.  A: adapters x rank x n and B: adapters x outs x rank, bf16; scales: fp32,
+    alpha / rank of each; ranks: int32, or None where all have the full rank."""
+
+    def __init__(self, A, B, scales, ranks=None):
+        self.A, self.B, self.scales, self.ranks = A, B, scales, ranks
+
+    def add(self, ctx, x, seqs, ids, y):
+        """y += the requests' adapters of x; ids: the adapter of every sequence, outside the adapters for none."""
+        wr.wr_adapters(ctx, x, self.A, self.B, self.scales, seqs.starts, ids, seqs.most_new, y, base=y, ranks=self.ranks)
+
+    def tensors(self):
+        return [t for t in (self.A, self.B, self.scales, self.ranks) if t is not None]
+
+
+class Int8Attention:
+    """qkv: Int8Linear of (heads + 2 cache heads) * dim x n, the rows of the queries, keys and values one after the other; out:
+    Int8Linear of n x heads * dim; cache: the KvCache, whose heads and dim are the keys'; w_pre, w_post, gate as in Int8Mlp;
+    q_norm, k_norm: weights of the norms of each head (dim values) or None; freqs: fp64, an angle per position for each
+    rotary pair (none: no rotation), with axis_of and interleaved as in wr_rotary; adapters: a dict with Adapters for any of
+    "q", "k", "v" and "out"."""
+
+    def __init__(self, ctx, qkv, out, cache, w_pre, w_post=None, gate=None, q_norm=None, k_norm=None, freqs=None, axis_of=None,
+                 interleaved=False, scale=None, window=0, eps=1e-6, most_tokens=4096, adapters=None):
+        self.ctx, self.out, self.cache, self.eps, self.most = ctx, out, cache, eps, most_tokens
+        self.w_pre, self.w_post, self.gate, self.q_norm, self.k_norm = w_pre, w_post, gate, q_norm, k_norm
+        self.freqs, self.axis_of, self.interleaved, self.window = freqs, axis_of, interleaved, window
+        self.scale = cache.dim ** -0.5 if scale is None else scale
+        self.adapters = dict(adapters or {})
+        n, wide = qkv.codes.shape[1], out.codes.shape[1]
+        if wide % cache.dim or qkv.codes.shape[0] != wide + 2 * cache.width or out.codes.shape[0] != n:
+            raise ValueError("qkv must be (heads + 2 cache heads) * dim x n and out n x heads * dim")
+        if set(self.adapters) - {"q", "k", "v", "out"}:
+            raise ValueError("adapters may be given for q, k, v and out")
+        self.n, self.wide = n, wide
+        ends = (0, wide, wide + cache.width, wide + 2 * cache.width)
+        self.parts = [(name, qkv.codes[a:b], qkv.scales[a:b]) for name, a, b in zip("qkv", ends, ends[1:])]
+        given = [w_pre, w_post, gate, q_norm, k_norm, freqs, axis_of, qkv.codes, qkv.scales, out.codes, out.scales, cache.buf]
+        with ctx.behind_caller(*given, *[t for a in self.adapters.values() for t in a.tensors()]):
+            new = lambda width: torch.empty(most_tokens, width, dtype=torch.bfloat16, device=ctx.device)  # noqa: E731
+            self.tokens, self.mixed = int8.Tokens(most_tokens, n, ctx.device), int8.Tokens(most_tokens, wide, ctx.device)
+            self.rows = {"q": new(wide), "k": new(cache.width), "v": new(cache.width)}
+            self.attended = new(wide)
+            self.normed = new(n) if set(self.adapters) & {"q", "k", "v"} else None
+
+    def __call__(self, resid, branch, seqs, positions=None, ids=None):
+        """(x', the attention's output) for the new tokens of the sequences (wr.Sequences; their rows are branch's, in order).
+        positions: int32, rows or axes x rows, for the rotation; ids: int32, the adapter of every sequence."""
+        rows = branch.shape[0]
+        if rows > self.most:
+            raise ValueError(f"{rows} tokens, but space for {self.most}")
+        if (positions is None) != (self.freqs is None):
+            raise ValueError("positions belong to freqs")
+        if (ids is None) != (not self.adapters):
+            raise ValueError("ids belong to adapters")
+        ctx, dim = self.ctx, self.cache.dim
+        with ctx.behind_caller(resid, branch, positions, ids, seqs.starts, seqs.lengths, seqs.table) as made:
+            out = torch.empty_like(branch, memory_format=torch.contiguous_format)
+            resid_out = torch.empty_like(resid, memory_format=torch.contiguous_format)
+            q8, scales = self.tokens.of(rows)
+            normed = None if self.normed is None else self.normed[:rows]
+            wr.wr_block_norm(ctx, self.eps, branch=branch, resid=resid, w_post=self.w_post, gate=self.gate, w_pre=self.w_pre,
+                             resid_out=resid_out, y=normed, q=q8, q_scales=scales)
+            q, k, v = (self.rows[name][:rows] for name in "qkv")
+            for (name, codes, wscales), y in zip(self.parts, (q, k, v)):
+                wr.wr_matmul_i8(ctx, q8, scales, codes, wscales, y)
+                if name in self.adapters:
+                    self.adapters[name].add(ctx, normed, seqs, ids, y)
+            for y, weight in ((q, self.q_norm), (k, self.k_norm)):
+                if weight is not None:
+                    heads = y.view(-1, dim)
+                    wr.wr_block_norm(ctx, self.eps, branch=heads, w_pre=weight, y=heads)
+                if positions is not None:
+                    wr.wr_rotary(ctx, y, y, positions, self.freqs, dim, axis_of=self.axis_of, interleaved=self.interleaved)
+            wr.wr_kv_write(ctx, self.cache, seqs, k, v)
+            attended = self.attended[:rows]
+            wr.wr_kv_attention(ctx, self.cache, seqs, q, attended, self.scale, window=self.window)
+            a8, ascales = self.mixed.of(rows)
+            wr.wr_quant_rows_i8(ctx, attended, a8, ascales)
+            wr.wr_matmul_i8(ctx, a8, ascales, self.out.codes, self.out.scales, out)
+            if "out" in self.adapters:
+                self.adapters["out"].add(ctx, attended, seqs, ids, out)
+            made += [resid_out, out]
+        return resid_out, out
+
+
+def rotary_freqs(dim, base=1e6, device="cuda"):
+    """The usual frequencies of dim / 2 pairs, base ** (-2 i / dim), in fp64."""
+    return torch.pow(torch.tensor(float(base), dtype=torch.float64, device=device),
+                     -torch.arange(dim // 2, dtype=torch.float64, device=device) * 2 / dim)
+
+
+def main(argv=None):
+    ap = argparse.ArgumentParser(description="8-bit attention over a 4-bit cache on synthetic packed modules: time, and what the "
+                                             "cache's rounding costs.")
+    ap.add_argument("--sequences", type=int, default=4)
+    ap.add_argument("--prompt", type=int, default=512)
+    ap.add_argument("--steps", type=int, default=32)
+    ap.add_argument("--hidden", type=int, default=2560)
+    ap.add_argument("--heads", type=int, default=32)
+    ap.add_argument("--cache-heads", type=int, default=8)
+    ap.add_argument("--dim", type=int, default=128)
+    ap.add_argument("--page", type=int, default=64)
+    ap.add_argument("--group", type=int, default=64)
+    ap.add_argument("--adapters", type=int, default=0)
+    ap.add_argument("--rank", type=int, default=16)
+    a = ap.parse_args(argv)
+    ctx = wr.Context(0)
+    dev = ctx.device
+    g = torch.Generator(device=dev).manual_seed(4)
+    wide, kv = a.heads * a.dim, a.cache_heads * a.dim
+    mods = [int8.synthetic_module(ctx, r, n, 2, 64, s) for r, n, s in ((wide, a.hidden, 1), (kv, a.hidden, 2), (kv, a.hidden, 3),
+                                                                      (a.hidden, wide, 4))]
+    most = a.prompt + a.steps
+    width = -(-most // a.page)
+    cache = wr.KvCache(a.sequences * width, a.cache_heads, a.dim, page_tokens=a.page, group=a.group, device=dev)
+    table = torch.randperm(a.sequences * width, generator=g, device=dev).to(torch.int32).view(a.sequences, width)
+    norm = (1 + 0.1 * torch.randn(a.hidden, device=dev, generator=g)).to(torch.bfloat16)
+    head_norms = (1 + 0.1 * torch.randn(2, a.dim, device=dev, generator=g)).to(torch.bfloat16)
+    adapters, ids = None, None
+    if a.adapters:
+        ids = torch.arange(a.sequences, dtype=torch.int32, device=dev) % (a.adapters + 1) - 1  # some have none
+        adapters = {name: Adapters(torch.randn(a.adapters, a.rank, n, device=dev, generator=g).mul_(n ** -0.5).bfloat16(),
+                                   torch.randn(a.adapters, outs, a.rank, device=dev, generator=g).mul_(0.1 * a.rank ** -0.5).bfloat16(),
+                                   torch.ones(a.adapters, device=dev))
+                    for name, n, outs in (("q", a.hidden, wide), ("v", a.hidden, kv), ("out", wide, a.hidden))}
+    block = Int8Attention(ctx, int8.Int8Linear.from_packed(ctx, mods[:3]), int8.Int8Linear.from_packed(ctx, mods[3:]), cache, norm,
+                          q_norm=head_norms[0], k_norm=head_norms[1], freqs=rotary_freqs(a.dim, device=dev),
+                          most_tokens=a.sequences * a.prompt, adapters=adapters)
+
+    def sequences(new, length):
+        starts = torch.arange(a.sequences + 1, dtype=torch.int32, device=dev) * new
+        lengths = torch.full((a.sequences,), length, dtype=torch.int32, device=dev)
+        positions = torch.arange(length - new, length, dtype=torch.int32, device=dev).repeat(a.sequences)
+        return wr.Sequences(starts, lengths, table, new, most), positions
+
+    def tokens(rows):
+        return [torch.randn(rows, a.hidden, device=dev, generator=g).to(torch.bfloat16) for _ in range(2)]
+
+    def timed(new, length):
+        seqs, positions = sequences(new, length)
+        resid, branch = tokens(a.sequences * new)
+        torch.cuda.synchronize()
+        began = time.perf_counter()
+        out = block(resid, branch, seqs, positions, ids)[1]
+        torch.cuda.synchronize()
+        return time.perf_counter() - began, out
+
+    prompt = timed(a.prompt, a.prompt)[0]
+    steps = [timed(1, a.prompt + 1 + i) for i in range(a.steps)]
+    # the last step's queries over what the cache holds, in fp32
+    seqs = sequences(most, most)[0]
+    k, v = (torch.empty(a.sequences * most, kv, dtype=torch.float32, device=dev) for _ in range(2))
+    wr.wr_kv_read(ctx, cache, seqs, k, v)
+    q = block.rows["q"][:a.sequences].float().view(a.sequences, a.cache_heads, -1, a.dim)
+    k, v = (t.view(a.sequences, most, a.cache_heads, a.dim).transpose(1, 2).contiguous() for t in (k, v))
+    p = torch.softmax(q @ k.transpose(2, 3).contiguous() * block.scale, 3)
+    ref = (p @ v).reshape(a.sequences, wide)
+    got = block.attended[:a.sequences].float()
+    error = float((got - ref).norm() / ref.norm())
+    print(json.dumps(dict(sequences=a.sequences, prompt=a.prompt, steps=a.steps, ms_prompt=round(prompt * 1e3, 3),
+                          us_per_step=round(sorted(t for t, _ in steps)[len(steps) // 2] * 1e6, 1) if steps else None,
+                          cache_bytes_per_token=cache.page_bytes / a.page, attention_error=error)))
+    return 0 if error < 0.01 and all(bool(torch.isfinite(o.float()).all()) for _, o in steps) else 1
+
+
+if __name__ == "__main__":
+    raise SystemExit(main())
