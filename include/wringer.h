@@ -426,7 +426,7 @@ int wr_block_norm_backward(wr_ctx* ctx, int64_t rows, int64_t n, const void* bra
  *   (x0 cos a - x1 sin a, x0 sin a + x1 cos a),
  * or with WR_ROTARY_INVERSE the same with -a, which is also the gradient of the forward form.
  * Values behind the pairs are copied.  positions: axes x rows int32 (row stride ldp); axis_of: pairs int32,
- * or null when axes is 1; a pair whose axis is outside 0 .. axes - 1 is copied.  freqs: pairs fp64,
+ * or null when axes is 1; a pair whose axis is outside 0 .. axes - 1 has the angle 0.  freqs: pairs fp64,
  * in radians per position.  Angles are formed and reduced in fp64, everything else is fp32, and y (as x, ld
  * ldy) is rounded once.  y may be x with the same ld; other overlaps are not allowed.  pairs may be 0; dim <= 1024
  * and axes <= 8 (WR_EUNSUPPORTED above); rows may be 0.  Any alignment to the type.  No workspace.
@@ -463,7 +463,8 @@ typedef struct {
  * page table[i * ldt + p / page_tokens].  starts (n + 1), lengths (n) and table (n x width) are int32 device
  * memory that the kernels read; most_new and most_tokens are what the host knows of them.
  * A sequence is left out - nothing of it is read or written - unless 0 <= starts[i] <= starts[i + 1] <= rows,
- * new_i <= most_new and 0 <= lengths[i] <= min(most_tokens, width * page_tokens).  A position below 0
+ * new_i <= most_new and 0 <= lengths[i] <= min(most_tokens, width * page_tokens), which is at most 2^30, as is
+ * most_new (WR_EUNSUPPORTED above, and where a launch cannot have the workgroups for n * most_new rows).  A position below 0
  * (new_i > lengths[i]), and one in a page outside 0 .. count - 1, is absent.
  */
 typedef struct {
@@ -500,7 +501,7 @@ int wr_kv_read(wr_ctx* ctx, const wr_kv_cache* cache, const wr_kv_seqs* seqs, vo
  * of sequence i, at position p = lengths[i] - new_i + j, sees positions 0 .. lengths[i] - 1, with
  * WR_ATTENTION_CAUSAL only those up to p, and with window > 0 only those above p - window (and, without
  * the flag, below p + window).  Absent positions are not seen, whatever the cache holds.  A row that sees nothing, or
- * whose scores are all -infinity, becomes 0.  scale is finite.  Sums, scores and the softmax are fp32; the matrix
+ * whose scores are all -infinity, becomes 0.  scale is within +-2^126.  Sums, scores and the softmax are fp32; the matrix
  * cores take the cache's values and the weights rounded to fp16 (2^-11 relative).  Outputs of left-out sequences and of no sequence stay as they were.
  * out may not overlap q.  Workspace: WR_OP_KV_ATTENTION (rows, heads * dim, dim).
  */

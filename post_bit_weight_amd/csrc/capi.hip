@@ -68,6 +68,8 @@ constexpr int64_t kRowsMax = 2147483647;
 constexpr int32_t kRotaryDim = 1024;   // widest head (the angles in a workgroup's LDS)
 constexpr int32_t kRotaryAxes = 8;
 constexpr int32_t kShareMax = 64;      // query heads of a head of the cache
+constexpr int32_t kTokensMax = 1 << 30;  // positions and new rows of a sequence: their sums stay in an int32
+constexpr float kScaleMax = 0x1p126f;  // of scores; times log2(e) it is still finite
 constexpr int32_t kRankMax = 256;      // widest adapter
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -487,6 +489,8 @@ static int kv_args_ok(wr_ctx* ctx, const wr_kv_cache* c, const wr_kv_seqs* s, in
   if (wr_kv_page_bytes(c->heads, c->dim, c->page_tokens, c->group) == 0) return WR_EUNSUPPORTED;
   nothing = rows == 0 || s->n == 0 || s->most_new == 0;
   if (nothing) return WR_OK;
+  if (s->most_new > kTokensMax || std::min<int64_t>(s->most_tokens, (int64_t)s->width * c->page_tokens) > kTokensMax)
+    return WR_EUNSUPPORTED;
   if (!c->pages || c->count == 0 || !aligned(c->pages, 16) || !s->starts || !s->lengths || !aligned(s->starts, 4) ||
       !aligned(s->lengths, 4) || !aligned(s->table, 4) || (s->width > 0 && !s->table) || (s->ldt < s->width && s->n > 1))
     return WR_EINVAL;
@@ -503,6 +507,12 @@ static int kv_rows_args(wr_ctx* ctx, const wr_kv_cache* cache, const wr_kv_seqs*
   return wr_kv_blocks(*cache, *seqs) > kRowsMax ? WR_EUNSUPPORTED : WR_OK;
 }
 
+// The sequences, with no more new rows than there are rows.
+static wr_kv_seqs of_rows(wr_kv_seqs s, int64_t rows) {
+  s.most_new = (int32_t)std::min<int64_t>(s.most_new, rows);
+  return s;
+}
+
 int wr_kv_write(wr_ctx* ctx, const wr_kv_cache* cache, const wr_kv_seqs* seqs, const void* k, int64_t ldk, const void* v,
                 int64_t ldv, int dtype, int64_t rows) {
   bool nothing = false;
@@ -510,7 +520,7 @@ int wr_kv_write(wr_ctx* ctx, const wr_kv_cache* cache, const wr_kv_seqs* seqs, c
   if (rc != WR_OK || nothing) return rc;
   DeviceScope ds(ctx->device);
   if (!ds.ok) return WR_EHIP;
-  return wr_kv_write_impl(ctx, *cache, *seqs, k, ldk, v, ldv, dtype, rows);
+  return wr_kv_write_impl(ctx, *cache, of_rows(*seqs, rows), k, ldk, v, ldv, dtype, rows);
 }
 
 int wr_kv_read(wr_ctx* ctx, const wr_kv_cache* cache, const wr_kv_seqs* seqs, void* k, int64_t ldk, void* v, int64_t ldv,
@@ -520,24 +530,25 @@ int wr_kv_read(wr_ctx* ctx, const wr_kv_cache* cache, const wr_kv_seqs* seqs, vo
   if (rc != WR_OK || nothing) return rc;
   DeviceScope ds(ctx->device);
   if (!ds.ok) return WR_EHIP;
-  return wr_kv_read_impl(ctx, *cache, *seqs, k, ldk, v, ldv, dtype, rows);
+  return wr_kv_read_impl(ctx, *cache, of_rows(*seqs, rows), k, ldk, v, ldv, dtype, rows);
 }
 
 int wr_kv_attention(wr_ctx* ctx, const wr_kv_cache* cache, const wr_kv_seqs* seqs, const void* q, int64_t ldq,
                     int64_t rows, int32_t heads, float scale, int flags, int32_t window, void* out, int64_t ldo) {
   if ((flags & ~WR_ATTENTION_CAUSAL) || window < 0 || heads <= 0 || !std::isfinite(scale)) return WR_EINVAL;
+  if (std::fabs(scale) > kScaleMax) return WR_EUNSUPPORTED;
   bool nothing = false;
   const int rc = kv_args_ok(ctx, cache, seqs, rows, nothing);
   if (rc != WR_OK) return rc;
   if (heads % cache->heads != 0) return WR_EINVAL;
   const int32_t share = heads / cache->heads;
-  if (share > kShareMax || (int64_t)seqs->most_new * share > 1 << 30) return WR_EUNSUPPORTED;
+  if (share > kShareMax || (int64_t)seqs->most_new * share > kTokensMax) return WR_EUNSUPPORTED;
   if (nothing) return WR_OK;
   const int64_t n = (int64_t)heads * cache->dim;
   if (!q || !out || !rows_ok(q, WR_BF16, rows, n, ldq) || !rows_ok(out, WR_BF16, rows, n, ldo)) return WR_EINVAL;
   DeviceScope ds(ctx->device);
   if (!ds.ok) return WR_EHIP;
-  return wr_kv_attention_impl(ctx, *cache, *seqs, q, ldq, rows, heads, scale, flags, window, out, ldo);
+  return wr_kv_attention_impl(ctx, *cache, of_rows(*seqs, rows), q, ldq, rows, heads, scale, flags, window, out, ldo);
 }
 
 int wr_adapters(wr_ctx* ctx, const void* x, int x_dtype, int64_t rows, int64_t n, int64_t ldx, const void* A, const void* B,

@@ -317,7 +317,7 @@ __global__ __launch_bounds__(256, KS <= 4 ? 2 : 1) void adapters_out_kernel(Adap
   }
 }
 
-constexpr int64_t kMostBlocks = 1 << 30;
+constexpr int64_t kMostThreads = 4294967295;  // of a launch, in x
 
 }  // namespace
 
@@ -350,7 +350,7 @@ int wr_adapters_impl(wr_ctx* ctx, const void* x, int x_dtype, int64_t rows, int6
   // empty round.  Few: up to four on each.
   const int64_t row_tiles = std::min<int64_t>(out_tiles * n_seqs, rows / out_rows + n_seqs);
   const int64_t out_parts = std::max<int64_t>(1, std::min(out_steps, (many ? 2 : 4) * (int64_t)ctx->num_cu / row_tiles));
-  if (std::max(in_tiles * std::max<int64_t>(1, rank_tiles), out_tiles * out_parts) * n_seqs > kMostBlocks) return WR_EUNSUPPORTED;
+  if (std::max(in_tiles * rank_tiles * 512, out_tiles * out_parts * 256) > kMostThreads / n_seqs) return WR_EUNSUPPORTED;
   if (a.adapters > 0) {
     a.tiles = (uint32_t)in_tiles;
     const dim3 grid((uint32_t)(in_tiles * n_seqs * rank_tiles));

@@ -562,7 +562,7 @@ int wr_kv_attention_impl(wr_ctx* ctx, const wr_kv_cache& c, const wr_kv_seqs& s,
   const int tile = most_rows <= 16 ? 16 : 32;
   const int64_t most_units = (int64_t)s.n * c.heads * ((a.kv.most_tokens + 15 + kUnit) / kUnit + 1);
   const int64_t joins = (int64_t)s.n * s.most_new * heads;
-  if (most_units > 1 << 30 || joins > 1 << 30) return WR_EUNSUPPORTED;
+  if (most_units > 1 << 30 || joins > kMostThreads / 256) return WR_EUNSUPPORTED;
   const int groups = (int)std::min<int64_t>(groups_per_cu(c.dim, tile / 16) * std::min(ctx->num_cu, kMostCUs), most_units);
   const size_t parts = (size_t)groups * 2 * tile;
   if (ctx->ws_bytes < parts * (c.dim + 2) * sizeof(float)) return WR_EWORKSPACE;

@@ -135,7 +135,7 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvArgs a, Work work,
   load(head);
   if (t.page < 0 || t.page >= a.count) return;
   const KvLayout<DIM, GROUP> at{1 << a.page_shift};
-  uint8_t* base = a.pages + (int64_t)t.page * ((int64_t)a.heads * at.head_bytes()) + head * at.head_bytes();
+  uint8_t* base = a.pages + (int64_t)t.page * ((int64_t)a.heads * at.head_bytes()) + (int64_t)head * at.head_bytes();
   for (int which = 0; head < end; ++head, which ^= 1, base += at.head_bytes()) {
     uint32_t codes[ITERS], meta[ITERS];
 #pragma unroll
@@ -205,7 +205,7 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvArgs a, Work work, 
   const int end = min(head + work.per, a.heads);
   const bool there = t.page >= 0 && t.page < a.count;
   const KvLayout<DIM, GROUP> at{1 << a.page_shift};
-  const uint8_t* base = a.pages + (int64_t)(there ? t.page : 0) * ((int64_t)a.heads * at.head_bytes()) + head * at.head_bytes();
+  const uint8_t* base = a.pages + (int64_t)(there ? t.page : 0) * ((int64_t)a.heads * at.head_bytes()) + (int64_t)head * at.head_bytes();
   for (int which = 0; head < end; ++head, which ^= 1, base += at.head_bytes()) {
     if (v) {
       const uint8_t* tile = base + at.v_codes() + t.at * (DIM / 2);
@@ -275,21 +275,24 @@ static int64_t tiles_of(const wr_kv_seqs& s) { return ((int64_t)s.most_new + 14)
 
 int64_t wr_kv_blocks(const wr_kv_cache& c, const wr_kv_seqs& s) { return (int64_t)c.heads * s.n * tiles_of(s); }
 
-// One head a block until the card is full eight times over, then as many as leave it that.
-static Work work_of(wr_ctx* ctx, const wr_kv_cache& c, const wr_kv_seqs& s, dim3& grid) {
+// One head a block until the card is full eight times over, then as many as leave it that.  False: more blocks than a launch has.
+static bool work_of(wr_ctx* ctx, const wr_kv_cache& c, const wr_kv_seqs& s, dim3& grid, Work& work) {
   const int64_t full = 8 * (int64_t)ctx->num_cu, tiles = s.n * tiles_of(s);
   const int per = (int)std::min<int64_t>(c.heads, std::max<int64_t>(1, c.heads * tiles / full));
-  grid = dim3((uint32_t)(tiles * ((c.heads + per - 1) / per)));
-  return Work{(int)tiles_of(s), per};
+  const int64_t blocks = tiles * ((c.heads + per - 1) / per);
+  grid = dim3((uint32_t)blocks);
+  work = Work{(int)tiles_of(s), per};
+  return blocks <= kMostThreads / kThreads;
 }
 
 int wr_kv_write_impl(wr_ctx* ctx, const wr_kv_cache& c, const wr_kv_seqs& s, const void* k, int64_t ldk, const void* v,
                      int64_t ldv, int dtype, int64_t rows) {
   const KvArgs a = kv_args(c, s, rows);
+  dim3 grid;
+  Work work;
+  if (!work_of(ctx, c, s, grid, work)) return WR_EUNSUPPORTED;
   const bool there = kv_form(c.dim, c.group, [&](auto d, auto g) {
     constexpr int D = decltype(d)::value, G = decltype(g)::value;
-    dim3 grid;
-    const Work work = work_of(ctx, c, s, grid);
     if (dtype == WR_BF16)
       hipLaunchKernelGGL((kv_write_kernel<D, G, uint16_t>), grid, dim3(kThreads), 0, ctx->stream, a, work,
                          static_cast<const uint16_t*>(k), ldk, static_cast<const uint16_t*>(v), ldv);
@@ -305,10 +308,11 @@ int wr_kv_write_impl(wr_ctx* ctx, const wr_kv_cache& c, const wr_kv_seqs& s, con
 int wr_kv_read_impl(wr_ctx* ctx, const wr_kv_cache& c, const wr_kv_seqs& s, void* k, int64_t ldk, void* v, int64_t ldv,
                     int dtype, int64_t rows) {
   const KvArgs a = kv_args(c, s, rows);
+  dim3 grid;
+  Work work;
+  if (!work_of(ctx, c, s, grid, work)) return WR_EUNSUPPORTED;
   const bool there = kv_form(c.dim, c.group, [&](auto d, auto g) {
     constexpr int D = decltype(d)::value, G = decltype(g)::value;
-    dim3 grid;
-    const Work work = work_of(ctx, c, s, grid);
     if (dtype == WR_BF16)
       hipLaunchKernelGGL((kv_read_kernel<D, G, uint16_t>), grid, dim3(kThreads), 0, ctx->stream, a, work,
                          static_cast<uint16_t*>(k), ldk, static_cast<uint16_t*>(v), ldv);

@@ -14,6 +14,13 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kRows = 256;
 
+// Where the parts of a tile of rows lie: by sequence, tile, head and chunk, whatever rows of the call belong to no sequence.
+__device__ __forceinline__ int64_t part_of(const AttentionArgs& a, int seq, int tile, int head, int split) {
+  const uint32_t rows = (uint32_t)a.kv.most_new * a.share;
+  const int64_t group = ((int64_t)seq * ((rows + kRows - 1) / kRows) + tile) * a.kv.heads + head;
+  return (group * a.splits + split) * min(rows, (uint32_t)kRows);
+}
+
 __device__ __forceinline__ f32x16 mfma32x32x16_f16(const u32x4& a, const u32x4& b, const f32x16& c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
@@ -323,7 +330,7 @@ __global__ __launch_bounds__(kThreads, 1) void attend_many_kernel(AttentionArgs 
   den += __shfl_xor(den, 32);
   if (!live) return;
   const float inv = den == 0.0f ? 0.0f : 1.0f / den;
-  const int64_t row = s.row + query, slot = (row * a.heads + out_head) * a.splits + split;
+  const int64_t row = s.row + query, slot = a.splits == 1 ? 0 : part_of(a, seq, tile, head, split) + wave * 32 + col;
 #pragma unroll
   for (int x = 0; x < SL; ++x)
 #pragma unroll
@@ -355,22 +362,25 @@ __global__ __launch_bounds__(256) void attend_chunks_kernel(AttentionArgs a) {
   if (seq >= a.kv.n) return;
   const KvSeq s = kv_seq(a.kv, seq);
   if (j >= s.fresh) return;
-  const RowTile rt = row_tile(a, s, (j * a.share + h % a.share) / kRows, kRows);
+  const int m = j * a.share + h % a.share;
+  const RowTile rt = row_tile(a, s, m / kRows, kRows);
   const Span all = seen(a, s, rt.first, rt.last);
   const int parts = min(a.splits, max(1, (all.hi - (all.lo & ~15) + a.chunk - 1) / a.chunk));
-  const int64_t slot = ((int64_t)(s.row + j) * a.heads + h) * a.splits;
+  const int64_t slot = part_of(a, seq, m / kRows, h / a.share, 0) + m % kRows;
+  const int next = min(a.kv.most_new * a.share, kRows);
   float top = kLowest, total = 0.0f, sum[PER];
-  for (int c = lane; c < parts; c += kWave) top = fmaxf(top, a.stats[slot + c].x);
+  for (int c = lane; c < parts; c += kWave) top = fmaxf(top, a.stats[slot + (int64_t)c * next].x);
   for (int x = 1; x < kWave; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
 #pragma unroll
   for (int e = 0; e < PER; ++e) sum[e] = 0.0f;
 #pragma unroll 4
   for (int c = 0; c < parts; ++c) {
-    const f32x2 st = a.stats[slot + c];
+    const int64_t at = slot + (int64_t)c * next;
+    const f32x2 st = a.stats[at];
     const float keep = exp2_fast(st.x - top);
     total = fmaf(st.y, keep, total);
 #pragma unroll
-    for (int e = 0; e < PER; ++e) sum[e] = fmaf(a.part[(slot + c) * DIM + e * kWave + lane], keep, sum[e]);
+    for (int e = 0; e < PER; ++e) sum[e] = fmaf(a.part[at * DIM + e * kWave + lane], keep, sum[e]);
   }
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   uint16_t* o = a.out + (int64_t)(s.row + j) * a.ldo + (int64_t)h * DIM;
@@ -386,7 +396,7 @@ constexpr int kWanted = 512;  // workgroups, two for every compute unit, below w
 
 using namespace wr;
 
-// rows * heads * splits stays below kWanted workgroups' rows.
+// Where positions are split there are at most kWanted workgroups, with a tile's rows each.
 size_t wr_kv_many_ws_bytes(int64_t rows, int64_t n, int32_t dim) {
   return (size_t)std::min<int64_t>(rows * (n / dim), kRows) * kWanted * (dim + 2) * sizeof(float);
 }
@@ -403,9 +413,10 @@ int wr_kv_many_impl(wr_ctx* ctx, const wr_kv_cache& c, const wr_kv_seqs& s, Atte
   a.chunk = (int)std::min<int64_t>(((span + splits - 1) / splits + 127) / 128 * 128, 1 << 30);
   a.splits = (int)std::max<int64_t>(1, (span + a.chunk - 1) / a.chunk);
   const int64_t blocks = groups * a.splits, joins = ((int64_t)s.n * s.most_new * a.heads + 3) / 4;
-  if (blocks > 1 << 30 || (a.splits > 1 && joins > 1 << 28)) return WR_EUNSUPPORTED;
-  if (a.splits > 1 && ctx->ws_bytes < (size_t)a.kv.rows * a.heads * a.splits * (c.dim + 2) * sizeof(float)) return WR_EWORKSPACE;
-  a.stats = reinterpret_cast<f32x2*>(a.part + (size_t)a.kv.rows * a.heads * a.splits * c.dim);
+  if (blocks > kMostThreads / kThreads || (a.splits > 1 && joins > kMostThreads / 256)) return WR_EUNSUPPORTED;
+  const size_t parts = a.splits > 1 ? (size_t)blocks * std::min<int64_t>(most, kRows) : 0;
+  if (ctx->ws_bytes < parts * (c.dim + 2) * sizeof(float)) return WR_EWORKSPACE;
+  a.stats = reinterpret_cast<f32x2*>(a.part + parts * c.dim);
   bool limits = true;
   const bool there = kv_form(c.dim, c.group, [&](auto d, auto g) {
     constexpr int D = decltype(d)::value, G = decltype(g)::value;

@@ -117,7 +117,7 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, int bloc
 using namespace wr;
 
 template <typename T>
-static void rotary_launch(wr_ctx* ctx, const RotaryArgs& a, const void* x, void* y) {
+static int rotary_launch(wr_ctx* ctx, const RotaryArgs& a, const void* x, void* y) {
   const int vec = a.pairs % 8 == 0 && a.dim % 8 == 0 ? 8 : a.pairs % 4 == 0 && a.dim % 4 == 0 ? 4 : 1;
   // Rows enough for five units a thread share a workgroup and its latency of forming angles; a workgroup of one row has about
   // 256 units of it, so that few rows still go to many compute units.
@@ -125,8 +125,9 @@ static void rotary_launch(wr_ctx* ctx, const RotaryArgs& a, const void* x, void*
   const int64_t per_row = per_head * a.heads;
   int64_t rows = std::max<int64_t>(1, std::min<int64_t>({kThreads * 5 / per_row, a.rows, 16 * kPairs / std::max(a.pairs, 1) / 4}));
   rows = std::max<int64_t>(1, std::min(rows, a.rows / (4 * (int64_t)ctx->num_cu)));
-  const int64_t heads = rows > 1 ? a.heads : std::min<int64_t>(a.heads, std::max<int64_t>(1, kThreads / per_head));
+  const int64_t heads = rows > 1 ? a.heads : std::min<int64_t>(a.heads, std::max<int64_t>({1, kThreads / per_head, (a.heads + 65534) / 65535}));
   const int64_t blocks = (a.rows + rows - 1) / rows, parts = (a.heads + heads - 1) / heads;
+  if (blocks > 4294967295 / kThreads) return WR_EUNSUPPORTED;
   const size_t lds = (size_t)rows * std::max(a.pairs, 1) * sizeof(f32x2);
   auto go = [&](auto v, auto inter) {
     constexpr int VEC = decltype(v)::value;
@@ -141,6 +142,8 @@ static void rotary_launch(wr_ctx* ctx, const RotaryArgs& a, const void* x, void*
   };
   if (a.interleaved) with(std::true_type{});
   else with(std::false_type{});
+  WR_CHECK_LAUNCH();
+  return WR_OK;
 }
 
 int wr_rotary_impl(wr_ctx* ctx, const void* x, int dtype, int64_t rows, int32_t heads, int32_t dim, int64_t ldx,
@@ -149,10 +152,5 @@ int wr_rotary_impl(wr_ctx* ctx, const void* x, int dtype, int64_t rows, int32_t 
   const RotaryArgs a{ldx,   ldy,  ldp, positions, axis_of, freqs,
                      rows,  heads, dim, pairs,     axes,    (flags & WR_ROTARY_INTERLEAVED) != 0,
                      (flags & WR_ROTARY_INVERSE) != 0, x == y};
-  if (dtype == WR_BF16)
-    rotary_launch<uint16_t>(ctx, a, x, y);
-  else
-    rotary_launch<float>(ctx, a, x, y);
-  WR_CHECK_LAUNCH();
-  return WR_OK;
+  return dtype == WR_BF16 ? rotary_launch<uint16_t>(ctx, a, x, y) : rotary_launch<float>(ctx, a, x, y);
 }

@@ -6,6 +6,8 @@ namespace wr {
 
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
+constexpr int64_t kMostThreads = 4294967295;  // of a launch, in x
+
 // What keys and values saturate at: the largest code's value, off + 15 scale with both rounded to fp16, stays in
 // fp16's range (off is off by 16 at most, scale by 4: 65024 + 16 + 60 < 65504).
 constexpr float kKvMost = 65024.0f;

@@ -138,3 +138,12 @@ def test_adapters_limits_and_nothing(lib):
     assert call(lib.wr_adapters, ADAPTERS, n_seqs=0, starts=None, ids=None) == OK
     assert call(lib.wr_adapters, ADAPTERS, most=0) == OK
     assert call(lib.wr_adapters, ADAPTERS, outs=0, y=None) == OK
+
+
+def test_lengths_that_an_int32_would_not_hold(lib, wr):
+    """A table so wide that a sequence could have more than 2^30 positions, and a scale that log2(e) takes out of range."""
+    for s in (seqs(wr, width=1 << 28, ldt=1 << 28, most_tokens=(1 << 30) + 1), seqs(wr, most_new=(1 << 30) + 1)):
+        assert lib.wr_kv_write(CTX, ctypes.byref(cache(wr)), ctypes.byref(s), *ROWS.values()) == EUNSUPPORTED
+        assert lib.wr_kv_attention(CTX, ctypes.byref(cache(wr)), ctypes.byref(s), *ATTEND.values()) == EUNSUPPORTED
+    for scale in (1.7e38, -3e38):
+        assert lib.wr_kv_attention(CTX, ctypes.byref(cache(wr)), ctypes.byref(seqs(wr)), *dict(ATTEND, scale=scale).values()) == EUNSUPPORTED

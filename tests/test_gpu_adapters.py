@@ -126,3 +126,41 @@ def test_nothing_and_refusals(wr, ctx):
         wr.wr_adapters(ctx, d["x"], torch.zeros(1, 257, 64, dtype=BF16).cuda(), torch.zeros(1, 64, 257, dtype=BF16).cuda(), d["scales"][:1], s, i, 4, y)
     with pytest.raises(ValueError):
         wr.wr_adapters(*ok, base=d["base"].float())
+
+
+def test_recorded_and_replayed_with_other_requests(wr):
+    """Recorded once and replayed with other values of x, starts and ids, beside eager work."""
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        c = wr.Context(0, stream)
+        d = inputs([40], 320, 192, 24, 3, BF16, BF16, 7)
+        starts, ids = int32([0, 10, 30, 40]), int32([0, 1, 2])
+        args = (d["x"], d["A"], d["B"], d["scales"], starts, ids, 20)
+        y, eager = torch.empty(40, 192, dtype=BF16, device="cuda"), torch.empty(40, 192, dtype=BF16, device="cuda")
+        wr.wr_adapters(c, *args, y, base=d["base"])
+        stream.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            wr.wr_adapters(c, *args, y, base=d["base"])
+        for i in range(4):
+            d["x"].copy_(torch.randn(40, 320, generator=torch.Generator().manual_seed(i)))
+            starts.copy_(int32([0, 20 - i, 20 + i, 40 - i])), ids.copy_(int32([i % 3, -1, (i + 1) % 3]))
+            y.fill_(77.0), eager.fill_(77.0)
+            graph.replay()
+            wr.wr_adapters(c, *args, eager, base=d["base"])
+            stream.synchronize()
+            assert torch.equal(y, eager)
+            check(d, y, starts.cpu().numpy(), ids.cpu().numpy(), rows=slice(0, 40 - i))
+            assert (y[40 - i:] == 77).all()
+
+
+@pytest.mark.parametrize("most", [2, 17])
+def test_many_requests(wr, ctx, most):
+    rng = np.random.default_rng(most)
+    counts = [int(n) for n in rng.integers(0, most + 1, 700)]
+    ids = [int(n) for n in rng.integers(-1, 5, 700)]
+    d = inputs(counts, 96, 130, 16, 5, BF16, F32, most)
+    starts = np.concatenate([[0], np.cumsum(counts)])
+    y = torch.empty(sum(counts), 130, device="cuda")
+    wr.wr_adapters(ctx, d["x"], d["A"], d["B"], d["scales"], int32(starts), int32(ids), most, y, base=d["base"])
+    check(d, y, starts, ids)

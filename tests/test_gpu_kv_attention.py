@@ -301,3 +301,113 @@ def test_refusals(wr, ctx):
         wr.Sequences(int32([0, 1]), int32([1]), int32([[0]]), -1, 1)
     with pytest.raises(ValueError):
         wr.KvCache(4, 2, 64, 16, 32, buf=torch.zeros(5, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("n", [64, 65, 300, 1500])
+def test_many_sequences(wr, ctx, n):
+    """One or two new tokens of many sequences, none in some."""
+    rng = np.random.default_rng(n)
+    lengths = [int(x) for x in rng.integers(1, 60, n)]
+    lengths[n // 2] = 2000
+    new = [int(x) for x in np.minimum(rng.integers(0, 3, n), lengths)]
+    attend(wr, ctx, lengths, new, 2, 4, 64, 16, 32, seed=n, pad=8)
+
+
+def test_many_sequences_with_prompts(wr, ctx):
+    lengths = [int(x) for x in np.random.default_rng(3).integers(1, 200, 80)]
+    attend(wr, ctx, lengths, [min(n, 1 + 7 * i % 90) for i, n in enumerate(lengths)], 1, 2, 64, 32, 32, seed=3)
+
+
+@pytest.mark.parametrize("new,behind", [(30, 5000), (1, 3000)])
+def test_a_batch_with_many_rows_behind_the_last_sequence(wr, new, behind):
+    """Positions are split, whatever the rows of no sequence are; a new context's workspace is sized for it."""
+    p = Paged(wr, [6000], 1, 64, 64, 64)
+    k, v = rows_of(6000, 64, 1), rows_of(6000, 64, 2)
+    c = wr.Context(0)
+    p.fill(c, k.cuda(), v.cuda())
+    q = rows_of(new + behind, 256, 3).cuda()
+    for most_new in (new, 2 * (new + behind)):
+        out = torch.full_like(q, 77.0)
+        wr.wr_kv_attention(c, p.cache, p.sequences([new], most_new=most_new), q, out, 0.125)
+        check(q, out, cached(k, 1, 64, 64), cached(v, 1, 64, 64), [(new, 6000)], 1, 64, 0.125, True, 0)
+
+
+@pytest.mark.parametrize("garbage", [0x00, 0x7b, 0x7c, 0xfb, -1])
+@pytest.mark.parametrize("new", [1, 40])
+def test_whatever_a_page_holds_behind_a_sequence(wr, ctx, new, garbage):
+    """The last page's rest and unused pages hold zeros, the largest numbers, infinities or any bytes."""
+    for lengths in ([41, 90], [63, 100]):
+        p = Paged(wr, lengths, 2, 128, 32, 64)
+        if garbage < 0:
+            p.cache.buf.copy_(torch.randint(0, 256, p.cache.buf.shape, generator=torch.Generator().manual_seed(4), dtype=torch.uint8))
+        else:
+            p.cache.buf.fill_(garbage)
+        k, v = rows_of(sum(lengths), 256, 1), rows_of(sum(lengths), 256, 2)
+        p.fill(ctx, k.cuda(), v.cuda())
+        for window in (0, 20):
+            q = rows_of(2 * new, 512, 3).cuda()
+            out = torch.empty_like(q)
+            wr.wr_kv_attention(ctx, p.cache, p.sequences([new, new]), q, out, 0.1, window=window)
+            check(q, out, cached(k, 2, 128, 64), cached(v, 2, 128, 64), [(new, n) for n in lengths], 2, 128, float(np.float32(0.1)), True, window)
+
+
+@pytest.mark.parametrize("new", [1, 50])
+def test_pages_past_4_gib(wr, ctx, new):
+    heads, dim, page, group, length = 16, 256, 256, 32, 300
+    count = (5 << 30) // int(wr.load().wr_kv_page_bytes(heads, dim, page, group)) + 1
+    cache = wr.KvCache(count, heads, dim, page_tokens=page, group=group)
+    k, v = rows_of(length, heads * dim, 1), rows_of(length, heads * dim, 2)
+    table = int32([[count - 1, count - 3]])
+    wr.wr_kv_write(ctx, cache, wr.Sequences(int32([0, length]), int32([length]), table, length, length), k.cuda(), v.cuda())
+    q = rows_of(new, heads * dim, 3).cuda()
+    out = torch.empty_like(q)
+    wr.wr_kv_attention(ctx, cache, wr.Sequences(int32([0, new]), int32([length]), table, new, length), q, out, 0.0625)
+    check(q, out, cached(k, heads, dim, group), cached(v, heads, dim, group), [(new, length)], heads, dim, 0.0625, True, 0)
+
+
+def test_a_recorded_call_keeps_its_workspace(wr):
+    """The context's workspace is replaced by a larger one after a call was recorded; the replay still has its own."""
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        c = wr.Context(0, stream)
+        p = Paged(wr, [3000], 1, 64, 64, 64)
+        k, v = rows_of(3000, 64, 1).cuda(), rows_of(3000, 64, 2).cuda()
+        p.fill(c, k, v)
+        q = rows_of(1, 128, 3).cuda()
+        out, eager = torch.empty_like(q), torch.empty_like(q)
+        seqs = p.sequences([1])
+        wr.wr_kv_attention(c, p.cache, seqs, q, out, 0.125)
+        stream.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            wr.wr_kv_attention(c, p.cache, seqs, q, out, 0.125)
+        c.ensure_workspace(3 * c.workspace.numel())
+        c.workspace.fill_(255)
+        for i in range(3):
+            q.copy_(rows_of(1, 128, 4 + i))
+            graph.replay()
+            wr.wr_kv_attention(c, p.cache, seqs, q, eager, 0.125)
+            stream.synchronize()
+            assert torch.equal(out, eager)
+
+
+def test_two_contexts_on_two_streams(wr):
+    """Each has its own workspace, so calls at the same time give what they give alone."""
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    p = Paged(wr, [5000, 200], 2, 128, 64, 64)
+    k, v = rows_of(5200, 256, 1).cuda(), rows_of(5200, 256, 2).cuda()
+    contexts = [wr.Context(0, s) for s in streams]
+    first = wr.Context(0)
+    p.fill(first, k, v)
+    qs = [rows_of(n, 1024, 3 + n).cuda() for n in (2, 100)]
+    seqs = [p.sequences([1, 1]), p.sequences([60, 40])]
+    alone = [torch.empty_like(q) for q in qs]
+    for s, q, o in zip(seqs, qs, alone):
+        wr.wr_kv_attention(first, p.cache, s, q, o, 0.1)
+    outs = [[torch.zeros_like(q) for _ in range(10)] for q in qs]
+    torch.cuda.synchronize()
+    for i in range(10):
+        for c, s, q, o in zip(contexts, seqs, qs, outs):
+            wr.wr_kv_attention(c, p.cache, s, q, o[i], 0.1)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, a) for a, each in zip(alone, outs) for o in each)

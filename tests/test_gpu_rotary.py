@@ -123,3 +123,35 @@ def test_nothing_and_refusals(wr, ctx):
                 lambda: wr.wr_rotary(ctx, x, y, *args, axis_of=int32([0] * 31))):
         with pytest.raises((ValueError, wr.WringerError)):
             bad()
+
+
+def test_more_heads_than_a_grid_has_rows(wr, ctx):
+    heads, dim = 270000, 1024
+    x = torch.randn(1, heads * dim, device="cuda").to(torch.bfloat16)
+    y, few = torch.empty_like(x), torch.empty(1, 3 * dim, dtype=torch.bfloat16, device="cuda")
+    pos = torch.tensor([77], dtype=torch.int32, device="cuda")
+    freqs = torch.rand(dim // 2, dtype=torch.float64, generator=torch.Generator().manual_seed(2)).cuda()
+    wr.wr_rotary(ctx, x, y, pos, freqs, dim)
+    for h in (0, 65535, 139999, heads - 3):
+        wr.wr_rotary(ctx, x[:, h * dim:(h + 3) * dim], few, pos, freqs, dim)
+        assert torch.equal(y[:, h * dim:(h + 3) * dim], few)
+
+
+def test_recorded_and_replayed_on_new_positions(wr):
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        c = wr.Context(0, stream)
+        x = torch.randn(5, 256, device="cuda")
+        pos, freqs = torch.zeros(5, dtype=torch.int32, device="cuda"), torch.rand(32, dtype=torch.float64, device="cuda")
+        y, eager = torch.empty_like(x), torch.empty_like(x)
+        wr.wr_rotary(c, x, y, pos, freqs, 64)
+        stream.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            wr.wr_rotary(c, x, y, pos, freqs, 64)
+        for i in range(4):
+            x.add_(1.0), pos.add_(3)
+            graph.replay()
+            wr.wr_rotary(c, x, eager, pos, freqs, 64)
+            stream.synchronize()
+            assert torch.equal(y, eager)
