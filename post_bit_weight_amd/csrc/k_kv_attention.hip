@@ -10,7 +10,10 @@ namespace wr {
 namespace {
 
 constexpr int kPaged = 1024;  // tokens whose pages a wave holds: one of 64 tiles of 16 a lane
-constexpr int kUnit = 128;     // tokens of a round of a workgroup's four waves
+// Where rows see little, or there are sequences and heads enough, each is one unit, and nothing is left to join.  One new token, eight
+// heads of 128, shared out and whole: one sequence of 256 tokens 10.1 and 7.7 us, 16 of 512 13.4 and 11.1, 64 of up to 2048 38 and 31; one
+// of 1024 10.5 and 14.4, 16 of up to 2048 21 and 24.
+constexpr int kWholeShift = 11;
 
 // What a lane holds of 32 tokens in two tiles of 16.
 template <int DIM, int GROUP>
@@ -46,15 +49,9 @@ __device__ __forceinline__ void load_tile(Step<DIM, GROUP>& f, int tt, const uin
 }
 
 // ---------------------------------------------------------------- who does what
-// The work is cut into units of kUnit tokens of a sequence and head, numbered sequence first, then head, then unit; every
-// workgroup gets an equal run of them, whatever the lengths are, and so takes the end of one (sequence, head), whole ones and
-// the start of another.  Only the device knows the lengths: each workgroup sums the sequences' units itself.
-
-// Units of a sequence and head; 1 for rows that see nothing, which get their zeros, and 0 for a sequence without rows.
+// Units of a sequence and head, 0 for a sequence without rows.
 __device__ __forceinline__ uint32_t units_of(const AttentionArgs& a, const KvSeq& s) {
-  if (s.fresh <= 0) return 0;
-  const Span all = seen(a, s, 0, s.fresh - 1);
-  return max(1u, (uint32_t)(all.hi - (all.lo & ~15) + kUnit - 1) / kUnit);
+  return s.fresh <= 0 ? 0 : units_in(a, seen(a, s, 0, s.fresh - 1));
 }
 
 struct Found {
@@ -65,9 +62,9 @@ struct Found {
 struct FoundShared {
   uint32_t waves[4], seq, before;
 };
-// The sequence of unit at(total), or, with sequence >= 0, what comes before that sequence.  For all 256 threads.
+// The sequence of unit at(total).  For all 256 threads.
 template <typename F>
-__device__ __forceinline__ Found find_units(const AttentionArgs& a, FoundShared& f, int sequence, F&& at) {
+__device__ __forceinline__ Found find_units(const AttentionArgs& a, FoundShared& f, F&& at) {
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   if (a.kv.n <= kWave) {  // each wave by itself
     const uint32_t mine = lane < a.kv.n ? units_of(a, kv_seq(a.kv, lane)) * a.kv.heads : 0;
@@ -77,11 +74,8 @@ __device__ __forceinline__ Found find_units(const AttentionArgs& a, FoundShared&
       if (lane >= m) upto += below;
     }
     const uint32_t total = __builtin_amdgcn_readlane(upto, a.kv.n - 1);
-    if (sequence < 0) {  // the first that reaches past x
-      const uint64_t past = __builtin_amdgcn_ballot_w64(upto > at(total));
-      sequence = past ? __builtin_ctzll(past) : 0;
-    }
-    sequence = __builtin_amdgcn_readfirstlane(sequence);
+    const uint64_t past = __builtin_amdgcn_ballot_w64(upto > at(total));  // the first that reaches past it
+    const int sequence = __builtin_amdgcn_readfirstlane(past ? __builtin_ctzll(past) : 0);
     return Found{total, (uint32_t)sequence, (uint32_t)__builtin_amdgcn_readlane(upto - mine, sequence)};
   }
   const int per = (a.kv.n + 255) / 256;
@@ -103,11 +97,11 @@ __device__ __forceinline__ Found find_units(const AttentionArgs& a, FoundShared&
     if (w < wave) before += f.waves[w];
   }
   const uint32_t x = at(total);
-  if (sequence >= 0 ? sequence >= begin && sequence < end : x >= before && x < before + mine) {
+  if (x >= before && x < before + mine) {
     int i = begin;
     for (; i + 1 < end; ++i) {
       const uint32_t u = units_of(a, kv_seq(a.kv, i)) * a.kv.heads;
-      if (sequence >= 0 ? i == sequence : x < before + u) break;
+      if (x < before + u) break;
       before += u;
     }
     f.seq = i;
@@ -116,15 +110,6 @@ __device__ __forceinline__ Found find_units(const AttentionArgs& a, FoundShared&
   __syncthreads();
   return Found{total, f.seq, f.before};
 }
-// Unit where a workgroup begins; those beyond one for each unit have nothing.
-__device__ __forceinline__ uint32_t first_unit(uint32_t total, uint32_t group, uint32_t groups) {
-  groups = min(groups, total);
-  return group >= groups ? total : (uint32_t)((uint64_t)total * group / groups);
-}
-__device__ __forceinline__ uint32_t group_of(uint32_t total, uint32_t unit, uint32_t groups) {
-  return (uint32_t)((((uint64_t)unit + 1) * min(groups, total) - 1) / total);
-}
-
 // ---------------------------------------------------------------- the rows of a step
 // Workgroups that a compute unit holds at once, by the registers they take; as many are launched, since more would wait
 // and leave the end uneven.
@@ -141,7 +126,7 @@ __global__ __launch_bounds__(256, groups_per_cu(DIM, NT)) void attend_rows_kerne
   const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int col = lane % 16, g = lane / 16;
   const uint32_t groups = gridDim.x;
-  const Found f0 = find_units(a, found, -1, [&](uint32_t total) { return first_unit(total, blockIdx.x, groups); });
+  const Found f0 = find_units(a, found, [&](uint32_t total) { return first_unit(total, blockIdx.x, groups); });
   uint32_t x = __builtin_amdgcn_readfirstlane(first_unit(f0.total, blockIdx.x, groups));
   const uint32_t x1 = __builtin_amdgcn_readfirstlane(first_unit(f0.total, blockIdx.x + 1, groups));
   int seq = __builtin_amdgcn_readfirstlane(f0.seq);
@@ -156,11 +141,13 @@ __global__ __launch_bounds__(256, groups_per_cu(DIM, NT)) void attend_rows_kerne
   }
   const int head = y / units, unit0 = y % units;
   const int taken = min(units - unit0, x1 - x);
+  if (unit0 == 0 && a.who && threadIdx.x == 0)
+    a.who[who_at(a, s, 0, head)] = u32x2{blockIdx.x, group_of(f0.total, x + units - 1, groups)};
   x += taken;
   y += taken;
   const Span all = seen(a, s, 0, s.fresh - 1);
-  const int begin = (all.lo & ~15) + unit0 * kUnit;
-  const int end = min(all.hi, begin + taken * kUnit);
+  const int begin = (all.lo & ~15) + (unit0 << a.unit_shift);
+  const int end = min(all.hi, begin + (taken << a.unit_shift));
   const int32_t* table = a.kv.table + (int64_t)seq * a.kv.ldt;
   int pages = -1;
 
@@ -436,8 +423,8 @@ __global__ __launch_bounds__(256, groups_per_cu(DIM, NT)) void attend_rows_kerne
       o[0] = pack_bf16(v[0] * inv, v[1] * inv);
       o[1] = pack_bf16(v[2] * inv, v[3] * inv);
       *reinterpret_cast<u32x2_any*>(a.out + row * a.ldo + (int64_t)h * DIM + d) = o;
-    } else {  // a workgroup has at most one part that others began and one that others go on with
-      const int64_t slot = ((int64_t)blockIdx.x * 2 + (unit0 == 0)) * (16 * NT) + r;
+    } else {
+      const int64_t slot = part_slot(blockIdx.x, unit0 == 0) * (16 * NT) + r;
       *reinterpret_cast<f32x4*>(a.part + slot * DIM + d) = v;
       if (d == 0) a.stats[slot] = f32x2{now, total};
     }
@@ -446,75 +433,99 @@ __global__ __launch_bounds__(256, groups_per_cu(DIM, NT)) void attend_rows_kerne
   }
 }
 
-// The parts of a row and head that went to several workgroups: a workgroup each, of 4 waves that take every fourth part.
+// ---------------------------------------------------------------- joining the parts
+// A row and head: where its parts are.
+struct Joined {
+  int64_t row;  // of the call; -1: there is nothing to join
+  int head;
+  uint32_t first, r;  // the first workgroup with a part, the row's place in its tile
+  int parts;
+  __device__ __forceinline__ int64_t slot(int c, int rows) const { return part_slot(first + c, c == 0) * rows + r; }
+};
+__device__ __forceinline__ Joined joined(const AttentionArgs& a, int rows, uint32_t unit) {
+  Joined p{-1, (int)(unit % (uint32_t)a.heads), 0, 0, 0};
+  const uint32_t rest = unit / (uint32_t)a.heads;
+  const int j = rest % (uint32_t)a.kv.most_new, seq = rest / (uint32_t)a.kv.most_new;
+  if (seq >= a.kv.n) return p;
+  const KvSeq s = kv_seq(a.kv, seq);
+  if (j >= s.fresh) return p;
+  const uint32_t m = j * a.share + p.head % (uint32_t)a.share, nth = m / (uint32_t)rows;
+  const u32x2 who = a.who[who_at(a, s, nth * rows / (uint32_t)a.share, p.head / (uint32_t)a.share)];
+  if (who.x == who.y) return p;  // that workgroup has written the row
+  p.row = s.row + j;
+  p.first = who.x;
+  p.r = m - nth * rows;
+  p.parts = who.y - who.x + 1;
+  return p;
+}
+// The sum of parts first, first + step, ...: BATCH of them at a time, the lane's PER values from `at`, strided.
+template <int DIM, int BATCH, int PER, int STRIDE>
+struct Join {
+  float top = kLowest, total = 0.0f, sum[PER] = {};
+  __device__ __forceinline__ void add(const AttentionArgs& a, const Joined& p, int rows, int first, int step, int at) {
+    for (int c0 = first; c0 < p.parts; c0 += step * BATCH) {
+      f32x2 st[BATCH];
+      float v[BATCH][PER];
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const int64_t slot = p.slot(min(c0 + step * i, p.parts - 1), rows);
+        st[i] = a.stats[slot];
+        if (c0 + step * i >= p.parts) st[i] = f32x2{kLowest, 0.0f};
+        const float* part = a.part + slot * DIM + at;
+        if constexpr (STRIDE == 1) {
+          __builtin_memcpy(v[i], __builtin_assume_aligned(part, 16), sizeof(v[i]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < PER; ++e) v[i][e] = part[e * STRIDE];
+        }
+      }
+      float now = top;
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) now = fmaxf(now, st[i].x);
+      float keep = exp2_fast(top - now);
+      top = now;
+      total *= keep;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) sum[e] *= keep;
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        if (c0 + step * i >= p.parts) break;
+        keep = exp2_fast(st[i].x - now);
+        total = fmaf(st[i].y, keep, total);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) sum[e] = fmaf(v[i][e], keep, sum[e]);
+      }
+    }
+  }
+};
+
+// Few rows, each of many parts: a row and head for a workgroup, whose four waves take every fourth part.
 template <int DIM>
-__global__ __launch_bounds__(256) void attend_join_kernel(AttentionArgs a, int rows, uint32_t groups) {
+__global__ __launch_bounds__(256) void join_few_kernel(AttentionArgs a, int rows) {
   constexpr int PER = DIM / kWave, WAVES = 4;
   __shared__ float sums[WAVES][DIM], dens[WAVES], tops[WAVES];
-  __shared__ FoundShared found;
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  const int h = blockIdx.x % (uint32_t)a.heads;
-  const uint32_t rest = blockIdx.x / (uint32_t)a.heads;
-  const int j = rest % (uint32_t)a.kv.most_new;
-  const int seq = rest / (uint32_t)a.kv.most_new;
-  const Found f = find_units(a, found, seq, [](uint32_t) { return 0u; });
-  const KvSeq s = kv_seq(a.kv, seq);
-  if (j >= s.fresh) return;
-  const uint32_t units = units_of(a, s), first = f.before + h / a.share * units;
-  const uint32_t b0 = group_of(f.total, first, groups), b1 = group_of(f.total, first + units - 1, groups);
-  if (b0 == b1) return;  // it has written the row
-  const int m = j * a.share + h % a.share, parts = b1 - b0 + 1;
-  float top = kLowest, total = 0.0f, sum[PER];
+  const Joined p = joined(a, rows, blockIdx.x);
+  if (p.row < 0) return;
+  Join<DIM, 8, PER, kWave> mine;
+  mine.add(a, p, rows, wave, WAVES, lane);
 #pragma unroll
-  for (int e = 0; e < PER; ++e) sum[e] = 0.0f;
-  for (int c0 = wave; c0 < parts; c0 += WAVES * 8) {  // eight parts at a time
-    f32x2 st[8];
-    float v[8][PER];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = min(c0 + WAVES * i, parts - 1);
-      const int64_t slot = ((int64_t)(b0 + c) * 2 + (c == 0)) * rows + m;
-      st[i] = a.stats[slot];
-      if (c0 + WAVES * i >= parts) st[i] = f32x2{kLowest, 0.0f};
-#pragma unroll
-      for (int e = 0; e < PER; ++e) v[i][e] = a.part[slot * DIM + e * kWave + lane];
-    }
-    float now = top;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) now = fmaxf(now, st[i].x);
-    float keep = exp2_fast(top - now);
-    top = now;
-    total *= keep;
-#pragma unroll
-    for (int e = 0; e < PER; ++e) sum[e] *= keep;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (c0 + WAVES * i >= parts) break;
-      keep = exp2_fast(st[i].x - now);
-      total = fmaf(st[i].y, keep, total);
-#pragma unroll
-      for (int e = 0; e < PER; ++e) sum[e] = fmaf(v[i][e], keep, sum[e]);
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < PER; ++e) sums[wave][e * kWave + lane] = sum[e];
+  for (int e = 0; e < PER; ++e) sums[wave][e * kWave + lane] = mine.sum[e];
   if (lane == 0) {
-    dens[wave] = total;
-    tops[wave] = top;
+    dens[wave] = mine.total;
+    tops[wave] = mine.top;
   }
   __syncthreads();
-  float now = kLowest;
+  float now = kLowest, total = 0.0f, keep[WAVES];
 #pragma unroll
   for (int w = 0; w < WAVES; ++w) now = fmaxf(now, tops[w]);
-  total = 0.0f;
-  float keep[WAVES];
 #pragma unroll
   for (int w = 0; w < WAVES; ++w) {
     keep[w] = exp2_fast(tops[w] - now);
     total = fmaf(dens[w], keep[w], total);
   }
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-  uint16_t* o = a.out + (int64_t)(s.row + j) * a.ldo + (int64_t)h * DIM;
+  uint16_t* o = a.out + p.row * a.ldo + (int64_t)p.head * DIM;
   for (int d = threadIdx.x; d < DIM; d += 256) {
     float v = 0.0f;
 #pragma unroll
@@ -523,21 +534,64 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttentionArgs a, int r
   }
 }
 
+// Many rows, each of a few parts: DIM / 4 lanes for a row and head.
+template <int DIM>
+__global__ __launch_bounds__(256) void join_many_kernel(AttentionArgs a, int rows) {
+  const int at = threadIdx.x % (DIM / 4) * 4;
+  const Joined p = joined(a, rows, blockIdx.x * (1024 / DIM) + threadIdx.x / (DIM / 4));
+  if (p.row < 0) return;
+  Join<DIM, 4, 4, 1> all;
+  all.add(a, p, rows, 0, 1, at);
+  const float inv = all.total == 0.0f ? 0.0f : 1.0f / all.total;
+  u32x2_any o;
+  o[0] = pack_bf16(all.sum[0] * inv, all.sum[1] * inv);
+  o[1] = pack_bf16(all.sum[2] * inv, all.sum[3] * inv);
+  *reinterpret_cast<u32x2_any*>(a.out + p.row * a.ldo + (int64_t)p.head * DIM + at) = o;
+}
+
 constexpr int kMostCUs = 256;  // what the workspace is sized for
+constexpr int kFewJoins = 4096;  // rows and heads up to which they get a workgroup each
 
 }  // namespace
+
+int wr_kv_parts(wr_ctx* ctx, AttentionArgs& a, int dim, int64_t slots) {
+  const size_t part = (size_t)slots * dim * sizeof(float), stats = (size_t)slots * sizeof(f32x2);
+  if (ctx->ws_bytes < part + stats + (size_t)a.kv.rows * a.kv.heads * sizeof(u32x2)) return WR_EWORKSPACE;
+  char* ws = static_cast<char*>(ctx->ws);
+  a.part = reinterpret_cast<float*>(ws);
+  a.stats = reinterpret_cast<f32x2*>(ws + part);
+  a.who = reinterpret_cast<u32x2*>(ws + part + stats);
+  const int64_t joins = (int64_t)a.kv.n * a.kv.most_new * a.heads;
+  return joins > 1 << 24 ? WR_EUNSUPPORTED : WR_OK;
+}
+
+int wr_kv_join(wr_ctx* ctx, const AttentionArgs& a, int dim, int rows) {
+  const int64_t units = (int64_t)a.kv.n * a.kv.most_new * a.heads;
+  auto go = [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    if (units <= kFewJoins)
+      hipLaunchKernelGGL(join_few_kernel<D>, dim3((uint32_t)units), dim3(256), 0, ctx->stream, a, rows);
+    else
+      hipLaunchKernelGGL(join_many_kernel<D>, dim3((uint32_t)((units * D + 1023) / 1024)), dim3(256), 0, ctx->stream, a, rows);
+  };
+  if (dim == 64) go(std::integral_constant<int, 64>{});
+  else if (dim == 128) go(std::integral_constant<int, 128>{});
+  else go(std::integral_constant<int, 256>{});
+  WR_CHECK_LAUNCH();
+  return WR_OK;
+}
 
 }  // namespace wr
 
 using namespace wr;
 
-size_t wr_kv_many_ws_bytes(int64_t rows, int64_t n, int32_t dim);
-int wr_kv_many_impl(wr_ctx* ctx, const wr_kv_cache& c, const wr_kv_seqs& s, AttentionArgs a, int flags);
+size_t wr_kv_many_parts();
+int wr_kv_many_impl(wr_ctx* ctx, const wr_kv_cache& c, const wr_kv_seqs& s, AttentionArgs a, int64_t span);
 
 size_t wr_kv_attention_ws_bytes(int64_t rows, int64_t n, int32_t dim) {
-  size_t parts = 0;
+  size_t parts = wr_kv_many_parts();
   for (int r : {16, 32}) parts = std::max(parts, (size_t)groups_per_cu(dim, r / 16) * kMostCUs * 2 * r);
-  return std::max(parts * (dim + 2) * sizeof(float), wr_kv_many_ws_bytes(rows, n, dim));
+  return parts * (dim + 2) * sizeof(float) + (size_t)rows * (n / dim) * sizeof(u32x2);
 }
 
 int wr_kv_attention_impl(wr_ctx* ctx, const wr_kv_cache& c, const wr_kv_seqs& s, const void* q, int64_t ldq, int64_t rows,
@@ -546,8 +600,9 @@ int wr_kv_attention_impl(wr_ctx* ctx, const wr_kv_cache& c, const wr_kv_seqs& s,
   a.kv = kv_args(c, s, rows);
   a.q = static_cast<const uint16_t*>(q);
   a.out = static_cast<uint16_t*>(out);
-  a.part = static_cast<float*>(ctx->ws);
+  a.part = nullptr;
   a.stats = nullptr;
+  a.who = nullptr;
   a.ldq = ldq;
   a.ldo = ldo;
   a.heads = heads;
@@ -555,27 +610,31 @@ int wr_kv_attention_impl(wr_ctx* ctx, const wr_kv_cache& c, const wr_kv_seqs& s,
   a.scale = scale * 1.4426950408889634f;
   a.window = window;
   a.causal = flags & WR_ATTENTION_CAUSAL;
-  a.chunk = a.splits = 0;
+  a.unit_shift = kUnitShift;
+  a.begun = 0;
   const int64_t most_rows = (int64_t)s.most_new * a.share;
-  if (most_rows > 32) return wr_kv_many_impl(ctx, c, s, a, flags);
+  int64_t span = std::max(a.kv.most_tokens, 1);  // that a sequence's rows see, from a multiple of 16
+  if (window > 0) span = std::min(span, (int64_t)window * (flags & WR_ATTENTION_CAUSAL ? 1 : 2) + s.most_new + 15);
+  if (most_rows > 32) return wr_kv_many_impl(ctx, c, s, a, span);
 
   const int tile = most_rows <= 16 ? 16 : 32;
-  const int64_t most_units = (int64_t)s.n * c.heads * ((a.kv.most_tokens + 15 + kUnit) / kUnit + 1);
-  const int64_t joins = (int64_t)s.n * s.most_new * heads;
-  if (most_units > 1 << 30 || joins > kMostThreads / 256) return WR_EUNSUPPORTED;
+  const bool whole = span <= std::min(512, 65536 / c.dim) || (span <= 1 << kWholeShift && (int64_t)s.n * c.heads >= ctx->num_cu);
+  if (whole) a.unit_shift = kWholeShift;
+  const int64_t most_units = (int64_t)s.n * c.heads * (((span - 1) >> a.unit_shift) + 1);
+  if (most_units > 1 << 30) return WR_EUNSUPPORTED;
   const int groups = (int)std::min<int64_t>(groups_per_cu(c.dim, tile / 16) * std::min(ctx->num_cu, kMostCUs), most_units);
-  const size_t parts = (size_t)groups * 2 * tile;
-  if (ctx->ws_bytes < parts * (c.dim + 2) * sizeof(float)) return WR_EWORKSPACE;
-  a.stats = reinterpret_cast<f32x2*>(a.part + parts * c.dim);
+  if (!whole) {
+    const int rc = wr_kv_parts(ctx, a, c.dim, (int64_t)groups * 2 * tile);
+    if (rc != WR_OK) return rc;
+  }
   const bool there = kv_form(c.dim, c.group, [&](auto d, auto g) {
     constexpr int D = decltype(d)::value, G = decltype(g)::value;
     if (tile == 16)
       hipLaunchKernelGGL((attend_rows_kernel<D, G, 1>), dim3(groups), dim3(256), 0, ctx->stream, a);
     else
       hipLaunchKernelGGL((attend_rows_kernel<D, G, 2>), dim3(groups), dim3(256), 0, ctx->stream, a);
-    hipLaunchKernelGGL(attend_join_kernel<D>, dim3((uint32_t)joins), dim3(256), 0, ctx->stream, a, tile, (uint32_t)groups);
   });
   if (!there) return WR_EUNSUPPORTED;
   WR_CHECK_LAUNCH();
-  return WR_OK;
+  return whole ? WR_OK : wr_kv_join(ctx, a, c.dim, tile);
 }

@@ -14,12 +14,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kRows = 256;
 
-// Where the parts of a tile of rows lie: by sequence, tile, head and chunk, whatever rows of the call belong to no sequence.
-__device__ __forceinline__ int64_t part_of(const AttentionArgs& a, int seq, int tile, int head, int split) {
-  const uint32_t rows = (uint32_t)a.kv.most_new * a.share;
-  const int64_t group = ((int64_t)seq * ((rows + kRows - 1) / kRows) + tile) * a.kv.heads + head;
-  return (group * a.splits + split) * min(rows, (uint32_t)kRows);
-}
+constexpr int kPairs = 512;  // of a sequence and a tile of its rows, whose work is shared out: one a thread
 
 __device__ __forceinline__ f32x16 mfma32x32x16_f16(const u32x4& a, const u32x4& b, const f32x16& c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
@@ -43,9 +38,49 @@ template <int DIM>
 struct Shared {
   Tile<DIM> tile[3];
   int bad;  // the last tile among whose values a NaN was met, -1: none
+  uint32_t upto[kPairs], waves[kThreads / kWave], pair;  // units of the pairs up to this one, of each wave's; of the first unit
 };
 
-template <int DIM, int GROUP>
+// Shares the work out: the first unit of this workgroup, the one behind its last, and the pair of the first.
+template <int DIM>
+__device__ __forceinline__ void find_pair(const AttentionArgs& a, uint32_t tiles, Shared<DIM>& f, uint32_t& total, uint32_t& x, uint32_t& x1,
+                                          uint32_t& pair) {
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const uint32_t seq = threadIdx.x / tiles, tile = threadIdx.x - seq * tiles;
+  uint32_t mine = 0;
+  if (seq < (uint32_t)a.kv.n) {
+    const KvSeq s = kv_seq(a.kv, seq);
+    if (s.fresh > 0 && (int)tile * kRows < s.fresh * a.share) {
+      const RowTile rt = row_tile(a, s, tile, kRows);
+      mine = (a.begun + units_in(a, seen(a, s, rt.first, rt.last))) * a.kv.heads;
+    }
+  }
+  uint32_t upto = mine;
+#pragma unroll
+  for (int m = 1; m < kWave; m <<= 1) {
+    const uint32_t below = __shfl_up(upto, m);
+    if (lane >= m) upto += below;
+  }
+  if (lane == kWave - 1) f.waves[wave] = upto;
+  __syncthreads();
+  total = 0;
+  for (int w = 0; w < kThreads / kWave; ++w) {
+    if (w < wave) upto += f.waves[w];
+    total += f.waves[w];
+  }
+  f.upto[threadIdx.x] = upto;
+  x = first_unit(total, blockIdx.x, gridDim.x);
+  x1 = first_unit(total, blockIdx.x + 1, gridDim.x);
+  if (x < upto && x >= upto - mine) f.pair = threadIdx.x;
+  __syncthreads();
+  total = __builtin_amdgcn_readfirstlane(total);
+  x = __builtin_amdgcn_readfirstlane(x);
+  x1 = __builtin_amdgcn_readfirstlane(x1);
+  pair = x < x1 ? __builtin_amdgcn_readfirstlane(f.pair) : 0;
+}
+
+// SHARED: every workgroup takes an equal share of all units; else a tile of rows and head.
+template <int DIM, int GROUP, bool SHARED>
 __global__ __launch_bounds__(kThreads, 1) void attend_many_kernel(AttentionArgs a, uint32_t tiles) {
   using T = Tile<DIM>;
   constexpr int TOKENS = T::TOKENS, N16 = TOKENS / 16, NB = TOKENS / 32, KS = DIM / 16, SL = DIM / 32;
@@ -53,21 +88,45 @@ __global__ __launch_bounds__(kThreads, 1) void attend_many_kernel(AttentionArgs 
   Shared<DIM>& shared = *reinterpret_cast<Shared<DIM>*>(lds);
   T* buf = shared.tile;
 
-  uint32_t block = blockIdx.x;
-  const int head = block % (uint32_t)a.kv.heads;
-  block /= (uint32_t)a.kv.heads;
-  const int seq = block % (uint32_t)a.kv.n;
-  block /= (uint32_t)a.kv.n;
-  const int split = block % (uint32_t)a.splits;
-  const int tile = tiles - 1 - block / (uint32_t)a.splits;  // those that see most first
-
+  uint32_t total = 1, x = 0, x1 = 1, pair = 0;
+  if constexpr (SHARED) find_pair<DIM>(a, tiles, shared, total, x, x1, pair);
+  for (;;) {
+  if (SHARED && x >= x1) return;
+  int head, seq, tile, unit0 = 0;
+  uint32_t units = 1, taken = 1, item = 0;  // item: its first unit among all
+  if constexpr (SHARED) {
+    uint32_t upto;
+    for (;; ++pair) {
+      upto = __builtin_amdgcn_readfirstlane(shared.upto[pair]);
+      if (x < upto) break;
+    }
+    const uint32_t before = pair ? __builtin_amdgcn_readfirstlane(shared.upto[pair - 1]) : 0;
+    units = (upto - before) / (uint32_t)a.kv.heads;
+    head = (x - before) / units;
+    const uint32_t at = (x - before) - head * units, run = min(units - at, x1 - x);
+    item = x - at + a.begun;
+    x += run;
+    if (at + run <= a.begun) continue;  // only of the beginning: the next workgroup begins it
+    units -= a.begun;
+    unit0 = max((int)(at - a.begun), 0);
+    taken = at + run - a.begun - unit0;
+    seq = pair / tiles;
+    tile = pair - seq * tiles;
+  } else {
+    uint32_t block = blockIdx.x;
+    head = block % (uint32_t)a.kv.heads;
+    block /= (uint32_t)a.kv.heads;
+    seq = block % (uint32_t)a.kv.n;
+    tile = tiles - 1 - block / (uint32_t)a.kv.n;  // those that see most first
+  }
   const KvSeq s = kv_seq(a.kv, seq);
-  if (s.fresh <= 0 || tile * kRows >= s.fresh * a.share) return;
+  if (s.fresh <= 0 || tile * kRows >= s.fresh * a.share) return;  // only of those that were not found
   const RowTile rt = row_tile(a, s, tile, kRows);
+  if (SHARED && unit0 == 0 && threadIdx.x == 0)
+    a.who[who_at(a, s, rt.first, head)] = u32x2{blockIdx.x, group_of(total, item + units - 1, gridDim.x)};
   const Span all = seen(a, s, rt.first, rt.last);
-  const int begin = (all.lo & ~15) + split * a.chunk;
-  const int end = min(all.hi, begin + a.chunk);
-  if (split > 0 && begin >= end) return;  // the first chunk of rows that see nothing writes their zeros
+  const int begin = (all.lo & ~15) + (SHARED ? unit0 << a.unit_shift : 0);
+  const int end = !SHARED || taken == units ? all.hi : min(all.hi, begin + (int)(taken << a.unit_shift));
 
   const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int col = lane % 32, h = lane / 32;
@@ -328,67 +387,33 @@ __global__ __launch_bounds__(kThreads, 1) void attend_many_kernel(AttentionArgs 
   }
 
   den += __shfl_xor(den, 32);
-  if (!live) return;
-  const float inv = den == 0.0f ? 0.0f : 1.0f / den;
-  const int64_t row = s.row + query, slot = a.splits == 1 ? 0 : part_of(a, seq, tile, head, split) + wave * 32 + col;
+  if (live) {
+    const float inv = den == 0.0f ? 0.0f : 1.0f / den;
+    const int64_t row = s.row + query, slot = part_slot(blockIdx.x, unit0 == 0) * kRows + wave * 32 + col;
 #pragma unroll
-  for (int x = 0; x < SL; ++x)
+    for (int x = 0; x < SL; ++x)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int d = 32 * x + 8 * i + 4 * h;
-      const f32x4 v{acc[x][4 * i], acc[x][4 * i + 1], acc[x][4 * i + 2], acc[x][4 * i + 3]};
-      if (a.splits == 1) {
-        u32x2_any o;
-        o[0] = pack_bf16(v[0] * inv, v[1] * inv);
-        o[1] = pack_bf16(v[2] * inv, v[3] * inv);
-        *reinterpret_cast<u32x2_any*>(a.out + row * a.ldo + (int64_t)out_head * DIM + d) = o;
-      } else {
-        *reinterpret_cast<f32x4*>(a.part + slot * DIM + d) = v;
+      for (int i = 0; i < 4; ++i) {
+        const int d = 32 * x + 8 * i + 4 * h;
+        const f32x4 v{acc[x][4 * i], acc[x][4 * i + 1], acc[x][4 * i + 2], acc[x][4 * i + 3]};
+        if (!SHARED || taken == units) {
+          u32x2_any o;
+          o[0] = pack_bf16(v[0] * inv, v[1] * inv);
+          o[1] = pack_bf16(v[2] * inv, v[3] * inv);
+          *reinterpret_cast<u32x2_any*>(a.out + row * a.ldo + (int64_t)out_head * DIM + d) = o;
+        } else {
+          *reinterpret_cast<f32x4*>(a.part + slot * DIM + d) = v;
+        }
       }
-    }
-  if (a.splits > 1 && h == 0) a.stats[slot] = f32x2{top, den};
-}
-
-// The chunks' parts of a row and head, in the chunks' order: a wave each.
-template <int DIM>
-__global__ __launch_bounds__(256) void attend_chunks_kernel(AttentionArgs a) {
-  constexpr int PER = DIM / kWave;
-  const int lane = threadIdx.x % kWave;
-  const uint32_t unit = blockIdx.x * 4 + threadIdx.x / kWave;
-  const int h = unit % (uint32_t)a.heads;
-  const uint32_t rest = unit / (uint32_t)a.heads;
-  const int j = rest % (uint32_t)a.kv.most_new;
-  const int seq = rest / (uint32_t)a.kv.most_new;
-  if (seq >= a.kv.n) return;
-  const KvSeq s = kv_seq(a.kv, seq);
-  if (j >= s.fresh) return;
-  const int m = j * a.share + h % a.share;
-  const RowTile rt = row_tile(a, s, m / kRows, kRows);
-  const Span all = seen(a, s, rt.first, rt.last);
-  const int parts = min(a.splits, max(1, (all.hi - (all.lo & ~15) + a.chunk - 1) / a.chunk));
-  const int64_t slot = part_of(a, seq, m / kRows, h / a.share, 0) + m % kRows;
-  const int next = min(a.kv.most_new * a.share, kRows);
-  float top = kLowest, total = 0.0f, sum[PER];
-  for (int c = lane; c < parts; c += kWave) top = fmaxf(top, a.stats[slot + (int64_t)c * next].x);
-  for (int x = 1; x < kWave; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
-#pragma unroll
-  for (int e = 0; e < PER; ++e) sum[e] = 0.0f;
-#pragma unroll 4
-  for (int c = 0; c < parts; ++c) {
-    const int64_t at = slot + (int64_t)c * next;
-    const f32x2 st = a.stats[at];
-    const float keep = exp2_fast(st.x - top);
-    total = fmaf(st.y, keep, total);
-#pragma unroll
-    for (int e = 0; e < PER; ++e) sum[e] = fmaf(a.part[at * DIM + e * kWave + lane], keep, sum[e]);
+    if (SHARED && taken != units && h == 0) a.stats[slot] = f32x2{top, den};
   }
-  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-  uint16_t* o = a.out + (int64_t)(s.row + j) * a.ldo + (int64_t)h * DIM;
-#pragma unroll
-  for (int e = 0; e < PER; ++e) o[e * kWave + lane] = (uint16_t)f32_to_bf16_bits(sum[e] * inv);
+  if (!SHARED) return;
+  __syncthreads();  // the tiles and `bad` are free
+  }
 }
 
-constexpr int kWanted = 512;  // workgroups, two for every compute unit, below which the positions are split as well
+constexpr int kMostGroups = 256;  // that share work
+constexpr int kMostTiles = 512;   // of rows and head for which the work is shared
 
 }  // namespace
 
@@ -396,38 +421,41 @@ constexpr int kWanted = 512;  // workgroups, two for every compute unit, below w
 
 using namespace wr;
 
-// Where positions are split there are at most kWanted workgroups, with a tile's rows each.
-size_t wr_kv_many_ws_bytes(int64_t rows, int64_t n, int32_t dim) {
-  return (size_t)std::min<int64_t>(rows * (n / dim), kRows) * kWanted * (dim + 2) * sizeof(float);
-}
+size_t wr_kv_many_parts() { return (size_t)kMostGroups * 2 * kRows; }
 
-int wr_kv_many_impl(wr_ctx* ctx, const wr_kv_cache& c, const wr_kv_seqs& s, AttentionArgs a, int flags) {
-  const int64_t most = (int64_t)s.most_new * a.share;
-  const int64_t tiles = (most + kRows - 1) / kRows;
-  // positions that a tile's rows can see, from a multiple of 16
-  int64_t span = a.kv.most_tokens;
-  const int64_t queries = std::min<int64_t>(s.most_new, (kRows + a.share - 2) / a.share + 1);
-  if (a.window > 0) span = std::min(span, (int64_t)a.window * (flags & WR_ATTENTION_CAUSAL ? 1 : 2) + queries + 15);
-  const int64_t groups = std::max<int64_t>(1, s.n * tiles * c.heads);
-  const int64_t splits = std::max<int64_t>(1, std::min((span + 511) / 512, kWanted / groups));
-  a.chunk = (int)std::min<int64_t>(((span + splits - 1) / splits + 127) / 128 * 128, 1 << 30);
-  a.splits = (int)std::max<int64_t>(1, (span + a.chunk - 1) / a.chunk);
-  const int64_t blocks = groups * a.splits, joins = ((int64_t)s.n * s.most_new * a.heads + 3) / 4;
-  if (blocks > kMostThreads / kThreads || (a.splits > 1 && joins > kMostThreads / 256)) return WR_EUNSUPPORTED;
-  const size_t parts = a.splits > 1 ? (size_t)blocks * std::min<int64_t>(most, kRows) : 0;
-  if (ctx->ws_bytes < parts * (c.dim + 2) * sizeof(float)) return WR_EWORKSPACE;
-  a.stats = reinterpret_cast<f32x2*>(a.part + parts * c.dim);
+int wr_kv_many_impl(wr_ctx* ctx, const wr_kv_cache& c, const wr_kv_seqs& s, AttentionArgs a, int64_t span) {
+  const int64_t tiles = ((int64_t)s.most_new * a.share + kRows - 1) / kRows, blocks = s.n * tiles * c.heads;
+  if (blocks > kMostThreads / kThreads) return WR_EUNSUPPORTED;
+  const int64_t most_units = ((span - 1) >> a.unit_shift) + 1, most_groups = std::min(ctx->num_cu, kMostGroups);
+  // Sharing costs the joining (5 us and more) and the beginnings of tiles, about 8 us each.  It gains the units that compute units would be
+  // idle for, by what the host knows: the tiles that so many rows can have, and what a causal prompt sees on average.  Two units are
+  // enough where tiles are fewer than compute units; else long tiles go first, and leave less idle than they seem to.  Direct and
+  // shared, eight heads shared by four, dim 128: 512 rows of 1000 tokens 48 and 38 us, 1024 of 1024 49 and 44, 2500 of 8192 450 and 360;
+  // 2500 of 2500 101 and 107, 512 of 1000 of four sequences 53 and 72, 300 of 700 of eight 64 and 77.
+  const int64_t busy = std::min<int64_t>(s.n * tiles, a.kv.rows * a.share / kRows + s.n) * c.heads;
+  const int64_t usual = span - (a.causal && a.window == 0 ? std::min<int64_t>(s.most_new, span) / 2 : 0);
+  const int64_t idle = (most_groups - 1 - (busy - 1) % most_groups) * (usual >> a.unit_shift);
+  const bool few = most_units > 1 && blocks * most_units <= most_groups;  // at most one unit for each
+  a.begun = few ? 0 : 2;
+  const bool shared = blocks <= kMostTiles && blocks * (most_units + a.begun) <= 1 << 30 && (few || idle >= most_groups * (busy <= most_groups ? 2 : 16));
+  const int64_t groups = shared ? std::min<int64_t>(most_groups, blocks * most_units) : blocks;
+  if (shared) {
+    const int rc = wr_kv_parts(ctx, a, c.dim, groups * 2 * kRows);
+    if (rc != WR_OK) return rc;
+  }
   bool limits = true;
   const bool there = kv_form(c.dim, c.group, [&](auto d, auto g) {
     constexpr int D = decltype(d)::value, G = decltype(g)::value;
     constexpr int bytes = sizeof(Shared<D>);
-    limits = lds_limit(reinterpret_cast<const void*>(&attend_many_kernel<D, G>), bytes);
-    if (!limits) return;
-    hipLaunchKernelGGL((attend_many_kernel<D, G>), dim3((uint32_t)blocks), dim3(kThreads), bytes, ctx->stream, a, (uint32_t)tiles);
-    if (a.splits > 1) hipLaunchKernelGGL(attend_chunks_kernel<D>, dim3((uint32_t)joins), dim3(256), 0, ctx->stream, a);
+    auto go = [&](auto kernel) {
+      limits = lds_limit(reinterpret_cast<const void*>(kernel), bytes);
+      if (limits) hipLaunchKernelGGL(kernel, dim3((uint32_t)groups), dim3(kThreads), bytes, ctx->stream, a, (uint32_t)tiles);
+    };
+    if (shared) go(&attend_many_kernel<D, G, true>);
+    else go(&attend_many_kernel<D, G, false>);
   });
   if (!there) return WR_EUNSUPPORTED;
   if (!limits) return WR_EHIP;
   WR_CHECK_LAUNCH();
-  return WR_OK;
+  return shared ? wr_kv_join(ctx, a, c.dim, kRows) : WR_OK;
 }

@@ -54,18 +54,23 @@ __device__ __forceinline__ uint32_t row_lane(uint32_t v) {
   return __builtin_amdgcn_update_dpp(0, v, 0x150 + N, 0xf, 0xf, true);
 }
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
 struct AttentionArgs {
   KvArgs kv;
   const uint16_t* q;
   uint16_t* out;
-  float* part;   // unnormalised outputs of parts of a row's positions
+  // Of rows whose positions went to several workgroups:
+  float* part;   // [slot][row of the tile] unnormalised outputs of parts of their positions
   f32x2* stats;  // their maximum (of log2 weights) and sum
+  u32x2* who;    // [first row of a tile][head of the cache]: the first workgroup with a part of it, and the last
   int64_t ldq, ldo;
   int heads, share;  // query heads, and how many of them share a head of the cache
   float scale;       // times log2(e)
   int window;
   bool causal;
-  int chunk, splits;  // many rows: tokens that a workgroup takes, chunks of a row at most
+  int unit_shift;     // a unit of work is 1 << unit_shift tokens
+  uint32_t begun;     // many rows: what it costs to begin a tile, in units
 };
 
 // The positions that queries first .. last of a sequence see: lo .. hi - 1.
@@ -82,6 +87,30 @@ __device__ __forceinline__ Span seen(const AttentionArgs& a, const KvSeq& s, int
   return Span{(int)lo, (int)hi};
 }
 
+// ---------------------------------------------------------------- who does what
+// The work is cut into units of 128 tokens of a sequence, tile of its rows and head of the cache, and every workgroup gets an equal run of
+// them, whatever the lengths are: the end of one (sequence, tile, head), whole ones and the start of another.  Only the device
+// knows the lengths, so each workgroup sums the units itself.
+constexpr int kUnitShift = 7;
+
+// Units of the rows that see these positions; 1 for rows that see nothing, which get their zeros.
+__device__ __forceinline__ uint32_t units_in(const AttentionArgs& a, const Span& all) {
+  return max(1u, (uint32_t)(all.hi - (all.lo & ~15) + (1 << a.unit_shift) - 1) >> a.unit_shift);
+}
+// Unit where a workgroup begins; those beyond one for each unit have nothing.
+__device__ __forceinline__ uint32_t first_unit(uint32_t total, uint32_t group, uint32_t groups) {
+  groups = min(groups, total);
+  return group >= groups ? total : (uint32_t)((uint64_t)total * group / groups);
+}
+__device__ __forceinline__ uint32_t group_of(uint32_t total, uint32_t unit, uint32_t groups) {
+  return (uint32_t)((((uint64_t)unit + 1) * min(groups, total) - 1) / total);
+}
+// A workgroup has at most one part that others began, its slot 0, and one that others go on with, its slot 1.
+__device__ __forceinline__ int64_t part_slot(uint32_t group, bool first) { return (int64_t)group * 2 + first; }
+__device__ __forceinline__ int64_t who_at(const AttentionArgs& a, const KvSeq& s, int query, int head) {
+  return (int64_t)(s.row + query) * a.kv.heads + head;
+}
+
 // The queries of a tile of rows (query, head of the share), numbered query first.
 struct RowTile {
   int first, last;
@@ -90,5 +119,9 @@ __device__ __forceinline__ RowTile row_tile(const AttentionArgs& a, const KvSeq&
   const uint32_t m0 = tile * rows, m1 = min(m0 + rows, (uint32_t)(s.fresh * a.share)) - 1;
   return RowTile{(int)(m0 / (uint32_t)a.share), (int)(m1 / (uint32_t)a.share)};
 }
+
+// Lays out the workspace for `slots` rows of parts, and joins the parts of tiles of `rows` rows.
+int wr_kv_parts(wr_ctx* ctx, AttentionArgs& a, int dim, int64_t slots);
+int wr_kv_join(wr_ctx* ctx, const AttentionArgs& a, int dim, int rows);
 
 }  // namespace wr
