@@ -1,12 +1,14 @@
 // Low-rank adapters of many requests beside a shared projection: y = base + s B (A x).
 //
-// Two launches.  The first forms t = A x (rows x rank, as three bf16 parts, in the workspace): x is read once, a workgroup takes 16
-// or 32 rows of a request and up to 64 rows of A, and its eight waves cut the sum over n, which is what fills the card when
-// there are few rows.  The second forms y: a wave keeps its rows of t as matrix operands and walks the outputs 64 at a
-// time; the matrix product's rows are dealt to outputs so that a lane ends up with 8 neighbouring ones, and base
-// is read and y written in whole 16-byte accesses, 64 neighbouring bytes of a row each.  One token is bound by
-// the two launches and the latency of a few dependent loads, long prompts by the bytes of x, base and y: the products, three
-// of bf16 parts for each of fp32 (x = x0 + x1 + x2 exactly, t likewise), stay below a tenth of the matrix cores' rate.
+// Two launches.  The first forms t = A x (rows x rank, as three bf16 parts, in the workspace): a workgroup takes 16 or 32 rows of a
+// request and up to 32 rows of A, and its eight waves cut the sum over n, which is what fills the card when there are few rows.  (64
+// rows of A halve the reads of x, but leave too few workgroups: 29 instead of 23.5 us for 8290 rows x 2560 of four requests, rank 64.)
+// The second forms y: a wave keeps its rows of t as matrix operands and walks the outputs 64 at a time; the matrix product's
+// rows are dealt to outputs so that a lane ends up with 8 neighbouring ones, and base is read and y written in whole 16-byte
+// accesses, 64 neighbouring bytes of a row each (8290 x 4096 bf16, rank 64: 41 us, at 175 MB with t and B 4.2 TB/s).  One token of
+// 48 requests, 2560 -> 4096 with rank 16, takes 5.3 + 5 us, which is launches and a few dependent loads; long prompts the bytes
+// of x, base and y: the products, three of bf16 parts for each of fp32 (x = x0 + x1 + x2 exactly, t likewise), stay below a tenth of
+// the matrix cores' rate.
 #include "rowops.hpp"
 
 namespace wr {
@@ -24,7 +26,7 @@ struct AdapterArgs {
   int64_t rows, n, outs, most;
   int64_t ldx, ldb, ldy;
   int32_t adapters, rank, wide;  // wide: rank, up to a multiple of 8
-  uint32_t tiles;  // row tiles of a request
+  int32_t n_seqs;
 };
 
 struct Request {
@@ -32,15 +34,36 @@ struct Request {
   int adapter, rank;   // adapter -1: none
 };
 
-// The rows of a request from its row `first`.
-__device__ __forceinline__ Request request_of(const AdapterArgs& a, int i, int64_t first) {
-  const int64_t b = a.starts[i], e = a.starts[i + 1];
-  const bool ok = b >= 0 && e >= b && e <= a.rows && e - b <= a.most;
-  int id = a.ids[i];
-  if (id < 0 || id >= a.adapters) id = -1;
-  int rank = a.rank;
-  if (id >= 0 && a.ranks) rank = min(max(a.ranks[id], 0), a.rank);
-  return Request{b + first, ok ? e - b - first : 0, id, id >= 0 ? rank : 0};
+// The rows of tile `tile` of all requests' tiles of `rows` rows, one request after the other: so many workgroups as there may be tiles
+// find theirs, and those without one are the last.
+__device__ __forceinline__ Request request_of(const AdapterArgs& a, uint32_t tile, int rows) {
+  const int lane = threadIdx.x % kWave;
+  for (int i0 = 0; i0 < a.n_seqs; i0 += kWave) {
+    const int i = min(i0 + lane, a.n_seqs - 1);
+    const int64_t b = a.starts[i], e = a.starts[i + 1];
+    int id = a.ids[i];
+    const bool ok = i0 + lane < a.n_seqs && b >= 0 && e >= b && e <= a.rows && e - b <= a.most;
+    const uint32_t mine = ok ? (uint32_t)((e - b + rows - 1) / rows) : 0;
+    uint32_t upto = mine;
+    for (int m = 1; m < kWave; m <<= 1) {
+      const uint32_t below = __shfl_up(upto, m);
+      if (lane >= m) upto += below;
+    }
+    const uint64_t past = __builtin_amdgcn_ballot_w64(upto > tile);
+    if (past == 0) {
+      tile -= __builtin_amdgcn_readlane(upto, kWave - 1);
+      continue;
+    }
+    const int at = __builtin_ctzll(past);
+    const int64_t first = (int64_t)(tile - __builtin_amdgcn_readlane(upto - mine, at)) * rows;
+    id = __builtin_amdgcn_readlane(id, at);
+    if (id < 0 || id >= a.adapters) id = -1;
+    int rank = a.rank;
+    if (id >= 0 && a.ranks) rank = min(max(a.ranks[id], 0), a.rank);
+    const int64_t row = __builtin_amdgcn_readlane((int)b, at);
+    return Request{row + first, __builtin_amdgcn_readlane((int)(e - b), at) - first, id, id >= 0 ? rank : 0};
+  }
+  return Request{0, 0, -1, 0};
 }
 
 __device__ __forceinline__ f32x4 mfma16x16x32_bf16(const u32x4& a, const u32x4& b, const f32x4& c) {
@@ -61,6 +84,20 @@ __device__ __forceinline__ void load8(Raw8<T>& r, const T* row, int64_t k, int64
 }
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// Memory is read and written with four neighbouring lanes on 64 neighbouring bytes of a row (lane 4 r + c: part c of row r): a load
+// whose neighbouring lanes are in different rows, as the matrix cores want them (lane 16 c + r), takes four times the cycles.
+// What a lane then needs comes from the lane `from`.
+template <typename R>
+__device__ __forceinline__ R from_lane(const R& r, int from) {
+  uint32_t w[sizeof(R) / 4];
+  __builtin_memcpy(w, &r, sizeof(R));
+#pragma unroll
+  for (auto& x : w) x = __builtin_amdgcn_ds_bpermute(4 * from, x);
+  R out;
+  __builtin_memcpy(&out, w, sizeof(R));
+  return out;
+}
 
 // The values rounded to bf16, and what is left of them.  Three times makes any fp32 value exactly; of an infinity or NaN
 // nothing is left.
@@ -99,11 +136,11 @@ __global__ __launch_bounds__(512) void adapters_in_kernel(AdapterArgs a, const X
   constexpr int WAVES = 8;
   __shared__ f32x4 part[WAVES][MT][NT][kWave];
   const uint32_t rt = blockIdx.x % rank_tiles, rest = blockIdx.x / rank_tiles;
-  const Request q = request_of(a, rest / a.tiles, (int64_t)(rest % a.tiles) * 16 * MT);
+  const Request q = request_of(a, rest, 16 * MT);
   const int r0 = rt * 16 * NT;
   if (q.count <= 0 || r0 >= q.rank) return;
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  const int low = lane % 16, g = lane / 16;
+  const int low = lane / 4, g = lane % 4, from = lane % 16 * 4 + lane / 16;
   const X* xr[MT];
   const uint16_t* ar[NT];
 #pragma unroll
@@ -137,15 +174,19 @@ __global__ __launch_bounds__(512) void adapters_in_kernel(AdapterArgs a, const X
   };
   auto multiply = [&](const Step& f) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h) {
+      u32x4 ranks[NT];
+#pragma unroll
+      for (int c = 0; c < NT; ++c) ranks[c] = from_lane(f.a[h][c].v, from);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const Parts<X> p(f.x[h][m]);
+        const Parts<X> p(from_lane(f.x[h][m], from));
 #pragma unroll
         for (int i = 0; i < Parts<X>::N; ++i)
 #pragma unroll
-          for (int c = 0; c < NT; ++c) acc[m][c] = mfma16x16x32_bf16(f.a[h][c].v, p.p[i], acc[m][c]);
+          for (int c = 0; c < NT; ++c) acc[m][c] = mfma16x16x32_bf16(ranks[c], p.p[i], acc[m][c]);
       }
+    }
   };
   // two steps in turn, each loaded while the other is worked on
   constexpr int64_t kRound = 64 * WAVES;
@@ -196,9 +237,9 @@ template <typename Y, int MT, int KS, bool ROWS>
 __global__ __launch_bounds__(256, KS <= 4 ? 2 : 1) void adapters_out_kernel(AdapterArgs a, const Y* base, Y* y, uint32_t out_parts) {
   constexpr int WAVES = 4;
   const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int low = lane % 16, g = lane / 16;
+  const int low = lane / 4, g = lane % 4, from = lane % 16 * 4 + lane / 16, back = g * 16 + low;
   const uint32_t nth = blockIdx.x % out_parts, rest = blockIdx.x / out_parts;
-  const Request q = request_of(a, rest / a.tiles, (int64_t)(ROWS ? rest % a.tiles * WAVES + wave : rest % a.tiles) * 16 * MT);
+  const Request q = request_of(a, ROWS ? rest * WAVES + wave : rest, 16 * MT);
   if (q.count <= 0 || (q.rank == 0 && base == y)) return;
   const float s = q.rank > 0 ? a.scales[q.adapter] : 0.0f;
   u32x4 t[MT][KS][3];
@@ -210,7 +251,7 @@ __global__ __launch_bounds__(256, KS <= 4 ? 2 : 1) void adapters_out_kernel(Adap
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
         const int r = 32 * ks + 8 * g;
-        t[m][ks][i] = r < q.rank ? *reinterpret_cast<const u32x4*>(tr + i * a.wide + r) : u32x4{0, 0, 0, 0};
+        t[m][ks][i] = from_lane(r < q.rank ? *reinterpret_cast<const u32x4*>(tr + i * a.wide + r) : u32x4{0, 0, 0, 0}, from);
       }
   }
   const uint16_t* bp = a.B + (int64_t)max(q.adapter, 0) * a.outs * a.rank;
@@ -218,8 +259,8 @@ __global__ __launch_bounds__(256, KS <= 4 ? 2 : 1) void adapters_out_kernel(Adap
     Raw8<uint16_t> b[4][KS];
     Raw8<Y> v[MT][2];
   };
-  // row `low` of product j is output 32 (j / 2) + 8 (low / 4) + 4 (j % 2) + low % 4, so that a lane gets outputs 8 g .. 8 g + 7 and
-  // 32 more of row `low`, and four lanes 64 neighbouring bytes of bf16
+  // row r of product j is output 32 (j / 2) + 8 (r / 4) + 4 (j % 2) + r % 4, so that a lane gets eight neighbouring outputs of a
+  // row, and eight 32 further on
   auto multiply = [&](Step& f, int64_t o0, auto whole) {
     f32x4 acc[MT][4];
 #pragma unroll
@@ -230,11 +271,17 @@ __global__ __launch_bounds__(256, KS <= 4 ? 2 : 1) void adapters_out_kernel(Adap
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
+        for (int ks = 0; ks < KS; ++ks) {
+          const u32x4 b = from_lane(32 * ks + 8 * g < q.rank ? f.b[j][ks].v : u32x4{0, 0, 0, 0}, from);
 #pragma unroll
           for (int i = 0; i < 3; ++i)
 #pragma unroll
-            for (int m = 0; m < MT; ++m) acc[m][j] = mfma16x16x32_bf16(f.b[j][ks].v, t[m][ks][i], acc[m][j]);
+            for (int m = 0; m < MT; ++m) acc[m][j] = mfma16x16x32_bf16(b, t[m][ks][i], acc[m][j]);
+        }
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[m][j] = from_lane(acc[m][j], back);
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -262,24 +309,27 @@ __global__ __launch_bounds__(256, KS <= 4 ? 2 : 1) void adapters_out_kernel(Adap
   };
   const int64_t stride = (int64_t)out_parts * (ROWS ? 64 : WAVES * 64);
   int64_t o0 = ROWS ? (int64_t)nth * 64 : ((int64_t)nth * WAVES + wave) * 64;
-  const Y* from = base ? base : y;  // what is read without a base is not used
+  const Y* below = base ? base : y;  // what is read without a base is not used
   const int64_t ldf = base ? a.ldb : a.ldy;
   if constexpr (KS <= 2) {
     // Whole steps, each loaded while the one before it is worked on.  The loads are not conditional, or waiting for one step
     // would mean waiting for the next as well; past the end they repeat the last one.
     const int64_t last = a.outs / 64 * 64 - 64;
-    if (q.rank == 32 * KS && o0 <= last) {
+    if (q.rank > 0 && q.rank % 8 == 0 && o0 <= last) {
       auto fetch = [&](Step& f, int64_t at) {
         at = min(at, last);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) f.b[j][ks].load(bp + (at + 32 * (j / 2) + 8 * (low / 4) + 4 * (j % 2) + low % 4) * a.rank + 32 * ks + 8 * g);
+          for (int ks = 0; ks < KS; ++ks) {
+            const int k = 32 * ks + 8 * g;
+            f.b[j][ks].load(bp + (at + 32 * (j / 2) + 8 * (low / 4) + 4 * (j % 2) + low % 4) * a.rank + min(k, q.rank - 8));
+          }
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            f.v[m][h].load(from + (q.row + min((int64_t)(16 * m + low), q.count - 1)) * ldf + at + 32 * h + 8 * g);
+            f.v[m][h].load(below + (q.row + min((int64_t)(16 * m + low), q.count - 1)) * ldf + at + 32 * h + 8 * g);
       };
       Step even, odd;
       fetch(even, o0);
@@ -335,32 +385,29 @@ int wr_adapters_impl(wr_ctx* ctx, const void* x, int x_dtype, int64_t rows, int6
                      const int32_t* ranks, const int32_t* starts, const int32_t* ids, int32_t n_seqs, int64_t most,
                      const void* base, int64_t ldb, void* y, int y_dtype, int64_t ldy) {
   AdapterArgs a{starts, ids, ranks, scales, static_cast<const uint16_t*>(A), static_cast<const uint16_t*>(B),
-                static_cast<uint16_t*>(ctx->ws), rows, n, outs, most, ldx, ldb, ldy, rank > 0 ? adapters : 0, rank, (rank + 7) / 8 * 8, 1};
+                static_cast<uint16_t*>(ctx->ws), rows, n, outs, most, ldx, ldb, ldy, rank > 0 ? adapters : 0, rank, (rank + 7) / 8 * 8, n_seqs};
   if (a.adapters > 0 && ctx->ws_bytes < wr_adapters_ws_bytes(rows, n, rank)) return WR_EWORKSPACE;
   most = std::min(most, rows);
-  // single tokens and steps of a few: 16 rows a tile; else 32 for the first product and four times 32 (16 of wide adapters, whose
-  // parts fill the registers) for the second
+  // single tokens and steps of a few: 16 rows a tile; else 32 for the first product, and for the second a wave's 32 (16 of wide adapters,
+  // whose parts fill the registers)
   const bool many = most > 16;
-  const int64_t in_rows = many ? 32 : 16, out_rows = !many ? 16 : rank > 64 ? 64 : 128;
-  const int64_t in_tiles = (most + in_rows - 1) / in_rows, out_tiles = (most + out_rows - 1) / out_rows;
-  const int nt = rank <= 16 ? 1 : rank <= 32 ? 2 : 4;
+  auto tiles_of = [&](int64_t r) { return std::min((most + r - 1) / r * n_seqs, (rows + n_seqs * (r - 1)) / r); };  // at most
+  const int64_t in_tiles = tiles_of(many ? 32 : 16), out_tiles = many ? (tiles_of(rank > 64 ? 16 : 32) + 3) / 4 : tiles_of(16);
+  const int nt = rank <= 16 ? 1 : 2;
   const int64_t rank_tiles = (rank + 16 * nt - 1) / (16 * nt);
   const int64_t out_steps = (outs + (many ? 63 : 255)) / (many ? 64 : 256);
   // Many rows: as many workgroups as two on each compute unit, which is what registers leave room for; more would be a second, mostly
   // empty round.  Few: up to four on each.
-  const int64_t row_tiles = std::min<int64_t>(out_tiles * n_seqs, rows / out_rows + n_seqs);
-  const int64_t out_parts = std::max<int64_t>(1, std::min(out_steps, (many ? 2 : 4) * (int64_t)ctx->num_cu / row_tiles));
-  if (std::max(in_tiles * rank_tiles * 512, out_tiles * out_parts * 256) > kMostThreads / n_seqs) return WR_EUNSUPPORTED;
+  const int64_t out_parts = std::max<int64_t>(1, std::min(out_steps, (many ? 2 : 4) * (int64_t)ctx->num_cu / out_tiles));
+  if (std::max(in_tiles * rank_tiles * 512, out_tiles * out_parts * 256) > kMostThreads) return WR_EUNSUPPORTED;
   if (a.adapters > 0) {
-    a.tiles = (uint32_t)in_tiles;
-    const dim3 grid((uint32_t)(in_tiles * n_seqs * rank_tiles));
+    const dim3 grid((uint32_t)(in_tiles * rank_tiles));
     auto go = [&](auto type, auto m) {
       using X = decltype(type);
       constexpr int MT = decltype(m)::value;
       const X* xp = static_cast<const X*>(x);
       if (nt == 1) hipLaunchKernelGGL((adapters_in_kernel<X, MT, 1>), grid, dim3(512), 0, ctx->stream, a, xp, (uint32_t)rank_tiles);
-      else if (nt == 2) hipLaunchKernelGGL((adapters_in_kernel<X, MT, 2>), grid, dim3(512), 0, ctx->stream, a, xp, (uint32_t)rank_tiles);
-      else hipLaunchKernelGGL((adapters_in_kernel<X, MT, 4>), grid, dim3(512), 0, ctx->stream, a, xp, (uint32_t)rank_tiles);
+      else hipLaunchKernelGGL((adapters_in_kernel<X, MT, 2>), grid, dim3(512), 0, ctx->stream, a, xp, (uint32_t)rank_tiles);
     };
     auto with_rows = [&](auto type) {
       if (many) go(type, std::integral_constant<int, 2>{});
@@ -370,8 +417,7 @@ int wr_adapters_impl(wr_ctx* ctx, const void* x, int x_dtype, int64_t rows, int6
     else with_rows(float{});
     WR_CHECK_LAUNCH();
   }
-  a.tiles = (uint32_t)out_tiles;
-  const dim3 grid((uint32_t)(out_tiles * n_seqs * out_parts));
+  const dim3 grid((uint32_t)(out_tiles * out_parts));
   auto go = [&](auto type, auto m, auto ks, auto by_rows) {
     using Y = decltype(type);
     hipLaunchKernelGGL((adapters_out_kernel<Y, decltype(m)::value, decltype(ks)::value, decltype(by_rows)::value>), grid, dim3(256), 0,
