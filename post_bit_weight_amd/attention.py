@@ -74,7 +74,8 @@ class Int8Attention:
 
     def __call__(self, resid, branch, seqs, positions=None, ids=None):
         """(x', the attention's output) for the new tokens of the sequences (wr.Sequences; their rows are branch's, in order).
-        positions: int32, rows or axes x rows, for the rotation; ids: int32, the adapter of every sequence."""
+        positions: int32, rows or axes x rows, for the rotation; ids: int32, the adapter of every sequence.  The outputs of rows of no
+        sequence mean nothing."""
         rows = branch.shape[0]
         if rows > self.most:
             raise ValueError(f"{rows} tokens, but space for {self.most}")

@@ -4,6 +4,9 @@ The oracle takes keys and values as the cache holds them (read back), everything
 fp64.  Rounding to 8 bits costs each of the two products' two factors 0.6 % to 1 % of the rms, as in the MLP's test; the
 queries' error changes a score by a part of itself, which the softmax passes on at most twice: 4 % in all, held to 6 %.
 """
+import os
+import re
+
 import numpy as np
 import pytest
 import torch
@@ -12,6 +15,7 @@ import oracle
 from attention_inputs import BF16, F32, int32
 
 pytestmark = pytest.mark.gpu
+README = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")
 
 
 def build(heads, cache_heads, dim, n, page, group, most, seqs, adapted, window=0, stream=None, seed=1, interleaved=False):
@@ -141,3 +145,25 @@ def test_command_prints_a_line(capsys):
     args = "--sequences 3 --prompt 70 --steps 4 --hidden 256 --heads 4 --cache-heads 2 --dim 64 --page 16 --group 32 --adapters 2 --rank 4"
     assert attention.main(args.split()) == 0
     assert "us_per_step" in capsys.readouterr().out
+
+
+@pytest.mark.skipif(not os.path.exists(README), reason="this copy is without its documents")
+def test_the_calls_in_the_readme():
+    """Its step of four sequences runs, and the attention is the oracle's: one token each, which a softmax gives back."""
+    from post_bit_weight_amd import _lib as wr
+    with open(README) as f:
+        code = re.findall(r"```python\n(.*?)```", f.read(), re.S)[1]
+    g = torch.Generator(device="cuda").manual_seed(3)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(BF16)  # noqa: E731
+    space = dict(wr=wr, context=wr.Context(0), starts=int32(range(5)), lengths=int32([1] * 4), table=int32([[3], [0], [7], [5]]), q=r(4, 4096),
+                 k=r(4, 1024), v=r(4, 1024), out=torch.empty(4, 4096, dtype=BF16, device="cuda"), positions=int32([0] * 4),
+                 freqs=torch.ones(64, dtype=torch.float64, device="cuda"), A=r(2, 8, 4096), B=r(2, 64, 8), scales=torch.ones(2, device="cuda"),
+                 ids=int32([-1] * 4), y=r(4, 64))
+    before = space["y"].clone()
+    exec(code, space)
+    torch.cuda.synchronize()
+    x = space["v"].double().cpu().numpy().reshape(4, 8, 128)
+    want = np.repeat(oracle.kv_values(*oracle.kv_codes(x, 64), 64), 4, axis=1).reshape(4, -1)
+    # the value and the weight rounded to fp16, the output to bf16
+    assert (np.abs(h64(space["out"]) - want) <= (2.0 ** -10 + 2.0 ** -8) * np.abs(want) + 2.0 ** -24).all()
+    assert torch.equal(space["y"], before)  # no request has an adapter
