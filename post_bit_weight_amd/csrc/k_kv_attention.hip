@@ -208,7 +208,7 @@ __global__ __launch_bounds__(256, groups_per_cu(DIM, NT)) void attend_rows_kerne
     // 2^e <= big < 2^(e + 1), within what has a reciprocal in fp32
     const int e = min(max((int)(__float_as_uint(big) >> 23) - 127, -120), 120);
     const float down = copysignf(__uint_as_float((uint32_t)(127 - e) << 23), a.scale);
-    unit[n] = fabsf(a.scale) * __uint_as_float((uint32_t)(127 + e) << 23);
+    unit[n] = fmaxf(fabsf(a.scale) * __uint_as_float((uint32_t)(127 + e) << 23), 0x1p-126f);  // -infinity times it is no NaN
 #pragma unroll
     for (int sl = 0; sl < SL; ++sl)
 #pragma unroll
@@ -251,28 +251,24 @@ __global__ __launch_bounds__(256, groups_per_cu(DIM, NT)) void attend_rows_kerne
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float p[2][4];
-      int ok = 255;
 #pragma unroll
       for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) p[tt][i] = score[n][tt][i];
       if (!whole) {
         asm volatile("");  // a branch, not selects in every step
-        ok = 0;
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int t = t0 + 16 * tt + 4 * g + i;
-            const bool in = there[tt] && t >= mine[n].lo && t < mine[n].hi;
-            ok |= in << (4 * tt + i);
-            if (!in) p[tt][i] = -INFINITY;
+            if (!(there[tt] && t >= mine[n].lo && t < mine[n].hi)) p[tt][i] = -INFINITY;
           }
       }
       float high = fmaxf(fmaxf(fmaxf(p[0][0], p[0][1]), fmaxf(p[0][2], p[0][3])),
                          fmaxf(fmaxf(p[1][0], p[1][1]), fmaxf(p[1][2], p[1][3])));
       high = max_of_four(high);
-      high = high == -INFINITY ? kLowest : high * unit[n];
+      high = fmaxf(high * unit[n], kLowest);
       if (__builtin_amdgcn_ballot_w64(high > top[n]) != 0) {
         const float now = fmaxf(high, top[n]);
         const float keep = exp2_fast(top[n] - now);
@@ -289,14 +285,6 @@ __global__ __launch_bounds__(256, groups_per_cu(DIM, NT)) void attend_rows_kerne
       for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) p[tt][i] = exp2_fast(fmaf(p[tt][i], unit[n], -less));
-      if (!whole) {
-        asm volatile("");
-#pragma unroll
-        for (int tt = 0; tt < 2; ++tt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (!(ok >> (4 * tt + i) & 1)) p[tt][i] = 0.0f;
-      }
 #pragma unroll
       for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
