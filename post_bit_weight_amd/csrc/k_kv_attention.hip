@@ -126,9 +126,10 @@ __global__ __launch_bounds__(256, groups_per_cu(DIM, NT)) void attend_rows_kerne
   const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int col = lane % 16, g = lane / 16;
   const uint32_t groups = gridDim.x;
-  const Found f0 = find_units(a, found, [&](uint32_t total) { return first_unit(total, blockIdx.x, groups); });
-  uint32_t x = __builtin_amdgcn_readfirstlane(first_unit(f0.total, blockIdx.x, groups));
-  const uint32_t x1 = __builtin_amdgcn_readfirstlane(first_unit(f0.total, blockIdx.x + 1, groups));
+  const Found f0 = find_units(a, found, [&](uint32_t total) { return Runs(total, groups).first(blockIdx.x); });
+  const Runs runs(__builtin_amdgcn_readfirstlane(f0.total), groups);
+  uint32_t x = runs.first(blockIdx.x);
+  const uint32_t x1 = runs.first(blockIdx.x + 1);
   int seq = __builtin_amdgcn_readfirstlane(f0.seq);
   uint32_t y = x - __builtin_amdgcn_readfirstlane(f0.before);  // the unit's number in its sequence
   while (x < x1 && seq < a.kv.n) {
@@ -142,7 +143,7 @@ __global__ __launch_bounds__(256, groups_per_cu(DIM, NT)) void attend_rows_kerne
   const int head = y / units, unit0 = y % units;
   const int taken = min(units - unit0, x1 - x);
   if (unit0 == 0 && a.who && threadIdx.x == 0)
-    a.who[who_at(a, s, 0, head)] = u32x2{blockIdx.x, group_of(f0.total, x + units - 1, groups)};
+    a.who[who_at(a, s, 0, head)] = u32x2{blockIdx.x, runs.group_of(x + units - 1)};
   x += taken;
   y += taken;
   const Span all = seen(a, s, 0, s.fresh - 1);

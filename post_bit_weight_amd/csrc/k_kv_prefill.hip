@@ -41,10 +41,9 @@ struct Shared {
   uint32_t upto[kPairs], waves[kThreads / kWave], pair;  // units of the pairs up to this one, of each wave's; of the first unit
 };
 
-// Shares the work out: the first unit of this workgroup, the one behind its last, and the pair of the first.
+// Shares the work out: all units, and the pair of this workgroup's first.
 template <int DIM>
-__device__ __forceinline__ void find_pair(const AttentionArgs& a, uint32_t tiles, Shared<DIM>& f, uint32_t& total, uint32_t& x, uint32_t& x1,
-                                          uint32_t& pair) {
+__device__ __forceinline__ void find_pair(const AttentionArgs& a, uint32_t tiles, Shared<DIM>& f, uint32_t& total, uint32_t& pair) {
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const uint32_t seq = threadIdx.x / tiles, tile = threadIdx.x - seq * tiles;
   uint32_t mine = 0;
@@ -69,14 +68,11 @@ __device__ __forceinline__ void find_pair(const AttentionArgs& a, uint32_t tiles
     total += f.waves[w];
   }
   f.upto[threadIdx.x] = upto;
-  x = first_unit(total, blockIdx.x, gridDim.x);
-  x1 = first_unit(total, blockIdx.x + 1, gridDim.x);
+  total = __builtin_amdgcn_readfirstlane(total);
+  const uint32_t x = Runs(total, gridDim.x).first(blockIdx.x);
   if (x < upto && x >= upto - mine) f.pair = threadIdx.x;
   __syncthreads();
-  total = __builtin_amdgcn_readfirstlane(total);
-  x = __builtin_amdgcn_readfirstlane(x);
-  x1 = __builtin_amdgcn_readfirstlane(x1);
-  pair = x < x1 ? __builtin_amdgcn_readfirstlane(f.pair) : 0;
+  pair = x < total ? __builtin_amdgcn_readfirstlane(f.pair) : 0;
 }
 
 // SHARED: every workgroup takes an equal share of all units; else a tile of rows and head.  Two workgroups fit a compute unit at dim
@@ -89,8 +85,11 @@ __global__ __launch_bounds__(kThreads, DIM == 64 && !SHARED ? 4 : 2) void attend
   Shared<DIM>& shared = *reinterpret_cast<Shared<DIM>*>(lds);
   T* buf = shared.tile;
 
-  uint32_t total = 1, x = 0, x1 = 1, pair = 0;
-  if constexpr (SHARED) find_pair<DIM>(a, tiles, shared, total, x, x1, pair);
+  uint32_t total = 1, pair = 0;
+  if constexpr (SHARED) find_pair<DIM>(a, tiles, shared, total, pair);
+  const Runs runs(total, SHARED ? gridDim.x : 1);
+  uint32_t x = SHARED ? runs.first(blockIdx.x) : 0;
+  const uint32_t x1 = SHARED ? runs.first(blockIdx.x + 1) : 1;
   for (;;) {
   if (SHARED && x >= x1) return;
   int head, seq, tile, unit0 = 0;
@@ -124,7 +123,7 @@ __global__ __launch_bounds__(kThreads, DIM == 64 && !SHARED ? 4 : 2) void attend
   if (s.fresh <= 0 || tile * kRows >= s.fresh * a.share) return;  // only of those that were not found
   const RowTile rt = row_tile(a, s, tile, kRows);
   if (SHARED && unit0 == 0 && threadIdx.x == 0)
-    a.who[who_at(a, s, rt.first, head)] = u32x2{blockIdx.x, group_of(total, item + units - 1, gridDim.x)};
+    a.who[who_at(a, s, rt.first, head)] = u32x2{blockIdx.x, runs.group_of(item + units - 1)};
   const Span all = seen(a, s, rt.first, rt.last);
   const int begin = (all.lo & ~15) + (SHARED ? unit0 << a.unit_shift : 0);
   const int end = !SHARED || taken == units ? all.hi : min(all.hi, begin + (int)(taken << a.unit_shift));

@@ -97,14 +97,16 @@ constexpr int kUnitShift = 7;
 __device__ __forceinline__ uint32_t units_in(const AttentionArgs& a, const Span& all) {
   return max(1u, (uint32_t)(all.hi - (all.lo & ~15) + (1 << a.unit_shift) - 1) >> a.unit_shift);
 }
-// Unit where a workgroup begins; those beyond one for each unit have nothing.
-__device__ __forceinline__ uint32_t first_unit(uint32_t total, uint32_t group, uint32_t groups) {
-  groups = min(groups, total);
-  return group >= groups ? total : (uint32_t)((uint64_t)total * group / groups);
-}
-__device__ __forceinline__ uint32_t group_of(uint32_t total, uint32_t unit, uint32_t groups) {
-  return (uint32_t)((((uint64_t)unit + 1) * min(groups, total) - 1) / total);
-}
+// Runs of the units: `each` for every workgroup and one more for the first `more`.
+struct Runs {
+  uint32_t total, each, more;
+  __device__ __forceinline__ Runs(uint32_t total, uint32_t groups) : total(total), each(total / groups), more(total - each * groups) {}
+  __device__ __forceinline__ uint32_t first(uint32_t group) const { return group * each + min(group, more); }
+  __device__ __forceinline__ uint32_t group_of(uint32_t unit) const {
+    const uint32_t longer = more * (each + 1);
+    return unit < longer ? unit / (each + 1) : more + (unit - longer) / each;
+  }
+};
 // A workgroup has at most one part that others began, its slot 0, and one that others go on with, its slot 1.
 __device__ __forceinline__ int64_t part_slot(uint32_t group, bool first) { return (int64_t)group * 2 + first; }
 __device__ __forceinline__ int64_t who_at(const AttentionArgs& a, const KvSeq& s, int query, int head) {
