@@ -14,6 +14,10 @@ constexpr int kPaged = 1024;  // tokens whose pages a wave holds: one of 64 tile
 // heads of 128, shared out and whole: one sequence of 256 tokens 10.1 and 7.7 us, 16 of 512 13.4 and 11.1, 64 of up to 2048 38 and 31; one
 // of 1024 10.5 and 14.4, 16 of up to 2048 21 and 24.
 constexpr int kWholeShift = 11;
+// Many short ones: each wave has its own, and twelve are on their way on a compute unit instead of three.  Dim 128, eight heads,
+// together and alone: 300 sequences of up to 128 tokens 30 and 18 us, of up to 1024 71 and 67; 200 of up to 512 32 and 29, of up to
+// 1024 46 and 53; 100 of up to 256 16 and 15, of up to 512 19 and 23.
+constexpr int kAloneTokens = 256;  // for as many as there are workgroups, twice that for twice as many
 
 // What a lane holds of 32 tokens in two tiles of 16.
 template <int DIM, int GROUP>
@@ -60,9 +64,9 @@ struct Found {
   uint32_t before;  // units of the sequences before it
 };
 struct FoundShared {
-  uint32_t waves[4], seq, before;
+  uint32_t waves[4], seq[4], before[4];
 };
-// The sequence of unit at(total).  For all 256 threads.
+// The sequence of unit at(total, wave).  For all 256 threads.
 template <typename F>
 __device__ __forceinline__ Found find_units(const AttentionArgs& a, FoundShared& f, F&& at) {
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
@@ -74,7 +78,7 @@ __device__ __forceinline__ Found find_units(const AttentionArgs& a, FoundShared&
       if (lane >= m) upto += below;
     }
     const uint32_t total = __builtin_amdgcn_readlane(upto, a.kv.n - 1);
-    const uint64_t past = __builtin_amdgcn_ballot_w64(upto > at(total));  // the first that reaches past it
+    const uint64_t past = __builtin_amdgcn_ballot_w64(upto > at(total, wave));  // the first that reaches past it
     const int sequence = __builtin_amdgcn_readfirstlane(past ? __builtin_ctzll(past) : 0);
     return Found{total, (uint32_t)sequence, (uint32_t)__builtin_amdgcn_readlane(upto - mine, sequence)};
   }
@@ -96,40 +100,46 @@ __device__ __forceinline__ Found find_units(const AttentionArgs& a, FoundShared&
     total += f.waves[w];
     if (w < wave) before += f.waves[w];
   }
-  const uint32_t x = at(total);
-  if (x >= before && x < before + mine) {
-    int i = begin;
-    for (; i + 1 < end; ++i) {
-      const uint32_t u = units_of(a, kv_seq(a.kv, i)) * a.kv.heads;
-      if (x < before + u) break;
-      before += u;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const uint32_t x = at(total, w);
+    if (x >= before && x < before + mine) {
+      uint32_t b = before;
+      int i = begin;
+      for (; i + 1 < end; ++i) {
+        const uint32_t u = units_of(a, kv_seq(a.kv, i)) * a.kv.heads;
+        if (x < b + u) break;
+        b += u;
+      }
+      f.seq[w] = i;
+      f.before[w] = b;
     }
-    f.seq = i;
-    f.before = before;
   }
   __syncthreads();
-  return Found{total, f.seq, f.before};
+  return Found{total, f.seq[wave], f.before[wave]};
 }
 // ---------------------------------------------------------------- the rows of a step
 // Workgroups that a compute unit holds at once, by the registers they take; as many are launched, since more would wait
 // and leave the end uneven.
 constexpr int groups_per_cu(int dim, int nt) { return dim == 64 ? 5 - nt : dim * nt == 128 ? 3 : dim * nt == 256 ? 2 : 1; }
 
-template <int DIM, int GROUP, int NT>
+// WAVES waves work on a unit together: all four of the workgroup, or each by itself.
+template <int DIM, int GROUP, int NT, int WAVES>
 __global__ __launch_bounds__(256, groups_per_cu(DIM, NT)) void attend_rows_kernel(AttentionArgs a) {
   constexpr int SL = DIM / 32;      // slices of 32 dims: dwords a lane loads of a tile
   constexpr int NG = DIM / GROUP;
-  constexpr int WAVES = 4;
-  __shared__ __attribute__((aligned(16))) float sums[16 * NT][DIM + 4];
+  __shared__ __attribute__((aligned(16))) float sums[WAVES > 1 ? 16 * NT : 1][DIM + 4];
   __shared__ float tops[WAVES][16 * NT], dens[WAVES][16 * NT];
   __shared__ FoundShared found;
-  const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int lane = threadIdx.x % kWave, of_four = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), wave = of_four % WAVES;
   const int col = lane % 16, g = lane / 16;
-  const uint32_t groups = gridDim.x;
-  const Found f0 = find_units(a, found, [&](uint32_t total) { return Runs(total, groups).first(blockIdx.x); });
+  const uint32_t groups = gridDim.x * (4 / WAVES), group = blockIdx.x * (4 / WAVES) + of_four / WAVES;
+  const Found f0 = find_units(a, found, [&](uint32_t total, int w) {
+    return Runs(total, groups).first(blockIdx.x * (4 / WAVES) + w / WAVES);
+  });
   const Runs runs(__builtin_amdgcn_readfirstlane(f0.total), groups);
-  uint32_t x = runs.first(blockIdx.x);
-  const uint32_t x1 = runs.first(blockIdx.x + 1);
+  uint32_t x = runs.first(group);
+  const uint32_t x1 = runs.first(group + 1);
   int seq = __builtin_amdgcn_readfirstlane(f0.seq);
   uint32_t y = x - __builtin_amdgcn_readfirstlane(f0.before);  // the unit's number in its sequence
   while (x < x1 && seq < a.kv.n) {
@@ -143,7 +153,7 @@ __global__ __launch_bounds__(256, groups_per_cu(DIM, NT)) void attend_rows_kerne
   const int head = y / units, unit0 = y % units;
   const int taken = min(units - unit0, x1 - x);
   if (unit0 == 0 && a.who && threadIdx.x == 0)
-    a.who[who_at(a, s, 0, head)] = u32x2{blockIdx.x, runs.group_of(x + units - 1)};
+    a.who[who_at(a, s, 0, head)] = u32x2{group, runs.group_of(x + units - 1)};
   x += taken;
   y += taken;
   const Span all = seen(a, s, 0, s.fresh - 1);
@@ -359,11 +369,34 @@ __global__ __launch_bounds__(256, groups_per_cu(DIM, NT)) void attend_rows_kerne
     t0 += 2 * kRound;
   }
 
-  // the waves' parts: one maximum, then the sums in the waves' order
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     den[n] += __shfl_xor(den[n], 16);
     den[n] += __shfl_xor(den[n], 32);
+  }
+  if constexpr (WAVES == 1) {  // nothing to share
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const uint32_t m = 16 * n + col;
+      if (m >= (uint32_t)(s.fresh * a.share)) continue;
+      const float inv = den[n] == 0.0f ? 0.0f : 1.0f / den[n];
+      uint16_t* o = a.out + (int64_t)(s.row + m / (uint32_t)a.share) * a.ldo + (int64_t)(head * a.share + m % (uint32_t)a.share) * DIM;
+#pragma unroll
+      for (int k = 0; k < SL; ++k)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const f32x4 v = acc[n][half][k];
+          u32x2_any w;
+          w[0] = pack_bf16(v[0] * inv, v[1] * inv);
+          w[1] = pack_bf16(v[2] * inv, v[3] * inv);
+          *reinterpret_cast<u32x2_any*>(o + half * (DIM / 2) + 16 * k + 4 * g) = w;
+        }
+    }
+    continue;
+  }
+  // the waves' parts: one maximum, then the sums in the waves' order
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
     if (g == 0) {
       tops[wave][16 * n + col] = top[n];
       dens[wave][16 * n + col] = den[n];
@@ -611,17 +644,21 @@ int wr_kv_attention_impl(wr_ctx* ctx, const wr_kv_cache& c, const wr_kv_seqs& s,
   if (whole) a.unit_shift = kWholeShift;
   const int64_t most_units = (int64_t)s.n * c.heads * (((span - 1) >> a.unit_shift) + 1);
   if (most_units > 1 << 30) return WR_EUNSUPPORTED;
-  const int groups = (int)std::min<int64_t>(groups_per_cu(c.dim, tile / 16) * std::min(ctx->num_cu, kMostCUs), most_units);
+  const int64_t most_groups = (int64_t)groups_per_cu(c.dim, tile / 16) * std::min(ctx->num_cu, kMostCUs);
+  const bool alone = whole && tile == 16 && most_units >= most_groups && span * most_groups <= kAloneTokens * most_units;
+  const int groups = (int)std::min(most_groups, alone ? (most_units + 3) / 4 : most_units);
   if (!whole) {
     const int rc = wr_kv_parts(ctx, a, c.dim, (int64_t)groups * 2 * tile);
     if (rc != WR_OK) return rc;
   }
   const bool there = kv_form(c.dim, c.group, [&](auto d, auto g) {
     constexpr int D = decltype(d)::value, G = decltype(g)::value;
-    if (tile == 16)
-      hipLaunchKernelGGL((attend_rows_kernel<D, G, 1>), dim3(groups), dim3(256), 0, ctx->stream, a);
+    if (alone)
+      hipLaunchKernelGGL((attend_rows_kernel<D, G, 1, 1>), dim3(groups), dim3(256), 0, ctx->stream, a);
+    else if (tile == 16)
+      hipLaunchKernelGGL((attend_rows_kernel<D, G, 1, 4>), dim3(groups), dim3(256), 0, ctx->stream, a);
     else
-      hipLaunchKernelGGL((attend_rows_kernel<D, G, 2>), dim3(groups), dim3(256), 0, ctx->stream, a);
+      hipLaunchKernelGGL((attend_rows_kernel<D, G, 2, 4>), dim3(groups), dim3(256), 0, ctx->stream, a);
   });
   if (!there) return WR_EUNSUPPORTED;
   WR_CHECK_LAUNCH();

@@ -411,3 +411,25 @@ def test_two_contexts_on_two_streams(wr):
             wr.wr_kv_attention(c, p.cache, s, q, o[i], 0.1)
     torch.cuda.synchronize()
     assert all(torch.equal(o, a) for a, each in zip(alone, outs) for o in each)
+
+
+@pytest.mark.parametrize("dim,group,window", [(64, 32, 0), (128, 64, 0), (128, 128, 9), (256, 64, 0)])
+@pytest.mark.parametrize("n", [60, 300])
+def test_many_short_sequences(wr, ctx, n, dim, group, window):
+    """So many that each wave has its own: lengths from 1, sequences without rows, absent pages and rows behind the last."""
+    heads, share, page, rng = 20, 2, 16, np.random.default_rng(n + dim)
+    lengths = [int(x) for x in rng.integers(1, 70, n)]
+    new = [int(x) for x in np.minimum(rng.integers(0, 3, n), lengths)]
+    p = Paged(wr, lengths, heads, dim, page, group, seed=n)
+    k, v = rows_of(sum(lengths), heads * dim, 1), rows_of(sum(lengths), heads * dim, 2)
+    p.fill(ctx, k.cuda(), v.cuda())
+    absent = np.zeros(sum(lengths), bool)
+    for s in range(0, n, 7):
+        p.table[s, 0] = -1
+        at = sum(lengths[:s])
+        absent[at:at + min(page, lengths[s])] = True
+    q = rows_of(sum(new) + 3, heads * share * dim, 3).cuda()
+    out = torch.full_like(q, 77.0)
+    scale = float(np.float32(dim ** -0.5))
+    wr.wr_kv_attention(ctx, p.cache, p.sequences(new), q, out, scale, window=window)
+    check(q, out, cached(k, heads, dim, group), cached(v, heads, dim, group), list(zip(new, lengths)), heads, dim, scale, True, window, absent)
