@@ -545,7 +545,7 @@ int wr_kv_attention(wr_ctx* ctx, const wr_kv_cache* cache, const wr_kv_seqs* seq
   if (share > kShareMax || (int64_t)seqs->most_new * share > kTokensMax) return WR_EUNSUPPORTED;
   if (nothing) return WR_OK;
   const int64_t n = (int64_t)heads * cache->dim;
-  if (!q || !out || !rows_ok(q, WR_BF16, rows, n, ldq) || !rows_ok(out, WR_BF16, rows, n, ldo)) return WR_EINVAL;
+  if (!q || !out || q == out || !rows_ok(q, WR_BF16, rows, n, ldq) || !rows_ok(out, WR_BF16, rows, n, ldo)) return WR_EINVAL;
   DeviceScope ds(ctx->device);
   if (!ds.ok) return WR_EHIP;
   return wr_kv_attention_impl(ctx, *cache, of_rows(*seqs, rows), q, ldq, rows, heads, scale, flags, window, out, ldo);

@@ -147,3 +147,7 @@ def test_lengths_that_an_int32_would_not_hold(lib, wr):
         assert lib.wr_kv_attention(CTX, ctypes.byref(cache(wr)), ctypes.byref(s), *ATTEND.values()) == EUNSUPPORTED
     for scale in (1.7e38, -3e38):
         assert lib.wr_kv_attention(CTX, ctypes.byref(cache(wr)), ctypes.byref(seqs(wr)), *dict(ATTEND, scale=scale).values()) == EUNSUPPORTED
+
+
+def test_attention_does_not_write_over_its_queries(lib, wr):
+    assert lib.wr_kv_attention(CTX, ctypes.byref(cache(wr)), ctypes.byref(seqs(wr)), *dict(ATTEND, q=A, out=A).values()) == EINVAL

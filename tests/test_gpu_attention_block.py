@@ -167,3 +167,18 @@ def test_the_calls_in_the_readme():
     # the value and the weight rounded to fp16, the output to bf16
     assert (np.abs(h64(space["out"]) - want) <= (2.0 ** -10 + 2.0 ** -8) * np.abs(want) + 2.0 ** -24).all()
     assert torch.equal(space["y"], before)  # no request has an adapter
+
+
+def test_rows_behind_the_last_sequence_and_no_rows():
+    """A padded batch gives the sequences' rows what they get without padding; a batch of none gives none."""
+    wr, ctx, block, cache, table, p, pool, weights = build(8, 2, 64, 256, 16, 32, 60, 2, True)
+    g = torch.Generator().manual_seed(8)
+    resid, branch = torch.randn(50, 256, generator=g).cuda(), torch.randn(50, 256, generator=g).to(BF16).cuda()
+    positions, ids = int32(np.stack([np.arange(50), np.arange(50)])), int32([1, -1])
+    seqs = wr.Sequences(int32([0, 30, 37]), int32([30, 7]), table, 30, 60)
+    whole = block(resid, branch, seqs, positions, ids)
+    alone = block(resid[:37], branch[:37], seqs, positions[:, :37].contiguous(), ids)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a[:37], b) for a, b in zip(whole, alone))
+    none = block(resid[:0], branch[:0], seqs, positions[:, :0].contiguous(), ids)
+    assert none[0].shape == (0, 256) and none[1].shape == (0, 256)

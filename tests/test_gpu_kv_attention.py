@@ -433,3 +433,27 @@ def test_many_short_sequences(wr, ctx, n, dim, group, window):
     scale = float(np.float32(dim ** -0.5))
     wr.wr_kv_attention(ctx, p.cache, p.sequences(new), q, out, scale, window=window)
     check(q, out, cached(k, heads, dim, group), cached(v, heads, dim, group), list(zip(new, lengths)), heads, dim, scale, True, window, absent)
+
+
+@pytest.mark.parametrize("new", [1, 2, 40])
+def test_sequences_that_share_pages(wr, ctx, new):
+    """Three sequences begin with the same 64 positions; each then has its own."""
+    lengths, heads, dim, page, group = [64 + 45, 64 + 80, 64 + 41], 2, 128, 32, 64
+    p = Paged(wr, lengths, heads, dim, page, group)
+    k, v = rows_of(sum(lengths), heads * dim, 1), rows_of(sum(lengths), heads * dim, 2)
+    for t in (k, v):
+        t[lengths[0]:lengths[0] + 64] = t[lengths[0] + lengths[1]:lengths[0] + lengths[1] + 64] = t[:64]
+    p.fill(ctx, k.cuda(), v.cuda())
+    p.cache.buf.view(p.pages, -1)[torch.from_numpy(p.table[1:, :2].reshape(-1).astype(np.int64)).cuda()] = 255  # their own copies are gone
+    p.table[1:, :2] = p.table[0, :2]
+    q = rows_of(3 * new, heads * 3 * dim, 3).cuda()
+    out = torch.empty_like(q)
+    wr.wr_kv_attention(ctx, p.cache, p.sequences([new] * 3), q, out, 0.1)
+    check(q, out, cached(k, heads, dim, group), cached(v, heads, dim, group), [(new, n) for n in lengths], heads, dim, float(np.float32(0.1)), True, 0)
+
+
+def test_the_queries_are_not_the_output(wr, ctx):
+    p = Paged(wr, [32], 2, 64, 16, 32)
+    q = torch.zeros(2, 256, dtype=BF16, device="cuda")
+    with pytest.raises(wr.WringerError):
+        wr.wr_kv_attention(ctx, p.cache, p.sequences([2]), q, q, 0.125)
