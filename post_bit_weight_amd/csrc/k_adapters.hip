@@ -251,9 +251,18 @@ __global__ __launch_bounds__(256, KS <= 4 ? 2 : 1) void adapters_out_kernel(Adap
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
         const int r = 32 * ks + 8 * g;
-        t[m][ks][i] = from_lane(r < q.rank ? *reinterpret_cast<const u32x4*>(tr + i * a.wide + r) : u32x4{0, 0, 0, 0}, from);
+        t[m][ks][i] = r < q.rank ? *reinterpret_cast<const u32x4*>(tr + i * a.wide + r) : u32x4{0, 0, 0, 0};
       }
   }
+  auto turn = [&] {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) t[m][ks][i] = from_lane(t[m][ks][i], from);
+  };
+  bool turned = false;
   const uint16_t* bp = a.B + (int64_t)max(q.adapter, 0) * a.outs * a.rank;
   struct Step {  // what 64 outputs read
     Raw8<uint16_t> b[4][KS];
@@ -333,6 +342,8 @@ __global__ __launch_bounds__(256, KS <= 4 ? 2 : 1) void adapters_out_kernel(Adap
       };
       Step even, odd;
       fetch(even, o0);
+      turn();  // waits for t with the first step on its way
+      turned = true;
       for (;;) {
         fetch(odd, o0 + stride);
         multiply(even, o0, std::true_type{});
@@ -345,6 +356,7 @@ __global__ __launch_bounds__(256, KS <= 4 ? 2 : 1) void adapters_out_kernel(Adap
       }
     }
   }
+  if (!turned) turn();
   for (; o0 < a.outs; o0 += stride) {
     Step f;
     if (q.rank > 0) {
