@@ -784,7 +784,7 @@ def wr_adapters(ctx, x, A, B, scales, starts, ids, most, y, base=None, ranks=Non
     xcode, ycode = _type_code(x, "x"), _type_code(y, "y")
     px, ldx = _matrix(x, "x", x.dtype, xshape)
     py, ldy = _matrix(y, "y", y.dtype, (rows, outs))
-    pb, ldb = (None, outs) if base is None else _matrix(base, "base", y.dtype, (rows, outs))
+    pb, ldb = (None, outs) if base is None else (py, ldy) if base is y else _matrix(base, "base", y.dtype, (rows, outs))
     args = (ctx.handle, px, xcode, rows, n, ldx, _vector(A, "A", torch.bfloat16, adapters * rank * n),
             _vector(B, "B", torch.bfloat16, adapters * outs * rank), adapters, rank, outs,
             _vector(scales, "scales", torch.float32, adapters),

@@ -174,7 +174,8 @@ __global__ __launch_bounds__(kThreads, DIM == 64 && !SHARED ? 4 : 2) void attend
     const int64_t where = (there ? pages : 0) * page_bytes;
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-      const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)where, first16 + i), hi = __builtin_amdgcn_readlane((uint32_t)(where >> 32), first16 + i);
+      const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)where, first16 + i);
+      const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(where >> 32), first16 + i);
       const int in_page = (t0 + 16 * (first16 + i)) & (at.page_tokens - 1);
       const uint8_t* p = cache + ((uint64_t)hi << 32 | lo);
       const uint8_t *codes = p + in_page * (DIM / 2), *meta = p + in_page * 4;
@@ -429,7 +430,8 @@ int wr_kv_many_impl(wr_ctx* ctx, const wr_kv_cache& c, const wr_kv_seqs& s, Atte
   const int64_t idle = (most_groups - 1 - (busy - 1) % most_groups) * (usual >> a.unit_shift);
   const bool few = most_units > 1 && blocks * most_units <= most_groups;  // at most one unit for each
   a.begun = few ? 0 : 2;
-  const bool shared = blocks <= kMostTiles && blocks * (most_units + a.begun) <= 1 << 30 && (few || idle >= most_groups * (busy <= most_groups ? 2 : 16));
+  const bool worth = few || idle >= most_groups * (busy <= most_groups ? 2 : 16);
+  const bool shared = worth && blocks <= kMostTiles && blocks * (most_units + a.begun) <= 1 << 30;
   const int64_t groups = shared ? std::min<int64_t>(most_groups, blocks * most_units) : blocks;
   if (shared) {
     const int rc = wr_kv_parts(ctx, a, c.dim, groups * 2 * kRows);

@@ -457,3 +457,20 @@ def test_the_queries_are_not_the_output(wr, ctx):
     q = torch.zeros(2, 256, dtype=BF16, device="cuda")
     with pytest.raises(wr.WringerError):
         wr.wr_kv_attention(ctx, p.cache, p.sequences([2]), q, q, 0.125)
+
+
+@pytest.mark.parametrize("n,new", [(500, 1), (40, 50)])
+def test_more_sequences_than_rows(wr, n, new):
+    """All but two of many sequences are without new rows; a new context's workspace is sized for it."""
+    lengths = [30] * n
+    lengths[3], lengths[n - 2] = 3000, 1500
+    p = Paged(wr, lengths, 1, 64, 64, 64)
+    k, v = rows_of(sum(lengths), 64, 1), rows_of(sum(lengths), 64, 2)
+    c = wr.Context(0)
+    p.fill(c, k.cuda(), v.cuda())
+    fresh = [0] * n
+    fresh[3] = fresh[n - 2] = new
+    q = rows_of(2 * new, 256, 3).cuda()
+    out = torch.empty_like(q)
+    wr.wr_kv_attention(c, p.cache, p.sequences(fresh), q, out, 0.125)
+    check(q, out, cached(k, 1, 64, 64), cached(v, 1, 64, 64), list(zip(fresh, lengths)), 1, 64, 0.125, True, 0)
